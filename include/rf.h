@@ -94,7 +94,8 @@ extern "C" {
 typedef enum rf_status {
     RF_OK = 0,
     RF_ERR_INVALID_ARG = 1,     /* null pointer, bad size, in_dim not a whole number of blocks, ... */
-    RF_ERR_UNSUPPORTED_FMT = 2, /* fmt is not one of RF_Q4_0, RF_Q8_0, RF_MXFP4, RF_Q4_K, RF_Q6_K */
+    RF_ERR_UNSUPPORTED_FMT = 2, /* fmt is not one of RF_Q4_0, RF_Q8_0, RF_MXFP4, RF_Q4_K, RF_Q6_K;
+                                 * dtype not one of RF_F32, RF_F16, RF_BF16 */
     RF_ERR_NOT_PINNED = 3,      /* a host weight pointer is not page-locked */
     RF_ERR_ARENA_TOO_SMALL = 4, /* depth+1 one-row blocks do not fit the arena */
     RF_ERR_CUDA = 5,            /* a CUDA runtime call or launch failed */
@@ -576,9 +577,174 @@ RF_API rf_status rf_moe_ffn_noalloc(int fmt, const float *router_logits, int n_e
                                     int64_t n_ff, int64_t n_embd, int64_t block_rows,
                                     const float *x, float *y, void *stream);
 
+/* ------------------------------------------- between the projections */
+/* What a decoder layer computes around its projections and its FFN: the
+ * norms with the residual sums, the position rotation, the KV cache and the
+ * attention core.  (The source pages run these in their host frameworks and
+ * print no form; each is defined here.)
+ *
+ * Activations are fp32, fp16 or bf16 (one `dtype` per call, numbered like
+ * the GGML type ids); weights of norms, gates, sinks and the rotation's
+ * tables are fp32.  All arithmetic is in fp32 or wider sums; a 16-bit output
+ * is rounded once.  Innermost dimensions are contiguous; other strides are
+ * arguments, in elements.  Wide accesses are used where pointers and strides
+ * are 16-byte aligned, and narrow ones (with equal results) where not.
+ * flags: 0 or RF_CHAIN (weights and tables are static; the launch may be
+ * set up while the previous kernel on `stream` drains). */
+#define RF_F32 0
+#define RF_F16 1
+#define RF_BF16 30
+
+/* Norms before and after a block, with its gate and residual scale, for n_tok
+ * rows of n elements:
+ *     t  = x                                        without post_weight
+ *     t  = x * rsqrt(mean(x^2) + eps) * post_weight with it
+ *     r  = residual + scale * gate * t
+ *     y  = r * rsqrt(mean(r^2) + eps) * weight
+ * x, post_weight, gate, residual and weight may each be NULL and then drop
+ * out (t = 0, no norm, gate 1, residual 0, weight 1); residual_out (receives
+ * r) and y may each be NULL, not both.  y uses r before its rounding to
+ * dtype.  gate: n floats per row, rows ld_gate apart (0 = one row for all).
+ * residual_out may be residual and y may be x (with equal strides);
+ * other overlaps are not allowed.  post_weight, weight: n floats.
+ * Errors: RF_ERR_UNSUPPORTED_FMT (dtype); RF_ERR_INVALID_ARG (n < 1,
+ * n_tok < 0, a row stride below n, ld_gate neither 0 nor >= n, both outputs
+ * NULL, x and residual both NULL, eps negative or NaN, scale NaN, unknown
+ * flags); RF_ERR_MISALIGNED (a pointer not aligned to its element);
+ * RF_ERR_TOO_LARGE (n > 32768, n_tok > 2^31 - 1).  n_tok 0 is a no-op (the
+ * activation pointers may then be NULL). */
+RF_API rf_status rf_norm_residual(int dtype, int64_t n_tok, int64_t n, const void *x, int64_t ldx,
+                                  const float *post_weight, const float *gate, int64_t ld_gate,
+                                  float scale, const void *residual, int64_t ld_residual,
+                                  void *residual_out, int64_t ld_residual_out,
+                                  const float *weight, void *y, int64_t ldy, float eps,
+                                  unsigned flags, void *stream);
+
+/* Paged KV cache of 8-bit codes.  Keys and values of one head are held in
+ * blocks of 32 tokens; a block has one scale byte E and
+ * value = code * 2^(E-127), so every value is exact in fp32 (and a held code
+ * is re-rounded, never recomputed, when its block's scale grows).
+ *   k, v            int8  [n_pages][n_kv_heads][page_size][head_dim]
+ *   k_scale, v_scale uint8 [n_pages][n_kv_heads][page_size / 32]
+ * All device memory of the caller, 16-byte aligned (the scales: any
+ * alignment).  page_size: 32, 64, 128 or 256; head_dim: a multiple of 16 up
+ * to 256; n_kv_heads: 1..1024.  E = 255 marks a block that holds a value
+ * that is not a number, infinite or above 127 * 2^40: all of it reads as
+ * NaN.  Otherwise 87 <= E <= 167 when written by rf_kv_append; values below
+ * 2^-41 become 0. */
+typedef struct rf_kv_cache {
+    int8_t *k, *v;
+    uint8_t *k_scale, *v_scale;
+    int64_t n_pages;
+    int32_t page_size, n_kv_heads, head_dim;
+    int32_t reserved;   /* 0 */
+} rf_kv_cache;
+
+/* The tokens of one call, sequence after sequence: sequence s owns tokens
+ * [q_start[s], q_start[s+1]) of the call's n_tok, at positions past[s],
+ * past[s] + 1, ...; position p of sequence s lies in page
+ * page_table[s * table_stride + p / page_size].  The three arrays are device
+ * int32 (q_start: n_seq + 1, not decreasing; past: n_seq; n_seq 1..65536),
+ * read by the kernels, so that a captured step can be replayed with other
+ * lengths.  table_width: entries per sequence that may be read.  Tokens that
+ * belong to no sequence are allowed (a padded batch) and are skipped.  A
+ * token whose position has no page (a negative past, a position past the
+ * table, an entry outside [0, n_pages)), or none in the rotation's tables,
+ * is skipped too, and rf_device_status reports RF_ERR_INVALID_ARG. */
+typedef struct rf_kv_batch {
+    const int32_t *page_table;
+    const int32_t *past;
+    const int32_t *q_start;
+    int64_t table_stride;
+    int32_t table_width, n_seq, n_tok;
+    int32_t reserved;   /* 0 */
+} rf_kv_batch;
+
+/* Rotation styles: pairs (i, i + rot/2) or (2i, 2i + 1) of the first rot
+ * elements of a head. */
+#define RF_ROPE_HALF 0
+#define RF_ROPE_PAIRS 1
+
+/* Appends a batch's keys and values to the cache, rotated by position on the
+ * way, and rotates its queries, in one launch.
+ *   k, v: n_tok x n_kv_heads x head_dim (token and head strides given);
+ *   q: n_tok x n_heads x head_dim, or NULL; q_out: the rotated queries (may
+ *   be q with q's strides).
+ * Rotation of a pair (a, b) at position p, pair i, c = cos_tab[p][i],
+ * s = sin_tab[p][i]: (a*c - b*s, b*c + a*s), each product and the sum
+ * rounded in fp32; tables n_pos x rot/2, fp32; rot 0 (or a NULL table pair
+ * with rot 0): no rotation; v is never rotated.
+ * Block by block and head by head: E is the smallest byte in [87, 167] with
+ * max|new values| <= 127 * 2^(E-127); a block that already holds tokens
+ * keeps the larger of its E and this one, and its held codes become
+ * rint(code * 2^(E_old - E)); new codes are rint(value * 2^(127 - E)), ties
+ * to even.  A block's first token starts it afresh, whatever was in the
+ * page.  A page that a call writes may belong to one sequence only.
+ * Errors: RF_ERR_UNSUPPORTED_FMT (dtype); RF_ERR_INVALID_ARG (a null pointer
+ * or a field out of range, rot not a multiple of 8 in [0, head_dim], an
+ * unknown style or flag, strides below head_dim, n_heads < 1 with q);
+ * RF_ERR_MISALIGNED (codes not 16-byte aligned, other pointers not to their
+ * element); RF_ERR_TOO_LARGE (n_heads > 4096).  n_tok 0 is a no-op.  (A query is
+ * rotated, and q_out written, whenever its position lies in the tables.) */
+RF_API rf_status rf_kv_append(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype,
+                              const void *k, int64_t k_ld_tok, int64_t k_ld_head, const void *v,
+                              int64_t v_ld_tok, int64_t v_ld_head, const void *q,
+                              int64_t q_ld_tok, int64_t q_ld_head, void *q_out,
+                              int64_t q_out_ld_tok, int64_t q_out_ld_head, int n_heads,
+                              const float *cos_tab, const float *sin_tab, int64_t n_pos, int rot,
+                              int style, unsigned flags, void *stream);
+
+/* The values that the cache holds at the batch's positions: k_out, v_out are
+ * n_tok x n_kv_heads x head_dim floats, contiguous, 16-byte aligned; tokens
+ * that are skipped read as 0.  Errors: as rf_kv_append. */
+RF_API rf_status rf_kv_read(const rf_kv_cache *cache, const rf_kv_batch *batch, float *k_out,
+                            float *v_out, unsigned flags, void *stream);
+
+/* Attention of a batch's queries over the cache, which already holds the
+ * batch's own keys and values (rf_kv_append first).  Query head h reads K and
+ * V head h / (n_heads / n_kv_heads).  The query at position p sees positions
+ * j in (p - window, p] (window 0: all of [0, p]):
+ *     out = sum_j w_j v_j / (sum_j w_j + exp(sink_h - m)),
+ *     w_j = exp(scale * q.k_j - m)
+ * (sinks: n_heads floats, or NULL: no such term).  A row that sees nothing
+ * (its token belongs to no sequence or has no page) is 0.  Positions on
+ * invalid pages are not seen (and are reported, see rf_kv_batch); what lies
+ * beyond a sequence's last position in its pages is never used.
+ * max_len: an upper bound of past + new tokens over the sequences, for the
+ * launch shape and the workspace (0: the table's capacity); the rows of a
+ * longer sequence are undefined.
+ * Scores and softmax sums are fp32.  fp32 queries and the softmax weights
+ * then enter the tensor cores as two fp16 terms (22 bits); for 16-bit
+ * dtypes the weights are rounded once to fp16, and queries exactly
+ * representable in fp16 after scaling by a power of two are not rounded.
+ * Results do not depend on the other sequences' contents or on timing.
+ * q, out: n_tok x n_heads x head_dim with token and head strides; out may
+ * not overlap q.  workspace: device, 256-byte aligned, at least
+ * rf_attention_workspace_bytes(...) bytes (NULL if that is 0), overwritten.
+ * Errors: RF_ERR_UNSUPPORTED_FMT (dtype); RF_ERR_INVALID_ARG (null pointer,
+ * bad cache or batch field, n_heads not a positive multiple of n_kv_heads,
+ * strides below head_dim, window < 0, scale not finite, max_len < 0,
+ * workspace missing or too small, unknown flags); RF_ERR_MISALIGNED;
+ * RF_ERR_TOO_LARGE (n_heads > 4096, or n_pages * n_kv_heads * page_size
+ * above 2^40).  n_tok 0 is a no-op. */
+RF_API rf_status rf_attention(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype,
+                              const void *q, int64_t q_ld_tok, int64_t q_ld_head, int n_heads,
+                              float scale, int64_t window, const float *sinks, void *out,
+                              int64_t out_ld_tok, int64_t out_ld_head, int64_t max_len,
+                              void *workspace, size_t workspace_bytes, unsigned flags,
+                              void *stream);
+
+/* Bytes of workspace rf_attention needs for these arguments; 0 when it needs
+ * none or the arguments are invalid. */
+RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv_batch *batch,
+                                           int dtype, int n_heads, int64_t window,
+                                           int64_t max_len);
+
 /* --------------------------------------------------------------- status */
 /* Synchronizes the current device, then reports and clears the device status
- * word that kernels set when a bounded wait times out (RF_OK if none).
+ * word that kernels set when a bounded wait times out, or RF_ERR_INVALID_ARG
+ * for a batch whose device arrays name positions or pages that do not exist
+ * (RF_OK if none).
  * Returns RF_ERR_CUDA if the device reports an error. */
 RF_API rf_status rf_device_status(void);
 

@@ -21,6 +21,10 @@ FORMATS = {"Q4_0": Q4_0, "Q8_0": Q8_0, "Q4_K": Q4_K, "Q6_K": Q6_K, "MXFP4": MXFP
 BLOCK_BYTES = {Q4_0: 18, Q8_0: 34, Q4_K: 144, Q6_K: 210, MXFP4: 17}
 BLOCK_ELEMS = {Q4_0: 32, Q8_0: 32, Q4_K: 256, Q6_K: 256, MXFP4: 32}
 
+F32, F16, BF16 = 0, 1, 30           # activation types
+ROPE_HALF, ROPE_PAIRS = 0, 1        # rotation styles
+KV_BLOCK = 32                       # tokens that share a scale byte of the KV cache
+
 OK = 0
 CHAIN = 1   # RF_CHAIN launch flag
 STATUS = {0: "RF_OK", 1: "RF_ERR_INVALID_ARG", 2: "RF_ERR_UNSUPPORTED_FMT",
@@ -52,6 +56,20 @@ class ExpertCacheStats(ctypes.Structure):
                 ("evictions", ctypes.c_uint64), ("bytes_streamed", ctypes.c_uint64),
                 ("bytes_cached", ctypes.c_uint64), ("slots", ctypes.c_int32),
                 ("used", ctypes.c_int32)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class KVBatchStruct(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("past", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_width", ctypes.c_int32), ("n_seq", ctypes.c_int32),
+                ("n_tok", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -97,6 +115,14 @@ _SIGS = {
     "rf_expert_cache_stats": ([_P, ctypes.POINTER(ExpertCacheStats)], _I),
     "rf_moe_ffn_streamed": ([_I, _P, _I, _I, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P,
                              _P], _I),
+    "rf_norm_residual": ([_I, _I64, _I64, _P, _I64, _P, _P, _I64, ctypes.c_float, _P, _I64, _P, _I64,
+                          _P, _P, _I64, ctypes.c_float, ctypes.c_uint, _P], _I),
+    "rf_kv_append": ([_P, _P, _I, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64,
+                      _I, _P, _P, _I64, _I, _I, ctypes.c_uint, _P], _I),
+    "rf_kv_read": ([_P, _P, _P, _P, ctypes.c_uint, _P], _I),
+    "rf_attention": ([_P, _P, _I, _P, _I64, _I64, _I, ctypes.c_float, _I64, _P, _P, _I64, _I64,
+                      _I64, _P, _SZ, ctypes.c_uint, _P], _I),
+    "rf_attention_workspace_bytes": ([_P, _P, _I, _I, _I64, _I64], _SZ),
     "rf_device_status": ([], _I),
     "rf_debug_arm_wait_fault": ([ctypes.c_uint32], _I),
 }
@@ -500,6 +526,223 @@ def moe_workspace_views(workspace, top_k: int, n_ff: int):
     w = workspace[256:288].view(torch.float32)[:top_k]
     h = workspace[512:512 + 4 * top_k * n_ff].view(torch.float32).view(top_k, n_ff)
     return idx, w, h
+
+
+_DTYPES = None
+
+
+def _dtype(t) -> int:
+    """The activation type of a tensor."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"activations are float32, float16 or bfloat16, not {t.dtype}")
+    return d
+
+
+def _act(t, dims: int, what: str, like=None):
+    """Data pointer of an activation tensor with a contiguous last dimension."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must have {dims} dimensions, the last one contiguous")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+        raise ValueError(f"{what} must have the type and shape {like.dtype}, {tuple(like.shape)}")
+    return t.data_ptr()
+
+
+def _f32_ptr(t, n: int, what: str):
+    """Data pointer of n contiguous float32 device values, or None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.element_size() != 4 or not t.is_floating_point() or \
+            not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what} must be {n} contiguous float32 values on the device")
+    return t.data_ptr()
+
+
+def norm_residual(residual, x=None, *, post_weight=None, gate=None, scale: float = 1.0, weight=None,
+                  eps: float = 1e-5, residual_out=None, y=None, norm: bool = True, stream=None,
+                  flags: int = 0):
+    """rf_norm_residual: residual and x are (n_tok, n) (rows may be strided;
+    either may be None); gate is (n,) or (n_tok, n) float32.  Returns
+    (residual + scale * gate * post_norm(x), its norm); the norm is None with
+    norm=False."""
+    import torch
+    ref = residual if residual is not None else x
+    if ref is None:
+        raise ValueError("residual and x are both None")
+    px = _act(x, 2, "x", ref) if x is not None else None
+    pr = _act(residual, 2, "residual") if residual is not None else None
+    n_tok, n = ref.shape
+    if residual_out is None:
+        residual_out = torch.empty((n_tok, n), dtype=ref.dtype, device=ref.device)
+    if y is None and norm:
+        y = torch.empty((n_tok, n), dtype=ref.dtype, device=ref.device)
+    pg, ldg = None, 0
+    if gate is not None:
+        if gate.dim() == 2:
+            if gate.shape != ref.shape or gate.element_size() != 4 or not gate.is_floating_point():
+                raise ValueError("gate must be float32, (n,) or (n_tok, n)")
+            pg, ldg = _act(gate, 2, "gate"), gate.stride(0)
+        else:
+            pg = _f32_ptr(gate, n, "gate")
+    # The stride of a single row says nothing; n is always valid for it.
+    ld = lambda t: max(t.stride(0), n) if t is not None and n_tok == 1 else (t.stride(0) if t is not None else 0)  # noqa: E731
+    _check(lib().rf_norm_residual(_dtype(ref), n_tok, n, px, ld(x), _f32_ptr(post_weight, n, "post_weight"),
+                                  pg, ldg, scale, pr, ld(residual),
+                                  _act(residual_out, 2, "residual_out", ref), ld(residual_out),
+                                  _f32_ptr(weight, n, "weight"),
+                                  _act(y, 2, "y", ref) if y is not None else None, ld(y), eps, flags,
+                                  _stream(stream)), "rf_norm_residual")
+    return residual_out, y
+
+
+class KVCache:
+    """A paged KV cache over the caller's tensors: k, v int8 (n_pages,
+    n_kv_heads, page_size, head_dim) and k_scale, v_scale uint8 (n_pages,
+    n_kv_heads, page_size / 32)."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4 or v.shape != k.shape or k.dtype != torch.int8 or v.dtype != torch.int8:
+            raise ValueError("k and v must be int8, (n_pages, n_kv_heads, page_size, head_dim)")
+        n_pages, n_kv, page, dim = k.shape
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (n_pages, n_kv, page // KV_BLOCK):
+                raise ValueError(f"{what} must be uint8, (n_pages, n_kv_heads, page_size / {KV_BLOCK})")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, n_kv, page, dim
+        self.struct = KVCacheStruct(_dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(k_scale, "k_scale"),
+                                    _dev_ptr(v_scale, "v_scale"), n_pages, page, n_kv, dim, 0)
+        self.ref = ctypes.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+        import torch
+        codes = (n_pages, n_kv_heads, page_size, head_dim)
+        scales = (n_pages, n_kv_heads, page_size // KV_BLOCK)
+        return cls(torch.zeros(codes, dtype=torch.int8, device=device),
+                   torch.zeros(codes, dtype=torch.int8, device=device),
+                   torch.zeros(scales, dtype=torch.uint8, device=device),
+                   torch.zeros(scales, dtype=torch.uint8, device=device))
+
+
+class KVBatch:
+    """The tokens of one call (rf_kv_batch): page_table (n_seq, width), past
+    (n_seq,) and q_start (n_seq + 1,) are int32 device tensors that the
+    kernels read at run time; n_tok is the number of rows of the call."""
+
+    def __init__(self, page_table, past, q_start, n_tok: int):
+        import torch
+        n_seq = past.numel()
+        for t, what in ((page_table, "page_table"), (past, "past"), (q_start, "q_start")):
+            if not t.is_cuda or t.dtype != torch.int32 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+                raise ValueError(f"{what} must be an int32 CUDA tensor, its last dimension contiguous")
+        if page_table.dim() != 2 or page_table.shape[0] != n_seq or past.dim() != 1 or \
+                q_start.dim() != 1 or q_start.numel() != n_seq + 1:
+            raise ValueError("page_table is (n_seq, width), past (n_seq,), q_start (n_seq + 1,)")
+        self.page_table, self.past, self.q_start = page_table, past, q_start
+        self.n_seq, self.n_tok, self.width = n_seq, n_tok, page_table.shape[1]
+        stride = max(page_table.stride(0), self.width) if n_seq == 1 else page_table.stride(0)
+        self.struct = KVBatchStruct(page_table.data_ptr(), past.data_ptr(), q_start.data_ptr(),
+                                    stride, self.width, n_seq, n_tok, 0)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _heads(t, n_tok: int, dim: int, what: str):
+    """(pointer, token stride, head stride, heads) of a (n_tok, heads, dim) tensor."""
+    p = _act(t, 3, what)
+    shape, stride = t.shape, t.stride()
+    if shape[0] != n_tok or shape[2] != dim:
+        raise ValueError(f"{what} must be ({n_tok}, heads, {dim})")
+    # strides of dimensions of one element say nothing
+    return (p, stride[0] if n_tok > 1 else max(stride[0], dim),
+            stride[1] if shape[1] > 1 else max(stride[1], dim), shape[1])
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None, sin=None,
+              rope: int = ROPE_HALF, stream=None, flags: int = 0):
+    """rf_kv_append: k, v (n_tok, n_kv_heads, head_dim) go to the cache, rotated
+    (k) by the tables cos, sin (n_pos, rot / 2); returns the rotated q
+    (n_tok, n_heads, head_dim), or None without q."""
+    import torch
+    n_tok, dim = batch.n_tok, cache.head_dim
+    pk, klt, klh, kh = _heads(k, n_tok, dim, "k")
+    pv, vlt, vlh, vh = _heads(v, n_tok, dim, "v")
+    if kh != cache.n_kv_heads or vh != kh or v.dtype != k.dtype:
+        raise ValueError("k and v must have the cache's heads and one type")
+    pq = po = None
+    qlt = qlh = olt = olh = nh = 0
+    if q is not None:
+        if q.dtype != k.dtype:
+            raise ValueError("q, k and v must have one type")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        pq, qlt, qlh, nh = _heads(q, n_tok, dim, "q")
+        po, olt, olh, oh = _heads(q_out, n_tok, dim, "q_out")
+        if oh != nh or q_out.dtype != q.dtype:
+            raise ValueError("q_out must be like q")
+    pc = ps = None
+    n_pos = rot = 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be two (n_pos, rot / 2) tables")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        pc, ps = _f32_ptr(cos, cos.numel(), "cos"), _f32_ptr(sin, cos.numel(), "sin")
+    _check(lib().rf_kv_append(cache.ref, batch.ref, _dtype(k), pk, klt, klh, pv, vlt, vlh, pq, qlt, qlh,
+                              po, olt, olh, nh, pc, ps, n_pos, rot, rope, flags, _stream(stream)),
+           "rf_kv_append")
+    return q_out
+
+
+def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None, flags: int = 0):
+    """rf_kv_read: the cache's values at the batch's positions, two float32
+    tensors (n_tok, n_kv_heads, head_dim)."""
+    import torch
+    shape = (batch.n_tok, cache.n_kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.float32, device=cache.k.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.float32, device=cache.k.device)
+    n = shape[0] * shape[1] * shape[2]
+    _check(lib().rf_kv_read(cache.ref, batch.ref, _f32_ptr(k_out, n, "k_out"), _f32_ptr(v_out, n, "v_out"),
+                            flags, _stream(stream)), "rf_kv_read")
+    return k_out, v_out
+
+
+def attention_workspace(cache: KVCache, batch: KVBatch, q, max_len: int = 0, window: int = 0):
+    """Device workspace for attention() with these arguments, or None."""
+    import torch
+    n = lib().rf_attention_workspace_bytes(cache.ref, batch.ref, _dtype(q), q.shape[1], window, max_len)
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def attention(cache: KVCache, batch: KVBatch, q, out=None, scale: float | None = None, window: int = 0,
+              sinks=None, max_len: int = 0, workspace=None, stream=None, flags: int = 0):
+    """rf_attention: q (n_tok, n_heads, head_dim) against the cache, which
+    already holds the batch's own tokens; scale defaults to head_dim ** -0.5.
+    The workspace is allocated when not given."""
+    import torch
+    n_tok, dim = batch.n_tok, cache.head_dim
+    pq, qlt, qlh, nh = _heads(q, n_tok, dim, "q")
+    if out is None:
+        out = torch.empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+    po, olt, olh, oh = _heads(out, n_tok, dim, "out")
+    if oh != nh or out.dtype != q.dtype:
+        raise ValueError("out must be like q")
+    if workspace is None:
+        workspace = attention_workspace(cache, batch, q, max_len, window)
+    ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+        if workspace is not None else (None, 0)
+    _check(lib().rf_attention(cache.ref, batch.ref, _dtype(q), pq, qlt, qlh, nh,
+                              dim ** -0.5 if scale is None else scale, window,
+                              _f32_ptr(sinks, nh, "sinks"), po, olt, olh, max_len, ws, ws_bytes, flags,
+                              _stream(stream)), "rf_attention")
+    return out
 
 
 def device_status() -> int:

@@ -448,8 +448,12 @@ rf_status rf_device_status(void)
 {
     const rf_status a = read_and_clear_device_status();
     if (a == RF_ERR_CUDA) return a;
-    const rf_status b = read_and_clear_gemm_status();
-    return a != RF_OK ? a : b;
+    rf_status first = a;
+    for (rf_status (*word)() : {read_and_clear_gemm_status, read_and_clear_kv_status, read_and_clear_attn_status}) {
+        const rf_status b = word();
+        if (first == RF_OK) first = b;
+    }
+    return first;
 }
 
 rf_status rf_debug_arm_wait_fault(uint32_t limit_us) { return arm_wait_fault(limit_us); }

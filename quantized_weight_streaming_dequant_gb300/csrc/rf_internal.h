@@ -104,6 +104,10 @@ bool encode_u16_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t ro
                     uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows);
 // The prefill GEMM's own status word (bounded waits), read and cleared.
 rf_status read_and_clear_gemm_status();
+// Positions or pages that do not exist, seen by the cache and the attention
+// kernels, read and cleared.
+rf_status read_and_clear_kv_status();
+rf_status read_and_clear_attn_status();
 // Arms the one-shot wait fault of the next producer-mode launch
 // (rf_debug_arm_wait_fault).
 rf_status arm_wait_fault(uint32_t limit_us);

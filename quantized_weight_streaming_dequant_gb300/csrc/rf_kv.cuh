@@ -1,0 +1,144 @@
+// rf_kv.cuh -- what the kernels around the KV cache share: activation types,
+// the batch's token lookup, and the launch helper with a programmatic
+// dependency.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "rf.h"
+#include "rf_device.cuh"
+#include "rf_internal.h"
+
+namespace rf {
+
+constexpr int kKvBlock = 32;      // tokens that share a scale byte
+constexpr int kScaleMin = 87;     // 2^-40: the smallest unit written
+constexpr int kScaleMax = 167;    // 2^40: the largest
+constexpr int kScaleNan = 255;
+
+// ------------------------------------------------------------ activation types
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v)
+{
+    return __bfloat162float(v);
+}
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v)
+{
+    return __float2bfloat16_rn(v);
+}
+
+// Four consecutive elements.  vec: the address is aligned to all four.
+template <typename T>
+__device__ __forceinline__ void load4(const T *p, bool vec, float (&f)[4])
+{
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(p);
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        } else {
+            union { uint2 u; T t[4]; } a;
+            a.u = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = to_f32<T>(a.t[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = to_f32<T>(p[i]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T *p, bool vec, const float (&f)[4])
+{
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+            union { uint2 u; T t[4]; } a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a.t[i] = from_f32<T>(f[i]);
+            *reinterpret_cast<uint2 *>(p) = a.u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = from_f32<T>(f[i]);
+    }
+}
+
+// ------------------------------------------------------------------- batch
+// The sequence that owns token t, or -1: the last s with q_start[s] <= t,
+// if t < q_start[s+1].  Reads only q_start[0 .. n_seq].
+__device__ __forceinline__ int find_seq(const int32_t *__restrict__ q_start, int n_seq, int t)
+{
+    int lo = 0, hi = n_seq;   // q_start[lo] <= t (checked below); q_start[hi] > t or hi == n_seq
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (q_start[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
+}
+
+// The page of position `pos` of sequence s, or -1 if it has none.
+__device__ __forceinline__ int page_of(const rf_kv_batch &b, const rf_kv_cache &c, int s, int64_t pos)
+{
+    const int64_t i = pos >> (31 - __clz(c.page_size));   // a power of two
+    if (pos < 0 || i >= b.table_width) return -1;
+    const int page = b.page_table[(int64_t)s * b.table_stride + i];
+    return page >= 0 && page < c.n_pages ? page : -1;
+}
+
+// 2^(E-127) of a scale byte: E = 0 is the subnormal 2^-127, 255 is NaN.
+__device__ __forceinline__ float scale_value(uint32_t E)
+{
+    return __uint_as_float(E == 255u ? 0x7fc00000u : E == 0u ? 0x00400000u : E << 23);
+}
+
+// ---------------------------------------------------------------- host side
+inline bool dtype_ok(int dtype) { return dtype == RF_F32 || dtype == RF_F16 || dtype == RF_BF16; }
+inline int dtype_bytes(int dtype) { return dtype == RF_F32 ? 4 : 2; }
+inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// RF_OK if the fields of a cache and a batch are in range.
+rf_status check_kv(const rf_kv_cache *c, const rf_kv_batch *b);
+
+// Calls f with a value of the C++ type of `dtype`.
+template <typename F>
+rf_status with_dtype(int dtype, F &&f)
+{
+    switch (dtype) {
+    case RF_F32: return f(float());
+    case RF_F16: return f(__half());
+    default: return f(__nv_bfloat16());
+    }
+}
+
+// Launches kernel(args...); chain: with a programmatic dependency on the
+// previous kernel of the stream.
+template <typename... P, typename... A>
+rf_status launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                        bool chain, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = chain ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    cudaGetLastError();
+    return e == cudaSuccess ? RF_OK : RF_ERR_CUDA;
+}
+
+}  // namespace rf
