@@ -125,14 +125,18 @@ def attention(cache, table, past, q_start, n_tok, q, scale, window=0, sinks=None
     group = heads // cache.heads
     out, mag, xmag = np.zeros(q.shape), np.zeros(q.shape), np.zeros((n_tok, heads))
     for s in range(len(past)):
+        n = int(past[s]) + int(q_start[s + 1]) - int(q_start[s])
+        there = np.array([cache.at(table[s], j) is not None for j in range(max(n, 0))], bool)
+        zero = np.zeros((cache.heads, dim))
+        keys, vals = (np.stack([cache.values(table[s], j, side) if there[j] else zero for j in range(n)])
+                      if n > 0 else None for side in (0, 1))
         for t in range(int(q_start[s]), int(q_start[s + 1])):
             last = int(past[s]) + t - int(q_start[s])
-            first = max(0, last - window + 1) if window else 0
-            pos = [j for j in range(first, last + 1) if cache.at(table[s], j) is not None]
-            if not pos:
+            pos = np.arange(max(0, last - window + 1) if window else 0, last + 1)
+            pos = pos[there[pos]]
+            if not len(pos):
                 continue
-            k = np.stack([cache.values(table[s], j, 0) for j in pos])     # (n, kv heads, dim)
-            v = np.stack([cache.values(table[s], j, 1) for j in pos])
+            k, v = keys[pos], vals[pos]                                    # (n, kv heads, dim)
             for h in range(heads):
                 kh, vh = k[:, h // group], v[:, h // group]
                 z = float(scale) * (kh @ q[t, h])

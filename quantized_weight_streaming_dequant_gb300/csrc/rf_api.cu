@@ -449,7 +449,8 @@ rf_status rf_device_status(void)
     const rf_status a = read_and_clear_device_status();
     if (a == RF_ERR_CUDA) return a;
     rf_status first = a;
-    for (rf_status (*word)() : {read_and_clear_gemm_status, read_and_clear_kv_status, read_and_clear_attn_status}) {
+    for (rf_status (*word)() : {read_and_clear_gemm_status, read_and_clear_kv_status, read_and_clear_attn_status,
+                                read_and_clear_attn_tile_status}) {
         const rf_status b = word();
         if (first == RF_OK) first = b;
     }

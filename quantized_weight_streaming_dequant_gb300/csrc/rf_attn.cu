@@ -36,26 +36,6 @@ __device__ int g_attn_status = 0;   // positions or pages that do not exist
 
 constexpr int kWarps = 4;
 
-__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// Codes (sign bit flipped) b0, b1 or b2, b3 of a word as an fp16 pair:
-// 0x6400 | u is 1024 + code + 128, so subtracting 1152 is exact.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return h2_sub(prmt(w, 0x64646464u, 0x5140u), 0x64806480u); }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return h2_sub(prmt(w, 0x64646464u, 0x7362u), 0x64806480u); }
-
-__device__ __forceinline__ uint32_t pack_h2(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float2 unpack_h2(uint32_t v)
-{
-    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-}
 __device__ __forceinline__ uint32_t mov_trans(uint32_t v)
 {
     uint32_t r;
@@ -68,12 +48,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait_group()
@@ -497,12 +471,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     pdl_launch_dependents();
     pdl_wait();
     if (row >= (int64_t)p.b.n_tok * p.n_heads) return;
+    const int64_t tok = row / p.n_heads;
     const float2 *ml = p.part_ml + row * p.splits;
     float M = -INFINITY;
-    for (int k = lane; k < p.splits; k += 32) M = fmaxf(M, ml[k].x);
+    // a token that belongs to no sequence may have no parts
+    if (find_seq(p.b.q_start, p.b.n_seq, (int)tok) >= 0)
+        for (int k = lane; k < p.splits; k += 32) M = fmaxf(M, ml[k].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const int64_t tok = row / p.n_heads;
     const int h = (int)(row % p.n_heads);
     T *out = static_cast<T *>(p.out) + tok * p.o_lt + (int64_t)h * p.o_lh;
     float L = 0.f, a[2][4] = {};
@@ -673,6 +649,7 @@ size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv_batch 
 {
     AttnParams p = {};
     if (plan(cache, batch, dtype, n_heads, window, &max_len, &p) != RF_OK || batch->n_tok == 0) return 0;
+    if (attn_tile_takes(p)) return attn_tile_workspace(p, dtype, max_len);
     RowTiling tl;
     rows_tiling(p, &tl);
     choose_splits(&p, tl, max_len);
@@ -701,6 +678,10 @@ rf_status rf_attention(const rf_kv_cache *cache, const rf_kv_batch *batch, int d
     p.o_vec = aligned_to(out, 4 * b) && out_ld_tok % 4 == 0 && out_ld_head % 4 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chain = (flags & RF_CHAIN) != 0;
+    if (attn_tile_takes(p)) {
+        if (!workspace || workspace_bytes < attn_tile_workspace(p, dtype, max_len)) return RF_ERR_INVALID_ARG;
+        return launch_attn_tile(p, dtype, max_len, workspace, s, chain);
+    }
     RowTiling tl;
     const int nr = rows_tiling(p, &tl);
     choose_splits(&p, tl, max_len);

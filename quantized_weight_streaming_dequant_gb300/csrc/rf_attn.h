@@ -32,11 +32,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // The path for long chunks (128-row tiles on tcgen05), its workspace and
 // whether it takes the call.
-bool attn_tile_takes(const AttnParams &p, int64_t max_len);
+bool attn_tile_takes(const AttnParams &p);
 size_t attn_tile_workspace(const AttnParams &p, int dtype, int64_t max_len);
-rf_status launch_attn_tile(const AttnParams &p, int dtype, int64_t max_len, void *workspace,
-                           cudaStream_t s, bool chain);
-rf_status read_and_clear_attn_tile_status();
+rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *workspace, cudaStream_t s,
+                           bool chain);
 
 // Joins the parts of each row (part_o, part_ml) into out.
 rf_status launch_attn_join(const AttnParams &p, int dtype, cudaStream_t s);

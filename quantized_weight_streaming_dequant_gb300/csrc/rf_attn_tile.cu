@@ -1,0 +1,796 @@
+// rf_attn_tile.cu -- attention of long chunks on the fifth-generation tensor
+// cores (same mathematics as rf_attn.cu).
+//
+// Three launches:
+//   plan   one CTA lists the query tiles (heaviest first: later positions see
+//          more) and lays the sequences' 128-position tiles out end to end.
+//   stage  rewrites what the products read into the operand layouts, once per
+//          call instead of once per query tile: codes of K and V as fp16
+//          tiles (V transposed), queries as one or two fp16 terms per element
+//          scaled by a power of two per row, and the blocks' units.  It moves
+//          3 bytes per code (and 2 to 4 per query element), which 128-row
+//          tiles read back many times.
+//   tiles  a CTA owns two tiles of 128 query rows (tokens x heads of one K/V
+//          head) and walks the visible positions, 128 at a time:
+//              S = Q K^T (tcgen05.mma from shared memory, fp32 in tensor
+//              memory) -> weights by one thread per row (no shuffles) -> P in
+//              fp16 over S's own columns -> O += P V (P from tensor memory).
+//          One thread issues the products of the two tiles alternately, so
+//          that one tile's exponentials run under the other's products; O
+//          stays in tensor memory and is rescaled only when a row's maximum
+//          has grown by more than 2^7 (the weights' exponent range allows it;
+//          the factor cancels).
+// Bound: the tensor pipe for long rows: 4 * 128 * 128 * head_dim flops per
+// step and tile (twice that for fp32, whose queries and weights are two fp16
+// terms), against 16,384 exponentials.
+//
+// Every wait is bounded; after a failure every role stops, copies and
+// products already issued are waited for, and tensor memory is freed.
+#include <algorithm>
+#include <mutex>
+
+#include "rf_attn.h"
+#include "rf_tcgen05.cuh"
+
+namespace rf {
+namespace {
+
+__device__ int g_tile_status = 0;
+
+constexpr int kTile = 128;          // query rows, and positions, per tile
+constexpr int kMainThreads = 320;   // two softmax groups of four warps, MMA issue, copies
+constexpr int kPadParts = 8;        // CTAs that zero the rows of no sequence
+constexpr float kTileShift = 8.f;   // weights are 2^(x - m + 8) <= 2^15
+constexpr float kLazy = 7.f;        // growth of a maximum that is not yet applied
+
+// What the plan kernel leaves for the others.
+struct TilePlan {
+    int32_t n_q, n_kv;              // query tiles, position tiles
+};
+
+struct TileParams {
+    AttnParams a;
+    int hpt, head_tiles, tqt;       // heads per tile, tiles per K/V head, tokens per 128-row tile
+    int cap_q, cap_kv;              // capacities of the lists below
+    TilePlan *plan;
+    int2 *q_tiles;                  // [cap_q]: sequence, first token
+    int32_t *kv_base;               // [n_seq + 1]: first position tile of a sequence
+    int32_t *kv_first;              // [n_seq]: its position / 128 (window)
+    uint8_t *q_img;                 // [cap_q][kv head][head tile][2][NS][128 x DP] fp16
+    float *q_unit;                  // [cap_q][kv head][head tile][2][128]
+    uint8_t *k_img, *v_img;         // [kv head][cap_kv][128 x DP] fp16
+    float *units;                   // [kv head][cap_kv][12]: 2^ek, ev, 2^-ev of four blocks
+    int split_tiles;                // position tiles per part
+    float qk_abs;                   // |scale| * log2(e); its sign is in the queries
+    bool negate;
+    unsigned long long limit;
+};
+
+// ---------------------------------------------------------------------- plan
+// Exclusive prefix sum over the CTA's 1024 threads.
+__device__ __forceinline__ int scan1024(int v, int *part, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int y = part[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        part[lane] = y;
+    }
+    __syncthreads();
+    const int base = warp ? part[warp - 1] : 0;
+    *total = part[31];
+    __syncthreads();
+    return base + x - v;
+}
+
+__global__ void __launch_bounds__(1024) tile_plan_kernel(const __grid_constant__ TileParams p)
+{
+    __shared__ int part[32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const rf_kv_batch &b = p.a.b;
+    int kv_at = 0, q_at = 0;
+    for (int s0 = 0; s0 < b.n_seq; s0 += 1024) {
+        const int s = s0 + (int)threadIdx.x;
+        int nt = 0, first = 0, nq = 0, t0 = 0;
+        if (s < b.n_seq) {
+            t0 = max(b.q_start[s], 0);
+            nq = max(0, min(b.q_start[s + 1], b.n_tok) - t0);
+            const int64_t past = b.past[s], last = past + nq - 1;
+            if (nq > 0 && last >= 0) {
+                int64_t lo = 0;
+                if (p.a.window > 0) lo = max((int64_t)0, past - p.a.window + 1);
+                first = (int)(lo / kTile);
+                nt = (int)(min(last / kTile + 1, (int64_t)b.table_width * p.a.c.page_size / kTile + 1)) - first;
+                nt = max(nt, 0);
+            }
+            if (past < 0 && nq > 0) record_status(&g_tile_status, RF_ERR_INVALID_ARG);
+        }
+        int total;
+        int at = kv_at + scan1024(nt, part, &total);
+        if (s < b.n_seq) {
+            // past the capacity (a sequence longer than max_len): nothing of it is seen
+            if (nt > 0 && at + nt > p.cap_kv) record_status(&g_tile_status, RF_ERR_INVALID_ARG);
+            p.kv_base[s] = min(at, p.cap_kv);
+            p.kv_first[s] = first;
+        }
+        kv_at = min(kv_at + total, 1 << 30);
+        const int tiles = (nq + 2 * p.tqt - 1) / (2 * p.tqt);
+        at = q_at + scan1024(tiles, part, &total);
+        q_at = min(q_at + total, 1 << 30);
+        // later positions first: they see more
+        for (int i = 0; i < tiles; ++i)
+            if (at + i < p.cap_q) p.q_tiles[at + i] = make_int2(s, t0 + (tiles - 1 - i) * 2 * p.tqt);
+    }
+    if (threadIdx.x == 0) {
+        p.kv_base[b.n_seq] = min(kv_at, p.cap_kv);
+        p.plan->n_q = min(q_at, p.cap_q);
+        p.plan->n_kv = min(kv_at, p.cap_kv);
+    }
+}
+
+// --------------------------------------------------------------------- stage
+// One position tile of one K/V head by 256 threads.
+template <int DP>
+__device__ __forceinline__ void stage_kv(const TileParams &p, int tile, int head)
+{
+    __shared__ int64_t s_blk[4];   // cache block of each 32 positions, or -1
+    const rf_kv_cache &c = p.a.c;
+    const int D = c.head_dim, tid = threadIdx.x;
+    // the sequence: the last one whose first tile is not after this one
+    if (tid < 4) {
+        int lo = 0, hi = p.a.b.n_seq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.kv_base[mid] <= tile) lo = mid;
+            else hi = mid;
+        }
+        const int64_t pos = (int64_t)(p.kv_first[lo] + tile - p.kv_base[lo]) * kTile + 32 * tid;
+        const int end = min(p.a.b.q_start[lo + 1], p.a.b.n_tok);
+        const int64_t len = (int64_t)p.a.b.past[lo] + end - p.a.b.q_start[lo];
+        int64_t blk = -1;
+        if (pos < len) {
+            const int page = page_of(p.a.b, c, lo, pos);
+            const int per = c.page_size / kKvBlock;
+            if (page >= 0) blk = ((int64_t)page * c.n_kv_heads + head) * per + (pos / kKvBlock) % per;
+            else record_status(&g_tile_status, RF_ERR_INVALID_ARG);
+        }
+        s_blk[tid] = blk;
+        // a block that does not exist has unit 0 and exponent -inf: weight 0
+        const uint32_t ek = blk >= 0 ? c.k_scale[blk] : 0u, ev = blk >= 0 ? c.v_scale[blk] : 0u;
+        float *u = p.units + ((int64_t)head * p.cap_kv + tile) * 12;
+        const float nan = __uint_as_float(0x7fc00000u);
+        u[tid] = blk >= 0 ? scale_value(ek) : 0.f;
+        u[4 + tid] = blk < 0 ? -INFINITY : ev == 255u ? nan : (float)((int)ev - 127);
+        u[8 + tid] = blk < 0 ? 0.f : ev == 255u ? nan : scale_value(254u - ev);
+    }
+    __syncthreads();
+    const int64_t img = ((int64_t)head * p.cap_kv + tile) * (kTile * DP * 2);
+    // K: 16-byte unit (row n, elements 8k..) at (n/8) * 16 DP + k * 128 + (n%8) * 16.
+    uint8_t *ki = p.k_img + img;
+    for (int w = tid; w < kTile * DP / 8; w += 256) {
+        const int n8 = w & 7, k = (w >> 3) % (DP / 8), n = (w >> 3) / (DP / 8) * 8 + n8;
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        const int64_t blk = s_blk[n >> 5];
+        if (blk >= 0 && 8 * k < D) {
+            uint2 v = *reinterpret_cast<const uint2 *>(c.k + (blk * kKvBlock + (n & 31)) * D + 8 * k);
+            v.x ^= 0x80808080u, v.y ^= 0x80808080u;
+            o = make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y));
+        }
+        *reinterpret_cast<uint4 *>(ki + (int64_t)w * 16) = o;
+    }
+    // V transposed: unit (row d, positions 8t..) at (d/8) * 2048 + t * 128 + (d%8) * 16;
+    // a thread turns 8 positions x 4 elements.
+    uint8_t *vi = p.v_img + img;
+    for (int w = tid; w < kTile * DP / 32; w += 256) {
+        const int d = 4 * (w % (DP / 4)), t = w / (DP / 4);
+        uint32_t v[8];
+        const int64_t blk = s_blk[t >> 2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = blk >= 0 && d < D
+                       ? *reinterpret_cast<const uint32_t *>(c.v + (blk * kKvBlock + (8 * t + i) % 32) * D + d) ^ 0x80808080u
+                       : 0x80808080u;
+        uint4 o[4];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint32_t a = prmt(v[i], v[i + 1], 0x5140u), b = prmt(v[i], v[i + 1], 0x7362u);
+            const uint32_t x[4] = {codes_lo(a), codes_hi(a), codes_lo(b), codes_hi(b)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t *>(&o[e])[i / 2] = x[e];
+        }
+        uint8_t *dst = vi + (d / 8) * 2048 + t * 128 + (d % 8) * 16;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + 16 * e) = o[e];
+    }
+}
+
+// Two 128-row query tiles by 256 threads: a quarter- or half-warp per row
+// (DP / 8 lanes of eight elements).
+template <typename T, int DP>
+__device__ __forceinline__ void stage_q(const TileParams &p, int qt, int head, int ht)
+{
+    constexpr int NS = sizeof(T) == 4 ? 2 : 1, LPR = DP / 8, RPW = 32 / LPR;
+    const AttnParams &a = p.a;
+    const int2 q = p.q_tiles[qt];
+    const int end = min(a.b.q_start[q.x + 1], a.b.n_tok), D = a.c.head_dim;
+    const int h0 = head * a.group + ht * p.hpt, nh = min(p.hpt, a.group - ht * p.hpt);
+    const int64_t at = ((int64_t)qt * a.c.n_kv_heads + head) * p.head_tiles + ht;
+    uint8_t *img = p.q_img + at * (2 * NS * kTile * DP * 2);
+    float *unit = p.q_unit + at * (2 * kTile);
+    const int lane = threadIdx.x & 31, k = lane % LPR;
+    for (int r = (int)(threadIdx.x >> 5) * RPW + lane / LPR; r < 2 * kTile; r += 8 * RPW) {
+        const int x = r / kTile, n = r % kTile, ti = n / p.hpt, hi = n % p.hpt;
+        const int tok = q.y + x * p.tqt + ti;
+        const bool ok = ti < p.tqt && hi < nh && tok < end;
+        float f[8] = {};
+        if (ok && 8 * k < D) {
+            const T *src = static_cast<const T *>(a.q) + (int64_t)tok * a.q_lt + (int64_t)(h0 + hi) * a.q_lh + 8 * k;
+            float u[4], v[4];
+            load4<T>(src, a.q_vec, u);
+            load4<T>(src + 4, a.q_vec, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = u[i], f[4 + i] = v[i];
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // the row's maximum comes to [512, 1024)
+        const int ex = min(max(263 - (int)(__float_as_uint(amax) >> 23), 1), 253);
+        const float up = __uint_as_float((uint32_t)ex << 23) * (p.negate ? -1.f : 1.f);
+        if (k == 0) unit[r] = p.qk_abs * __uint_as_float((uint32_t)(254 - ex) << 23);
+        uint4 hi4, lo4;
+        uint32_t *ph = reinterpret_cast<uint32_t *>(&hi4), *pl = reinterpret_cast<uint32_t *>(&lo4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = f[2 * i] * up, v = f[2 * i + 1] * up;
+            ph[i] = pack_h2(u, v);
+            const float2 h = unpack_h2(ph[i]);
+            pl[i] = pack_h2(u - h.x, v - h.y);
+        }
+        uint8_t *dst = img + x * (NS * kTile * DP * 2) + (n / 8) * (16 * DP) + k * 128 + (n % 8) * 16;
+        *reinterpret_cast<uint4 *>(dst) = hi4;
+        if constexpr (NS == 2) *reinterpret_cast<uint4 *>(dst + kTile * DP * 2) = lo4;
+    }
+}
+
+// Rows of tokens before the first sequence and past the last (a padded
+// batch) read as zeros.
+template <typename T>
+__device__ __forceinline__ void zero_padding(const AttnParams &p, int part)
+{
+    const int head = max(0, min(p.b.q_start[0], p.b.n_tok)), tail = max(head, min(p.b.q_start[p.b.n_seq], p.b.n_tok));
+    const int per = p.n_heads * (p.c.head_dim / 4), n_pad = head + p.b.n_tok - tail;
+    const float zero[4] = {};
+    for (int64_t w = part * 256 + (int)threadIdx.x; w < (int64_t)n_pad * per; w += kPadParts * 256) {
+        const int j = (int)(w / per), h = (int)(w % per) / (p.c.head_dim / 4), d = 4 * ((int)(w % per) % (p.c.head_dim / 4));
+        const int64_t t = j < head ? j : tail + (j - head);
+        store4<T>(static_cast<T *>(p.out) + t * p.o_lt + (int64_t)h * p.o_lh + d, p.o_vec, zero);
+    }
+}
+
+// grid: position tiles x K/V heads, query tiles x K/V heads x head tiles,
+// then kPadParts CTAs for the rows of no sequence.
+template <typename T, int DP>
+__global__ void __launch_bounds__(256) tile_stage_kernel(const __grid_constant__ TileParams p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    int u = (int)blockIdx.x;
+    const int heads = p.a.c.n_kv_heads;
+    if (u < p.cap_kv * heads) {
+        const int tile = u / heads;
+        if (tile < p.plan->n_kv) stage_kv<DP>(p, tile, u % heads);
+        return;
+    }
+    u -= p.cap_kv * heads;
+    const int ht = u % p.head_tiles;
+    u /= p.head_tiles;
+    const int qt = u / heads;
+    if (qt >= p.cap_q) {
+        zero_padding<T>(p.a, (int)(gridDim.x - 1 - blockIdx.x));
+        return;
+    }
+    if (qt < p.plan->n_q) stage_q<T, DP>(p, qt, u % heads, ht);
+}
+
+// --------------------------------------------------------------------- tiles
+template <int DP, int NS> __host__ __device__ constexpr int ring_slots() { return (DP == 128 ? 7 : 14) - (DP == 128 ? 2 : 4) * NS; }
+template <int DP, int NS> __host__ __device__ constexpr size_t tile_smem()
+{
+    return (size_t)kTile * DP * 2 * (2 * NS + ring_slots<DP, NS>()) + 256;
+}
+
+__host__ __device__ constexpr uint32_t tile_idesc(int n)
+{
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams p)
+{
+    constexpr int NS = sizeof(T) == 4 ? 2 : 1;
+    constexpr int R = ring_slots<DP, NS>();
+    constexpr int SLOT = kTile * DP * 2;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_s = smem;                          // [2][NS][SLOT]
+    uint8_t *ring = smem + 2 * NS * SLOT;         // [R][SLOT]: K0 V0 K1 V1 ...
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + R * SLOT);
+    uint64_t *full = bars, *empty = bars + R;
+    uint64_t *qfull = bars + 2 * R, *sfull = qfull + 1, *pready = sfull + 2, *pvdone = pready + 2, *drained = pvdone + 2;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_stop;
+    volatile int *stop = &s_stop;
+    static_assert((2 * R + 8) * 8 <= 256, "barriers outgrow their room");
+
+    const AttnParams &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int u = (int)blockIdx.x;
+    const int part = u % a.splits;
+    u /= a.splits;
+    const int ht = u % p.head_tiles;
+    u /= p.head_tiles;
+    const int head = u % a.c.n_kv_heads, qt = u / a.c.n_kv_heads;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (qt >= p.plan->n_q) return;
+    const int2 q = p.q_tiles[qt];
+    const int seq = q.x, first = a.b.q_start[seq], end = min(a.b.q_start[seq + 1], a.b.n_tok);
+    const int64_t pos0 = (int64_t)a.b.past[seq] + (q.y - first);   // position of tile 0's first token
+    // Position tiles, counted from the sequence's first staged one: the first
+    // that tile 0 sees up to the last that each tile sees.
+    const int kv0 = p.kv_base[seq], kvn = p.kv_base[seq + 1] - kv0, kvf = p.kv_first[seq];
+    const bool fits = kv0 + kvn <= p.cap_kv;
+    int t_lo = 0, t_hi[2];
+    if (a.window > 0) t_lo = max(0, (int)(max((int64_t)0, pos0 - a.window + 1) / kTile) - kvf);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int toks = min(p.tqt, end - (q.y + x * p.tqt));
+        const int64_t last = pos0 + x * p.tqt + toks - 1;
+        t_hi[x] = toks > 0 && last >= 0 && fits ? min(kvn, (int)(last / kTile) + 1 - kvf) : 0;
+    }
+    const int from = t_lo + part * p.split_tiles;
+    int n[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int to = part == a.splits - 1 ? t_hi[x] : min(t_hi[x], from + p.split_tiles);
+        n[x] = max(0, to - from);
+    }
+    const int nmax = max(n[0], n[1]);
+    const int64_t at = ((int64_t)qt * a.c.n_kv_heads + head) * p.head_tiles + ht;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(qfull, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sfull[x], 1);
+            mbar_init(&pready[x], 4);
+            mbar_init(&pvdone[x], 1);
+        }
+        mbar_init(drained, 1);
+        s_stop = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&s_tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*stop) return false;
+        if (mbar_wait_bounded(bar, parity, &g_tile_status, p.limit)) return true;
+        *stop = 1;
+        return false;
+    };
+
+    if (warp == 9) {
+        // Copies: both query tiles, then K and V of each position tile.
+        if (lane == 0 && nmax > 0) {
+            mbar_arrive_expect_tx(qfull, 2 * NS * SLOT);
+            const uint8_t *src = p.q_img + at * (2 * NS * SLOT);
+#pragma unroll
+            for (int i = 0; i < 2 * NS; ++i) bulk_g2s(q_s + i * SLOT, src + i * SLOT, SLOT, qfull);
+            const int64_t img = ((int64_t)head * p.cap_kv + kv0 + from) * SLOT;
+            int issued = 0;
+            for (int i = 0; i < 2 * nmax; ++i) {
+                const int s = i % R;
+                if (!wait(&empty[s], ((i / R) & 1) ^ 1)) break;
+                mbar_arrive_expect_tx(&full[s], SLOT);
+                bulk_g2s(ring + s * SLOT, (i & 1 ? p.v_img : p.k_img) + img + (int64_t)(i >> 1) * SLOT, SLOT, &full[s]);
+                issued = i + 1;
+            }
+            mbar_drain(qfull, 0);
+            for (int i = max(0, issued - R); i < issued; ++i) mbar_drain(&full[i % R], (i / R) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // Products.  Tile x: S at columns 128 x, P over it (first term in
+        // its first 64 columns, second in the others), O at 256 + DP x.
+        if (lane == 0 && nmax > 0) {
+            const uint64_t qd = smem_desc(smem_addr(q_s), 16 * DP), kd = smem_desc(smem_addr(ring), 16 * DP);
+            const uint64_t vd = smem_desc(smem_addr(ring), 2048);
+            bool ok = wait(qfull, 0), any = false;
+            auto scores = [&](int x, int slot) {
+                tc_fence_after();
+#pragma unroll
+                for (int t = NS - 1; t >= 0; --t)
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        tc_mma(tmem + 128 * x, qd + (uint64_t)(((x * NS + t) * SLOT + k * 256) >> 4),
+                               kd + (uint64_t)((slot * SLOT + k * 256) >> 4), tile_idesc(kTile), !(t == NS - 1 && k == 0));
+                tc_commit(&sfull[x]);
+            };
+            auto values = [&](int x, int slot, bool add) {
+                tc_fence_after();
+#pragma unroll
+                for (int t = NS - 1; t >= 0; --t)
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 64 * t + 8 * k,
+                                  vd + (uint64_t)((slot * SLOT + k * 256) >> 4), tile_idesc(DP),
+                                  add || !(t == NS - 1 && k == 0));
+                tc_commit(&pvdone[x]);
+            };
+            if (ok && (ok = wait(&full[0], 0))) {
+                any = true;
+                for (int x = 0; x < 2; ++x)
+                    if (n[x] > 0) scores(x, 0);
+                tc_commit(&empty[0]);
+            }
+            for (int j = 0; ok && j < nmax; ++j) {
+                const int iv = 2 * j + 1, ik = 2 * j + 2;
+                const bool more = j + 1 < nmax;
+                if (!(ok = wait(&full[iv % R], (iv / R) & 1))) break;
+                if (more && !(ok = wait(&full[ik % R], (ik / R) & 1))) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (j < n[x]) {
+                        if (!(ok = wait(&pready[x], j & 1))) break;
+                        values(x, iv % R, j > 0);
+                    }
+                    if (x == 1) tc_commit(&empty[iv % R]);
+                    if (j + 1 < n[x]) scores(x, ik % R);
+                }
+                if (ok && more) tc_commit(&empty[ik % R]);
+            }
+            // Every issued product completes before tensor memory is freed.
+            if (any) {
+                tc_commit(drained);
+                mbar_drain(drained, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // Softmax: thread i of group x owns row i of tile x (tensor-memory
+        // lane i).
+        const int x = warp >> 2, i = threadIdx.x & 127;
+        const int ti = i / p.hpt, hi = i % p.hpt, nx = n[x];
+        const int tok = q.y + x * p.tqt + ti;
+        const bool row_ok = ti < p.tqt && hi < min(p.hpt, a.group - ht * p.hpt) && tok < end;
+        const int64_t top = row_ok ? pos0 + x * p.tqt + ti : -1;
+        const float bq = p.q_unit[at * (2 * kTile) + x * kTile + i];
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + DP * x;
+        float m = -INFINITY, l = 0.f;
+        const float4 *units = reinterpret_cast<const float4 *>(p.units + ((int64_t)head * p.cap_kv + kv0 + from) * 12);
+        bool ok = true;
+        // Newest visible column of the current tile and the first one.
+        int64_t base = (int64_t)(kvf + from) * kTile;
+        for (int j = 0; j < nx; ++j, base += kTile) {
+            const float4 ku = units[3 * j], ev = units[3 * j + 1], iv = units[3 * j + 2];
+            const float bk[4] = {bq * ku.x, bq * ku.y, bq * ku.z, bq * ku.w};
+            const float es[4] = {ev.x, ev.y, ev.z, ev.w}, is[4] = {iv.x, iv.y, iv.z, iv.w};
+            ok = __all_sync(0xffffffffu, wait(&sfull[x], j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s[b]);
+            tmem_ld_wait();
+            const int c_hi = (int)min((int64_t)kTile, max((int64_t)0, top + 1 - base));
+            const int c_lo = a.window > 0 ? (int)min((int64_t)kTile, max((int64_t)0, top - a.window + 1 - base)) : 0;
+            const bool edge = __any_sync(0xffffffffu, row_ok && (c_hi < kTile || c_lo > 0));
+            float mn = m;
+            if (edge) {
+                // x with hidden columns at -inf, then as if all units were 1
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int c = 32 * b + k;
+                        const float v = c >= c_lo && c < c_hi ? fmaf(__uint_as_float(s[b][k]), bk[b], es[b]) : -INFINITY;
+                        s[b][k] = __float_as_uint(v);
+                        mn = fmaxf(mn, v);
+                    }
+            } else {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float v = __uint_as_float(s[b][0]);
+#pragma unroll
+                    for (int k = 1; k < 32; ++k) v = fmaxf(v, __uint_as_float(s[b][k]));
+                    mn = fmaxf(mn, fmaf(v, bk[b], es[b]));
+                }
+            }
+            if (__any_sync(0xffffffffu, mn > m + kLazy)) {
+                const float mu = mn == -INFINITY ? 0.f : mn;
+                const float alpha = exp2_fast(m - mu);
+                m = mn;
+                l *= alpha;
+                if (j > 0) {
+                    ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int d = 0; d < DP; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(to + d, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tmem_st32(to + d, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float mu = (m == -INFINITY ? 0.f : m) - kTileShift;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float w[32];
+                float sum = 0.f;
+                if (edge) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int c = 32 * b + k;
+                        w[k] = exp2_fast(__uint_as_float(s[b][k]) - mu);
+                        sum += c >= c_lo && c < c_hi ? w[k] : 0.f;
+                    }
+                    l = c_hi > 32 * b && c_lo < 32 * b + 32 ? fmaf(sum, is[b], l) : l;
+                } else {
+                    const float off = es[b] - mu;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        w[k] = exp2_fast(fmaf(__uint_as_float(s[b][k]), bk[b], off));
+                        sum += w[k];
+                    }
+                    l = fmaf(sum, is[b], l);
+                }
+                uint32_t ph[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) ph[k] = pack_h2(w[2 * k], w[2 * k + 1]);
+                tmem_st16(ts + 16 * b, ph);
+                if constexpr (NS == 2) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 h = unpack_h2(ph[k]);
+                        ph[k] = pack_h2(w[2 * k] - h.x, w[2 * k + 1] - h.y);
+                    }
+                    tmem_st16(ts + 64 + 16 * b, ph);
+                }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pready[x]);
+        }
+        if (ok && nx > 0) ok = __all_sync(0xffffffffu, wait(&pvdone[x], (nx - 1) & 1));
+        if (ok) {
+            tc_fence_after();
+            const int h = head * a.group + ht * p.hpt + hi, D = a.c.head_dim;
+            const bool none = m == -INFINITY;
+            float inv = 0.f;
+            const int64_t prow = ((int64_t)tok * a.n_heads + h) * a.splits + part;
+            if (a.splits > 1) {
+                // in the join's convention: weights 2^(x - M + kWShift)
+                if (row_ok) a.part_ml[prow] = make_float2(none ? m : m + (kWShift - kTileShift), l);
+                inv = 1.f;
+            } else if (!none) {
+                if (a.sinks && row_ok) l += exp2_fast(fmaf(a.sinks[h], kLog2e, kTileShift - m));
+                inv = 1.f / l;
+            }
+#pragma unroll 1
+            for (int d = 0; d < DP; d += 32) {
+                uint32_t o[32];
+                if (nx > 0) {
+                    tmem_ld32(to + d, o);
+                    tmem_ld_wait();
+                }
+                if (row_ok) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        if (d + k >= D) break;
+                        float v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = none ? 0.f : __uint_as_float(o[k + e]) * inv;
+                        if (a.splits > 1) {
+                            if (!none) *reinterpret_cast<float4 *>(a.part_o + prow * D + d + k) = make_float4(v[0], v[1], v[2], v[3]);
+                        } else {
+                            store4<T>(static_cast<T *>(a.out) + (int64_t)tok * a.o_lt + (int64_t)h * a.o_lh + d + k, a.o_vec, v);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+struct Layout {
+    int64_t cap_q, cap_kv;
+    int splits, split_tiles;
+    size_t plan, q_tiles, kv_base, kv_first, q_img, q_unit, k_img, v_img, units, part_o, part_ml, total;
+};
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+void tile_shape(const AttnParams &p, TileParams *t)
+{
+    t->hpt = std::min(p.group, kTile);
+    t->head_tiles = (p.group + t->hpt - 1) / t->hpt;
+    t->tqt = kTile / t->hpt;
+}
+
+Layout layout(const AttnParams &p, const TileParams &t, int dtype, int64_t max_len)
+{
+    Layout L = {};
+    const int ns = dtype == RF_F32 ? 2 : 1, dp = p.c.head_dim > 64 ? 128 : 64;
+    const int64_t ctt = 2 * t.tqt;
+    L.cap_q = p.b.n_tok / ctt + std::min<int64_t>(p.b.n_seq, p.b.n_tok);
+    // No sequence's position tiles exceed max_len's; with a window, all of
+    // them together do not exceed the windows' and the new tokens'.
+    L.cap_kv = p.b.n_seq * ((max_len + kTile - 1) / kTile);
+    if (p.window > 0)
+        L.cap_kv = std::min<int64_t>(L.cap_kv, (p.b.n_seq * std::min(p.window, max_len) + p.b.n_tok) / kTile + 3LL * p.b.n_seq);
+    const int64_t kvh = p.c.n_kv_heads;
+    // Parts of the position tiles: enough CTAs to fill the SMs about twice,
+    // at least four tiles to a part.
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(L.cap_q, (p.b.n_tok + ctt - 1) / ctt) * kvh * t.head_tiles);
+    int64_t seen = (max_len + kTile - 1) / kTile;
+    if (p.window > 0) seen = std::min<int64_t>(seen, (p.window + ctt) / kTile + 2);
+    int64_t splits = std::max<int64_t>(1, 2LL * num_sms() / ctas);
+    splits = std::min<int64_t>(splits, std::max<int64_t>(1, seen / 4));
+    splits = std::min<int64_t>(splits, 64);
+    L.split_tiles = (int)((seen + splits - 1) / splits);
+    L.splits = (int)((seen + L.split_tiles - 1) / L.split_tiles);
+    size_t at = 0;
+    auto take = [&at](size_t n) {
+        const size_t here = at;
+        at += up256(n);
+        return here;
+    };
+    const size_t slot = (size_t)kTile * dp * 2;
+    L.plan = take(sizeof(TilePlan));
+    L.q_tiles = take(L.cap_q * sizeof(int2));
+    L.kv_base = take((p.b.n_seq + 1) * sizeof(int32_t));
+    L.kv_first = take(p.b.n_seq * sizeof(int32_t));
+    L.q_img = take(L.cap_q * kvh * t.head_tiles * 2 * ns * slot);
+    L.q_unit = take(L.cap_q * kvh * t.head_tiles * 2 * kTile * sizeof(float));
+    L.k_img = take(L.cap_kv * kvh * slot);
+    L.v_img = take(L.cap_kv * kvh * slot);
+    L.units = take(L.cap_kv * kvh * 12 * sizeof(float));
+    if (L.splits > 1) {
+        const size_t rows = (size_t)p.b.n_tok * p.n_heads * L.splits;
+        L.part_o = take(rows * p.c.head_dim * sizeof(float));
+        L.part_ml = take(rows * sizeof(float2));
+    }
+    L.total = at;
+    return L;
+}
+
+template <typename T, int DP>
+rf_status launch_tiles(const TileParams &t, cudaStream_t s, bool chain)
+{
+    constexpr int NS = sizeof(T) == 4 ? 2 : 1;
+    static_assert(tile_smem<DP, NS>() + 64 <= 232448, "tiles exceed the 227 KB of shared memory");
+    static std::once_flag once[64];
+    static bool okd[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return RF_ERR_CUDA;
+    }
+    std::call_once(once[dev & 63], [dev] {
+        okd[dev & 63] = cudaFuncSetAttribute(attn_tile_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)tile_smem<DP, NS>()) == cudaSuccess;
+        cudaGetLastError();
+    });
+    if (!okd[dev & 63]) return RF_ERR_CUDA;
+    const AttnParams &a = t.a;
+    const int64_t kvh = a.c.n_kv_heads, ctas = (int64_t)t.cap_q * kvh * t.head_tiles;
+    const int64_t stage = (int64_t)t.cap_kv * kvh + ctas + kPadParts;
+    if (stage > 0x7fffffffLL || ctas * a.splits > 0x7fffffffLL) return RF_ERR_TOO_LARGE;
+    if (const rf_status st = launch_kernel(tile_plan_kernel, dim3(1), dim3(1024), 0, s, chain, t)) return st;
+    if (const rf_status st = launch_kernel(tile_stage_kernel<T, DP>, dim3((unsigned)stage), dim3(256), 0, s, true, t))
+        return st;
+    return launch_kernel(attn_tile_kernel<T, DP>, dim3((unsigned)(ctas * a.splits)), dim3(kMainThreads),
+                         tile_smem<DP, NS>(), s, true, t);
+}
+
+}  // namespace
+
+bool attn_tile_takes(const AttnParams &p)
+{
+    // Tiles of 128 rows are worth their staging where a sequence's new rows
+    // (tokens x heads of a group) fill about half of one.
+    return p.c.head_dim <= 128 && (int64_t)p.b.n_tok * p.group >= 64LL * p.b.n_seq;
+}
+
+size_t attn_tile_workspace(const AttnParams &p, int dtype, int64_t max_len)
+{
+    TileParams t;
+    tile_shape(p, &t);
+    return layout(p, t, dtype, max_len).total;
+}
+
+rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *workspace, cudaStream_t s, bool chain)
+{
+    TileParams t;
+    tile_shape(p, &t);
+    const Layout L = layout(p, t, dtype, max_len);
+    if (L.cap_q > 0x3fffffffLL || L.cap_kv > 0x3fffffffLL) return RF_ERR_TOO_LARGE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.splits = L.splits;
+    p.split_blocks = 0;
+    p.part_o = reinterpret_cast<float *>(ws + L.part_o);
+    p.part_ml = reinterpret_cast<float2 *>(ws + L.part_ml);
+    t.a = p;
+    t.cap_q = (int)L.cap_q, t.cap_kv = (int)L.cap_kv;
+    t.plan = reinterpret_cast<TilePlan *>(ws + L.plan);
+    t.q_tiles = reinterpret_cast<int2 *>(ws + L.q_tiles);
+    t.kv_base = reinterpret_cast<int32_t *>(ws + L.kv_base);
+    t.kv_first = reinterpret_cast<int32_t *>(ws + L.kv_first);
+    t.q_img = ws + L.q_img;
+    t.q_unit = reinterpret_cast<float *>(ws + L.q_unit);
+    t.k_img = ws + L.k_img, t.v_img = ws + L.v_img;
+    t.units = reinterpret_cast<float *>(ws + L.units);
+    t.split_tiles = L.split_tiles;
+    t.qk_abs = p.qk_scale < 0.f ? -p.qk_scale : p.qk_scale;
+    t.negate = p.qk_scale < 0.f;
+    t.limit = kWaitLimitNs;
+    const bool small = p.c.head_dim <= 64;
+    rf_status st = with_dtype(dtype, [&](auto v) {
+        using T = decltype(v);
+        return small ? launch_tiles<T, 64>(t, s, chain) : launch_tiles<T, 128>(t, s, chain);
+    });
+    if (st != RF_OK) return st;
+    return p.splits > 1 ? launch_attn_join(p, dtype, s) : RF_OK;
+}
+
+rf_status read_and_clear_attn_tile_status()
+{
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_tile_status, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
+    if (v != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_tile_status, &zero, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
+    }
+    return static_cast<rf_status>(v);
+}
+
+}  // namespace rf

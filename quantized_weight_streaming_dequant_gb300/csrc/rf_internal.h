@@ -108,6 +108,7 @@ rf_status read_and_clear_gemm_status();
 // kernels, read and cleared.
 rf_status read_and_clear_kv_status();
 rf_status read_and_clear_attn_status();
+rf_status read_and_clear_attn_tile_status();
 // Arms the one-shot wait fault of the next producer-mode launch
 // (rf_debug_arm_wait_fault).
 rf_status arm_wait_fault(uint32_t limit_us);

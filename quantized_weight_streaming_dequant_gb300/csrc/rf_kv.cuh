@@ -72,10 +72,38 @@ __device__ __forceinline__ void store4(T *p, bool vec, const float (&f)[4])
     }
 }
 
+// ------------------------------------------------------------------- codes
+// Codes 0, 1 / 2, 3 of a word, their sign bits flipped, as an fp16 pair:
+// 0x6400 | u is 1024 + code + 128, so subtracting 1152 is exact.
+__device__ __forceinline__ uint32_t codes_sub(uint32_t a)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x64806480u));
+    return r;
+}
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return codes_sub(prmt(w, 0x64646464u, 0x5140u)); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return codes_sub(prmt(w, 0x64646464u, 0x7362u)); }
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t v)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // ------------------------------------------------------------------- batch
 // The sequence that owns token t, or -1: the last s with q_start[s] <= t,
 // if t < q_start[s+1].  Reads only q_start[0 .. n_seq].
-__device__ __forceinline__ int find_seq(const int32_t *__restrict__ q_start, int n_seq, int t)
+__device__ __forceinline__ int find_seq(const int32_t *q_start, int n_seq, int t)
 {
     int lo = 0, hi = n_seq;   // q_start[lo] <= t (checked below); q_start[hi] > t or hi == n_seq
     while (hi - lo > 1) {

@@ -73,11 +73,11 @@ template <int E>
 __device__ __forceinline__ void load_weights(const float *p, float (&f)[E])
 {
     if constexpr (E == 1) {
-        f[0] = __ldg(p);
+        f[0] = *p;
     } else {
 #pragma unroll
         for (int i = 0; i < E; i += 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p + i));
+            const float4 a = *reinterpret_cast<const float4 *>(p + i);
             f[i] = a.x, f[i + 1] = a.y, f[i + 2] = a.z, f[i + 3] = a.w;
         }
     }

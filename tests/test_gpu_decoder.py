@@ -387,3 +387,78 @@ def test_many_pages_pass_32_bit_offsets():
     ref, mag, xmag = od.attention(small, np.array([[0, 1, 2]]), [0], [0, 150], 150, q64, 0.125)
     assert (np.abs(out.double().cpu().numpy() - ref) <= od.attention_bound("float32", 64, 150, ref, mag, xmag)).all()
     assert rf.device_status() == rf.OK
+
+
+# ------------------------------------------------------------- long chunks
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim,heads,kv,page,past,new", [
+    (128, 4, 1, 64, [0], [300]), (64, 8, 1, 32, [0, 77, 3], [129, 200, 64]), (128, 2, 2, 128, [515], [257]),
+    (80, 5, 1, 256, [130, 0], [90, 31]), (16, 3, 1, 32, [0], [130]), (112, 7, 1, 64, [40], [75]),
+    (64, 130, 1, 64, [33], [3]), (128, 20, 1, 32, [0, 500], [40, 1]), (64, 64, 2, 64, [0, 10, 700, 0], [0, 5, 2, 30])])
+def test_attention_long_chunks(dtype, dim, heads, kv, page, past, new):
+    rng = np.random.default_rng([dim, heads, sum(new)])
+    su = Setup(rng, past, new, kv, dim, page, pad_tokens=3)
+    assert su.n_tok * heads // kv >= 64 * len(past)              # rows enough for the 128-row tiles
+    q, q64 = randn(rng, (su.n_tok, heads, dim), dtype, 2.0)
+    out = check_attention(su, q, q64, dtype)
+    assert not out[-3:].any()
+    sinks = rng.standard_normal(heads).astype(np.float32)
+    check_attention(su, q, q64, dtype, scale=-0.15, window=37, sinks=sinks, max_len=max(p + n for p, n in zip(past, new)))
+    assert rf.device_status() == rf.OK
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_long_chunks_split_and_joined(dtype, dim):
+    rng = np.random.default_rng(dim)
+    su = Setup(rng, [4000], [40], 1, dim, 64, pad_tokens=1)
+    q, q64 = randn(rng, (su.n_tok, 4, dim), dtype, 2.0)
+    a = check_attention(su, q, q64, dtype, max_len=4040)
+    assert torch.equal(a, rf.attention(su.cache, su.batch, q, max_len=4040))
+    check_attention(su, q, q64, dtype, window=1000, sinks=np.array([0.5, -1.0, 2.0, 0.0], np.float32))
+    check_attention(su, q, q64, dtype, scale=0.0)
+
+
+def test_attention_long_chunks_hide_missing_pages_and_nan_blocks():
+    rng = np.random.default_rng(18)
+    su = Setup(rng, [200], [100], 2, 64, 32)
+    su.table[0, 3] = -1                                         # positions 96..127 have no page
+    su.ref.scales[1][su.table[0, 0], 1] = 255                   # values 0..31, head 1
+    su.upload()
+    q, q64 = randn(rng, (su.n_tok, 4, 64))
+    out = check_attention(su, q, q64, "float32")
+    assert torch.isnan(out[:, 2:]).all() and torch.isfinite(out[:, :2]).all()
+    assert rf.device_status() == 1
+    out = check_attention(su, q, q64, "float32", window=150)    # the first row sees positions 51..
+    assert torch.isfinite(out).all()
+
+
+def test_attention_long_chunks_strides_streams_and_chains():
+    rng = np.random.default_rng(19)
+    su = Setup(rng, [64, 300], [90, 70], 2, 128, 64)
+    for dtype in DTYPES:
+        q, q64 = randn(rng, (su.n_tok, 8, 128), dtype)
+        want = check_attention(su, q, q64, dtype)
+        for pad in ((2, 0), (0, 8), (1, 3)):
+            qs, out = strided(q, *pad), strided(torch.zeros_like(q), *pad)
+            rf.attention(su.cache, su.batch, qs, out=out)
+            assert torch.equal(out, want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = rf.attention(su.cache, su.batch, q)
+            got2 = rf.attention(su.cache, su.batch, q, flags=rf.CHAIN)
+        side.synchronize()
+        assert torch.equal(got, want) and torch.equal(got2, want)
+
+
+def test_attention_tiles_and_rows_agree_on_one_token_at_a_time():
+    """A chunk gives each token what it gets alone (within both paths' bounds)."""
+    rng = np.random.default_rng(20)
+    su = Setup(rng, [150], [64], 1, 128, 64)
+    q, q64 = randn(rng, (64, 4, 128))
+    whole = check_attention(su, q, q64, "float32")
+    for t in (0, 31, 63):
+        one = rf.KVBatch(i32(su.table), i32([150 + t]), i32([0, 1]), 1)
+        alone = rf.attention(su.cache, one, q[t:t + 1].contiguous())
+        assert torch.allclose(alone[0], whole[t], rtol=1e-4, atol=1e-5)
