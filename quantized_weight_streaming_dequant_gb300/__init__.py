@@ -157,9 +157,10 @@ def _check(code: int, what: str) -> None:
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # The handle alone: building a torch.cuda.Stream costs 3 us a call.
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -537,31 +538,31 @@ def _dtype(t) -> int:
     if _DTYPES is None:
         import torch
         _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    d = _DTYPES.get(t.dtype)
+    d = _DTYPES.get(t.dtype)   # F32 is 0
     if d is None:
         raise ValueError(f"activations are float32, float16 or bfloat16, not {t.dtype}")
     return d
-
-
-def _act(t, dims: int, what: str, like=None):
-    """Data pointer of an activation tensor with a contiguous last dimension."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{what} must have {dims} dimensions, the last one contiguous")
-    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
-        raise ValueError(f"{what} must have the type and shape {like.dtype}, {tuple(like.shape)}")
-    return t.data_ptr()
 
 
 def _f32_ptr(t, n: int, what: str):
     """Data pointer of n contiguous float32 device values, or None."""
     if t is None:
         return None
-    if not t.is_cuda or t.element_size() != 4 or not t.is_floating_point() or \
-            not t.is_contiguous() or t.numel() != n:
+    if not t.is_cuda or _dtype(t) != F32 or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{what} must be {n} contiguous float32 values on the device")
     return t.data_ptr()
+
+
+def _rows(t, n_tok: int, n: int, dtype: int, what: str):
+    """(pointer, row stride) of a (n_tok, n) tensor with contiguous rows; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or _dtype(t) != dtype or t.shape != (n_tok, n):
+        raise ValueError(f"{what} must be a ({n_tok}, {n}) CUDA tensor of the call's type")
+    ld, one = t.stride()
+    if one != 1 and n > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.data_ptr(), ld if n_tok > 1 or ld > n else n   # the stride of one row says nothing
 
 
 def norm_residual(residual, x=None, *, post_weight=None, gate=None, scale: float = 1.0, weight=None,
@@ -572,32 +573,29 @@ def norm_residual(residual, x=None, *, post_weight=None, gate=None, scale: float
     (residual + scale * gate * post_norm(x), its norm); the norm is None with
     norm=False."""
     import torch
-    ref = residual if residual is not None else x
-    if ref is None:
-        raise ValueError("residual and x are both None")
-    px = _act(x, 2, "x", ref) if x is not None else None
-    pr = _act(residual, 2, "residual") if residual is not None else None
-    n_tok, n = ref.shape
+    like = residual if residual is not None else x
+    if like is None or like.dim() != 2:
+        raise ValueError("residual or x must be given, (n_tok, n)")
+    n_tok, n = like.shape
+    dt = _dtype(like)
+    px, ldx = _rows(x, n_tok, n, dt, "x")
+    pr, ldr = _rows(residual, n_tok, n, dt, "residual")
     if residual_out is None:
-        residual_out = torch.empty((n_tok, n), dtype=ref.dtype, device=ref.device)
+        residual_out = torch.empty((n_tok, n), dtype=like.dtype, device=like.device)
+        po, ldo = residual_out.data_ptr(), n
+    else:
+        po, ldo = _rows(residual_out, n_tok, n, dt, "residual_out")
     if y is None and norm:
-        y = torch.empty((n_tok, n), dtype=ref.dtype, device=ref.device)
+        y = torch.empty((n_tok, n), dtype=like.dtype, device=like.device)
+        py, ldy = y.data_ptr(), n
+    else:
+        py, ldy = _rows(y, n_tok, n, dt, "y")
     pg, ldg = None, 0
     if gate is not None:
-        if gate.dim() == 2:
-            if gate.shape != ref.shape or gate.element_size() != 4 or not gate.is_floating_point():
-                raise ValueError("gate must be float32, (n,) or (n_tok, n)")
-            pg, ldg = _act(gate, 2, "gate"), gate.stride(0)
-        else:
-            pg = _f32_ptr(gate, n, "gate")
-    # The stride of a single row says nothing; n is always valid for it.
-    ld = lambda t: max(t.stride(0), n) if t is not None and n_tok == 1 else (t.stride(0) if t is not None else 0)  # noqa: E731
-    _check(lib().rf_norm_residual(_dtype(ref), n_tok, n, px, ld(x), _f32_ptr(post_weight, n, "post_weight"),
-                                  pg, ldg, scale, pr, ld(residual),
-                                  _act(residual_out, 2, "residual_out", ref), ld(residual_out),
-                                  _f32_ptr(weight, n, "weight"),
-                                  _act(y, 2, "y", ref) if y is not None else None, ld(y), eps, flags,
-                                  _stream(stream)), "rf_norm_residual")
+        pg, ldg = _rows(gate, n_tok, n, F32, "gate") if gate.dim() == 2 else (_f32_ptr(gate, n, "gate"), 0)
+    _check(lib().rf_norm_residual(dt, n_tok, n, px, ldx, _f32_ptr(post_weight, n, "post_weight"), pg, ldg,
+                                  scale, pr, ldr, po, ldo, _f32_ptr(weight, n, "weight"), py, ldy, eps,
+                                  flags, _stream(stream)), "rf_norm_residual")
     return residual_out, y
 
 
@@ -653,15 +651,16 @@ class KVBatch:
         self.ref = ctypes.addressof(self.struct)
 
 
-def _heads(t, n_tok: int, dim: int, what: str):
+def _heads(t, n_tok: int, dim: int, dtype: int, what: str):
     """(pointer, token stride, head stride, heads) of a (n_tok, heads, dim) tensor."""
-    p = _act(t, 3, what)
-    shape, stride = t.shape, t.stride()
-    if shape[0] != n_tok or shape[2] != dim:
-        raise ValueError(f"{what} must be ({n_tok}, heads, {dim})")
+    if not t.is_cuda or _dtype(t) != dtype or t.dim() != 3:
+        raise ValueError(f"{what} must be a ({n_tok}, heads, {dim}) CUDA tensor of the call's type")
+    nt, heads, d = t.shape
+    lt, lh, one = t.stride()
+    if nt != n_tok or d != dim or one != 1:
+        raise ValueError(f"{what} must be ({n_tok}, heads, {dim}), the last dimension contiguous")
     # strides of dimensions of one element say nothing
-    return (p, stride[0] if n_tok > 1 else max(stride[0], dim),
-            stride[1] if shape[1] > 1 else max(stride[1], dim), shape[1])
+    return t.data_ptr(), lt if nt > 1 or lt > dim else dim, lh if heads > 1 or lh > dim else dim, heads
 
 
 def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None, sin=None,
@@ -669,22 +668,20 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None
     """rf_kv_append: k, v (n_tok, n_kv_heads, head_dim) go to the cache, rotated
     (k) by the tables cos, sin (n_pos, rot / 2); returns the rotated q
     (n_tok, n_heads, head_dim), or None without q."""
-    import torch
-    n_tok, dim = batch.n_tok, cache.head_dim
-    pk, klt, klh, kh = _heads(k, n_tok, dim, "k")
-    pv, vlt, vlh, vh = _heads(v, n_tok, dim, "v")
-    if kh != cache.n_kv_heads or vh != kh or v.dtype != k.dtype:
-        raise ValueError("k and v must have the cache's heads and one type")
+    n_tok, dim, dt = batch.n_tok, cache.head_dim, _dtype(k)
+    pk, klt, klh, kh = _heads(k, n_tok, dim, dt, "k")
+    pv, vlt, vlh, vh = _heads(v, n_tok, dim, dt, "v")
+    if kh != cache.n_kv_heads or vh != kh:
+        raise ValueError("k and v must have the cache's heads")
     pq = po = None
     qlt = qlh = olt = olh = nh = 0
     if q is not None:
-        if q.dtype != k.dtype:
-            raise ValueError("q, k and v must have one type")
+        pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        pq, qlt, qlh, nh = _heads(q, n_tok, dim, "q")
-        po, olt, olh, oh = _heads(q_out, n_tok, dim, "q_out")
-        if oh != nh or q_out.dtype != q.dtype:
+            import torch
+            q_out = torch.empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+        po, olt, olh, oh = _heads(q_out, n_tok, dim, dt, "q_out")
+        if oh != nh:
             raise ValueError("q_out must be like q")
     pc = ps = None
     n_pos = rot = 0
@@ -693,7 +690,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None
             raise ValueError("cos and sin must be two (n_pos, rot / 2) tables")
         n_pos, rot = cos.shape[0], 2 * cos.shape[1]
         pc, ps = _f32_ptr(cos, cos.numel(), "cos"), _f32_ptr(sin, cos.numel(), "sin")
-    _check(lib().rf_kv_append(cache.ref, batch.ref, _dtype(k), pk, klt, klh, pv, vlt, vlh, pq, qlt, qlh,
+    _check(lib().rf_kv_append(cache.ref, batch.ref, dt, pk, klt, klh, pv, vlt, vlh, pq, qlt, qlh,
                               po, olt, olh, nh, pc, ps, n_pos, rot, rope, flags, _stream(stream)),
            "rf_kv_append")
     return q_out
@@ -704,13 +701,15 @@ def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None,
     tensors (n_tok, n_kv_heads, head_dim)."""
     import torch
     shape = (batch.n_tok, cache.n_kv_heads, cache.head_dim)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.float32, device=cache.k.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.float32, device=cache.k.device)
-    n = shape[0] * shape[1] * shape[2]
-    _check(lib().rf_kv_read(cache.ref, batch.ref, _f32_ptr(k_out, n, "k_out"), _f32_ptr(v_out, n, "v_out"),
-                            flags, _stream(stream)), "rf_kv_read")
+    n, out = shape[0] * shape[1] * shape[2], []
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.float32, device=cache.k.device)
+            out += [t, t.data_ptr()]
+        else:
+            out += [t, _f32_ptr(t, n, what)]
+    k_out, pk, v_out, pv = out
+    _check(lib().rf_kv_read(cache.ref, batch.ref, pk, pv, flags, _stream(stream)), "rf_kv_read")
     return k_out, v_out
 
 
@@ -726,19 +725,19 @@ def attention(cache: KVCache, batch: KVBatch, q, out=None, scale: float | None =
     """rf_attention: q (n_tok, n_heads, head_dim) against the cache, which
     already holds the batch's own tokens; scale defaults to head_dim ** -0.5.
     The workspace is allocated when not given."""
-    import torch
-    n_tok, dim = batch.n_tok, cache.head_dim
-    pq, qlt, qlh, nh = _heads(q, n_tok, dim, "q")
+    n_tok, dim, dt = batch.n_tok, cache.head_dim, _dtype(q)
+    pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
     if out is None:
+        import torch
         out = torch.empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
-    po, olt, olh, oh = _heads(out, n_tok, dim, "out")
-    if oh != nh or out.dtype != q.dtype:
+    po, olt, olh, oh = _heads(out, n_tok, dim, dt, "out")
+    if oh != nh:
         raise ValueError("out must be like q")
     if workspace is None:
         workspace = attention_workspace(cache, batch, q, max_len, window)
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
-    _check(lib().rf_attention(cache.ref, batch.ref, _dtype(q), pq, qlt, qlh, nh,
+    _check(lib().rf_attention(cache.ref, batch.ref, dt, pq, qlt, qlh, nh,
                               dim ** -0.5 if scale is None else scale, window,
                               _f32_ptr(sinks, nh, "sinks"), po, olt, olh, max_len, ws, ws_bytes, flags,
                               _stream(stream)), "rf_attention")

@@ -27,6 +27,7 @@
 // Every wait is bounded; after a failure every role stops, copies and
 // products already issued are waited for, and tensor memory is freed.
 #include <algorithm>
+#include <cfloat>
 #include <mutex>
 
 #include "rf_attn.h"
@@ -38,7 +39,8 @@ namespace {
 __device__ int g_tile_status = 0;
 
 constexpr int kTile = 128;          // query rows, and positions, per tile
-constexpr int kMainThreads = 320;   // two softmax groups of four warps, MMA issue, copies
+constexpr int kMainThreads = 320;   // two softmax groups of four warps, product issue, copies
+constexpr int kFlush = 16;          // position tiles that fp32 sums stay in tensor memory
 constexpr int kPadParts = 8;        // CTAs that zero the rows of no sequence
 constexpr float kTileShift = 8.f;   // weights are 2^(x - m + 8) <= 2^15
 constexpr float kLazy = 7.f;        // growth of a maximum that is not yet applied
@@ -60,6 +62,7 @@ struct TileParams {
     float *q_unit;                  // [cap_q][kv head][head tile][2][128]
     uint8_t *k_img, *v_img;         // [kv head][cap_kv][128 x DP] fp16
     float *units;                   // [kv head][cap_kv][12]: 2^ek, ev, 2^-ev of four blocks
+    float4 *sums;                   // fp32: [CTA][2][DP / 4][128] sums taken out of tensor memory
     int split_tiles;                // position tiles per part
     float qk_abs;                   // |scale| * log2(e); its sign is in the queries
     bool negate;
@@ -320,6 +323,58 @@ __host__ __device__ constexpr uint32_t tile_idesc(int n)
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 
+// Two fp32 values per instruction.
+__device__ __forceinline__ uint64_t f2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// sums = sums * pend (or 0 at first) + O, or with `back` the result into O.
+template <int DP>
+__device__ __forceinline__ void flush(uint32_t to, float4 *sums, float pend, bool more, bool back = false)
+{
+#pragma unroll 1
+    for (int d = 0; d < DP; d += 16) {
+        uint32_t o[16];
+        float4 v[4] = {};
+        tmem_ld16(to + d, o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (more) v[k] = sums[(d / 4 + k) * kTile];
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k].x = fmaf(v[k].x, pend, __uint_as_float(o[4 * k]));
+            v[k].y = fmaf(v[k].y, pend, __uint_as_float(o[4 * k + 1]));
+            v[k].z = fmaf(v[k].z, pend, __uint_as_float(o[4 * k + 2]));
+            v[k].w = fmaf(v[k].w, pend, __uint_as_float(o[4 * k + 3]));
+            if (!back) sums[(d / 4 + k) * kTile] = v[k];
+            o[4 * k] = __float_as_uint(v[k].x), o[4 * k + 1] = __float_as_uint(v[k].y);
+            o[4 * k + 2] = __float_as_uint(v[k].z), o[4 * k + 3] = __float_as_uint(v[k].w);
+        }
+        if (back) tmem_st16(to + d, o);
+    }
+    if (back) tmem_st_wait();
+}
+
 template <typename T, int DP>
 __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams p)
 {
@@ -367,8 +422,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
     int n[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const int to = part == a.splits - 1 ? t_hi[x] : min(t_hi[x], from + p.split_tiles);
-        n[x] = max(0, to - from);
+        n[x] = max(0, min(t_hi[x], from + p.split_tiles) - from);
     }
     const int nmax = max(n[0], n[1]);
     const int64_t at = ((int64_t)qt * a.c.n_kv_heads + head) * p.head_tiles + ht;
@@ -425,8 +479,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
         }
         __syncwarp();
     } else if (warp == 8) {
-        // Products.  Tile x: S at columns 128 x, P over it (first term in
-        // its first 64 columns, second in the others), O at 256 + DP x.
+        // Products.  Tile x: S at columns 128 x, P over it (the weights of
+        // block b in S's columns 32 b: 16 columns of fp16 pairs a term), O at
+        // 256 + DP x.
         if (lane == 0 && nmax > 0) {
             const uint64_t qd = smem_desc(smem_addr(q_s), 16 * DP), kd = smem_desc(smem_addr(ring), 16 * DP);
             const uint64_t vd = smem_desc(smem_addr(ring), 2048);
@@ -447,7 +502,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                 for (int t = NS - 1; t >= 0; --t)
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 64 * t + 8 * k,
+                        tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 32 * (k >> 1) + 16 * t + 8 * (k & 1),
                                   vd + (uint64_t)((slot * SLOT + k * 256) >> 4), tile_idesc(DP),
                                   add || !(t == NS - 1 && k == 0));
                 tc_commit(&pvdone[x]);
@@ -467,7 +522,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                 for (int x = 0; x < 2; ++x) {
                     if (j < n[x]) {
                         if (!(ok = wait(&pready[x], j & 1))) break;
-                        values(x, iv % R, j > 0);
+                        values(x, iv % R, NS == 2 ? j % kFlush != 0 : j > 0);
                     }
                     if (x == 1) tc_commit(&empty[iv % R]);
                     if (j + 1 < n[x]) scores(x, ik % R);
@@ -481,7 +536,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
         // Softmax: thread i of group x owns row i of tile x (tensor-memory
         // lane i).
         const int x = warp >> 2, i = threadIdx.x & 127;
@@ -494,61 +549,84 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
         const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + DP * x;
         float m = -INFINITY, l = 0.f;
         const float4 *units = reinterpret_cast<const float4 *>(p.units + ((int64_t)head * p.cap_kv + kv0 + from) * 12);
+        // fp32: the tensor core truncates its sums, which drifts by about
+        // 1e-8 per step; so O is added to sums in memory every kFlush tiles.
+        // pend: growth of m since the last time.
+        float4 *sums = p.sums + ((int64_t)blockIdx.x * 2 + x) * (DP / 4) * kTile + i;
+        float pend = 1.f;
         bool ok = true;
-        // Newest visible column of the current tile and the first one.
         int64_t base = (int64_t)(kvf + from) * kTile;
         for (int j = 0; j < nx; ++j, base += kTile) {
             const float4 ku = units[3 * j], ev = units[3 * j + 1], iv = units[3 * j + 2];
-            const float bk[4] = {bq * ku.x, bq * ku.y, bq * ku.z, bq * ku.w};
-            const float es[4] = {ev.x, ev.y, ev.z, ev.w}, is[4] = {iv.x, iv.y, iv.z, iv.w};
+            float bk[4] = {bq * ku.x, bq * ku.y, bq * ku.z, bq * ku.w};
+            float es[4] = {ev.x, ev.y, ev.z, ev.w}, is[4] = {iv.x, iv.y, iv.z, iv.w};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) bk[b] = bk[b] == 0.f ? FLT_MIN : bk[b];   // -inf scores stay -inf
             ok = __all_sync(0xffffffffu, wait(&sfull[x], j & 1));
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s[b]);
-            tmem_ld_wait();
-            const int c_hi = (int)min((int64_t)kTile, max((int64_t)0, top + 1 - base));
-            const int c_lo = a.window > 0 ? (int)min((int64_t)kTile, max((int64_t)0, top - a.window + 1 - base)) : 0;
-            const bool edge = __any_sync(0xffffffffu, row_ok && (c_hi < kTile || c_lo > 0));
-            float mn = m;
+            // Visible columns [c_lo, c_hi); hidden scores become -inf, and the
+            // units of a block without a visible one do not count.
+            const bool edge = __any_sync(0xffffffffu, row_ok && (top < base + kTile - 1 || (a.window > 0 && top - a.window >= base)));
+            int c_lo = 0, c_hi = kTile;
             if (edge) {
-                // x with hidden columns at -inf, then as if all units were 1
+                c_hi = (int)min((int64_t)kTile, max((int64_t)0, top + 1 - base));
+                if (a.window > 0) c_lo = (int)min((int64_t)kTile, max((int64_t)0, top - a.window + 1 - base));
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
+                    if (c_hi <= 32 * b || c_lo >= 32 * b + 32) bk[b] = 1.f, es[b] = 0.f, is[b] = 0.f;
+            }
+            auto hide = [&](uint32_t (&s)[32], int b) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int c = 32 * b + k;
-                        const float v = c >= c_lo && c < c_hi ? fmaf(__uint_as_float(s[b][k]), bk[b], es[b]) : -INFINITY;
-                        s[b][k] = __float_as_uint(v);
-                        mn = fmaxf(mn, v);
-                    }
-            } else {
+                for (int k = 0; k < 32; ++k)
+                    if (32 * b + k < c_lo || 32 * b + k >= c_hi) s[k] = 0xff800000u;
+            };
+            // The maximum; the scores are read again for the weights, which
+            // keeps 32 of a row's 128 in registers instead of all.
+            float mn = m;
+            uint32_t s[2][32];
+            tmem_ld32(ts, s[0]);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float v = __uint_as_float(s[b][0]);
+            for (int b = 0; b < 4; ++b) {
+                tmem_ld_wait();
+                if (b < 3) tmem_ld32(ts + 32 * (b + 1), s[(b + 1) & 1]);
+                uint32_t (&sb)[32] = s[b & 1];
+                if (edge) hide(sb, b);
+                float v[4];
 #pragma unroll
-                    for (int k = 1; k < 32; ++k) v = fmaxf(v, __uint_as_float(s[b][k]));
-                    mn = fmaxf(mn, fmaf(v, bk[b], es[b]));
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = fmaxf(__uint_as_float(sb[e]), __uint_as_float(sb[4 + e]));
+#pragma unroll
+                    for (int k = 8; k < 32; k += 8)
+                        v[e] = fmaxf(fmaxf(v[e], __uint_as_float(sb[k + e])), __uint_as_float(sb[k + 4 + e]));
                 }
+                mn = fmaxf(mn, fmaf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), bk[b], es[b]));
+            }
+            tmem_ld32(ts, s[0]);
+            if (NS == 2 && j > 0 && j % kFlush == 0) {
+                ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                flush<DP>(to, sums, pend, j > kFlush);
+                pend = 1.f;
             }
             if (__any_sync(0xffffffffu, mn > m + kLazy)) {
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                const float alpha = exp2_fast(m - mu);
+                const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
                 m = mn;
                 l *= alpha;
-                if (j > 0) {
+                pend *= alpha;
+                if (NS == 2 ? j % kFlush != 0 : j > 0) {
                     ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int d = 0; d < DP; d += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + d, o);
+                    for (int d = 0; d < DP; d += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + d, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tmem_st32(to + d, o);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tmem_st16(to + d, o);
                     }
                     tmem_st_wait();
                 }
@@ -556,37 +634,35 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             const float mu = (m == -INFINITY ? 0.f : m) - kTileShift;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                float w[32];
-                float sum = 0.f;
-                if (edge) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int c = 32 * b + k;
-                        w[k] = exp2_fast(__uint_as_float(s[b][k]) - mu);
-                        sum += c >= c_lo && c < c_hi ? w[k] : 0.f;
-                    }
-                    l = c_hi > 32 * b && c_lo < 32 * b + 32 ? fmaf(sum, is[b], l) : l;
-                } else {
-                    const float off = es[b] - mu;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        w[k] = exp2_fast(fmaf(__uint_as_float(s[b][k]), bk[b], off));
-                        sum += w[k];
-                    }
-                    l = fmaf(sum, is[b], l);
-                }
+                tmem_ld_wait();
+                if (b < 3) tmem_ld32(ts + 32 * (b + 1), s[(b + 1) & 1]);
+                uint32_t (&sb)[32] = s[b & 1];
+                if (edge) hide(sb, b);
+                const uint64_t k2 = f2(bk[b], bk[b]), off = f2(es[b] - mu, es[b] - mu);
+                uint64_t sum[2] = {0, 0};
                 uint32_t ph[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) ph[k] = pack_h2(w[2 * k], w[2 * k + 1]);
-                tmem_st16(ts + 16 * b, ph);
+                for (int k = 0; k < 16; ++k) {
+                    float u, v;
+                    f2_split(f2_fma(f2(__uint_as_float(sb[2 * k]), __uint_as_float(sb[2 * k + 1])), k2, off), u, v);
+                    u = exp2_fast(u);
+                    v = exp2_fast(v);
+                    sum[k & 1] = f2_add(sum[k & 1], f2(u, v));
+                    ph[k] = pack_h2(u, v);
+                    if constexpr (NS == 2) sb[2 * k] = __float_as_uint(u), sb[2 * k + 1] = __float_as_uint(v);
+                }
+                tmem_st16(ts + 32 * b, ph);
                 if constexpr (NS == 2) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float2 h = unpack_h2(ph[k]);
-                        ph[k] = pack_h2(w[2 * k] - h.x, w[2 * k + 1] - h.y);
+                        ph[k] = pack_h2(__uint_as_float(sb[2 * k]) - h.x, __uint_as_float(sb[2 * k + 1]) - h.y);
                     }
-                    tmem_st16(ts + 64 + 16 * b, ph);
+                    tmem_st16(ts + 32 * b + 16, ph);
                 }
+                float u, v;
+                f2_split(f2_add(sum[0], sum[1]), u, v);
+                l = fmaf(u + v, is[b], l);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -598,6 +674,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             tc_fence_after();
             const int h = head * a.group + ht * p.hpt + hi, D = a.c.head_dim;
             const bool none = m == -INFINITY;
+            if (NS == 2 && nx > kFlush) flush<DP>(to, sums, pend, true, true);
             float inv = 0.f;
             const int64_t prow = ((int64_t)tok * a.n_heads + h) * a.splits + part;
             if (a.splits > 1) {
@@ -644,7 +721,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
 struct Layout {
     int64_t cap_q, cap_kv;
     int splits, split_tiles;
-    size_t plan, q_tiles, kv_base, kv_first, q_img, q_unit, k_img, v_img, units, part_o, part_ml, total;
+    size_t plan, q_tiles, kv_base, kv_first, q_img, q_unit, k_img, v_img, units, sums, part_o, part_ml, total;
 };
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -694,6 +771,8 @@ Layout layout(const AttnParams &p, const TileParams &t, int dtype, int64_t max_l
     L.k_img = take(L.cap_kv * kvh * slot);
     L.v_img = take(L.cap_kv * kvh * slot);
     L.units = take(L.cap_kv * kvh * 12 * sizeof(float));
+    if (ns == 2 && L.split_tiles > kFlush)
+        L.sums = take(L.cap_q * kvh * t.head_tiles * L.splits * 2 * (dp / 4) * kTile * sizeof(float4));
     if (L.splits > 1) {
         const size_t rows = (size_t)p.b.n_tok * p.n_heads * L.splits;
         L.part_o = take(rows * p.c.head_dim * sizeof(float));
@@ -769,6 +848,7 @@ rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *works
     t.q_unit = reinterpret_cast<float *>(ws + L.q_unit);
     t.k_img = ws + L.k_img, t.v_img = ws + L.v_img;
     t.units = reinterpret_cast<float *>(ws + L.units);
+    t.sums = reinterpret_cast<float4 *>(ws + L.sums);
     t.split_tiles = L.split_tiles;
     t.qk_abs = p.qk_scale < 0.f ? -p.qk_scale : p.qk_scale;
     t.negate = p.qk_scale < 0.f;
