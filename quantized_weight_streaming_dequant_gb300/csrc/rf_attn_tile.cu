@@ -13,7 +13,7 @@
 //   tiles  a CTA owns two tiles of 128 query rows (tokens x heads of one K/V
 //          head) and walks the visible positions, 128 at a time:
 //              S = Q K^T (tcgen05.mma from shared memory, fp32 in tensor
-//              memory) -> weights by one thread per row (no shuffles) -> P in
+//              memory) -> weights by two threads per row, 64 columns each -> P in
 //              fp16 over S's own columns -> O += P V (P from tensor memory).
 //          One thread issues the products of the two tiles alternately, so
 //          that one tile's exponentials run under the other's products; O
@@ -39,7 +39,8 @@ namespace {
 __device__ int g_tile_status = 0;
 
 constexpr int kTile = 128;          // query rows, and positions, per tile
-constexpr int kMainThreads = 320;   // two softmax groups of four warps, product issue, copies
+constexpr int kSoftWarps = 16;      // eight per tile: two threads per row
+constexpr int kMainThreads = 32 * (kSoftWarps + 2);   // ... and one warp each for products and copies
 constexpr int kFlush = 16;          // position tiles that fp32 sums stay in tensor memory
 constexpr int kPadParts = 8;        // CTAs that zero the rows of no sequence
 constexpr float kTileShift = 8.f;   // weights are 2^(x - m + 8) <= 2^15
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
     constexpr int NS = sizeof(T) == 4 ? 2 : 1;
     constexpr int R = ring_slots<DP, NS>();
     constexpr int SLOT = kTile * DP * 2;
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *q_s = smem;                          // [2][NS][SLOT]
     uint8_t *ring = smem + 2 * NS * SLOT;         // [R][SLOT]: K0 V0 K1 V1 ...
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + R * SLOT);
@@ -389,6 +390,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
     uint64_t *qfull = bars + 2 * R, *sfull = qfull + 1, *pready = sfull + 2, *pvdone = pready + 2, *drained = pvdone + 2;
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
+    // [tile][half][row]: a half row's maximum.  One buffer is enough: a step's
+    // scores are issued only after every warp has handed over the last step.
+    __shared__ float s_row[2][2][kTile];
     volatile int *stop = &s_stop;
     static_assert((2 * R + 8) * 8 <= 256, "barriers outgrow their room");
 
@@ -435,14 +439,14 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
         mbar_init(qfull, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sfull[x], 1);
-            mbar_init(&pready[x], 4);
+            mbar_init(&pready[x], 8);
             mbar_init(&pvdone[x], 1);
         }
         mbar_init(drained, 1);
         s_stop = 0;
         fence_barrier_init();
     }
-    if (warp == 8) {
+    if (warp == kSoftWarps) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
     }
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
         return false;
     };
 
-    if (warp == 9) {
+    if (warp == kSoftWarps + 1) {
         // Copies: both query tiles, then K and V of each position tile.
         if (lane == 0 && nmax > 0) {
             mbar_arrive_expect_tx(qfull, 2 * NS * SLOT);
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             for (int i = max(0, issued - R); i < issued; ++i) mbar_drain(&full[i % R], (i / R) & 1);
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == kSoftWarps) {
         // Products.  Tile x: S at columns 128 x, P over it (the weights of
         // block b in S's columns 32 b: 16 columns of fp16 pairs a term), O at
         // 256 + DP x.
@@ -536,44 +540,45 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             }
         }
         __syncwarp();
-    } else if (warp < 8) {
-        // Softmax: thread i of group x owns row i of tile x (tensor-memory
-        // lane i).
-        const int x = warp >> 2, i = threadIdx.x & 127;
+    } else {
+        // Softmax: row i of tile x (tensor-memory lane i) belongs to two
+        // threads, one per half of the columns and of O.
+        const int x = warp >> 3, half = (warp >> 2) & 1, i = (warp & 3) * 32 + lane;
         const int ti = i / p.hpt, hi = i % p.hpt, nx = n[x];
         const int tok = q.y + x * p.tqt + ti;
         const bool row_ok = ti < p.tqt && hi < min(p.hpt, a.group - ht * p.hpt) && tok < end;
         const int64_t top = row_ok ? pos0 + x * p.tqt + ti : -1;
         const float bq = p.q_unit[at * (2 * kTile) + x * kTile + i];
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + DP * x;
+        const uint32_t ts = tmem + lanes + 128 * x + 64 * half, to = tmem + lanes + 256 + DP * x + DP / 2 * half;
         float m = -INFINITY, l = 0.f;
-        const float4 *units = reinterpret_cast<const float4 *>(p.units + ((int64_t)head * p.cap_kv + kv0 + from) * 12);
+        // [position tile][2^ek, ev, 2^-ev][block]; this half's two blocks
+        const float2 *units = reinterpret_cast<const float2 *>(p.units + ((int64_t)head * p.cap_kv + kv0 + from) * 12) + half;
         // fp32: the tensor core truncates its sums, which drifts by about
         // 1e-8 per step; so O is added to sums in memory every kFlush tiles.
         // pend: growth of m since the last time.
-        float4 *sums = p.sums + ((int64_t)blockIdx.x * 2 + x) * (DP / 4) * kTile + i;
+        float4 *sums = p.sums + (((int64_t)blockIdx.x * 2 + x) * (DP / 4) + DP / 8 * half) * kTile + i;
         float pend = 1.f;
         bool ok = true;
-        int64_t base = (int64_t)(kvf + from) * kTile;
+        int64_t base = (int64_t)(kvf + from) * kTile + 64 * half;
+        float2 ku, ev, iv;
+        if (nx > 0) ku = units[0], ev = units[2], iv = units[4];
         for (int j = 0; j < nx; ++j, base += kTile) {
-            const float4 ku = units[3 * j], ev = units[3 * j + 1], iv = units[3 * j + 2];
-            float bk[4] = {bq * ku.x, bq * ku.y, bq * ku.z, bq * ku.w};
-            float es[4] = {ev.x, ev.y, ev.z, ev.w}, is[4] = {iv.x, iv.y, iv.z, iv.w};
+            float bk[2] = {bq * ku.x, bq * ku.y}, es[2] = {ev.x, ev.y}, is[2] = {iv.x, iv.y};
+            if (j + 1 < nx) ku = units[6 * j + 6], ev = units[6 * j + 8], iv = units[6 * j + 10];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) bk[b] = bk[b] == 0.f ? FLT_MIN : bk[b];   // -inf scores stay -inf
-            ok = __all_sync(0xffffffffu, wait(&sfull[x], j & 1));
-            if (!ok) break;
+            for (int b = 0; b < 2; ++b) bk[b] = bk[b] == 0.f ? FLT_MIN : bk[b];   // -inf scores stay -inf
+            ok = __all_sync(0xffffffffu, wait(&sfull[x], j & 1)) && ok;
             tc_fence_after();
             // Visible columns [c_lo, c_hi); hidden scores become -inf, and the
             // units of a block without a visible one do not count.
-            const bool edge = __any_sync(0xffffffffu, row_ok && (top < base + kTile - 1 || (a.window > 0 && top - a.window >= base)));
-            int c_lo = 0, c_hi = kTile;
+            const bool edge = __any_sync(0xffffffffu, row_ok && (top < base + 63 || (a.window > 0 && top - a.window >= base)));
+            int c_lo = 0, c_hi = 64;
             if (edge) {
-                c_hi = (int)min((int64_t)kTile, max((int64_t)0, top + 1 - base));
-                if (a.window > 0) c_lo = (int)min((int64_t)kTile, max((int64_t)0, top - a.window + 1 - base));
+                c_hi = (int)min((int64_t)64, max((int64_t)0, top + 1 - base));
+                if (a.window > 0) c_lo = (int)min((int64_t)64, max((int64_t)0, top - a.window + 1 - base));
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int b = 0; b < 2; ++b)
                     if (c_hi <= 32 * b || c_lo >= 32 * b + 32) bk[b] = 1.f, es[b] = 0.f, is[b] = 0.f;
             }
             auto hide = [&](uint32_t (&s)[32], int b) {
@@ -582,32 +587,33 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                     if (32 * b + k < c_lo || 32 * b + k >= c_hi) s[k] = 0xff800000u;
             };
             // The maximum; the scores are read again for the weights, which
-            // keeps 32 of a row's 128 in registers instead of all.
+            // keeps 32 of the 64 in registers at a time.
             float mn = m;
-            uint32_t s[2][32];
-            tmem_ld32(ts, s[0]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
+                uint32_t s[32];
+                tmem_ld32(ts + 32 * b, s);
                 tmem_ld_wait();
-                if (b < 3) tmem_ld32(ts + 32 * (b + 1), s[(b + 1) & 1]);
-                uint32_t (&sb)[32] = s[b & 1];
-                if (edge) hide(sb, b);
+                if (edge) hide(s, b);
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    v[e] = fmaxf(__uint_as_float(sb[e]), __uint_as_float(sb[4 + e]));
+                    v[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[4 + e]));
 #pragma unroll
                     for (int k = 8; k < 32; k += 8)
-                        v[e] = fmaxf(fmaxf(v[e], __uint_as_float(sb[k + e])), __uint_as_float(sb[k + 4 + e]));
+                        v[e] = fmaxf(fmaxf(v[e], __uint_as_float(s[k + e])), __uint_as_float(s[k + 4 + e]));
                 }
                 mn = fmaxf(mn, fmaf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), bk[b], es[b]));
             }
-            tmem_ld32(ts, s[0]);
+            // Both halves of a row go by one maximum.  (A wait that failed does
+            // not leave the loop: both warps meet at every barrier.)
+            s_row[x][half][i] = mn;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + (warp & 3)) : "memory");
+            mn = fmaxf(mn, s_row[x][half ^ 1][i]);
             if (NS == 2 && j > 0 && j % kFlush == 0) {
-                ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1));
-                if (!ok) break;
+                ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1)) && ok;
                 tc_fence_after();
-                flush<DP>(to, sums, pend, j > kFlush);
+                flush<DP / 2>(to, sums, pend, j > kFlush);
                 pend = 1.f;
             }
             if (__any_sync(0xffffffffu, mn > m + kLazy)) {
@@ -616,11 +622,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                 l *= alpha;
                 pend *= alpha;
                 if (NS == 2 ? j % kFlush != 0 : j > 0) {
-                    ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1));
-                    if (!ok) break;
+                    ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1)) && ok;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int d = 0; d < DP; d += 16) {
+                    for (int d = 0; d < DP / 2; d += 16) {
                         uint32_t o[16];
                         tmem_ld16(to + d, o);
                         tmem_ld_wait();
@@ -633,30 +638,30 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             }
             const float mu = (m == -INFINITY ? 0.f : m) - kTileShift;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
+                uint32_t s[32];
+                tmem_ld32(ts + 32 * b, s);
                 tmem_ld_wait();
-                if (b < 3) tmem_ld32(ts + 32 * (b + 1), s[(b + 1) & 1]);
-                uint32_t (&sb)[32] = s[b & 1];
-                if (edge) hide(sb, b);
+                if (edge) hide(s, b);
                 const uint64_t k2 = f2(bk[b], bk[b]), off = f2(es[b] - mu, es[b] - mu);
                 uint64_t sum[2] = {0, 0};
                 uint32_t ph[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     float u, v;
-                    f2_split(f2_fma(f2(__uint_as_float(sb[2 * k]), __uint_as_float(sb[2 * k + 1])), k2, off), u, v);
+                    f2_split(f2_fma(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), k2, off), u, v);
                     u = exp2_fast(u);
                     v = exp2_fast(v);
                     sum[k & 1] = f2_add(sum[k & 1], f2(u, v));
                     ph[k] = pack_h2(u, v);
-                    if constexpr (NS == 2) sb[2 * k] = __float_as_uint(u), sb[2 * k + 1] = __float_as_uint(v);
+                    if constexpr (NS == 2) s[2 * k] = __float_as_uint(u), s[2 * k + 1] = __float_as_uint(v);
                 }
                 tmem_st16(ts + 32 * b, ph);
                 if constexpr (NS == 2) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float2 h = unpack_h2(ph[k]);
-                        ph[k] = pack_h2(__uint_as_float(sb[2 * k]) - h.x, __uint_as_float(sb[2 * k + 1]) - h.y);
+                        ph[k] = pack_h2(__uint_as_float(s[2 * k]) - h.x, __uint_as_float(s[2 * k + 1]) - h.y);
                     }
                     tmem_st16(ts + 32 * b + 16, ph);
                 }
@@ -669,40 +674,45 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&pready[x]);
         }
-        if (ok && nx > 0) ok = __all_sync(0xffffffffu, wait(&pvdone[x], (nx - 1) & 1));
+        if (nx > 0) ok = __all_sync(0xffffffffu, wait(&pvdone[x], (nx - 1) & 1)) && ok;
+        // A row's sum is its halves'.
+        s_row[x][half][i] = l;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + (warp & 3)) : "memory");
+        l = s_row[x][0][i] + s_row[x][1][i];
         if (ok) {
             tc_fence_after();
             const int h = head * a.group + ht * p.hpt + hi, D = a.c.head_dim;
             const bool none = m == -INFINITY;
-            if (NS == 2 && nx > kFlush) flush<DP>(to, sums, pend, true, true);
+            if (NS == 2 && nx > kFlush) flush<DP / 2>(to, sums, pend, true, true);
             float inv = 0.f;
             const int64_t prow = ((int64_t)tok * a.n_heads + h) * a.splits + part;
             if (a.splits > 1) {
                 // in the join's convention: weights 2^(x - M + kWShift)
-                if (row_ok) a.part_ml[prow] = make_float2(none ? m : m + (kWShift - kTileShift), l);
+                if (row_ok && half == 0) a.part_ml[prow] = make_float2(none ? m : m + (kWShift - kTileShift), l);
                 inv = 1.f;
             } else if (!none) {
                 if (a.sinks && row_ok) l += exp2_fast(fmaf(a.sinks[h], kLog2e, kTileShift - m));
                 inv = 1.f / l;
             }
 #pragma unroll 1
-            for (int d = 0; d < DP; d += 32) {
+            for (int c = 0; c < DP / 2; c += 32) {
                 uint32_t o[32];
                 if (nx > 0) {
-                    tmem_ld32(to + d, o);
+                    tmem_ld32(to + c, o);
                     tmem_ld_wait();
                 }
                 if (row_ok) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
-                        if (d + k >= D) break;
+                        const int d = DP / 2 * half + c + k;
+                        if (d >= D) break;
                         float v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e] = none ? 0.f : __uint_as_float(o[k + e]) * inv;
                         if (a.splits > 1) {
-                            if (!none) *reinterpret_cast<float4 *>(a.part_o + prow * D + d + k) = make_float4(v[0], v[1], v[2], v[3]);
+                            if (!none) *reinterpret_cast<float4 *>(a.part_o + prow * D + d) = make_float4(v[0], v[1], v[2], v[3]);
                         } else {
-                            store4<T>(static_cast<T *>(a.out) + (int64_t)tok * a.o_lt + (int64_t)h * a.o_lh + d + k, a.o_vec, v);
+                            store4<T>(static_cast<T *>(a.out) + (int64_t)tok * a.o_lt + (int64_t)h * a.o_lh + d, a.o_vec, v);
                         }
                     }
                 }
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kSoftWarps) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -786,7 +796,7 @@ template <typename T, int DP>
 rf_status launch_tiles(const TileParams &t, cudaStream_t s, bool chain)
 {
     constexpr int NS = sizeof(T) == 4 ? 2 : 1;
-    static_assert(tile_smem<DP, NS>() + 64 <= 232448, "tiles exceed the 227 KB of shared memory");
+    static_assert(tile_smem<DP, NS>() + 4 * 4 * kTile + 64 <= 232448, "tiles exceed the 227 KB of shared memory");
     static std::once_flag once[64];
     static bool okd[64];
     int dev = 0;
