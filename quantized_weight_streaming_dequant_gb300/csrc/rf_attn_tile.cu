@@ -13,7 +13,7 @@
 //   tiles  a CTA owns two tiles of 128 query rows (tokens x heads of one K/V
 //          head) and walks the visible positions, 128 at a time:
 //              S = Q K^T (tcgen05.mma from shared memory, fp32 in tensor
-//              memory) -> weights by two threads per row, 64 columns each -> P in
+//              memory) -> weights by one thread per row (no shuffles) -> P in
 //              fp16 over S's own columns -> O += P V (P from tensor memory).
 //          One thread issues the products of the two tiles alternately, so
 //          that one tile's exponentials run under the other's products; O
@@ -28,6 +28,7 @@
 // products already issued are waited for, and tensor memory is freed.
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <mutex>
 
 #include "rf_attn.h"
@@ -39,8 +40,12 @@ namespace {
 __device__ int g_tile_status = 0;
 
 constexpr int kTile = 128;          // query rows, and positions, per tile
-constexpr int kSoftWarps = 16;      // eight per tile: two threads per row
-constexpr int kMainThreads = 32 * (kSoftWarps + 2);   // ... and one warp each for products and copies
+constexpr int kSoftWarps = 8;       // four per tile: a thread per row
+constexpr int kMainThreads = 32 * (kSoftWarps + 4);   // ... and a warpgroup of which two warps issue products and copies
+// Registers: 168 a thread at launch; the last warpgroup gives up what the
+// softmax warpgroups take (2 * 232 + 40 = 3 * 168), so that a thread holds
+// its row's 128 scores.
+constexpr int kRegsSoftmax = 232, kRegsOther = 40;
 constexpr int kFlush = 16;          // position tiles that fp32 sums stay in tensor memory
 constexpr int kPadParts = 8;        // CTAs that zero the rows of no sequence
 constexpr float kTileShift = 8.f;   // weights are 2^(x - m + 8) <= 2^15
@@ -49,6 +54,15 @@ constexpr float kLazy = 7.f;        // growth of a maximum that is not yet appli
 // What the plan kernel leaves for the others.
 struct TilePlan {
     int32_t n_q, n_kv;              // query tiles, position tiles
+    int32_t next;                   // work items drawn
+    int32_t pad;
+};
+// Two query tiles of a sequence: tokens [tok, end) at most, the first at
+// position pos; position tiles [t_lo, t_hi[x]) of the kvn staged at kv0 are
+// seen by tile x, staged tile 0 starting at position 128 * kvf.
+struct __align__(16) QTile {
+    int32_t seq, tok, end, kv0, kvf, t_lo, t_hi[2];
+    int64_t pos, pad;
 };
 
 struct TileParams {
@@ -56,8 +70,8 @@ struct TileParams {
     int hpt, head_tiles, tqt;       // heads per tile, tiles per K/V head, tokens per 128-row tile
     int cap_q, cap_kv;              // capacities of the lists below
     TilePlan *plan;
-    int2 *q_tiles;                  // [cap_q]: sequence, first token
-    int32_t *kv_base;               // [n_seq + 1]: first position tile of a sequence
+    QTile *q_tiles;                 // [cap_q]
+    int32_t *kv_base;               // [n_seq]: first position tile of a sequence
     int32_t *kv_first;              // [n_seq]: its position / 128 (window)
     uint8_t *q_img;                 // [cap_q][kv head][head tile][2][NS][128 x DP] fp16
     float *q_unit;                  // [cap_q][kv head][head tile][2][128]
@@ -72,28 +86,28 @@ struct TileParams {
 
 // ---------------------------------------------------------------------- plan
 // Exclusive prefix sum over the CTA's 1024 threads.
-__device__ __forceinline__ int scan1024(int v, int *part, int *total)
+__device__ __forceinline__ int64_t scan1024(int64_t v, int64_t *part, int64_t *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    int64_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) part[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int y = part[lane];
+        int64_t y = part[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
             if (lane >= o) y += z;
         }
         part[lane] = y;
     }
     __syncthreads();
-    const int base = warp ? part[warp - 1] : 0;
+    const int64_t base = warp ? part[warp - 1] : 0;
     *total = part[31];
     __syncthreads();
     return base + x - v;
@@ -101,48 +115,74 @@ __device__ __forceinline__ int scan1024(int v, int *part, int *total)
 
 __global__ void __launch_bounds__(1024) tile_plan_kernel(const __grid_constant__ TileParams p)
 {
-    __shared__ int part[32];
+    __shared__ int64_t part[32];
+    __shared__ int64_t s_at[1024], s_past[1024];    // of each sequence of a round: first query tile, ...
+    __shared__ int s_t0[1024], s_nq[1024], s_kv0[1024], s_kvn[1024], s_kvf[1024];
     pdl_launch_dependents();
     pdl_wait();
     const rf_kv_batch &b = p.a.b;
-    int kv_at = 0, q_at = 0;
+    const int ctt = 2 * p.tqt, tid = (int)threadIdx.x;
+    int64_t kv_at = 0, q_at = 0;
     for (int s0 = 0; s0 < b.n_seq; s0 += 1024) {
-        const int s = s0 + (int)threadIdx.x;
-        int nt = 0, first = 0, nq = 0, t0 = 0;
+        const int s = s0 + tid;
+        int64_t nt = 0, first = 0, past = 0;
+        int nq = 0, t0 = 0;
         if (s < b.n_seq) {
             t0 = max(b.q_start[s], 0);
             nq = max(0, min(b.q_start[s + 1], b.n_tok) - t0);
-            const int64_t past = b.past[s], last = past + nq - 1;
+            past = (int64_t)b.past[s] + (t0 - b.q_start[s]);
+            const int64_t last = past + nq - 1;
             if (nq > 0 && last >= 0) {
-                int64_t lo = 0;
-                if (p.a.window > 0) lo = max((int64_t)0, past - p.a.window + 1);
-                first = (int)(lo / kTile);
-                nt = (int)(min(last / kTile + 1, (int64_t)b.table_width * p.a.c.page_size / kTile + 1)) - first;
-                nt = max(nt, 0);
+                const int64_t lo = p.a.window > 0 ? max((int64_t)0, past - p.a.window + 1) : 0;
+                first = lo / kTile;
+                nt = max((int64_t)0, min(last / kTile + 1, (int64_t)b.table_width * p.a.c.page_size / kTile + 1) - first);
             }
             if (past < 0 && nq > 0) record_status(&g_tile_status, RF_ERR_INVALID_ARG);
         }
-        int total;
-        int at = kv_at + scan1024(nt, part, &total);
+        int64_t total_kv, total_q;
+        const int64_t kv0 = kv_at + scan1024(nt, part, &total_kv);
+        const int64_t at = q_at + scan1024((nq + ctt - 1) / ctt, part, &total_q);
+        // past the capacity (a sequence longer than max_len): not staged
+        const int64_t kvn = max((int64_t)0, min(nt, (int64_t)p.cap_kv - kv0));
+        if (kvn < nt) record_status(&g_tile_status, RF_ERR_INVALID_ARG);
         if (s < b.n_seq) {
-            // past the capacity (a sequence longer than max_len): nothing of it is seen
-            if (nt > 0 && at + nt > p.cap_kv) record_status(&g_tile_status, RF_ERR_INVALID_ARG);
-            p.kv_base[s] = min(at, p.cap_kv);
-            p.kv_first[s] = first;
+            p.kv_base[s] = (int)min(kv0, (int64_t)p.cap_kv);
+            p.kv_first[s] = (int)first;
         }
-        kv_at = min(kv_at + total, 1 << 30);
-        const int tiles = (nq + 2 * p.tqt - 1) / (2 * p.tqt);
-        at = q_at + scan1024(tiles, part, &total);
-        q_at = min(q_at + total, 1 << 30);
-        // later positions first: they see more
-        for (int i = 0; i < tiles; ++i)
-            if (at + i < p.cap_q) p.q_tiles[at + i] = make_int2(s, t0 + (tiles - 1 - i) * 2 * p.tqt);
+        s_at[tid] = at, s_past[tid] = past, s_t0[tid] = t0, s_nq[tid] = nq;
+        s_kv0[tid] = (int)min(kv0, (int64_t)p.cap_kv), s_kvn[tid] = (int)kvn, s_kvf[tid] = (int)first;
+        __syncthreads();
+        // The round's query tiles; later positions first: they see more.
+        for (int64_t i = q_at + tid; i < min(q_at + total_q, (int64_t)p.cap_q); i += 1024) {
+            int lo = 0, hi = 1024;                   // the last sequence that starts at i or before
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_at[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            const int tiles = (s_nq[lo] + ctt - 1) / ctt, off = (tiles - 1 - (int)(i - s_at[lo])) * ctt;
+            QTile q;
+            q.seq = s0 + lo;
+            q.tok = s_t0[lo] + off;
+            q.end = s_t0[lo] + s_nq[lo];
+            q.kv0 = s_kv0[lo];
+            q.kvf = s_kvf[lo];
+            q.pos = s_past[lo] + off;
+            q.pad = 0;
+            q.t_lo = p.a.window > 0 ? max(0, (int)(max((int64_t)0, q.pos - p.a.window + 1) / kTile) - q.kvf) : 0;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int toks = min(p.tqt, q.end - (q.tok + x * p.tqt));
+                const int64_t last = q.pos + x * p.tqt + toks - 1;
+                q.t_hi[x] = toks > 0 && last >= 0 ? (int)min((int64_t)s_kvn[lo], last / kTile + 1 - q.kvf) : 0;
+            }
+            p.q_tiles[i] = q;
+        }
+        __syncthreads();
+        kv_at += total_kv;
+        q_at += total_q;
     }
-    if (threadIdx.x == 0) {
-        p.kv_base[b.n_seq] = min(kv_at, p.cap_kv);
-        p.plan->n_q = min(q_at, p.cap_q);
-        p.plan->n_kv = min(kv_at, p.cap_kv);
-    }
+    if (tid == 0) *p.plan = TilePlan{(int)min(q_at, (int64_t)p.cap_q), (int)min(kv_at, (int64_t)p.cap_kv), 0, 0};
 }
 
 // --------------------------------------------------------------------- stage
@@ -228,8 +268,8 @@ __device__ __forceinline__ void stage_q(const TileParams &p, int qt, int head, i
 {
     constexpr int NS = sizeof(T) == 4 ? 2 : 1, LPR = DP / 8, RPW = 32 / LPR;
     const AttnParams &a = p.a;
-    const int2 q = p.q_tiles[qt];
-    const int end = min(a.b.q_start[q.x + 1], a.b.n_tok), D = a.c.head_dim;
+    const QTile q = p.q_tiles[qt];
+    const int end = q.end, D = a.c.head_dim;
     const int h0 = head * a.group + ht * p.hpt, nh = min(p.hpt, a.group - ht * p.hpt);
     const int64_t at = ((int64_t)qt * a.c.n_kv_heads + head) * p.head_tiles + ht;
     uint8_t *img = p.q_img + at * (2 * NS * kTile * DP * 2);
@@ -237,7 +277,7 @@ __device__ __forceinline__ void stage_q(const TileParams &p, int qt, int head, i
     const int lane = threadIdx.x & 31, k = lane % LPR;
     for (int r = (int)(threadIdx.x >> 5) * RPW + lane / LPR; r < 2 * kTile; r += 8 * RPW) {
         const int x = r / kTile, n = r % kTile, ti = n / p.hpt, hi = n % p.hpt;
-        const int tok = q.y + x * p.tqt + ti;
+        const int tok = q.tok + x * p.tqt + ti;
         const bool ok = ti < p.tqt && hi < nh && tok < end;
         float f[8] = {};
         if (ok && 8 * k < D) {
@@ -316,7 +356,7 @@ __global__ void __launch_bounds__(256) tile_stage_kernel(const __grid_constant__
 template <int DP, int NS> __host__ __device__ constexpr int ring_slots() { return (DP == 128 ? 7 : 14) - (DP == 128 ? 2 : 4) * NS; }
 template <int DP, int NS> __host__ __device__ constexpr size_t tile_smem()
 {
-    return (size_t)kTile * DP * 2 * (2 * NS + ring_slots<DP, NS>()) + 256;
+    return (size_t)kTile * DP * 2 * (2 * NS + ring_slots<DP, NS>());
 }
 
 __host__ __device__ constexpr uint32_t tile_idesc(int n)
@@ -376,73 +416,59 @@ __device__ __forceinline__ void flush(uint32_t to, float4 *sums, float pend, boo
     if (back) tmem_st_wait();
 }
 
+// One work item: two query tiles of one head tile against one part of their
+// positions.
+struct Item {
+    int64_t q_at;                   // index of the query images
+    int64_t pos;                    // position of tile 0's first token
+    int64_t base;                   // first position of the first tile walked
+    int32_t n[2];                   // position tiles walked by each query tile
+    int32_t kv;                     // index of the first staged one
+    int32_t tok, end, head, ht, part;
+    int32_t index;                  // of the item
+    int32_t stop;
+};
+
+// A persistent CTA: the copy warp draws items (heaviest first) and runs ahead
+// into the next one, whose first products start under the last one's output.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams p)
 {
     constexpr int NS = sizeof(T) == 4 ? 2 : 1;
     constexpr int R = ring_slots<DP, NS>();
     constexpr int SLOT = kTile * DP * 2;
+    constexpr int kItems = 4;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *q_s = smem;                          // [2][NS][SLOT]
     uint8_t *ring = smem + 2 * NS * SLOT;         // [R][SLOT]: K0 V0 K1 V1 ...
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + R * SLOT);
-    uint64_t *full = bars, *empty = bars + R;
-    uint64_t *qfull = bars + 2 * R, *sfull = qfull + 1, *pready = sfull + 2, *pvdone = pready + 2, *drained = pvdone + 2;
+    __shared__ uint64_t full[R], empty[R], qfull[1], qempty[1], sfull[2], pready[2], pvdone[2], drained[1];
+    __shared__ uint64_t ifull[kItems], iempty[kItems];
+    __shared__ Item items[kItems];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
-    // [tile][half][row]: a half row's maximum.  One buffer is enough: a step's
-    // scores are issued only after every warp has handed over the last step.
-    __shared__ float s_row[2][2][kTile];
     volatile int *stop = &s_stop;
-    static_assert((2 * R + 8) * 8 <= 256, "barriers outgrow their room");
 
     const AttnParams &a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int u = (int)blockIdx.x;
-    const int part = u % a.splits;
-    u /= a.splits;
-    const int ht = u % p.head_tiles;
-    u /= p.head_tiles;
-    const int head = u % a.c.n_kv_heads, qt = u / a.c.n_kv_heads;
-    pdl_launch_dependents();
-    pdl_wait();
-    if (qt >= p.plan->n_q) return;
-    const int2 q = p.q_tiles[qt];
-    const int seq = q.x, first = a.b.q_start[seq], end = min(a.b.q_start[seq + 1], a.b.n_tok);
-    const int64_t pos0 = (int64_t)a.b.past[seq] + (q.y - first);   // position of tile 0's first token
-    // Position tiles, counted from the sequence's first staged one: the first
-    // that tile 0 sees up to the last that each tile sees.
-    const int kv0 = p.kv_base[seq], kvn = p.kv_base[seq + 1] - kv0, kvf = p.kv_first[seq];
-    const bool fits = kv0 + kvn <= p.cap_kv;
-    int t_lo = 0, t_hi[2];
-    if (a.window > 0) t_lo = max(0, (int)(max((int64_t)0, pos0 - a.window + 1) / kTile) - kvf);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int toks = min(p.tqt, end - (q.y + x * p.tqt));
-        const int64_t last = pos0 + x * p.tqt + toks - 1;
-        t_hi[x] = toks > 0 && last >= 0 && fits ? min(kvn, (int)(last / kTile) + 1 - kvf) : 0;
-    }
-    const int from = t_lo + part * p.split_tiles;
-    int n[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        n[x] = max(0, min(t_hi[x], from + p.split_tiles) - from);
-    }
-    const int nmax = max(n[0], n[1]);
-    const int64_t at = ((int64_t)qt * a.c.n_kv_heads + head) * p.head_tiles + ht;
-
+    // A value taken from one lane is known to be the same in all, so that the
+    // products' operands live in uniform registers.
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < R; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sfull[x], 1);
-            mbar_init(&pready[x], 8);
+            mbar_init(&pready[x], 4);
             mbar_init(&pvdone[x], 1);
         }
         mbar_init(drained, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&ifull[i], 1);
+            mbar_init(&iempty[i], kSoftWarps + 1);
+        }
         s_stop = 0;
         fence_barrier_init();
     }
@@ -453,7 +479,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
         if (*stop) return false;
@@ -461,241 +487,356 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
         *stop = 1;
         return false;
     };
+    pdl_launch_dependents();
+    pdl_wait();
 
+    // (Registers are traded in each branch for good: the roles do not join
+    // again before the end.)
+    if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kSoftWarps + 1) {
-        // Copies: both query tiles, then K and V of each position tile.
-        if (lane == 0 && nmax > 0) {
-            mbar_arrive_expect_tx(qfull, 2 * NS * SLOT);
-            const uint8_t *src = p.q_img + at * (2 * NS * SLOT);
+        // Items and copies: both query tiles, then K and V of each position
+        // tile.
+        if (lane == 0) {
+            const int total = p.plan->n_q * a.c.n_kv_heads * p.head_tiles * a.splits;
+            uint32_t iq = 0, ikv = 0;              // items with copies, ring slots used
+            bool ok = true;
+            for (uint32_t it = 0; ok; ++it) {
+                const int slot = it % kItems;
+                if (!wait(&iempty[slot], ((it / kItems) & 1) ^ 1)) break;
+                Item &w = items[slot];
+                const int index = atomicAdd(&p.plan->next, 1);
+                w.stop = index >= total;
+                if (w.stop) {
+                    mbar_arrive(&ifull[slot]);
+                    break;
+                }
+                int u = index;
+                w.index = index;
+                w.part = u % a.splits;
+                u /= a.splits;
+                w.ht = u % p.head_tiles;
+                u /= p.head_tiles;
+                w.head = u % a.c.n_kv_heads;
+                const int qt = u / a.c.n_kv_heads;
+                const QTile q = p.q_tiles[qt];
+                w.q_at = ((int64_t)qt * a.c.n_kv_heads + w.head) * p.head_tiles + w.ht;
+                w.pos = q.pos, w.tok = q.tok, w.end = q.end;
+                const int from = q.t_lo + w.part * p.split_tiles;
+                int n[2];
 #pragma unroll
-            for (int i = 0; i < 2 * NS; ++i) bulk_g2s(q_s + i * SLOT, src + i * SLOT, SLOT, qfull);
-            const int64_t img = ((int64_t)head * p.cap_kv + kv0 + from) * SLOT;
-            int issued = 0;
-            for (int i = 0; i < 2 * nmax; ++i) {
-                const int s = i % R;
-                if (!wait(&empty[s], ((i / R) & 1) ^ 1)) break;
-                mbar_arrive_expect_tx(&full[s], SLOT);
-                bulk_g2s(ring + s * SLOT, (i & 1 ? p.v_img : p.k_img) + img + (int64_t)(i >> 1) * SLOT, SLOT, &full[s]);
-                issued = i + 1;
+                for (int x = 0; x < 2; ++x) w.n[x] = n[x] = max(0, min(q.t_hi[x], from + p.split_tiles) - from);
+                w.kv = q.kv0 + from;
+                w.base = (int64_t)(q.kvf + from) * kTile;
+                const int64_t q_at = w.q_at, img = ((int64_t)w.head * p.cap_kv + w.kv) * SLOT;
+                mbar_arrive(&ifull[slot]);
+                const int nmax = max(n[0], n[1]);
+                if (nmax == 0) continue;
+                if (!wait(qempty, (iq & 1) ^ 1)) break;
+                ++iq;
+                mbar_arrive_expect_tx(qfull, 2 * NS * SLOT);
+                const uint8_t *src = p.q_img + q_at * (2 * NS * SLOT);
+#pragma unroll
+                for (int i = 0; i < 2 * NS; ++i) bulk_g2s(q_s + i * SLOT, src + i * SLOT, SLOT, qfull);
+                for (int i = 0; i < 2 * nmax; ++i) {
+                    const int s = ikv % R;
+                    if (!(ok = wait(&empty[s], ((ikv / R) & 1) ^ 1))) break;
+                    mbar_arrive_expect_tx(&full[s], SLOT);
+                    bulk_g2s(ring + s * SLOT, (i & 1 ? p.v_img : p.k_img) + img + (int64_t)(i >> 1) * SLOT, SLOT, &full[s]);
+                    ++ikv;
+                }
             }
-            mbar_drain(qfull, 0);
-            for (int i = max(0, issued - R); i < issued; ++i) mbar_drain(&full[i % R], (i / R) & 1);
+            // Every copy issued lands before the CTA can exit.
+            if (iq > 0) mbar_drain(qfull, (iq - 1) & 1);
+            for (uint32_t i = ikv > R ? ikv - R : 0; i < ikv; ++i) mbar_drain(&full[i % R], (i / R) & 1);
         }
         __syncwarp();
     } else if (warp == kSoftWarps) {
         // Products.  Tile x: S at columns 128 x, P over it (the weights of
         // block b in S's columns 32 b: 16 columns of fp16 pairs a term), O at
-        // 256 + DP x.
-        if (lane == 0 && nmax > 0) {
-            const uint64_t qd = smem_desc(smem_addr(q_s), 16 * DP), kd = smem_desc(smem_addr(ring), 16 * DP);
-            const uint64_t vd = smem_desc(smem_addr(ring), 2048);
-            bool ok = wait(qfull, 0), any = false;
-            auto scores = [&](int x, int slot) {
-                tc_fence_after();
-#pragma unroll
+        // 256 + DP x.  All in one thread's order, which is what lets a tile's
+        // next scores follow its values over the same columns.  The warp runs
+        // as one; `leader` is the thread that issues.
+        const uint64_t qd = smem_desc(smem_addr(q_s), 16 * DP), kd = smem_desc(smem_addr(ring), 16 * DP);
+        const uint64_t vd = smem_desc(smem_addr(ring), 2048);
+        const bool leader = elect_one();
+        bool ok = true, any = false;
+        uint32_t iq = 0, steps[2] = {0, 0};
+        int ks = 0;                                // ring slot of the next K tile, and its phase
+        uint32_t kph = 0;
+        auto waits = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+        auto commit = [&](uint64_t *bar) {
+            if (leader) tc_commit(bar);
+        };
+        auto scores = [&](int x, int slot) {
+            tc_fence_after();
+            const uint64_t q0 = qd + (uint64_t)((x * NS * SLOT) >> 4), k0 = kd + (uint64_t)((slot * SLOT) >> 4);
+            if (leader) {
+#pragma unroll 1
                 for (int t = NS - 1; t >= 0; --t)
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k)
-                        tc_mma(tmem + 128 * x, qd + (uint64_t)(((x * NS + t) * SLOT + k * 256) >> 4),
-                               kd + (uint64_t)((slot * SLOT + k * 256) >> 4), tile_idesc(kTile), !(t == NS - 1 && k == 0));
+                        tc_mma(tmem + 128 * x, q0 + ((t * SLOT + k * 256) >> 4), k0 + 16 * k, tile_idesc(kTile),
+                               !(t == NS - 1 && k == 0));
                 tc_commit(&sfull[x]);
-            };
-            auto values = [&](int x, int slot, bool add) {
-                tc_fence_after();
-#pragma unroll
+            }
+        };
+        auto values = [&](int x, int slot, bool add) {
+            tc_fence_after();
+            const uint64_t v0 = vd + (uint64_t)((slot * SLOT) >> 4);
+            if (leader) {
+#pragma unroll 1
                 for (int t = NS - 1; t >= 0; --t)
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 32 * (k >> 1) + 16 * t + 8 * (k & 1),
-                                  vd + (uint64_t)((slot * SLOT + k * 256) >> 4), tile_idesc(DP),
-                                  add || !(t == NS - 1 && k == 0));
+                        tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 32 * (k >> 1) + 16 * t + 8 * (k & 1), v0 + 16 * k,
+                                  tile_idesc(DP), add || !(t == NS - 1 && k == 0));
                 tc_commit(&pvdone[x]);
-            };
-            if (ok && (ok = wait(&full[0], 0))) {
-                any = true;
-                for (int x = 0; x < 2; ++x)
-                    if (n[x] > 0) scores(x, 0);
-                tc_commit(&empty[0]);
             }
+        };
+        for (uint32_t it = 0; ok; ++it) {
+            const int slot = it % kItems;
+            if (!waits(&ifull[slot], (it / kItems) & 1)) break;
+            const int n0 = __shfl_sync(0xffffffffu, items[slot].n[0], 0), n1 = __shfl_sync(0xffffffffu, items[slot].n[1], 0);
+            const int end = __shfl_sync(0xffffffffu, items[slot].stop, 0);
+            __syncwarp();
+            if (leader) mbar_arrive(&iempty[slot]);
+            if (end) break;
+            const int nmax = max(n0, n1);
+            if (nmax == 0) continue;
+            if (!waits(qfull, iq & 1)) break;
+            ++iq;
+            if (!waits(&full[ks], kph)) break;
+            any = true;
+            if (n0 > 0) scores(0, ks);
+            if (n1 > 0) scores(1, ks);
+            commit(&empty[ks]);
+            if (nmax == 1) commit(qempty);
             for (int j = 0; ok && j < nmax; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;
+                const int vs = ks + 1 == R ? 0 : ks + 1, ns = vs + 1 == R ? 0 : vs + 1;
+                const uint32_t vph = vs ? kph : kph ^ 1u, nph = ns ? vph : vph ^ 1u;
                 const bool more = j + 1 < nmax;
-                if (!(ok = wait(&full[iv % R], (iv / R) & 1))) break;
-                if (more && !(ok = wait(&full[ik % R], (ik / R) & 1))) break;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (j < n[x]) {
-                        if (!(ok = wait(&pready[x], j & 1))) break;
-                        values(x, iv % R, NS == 2 ? j % kFlush != 0 : j > 0);
-                    }
-                    if (x == 1) tc_commit(&empty[iv % R]);
-                    if (j + 1 < n[x]) scores(x, ik % R);
+                if (!(ok = waits(&full[vs], vph))) break;
+                if (more && !(ok = waits(&full[ns], nph))) break;
+                const bool add = NS == 2 ? j % kFlush != 0 : j > 0;
+                if (j < n0) {
+                    if (!(ok = waits(&pready[0], steps[0] & 1))) break;
+                    ++steps[0];
+                    values(0, vs, add);
+                    if (j + 1 < n0) scores(0, ns);
                 }
-                if (ok && more) tc_commit(&empty[ik % R]);
+                if (j < n1) {
+                    if (!(ok = waits(&pready[1], steps[1] & 1))) break;
+                    ++steps[1];
+                    values(1, vs, add);
+                }
+                commit(&empty[vs]);
+                if (j + 1 < n1) scores(1, ns);
+                if (more) {
+                    commit(&empty[ns]);
+                    if (j + 2 == nmax) commit(qempty);
+                }
+                ks = ns;
+                kph = nph;
             }
-            // Every issued product completes before tensor memory is freed.
-            if (any) {
-                tc_commit(drained);
-                mbar_drain(drained, 0);
-            }
+        }
+        // Every issued product completes before tensor memory is freed.
+        if (any) {
+            commit(drained);
+            mbar_drain(drained, 0);
         }
         __syncwarp();
+    }
     } else {
-        // Softmax: row i of tile x (tensor-memory lane i) belongs to two
-        // threads, one per half of the columns and of O.
-        const int x = warp >> 3, half = (warp >> 2) & 1, i = (warp & 3) * 32 + lane;
-        const int ti = i / p.hpt, hi = i % p.hpt, nx = n[x];
-        const int tok = q.y + x * p.tqt + ti;
-        const bool row_ok = ti < p.tqt && hi < min(p.hpt, a.group - ht * p.hpt) && tok < end;
-        const int64_t top = row_ok ? pos0 + x * p.tqt + ti : -1;
-        const float bq = p.q_unit[at * (2 * kTile) + x * kTile + i];
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // Softmax: thread i of group x owns row i of tile x (tensor-memory
+        // lane i).
+        const int x = warp >> 2, i = (warp & 3) * 32 + lane;
+        const int ti = i / p.hpt, hi = i % p.hpt;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + 128 * x + 64 * half, to = tmem + lanes + 256 + DP * x + DP / 2 * half;
-        float m = -INFINITY, l = 0.f;
-        // [position tile][2^ek, ev, 2^-ev][block]; this half's two blocks
-        const float2 *units = reinterpret_cast<const float2 *>(p.units + ((int64_t)head * p.cap_kv + kv0 + from) * 12) + half;
-        // fp32: the tensor core truncates its sums, which drifts by about
-        // 1e-8 per step; so O is added to sums in memory every kFlush tiles.
-        // pend: growth of m since the last time.
-        float4 *sums = p.sums + (((int64_t)blockIdx.x * 2 + x) * (DP / 4) + DP / 8 * half) * kTile + i;
-        float pend = 1.f;
+        const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + DP * x;
+        uint32_t step = 0;                         // steps of this tile
         bool ok = true;
-        int64_t base = (int64_t)(kvf + from) * kTile + 64 * half;
-        float2 ku, ev, iv;
-        if (nx > 0) ku = units[0], ev = units[2], iv = units[4];
-        for (int j = 0; j < nx; ++j, base += kTile) {
-            float bk[2] = {bq * ku.x, bq * ku.y}, es[2] = {ev.x, ev.y}, is[2] = {iv.x, iv.y};
-            if (j + 1 < nx) ku = units[6 * j + 6], ev = units[6 * j + 8], iv = units[6 * j + 10];
+        for (uint32_t it = 0; ok; ++it) {
+            const int slot = it % kItems;
+            ok = __all_sync(0xffffffffu, wait(&ifull[slot], (it / kItems) & 1));
+            if (!ok) break;
+            const Item &w = items[slot];           // given back after the output
+            if (w.stop) break;
+            const int nx = w.n[x];
+            const bool row_ok = ti < p.tqt && hi < min(p.hpt, a.group - w.ht * p.hpt) && w.tok + x * p.tqt + ti < w.end;
+            // The visible positions [first, top] of the row, counted from the
+            // first tile's first.
+            const int top = row_ok ? (int)(w.pos - w.base) + x * p.tqt + ti : INT_MIN / 2;
+            const int first = a.window > 0 ? (int)max((int64_t)top - a.window + 1, (int64_t)INT_MIN / 2) : INT_MIN / 2;
+            const float bq = p.q_unit[w.q_at * (2 * kTile) + x * kTile + i];
+            float m = -INFINITY, l = 0.f;
+            // [position tile][2^ek, ev, 2^-ev][block]
+            const float4 *units = reinterpret_cast<const float4 *>(p.units + ((int64_t)w.head * p.cap_kv + w.kv) * 12);
+            // fp32: the tensor core truncates its sums, which drifts by about
+            // 1e-8 per step; so O is added to sums in memory every kFlush
+            // tiles.  pend: growth of m since the last time.
+            auto sums = [&] { return p.sums + ((int64_t)w.index * 2 + x) * (DP / 4) * kTile + i; };
+            float pend = 1.f;
+            float4 ku, ev, iv;
+            if (nx > 0) ku = units[0], ev = units[1], iv = units[2];
+            for (int j = 0; j < nx; ++j, ++step) {
+                float bk[4] = {bq * ku.x, bq * ku.y, bq * ku.z, bq * ku.w};
+                float es[4] = {ev.x, ev.y, ev.z, ev.w}, is[4] = {iv.x, iv.y, iv.z, iv.w};
+                units += 3;
+                if (j + 1 < nx) ku = units[0], ev = units[1], iv = units[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) bk[b] = bk[b] == 0.f ? FLT_MIN : bk[b];   // -inf scores stay -inf
-            ok = __all_sync(0xffffffffu, wait(&sfull[x], j & 1)) && ok;
-            tc_fence_after();
-            // Visible columns [c_lo, c_hi); hidden scores become -inf, and the
-            // units of a block without a visible one do not count.
-            const bool edge = __any_sync(0xffffffffu, row_ok && (top < base + 63 || (a.window > 0 && top - a.window >= base)));
-            int c_lo = 0, c_hi = 64;
-            if (edge) {
-                c_hi = (int)min((int64_t)64, max((int64_t)0, top + 1 - base));
-                if (a.window > 0) c_lo = (int)min((int64_t)64, max((int64_t)0, top - a.window + 1 - base));
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (c_hi <= 32 * b || c_lo >= 32 * b + 32) bk[b] = 1.f, es[b] = 0.f, is[b] = 0.f;
-            }
-            auto hide = [&](uint32_t (&s)[32], int b) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (32 * b + k < c_lo || 32 * b + k >= c_hi) s[k] = 0xff800000u;
-            };
-            // The maximum; the scores are read again for the weights, which
-            // keeps 32 of the 64 in registers at a time.
-            float mn = m;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t s[32];
-                tmem_ld32(ts + 32 * b, s);
-                tmem_ld_wait();
-                if (edge) hide(s, b);
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[4 + e]));
-#pragma unroll
-                    for (int k = 8; k < 32; k += 8)
-                        v[e] = fmaxf(fmaxf(v[e], __uint_as_float(s[k + e])), __uint_as_float(s[k + 4 + e]));
-                }
-                mn = fmaxf(mn, fmaf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), bk[b], es[b]));
-            }
-            // Both halves of a row go by one maximum.  (A wait that failed does
-            // not leave the loop: both warps meet at every barrier.)
-            s_row[x][half][i] = mn;
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + (warp & 3)) : "memory");
-            mn = fmaxf(mn, s_row[x][half ^ 1][i]);
-            if (NS == 2 && j > 0 && j % kFlush == 0) {
-                ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1)) && ok;
+                for (int b = 0; b < 4; ++b) bk[b] = bk[b] == 0.f ? FLT_MIN : bk[b];   // -inf scores stay -inf
+                ok = __all_sync(0xffffffffu, wait(&sfull[x], step & 1));
+                if (!ok) break;
                 tc_fence_after();
-                flush<DP / 2>(to, sums, pend, j > kFlush);
-                pend = 1.f;
-            }
-            if (__any_sync(0xffffffffu, mn > m + kLazy)) {
-                const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
-                m = mn;
-                l *= alpha;
-                pend *= alpha;
-                if (NS == 2 ? j % kFlush != 0 : j > 0) {
-                    ok = __all_sync(0xffffffffu, wait(&pvdone[x], (j - 1) & 1)) && ok;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int d = 0; d < DP / 2; d += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(to + d, o);
+                // Hidden scores become -inf, and the units of a block without a
+                // visible one do not count.
+                const int at = kTile * j;
+                const bool edge = __any_sync(0xffffffffu, row_ok && (top < at + kTile - 1 || first > at));
+                uint32_t seen[4];
+                if (edge) {
+                    const int c_hi = top + 1 - at, c_lo = first - at;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int hi_b = min(32, max(0, c_hi - 32 * b)), lo_b = min(32, max(0, c_lo - 32 * b));
+                        seen[b] = (uint32_t)(((1ull << hi_b) - 1) & ~((1ull << lo_b) - 1));
+                        if (seen[b] == 0u) bk[b] = 1.f, es[b] = 0.f, is[b] = 0.f;
+                    }
+                }
+                auto hide = [&](uint32_t (&v)[32], uint32_t see) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(see >> k & 1u)) v[k] = 0xff800000u;
+                };
+                auto most = [&](const uint32_t (&t)[32]) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = fmaxf(__uint_as_float(t[e]), __uint_as_float(t[4 + e]));
+#pragma unroll
+                        for (int k = 8; k < 32; k += 8)
+                            v[e] = fmaxf(fmaxf(v[e], __uint_as_float(t[k + e])), __uint_as_float(t[k + 4 + e]));
+                    }
+                    return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                };
+                // 16-bit types hold the row's scores between the maximum and
+                // the weights; fp32's second terms leave no registers for
+                // that, so its scores are read twice.
+                constexpr bool kHold = NS == 1;
+                uint32_t s[kHold ? 4 : 2][32];
+                float mn = m;
+                if constexpr (kHold) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s[b]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (edge) hide(s[b], seen[b]);
+                        mn = fmaxf(mn, fmaf(most(s[b]), bk[b], es[b]));
+                    }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 4; b += 2) {
+                        tmem_ld32(ts + 32 * b, s[0]);
+                        tmem_ld32(ts + 32 * b + 32, s[1]);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tmem_st16(to + d, o);
+                        for (int c = 0; c < 2; ++c) {
+                            if (edge) hide(s[c], seen[b + c]);
+                            mn = fmaxf(mn, fmaf(most(s[c]), bk[b + c], es[b + c]));
+                        }
                     }
-                    tmem_st_wait();
                 }
-            }
-            const float mu = (m == -INFINITY ? 0.f : m) - kTileShift;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t s[32];
-                tmem_ld32(ts + 32 * b, s);
-                tmem_ld_wait();
-                if (edge) hide(s, b);
-                const uint64_t k2 = f2(bk[b], bk[b]), off = f2(es[b] - mu, es[b] - mu);
-                uint64_t sum[2] = {0, 0};
-                uint32_t ph[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    float u, v;
-                    f2_split(f2_fma(f2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), k2, off), u, v);
-                    u = exp2_fast(u);
-                    v = exp2_fast(v);
-                    sum[k & 1] = f2_add(sum[k & 1], f2(u, v));
-                    ph[k] = pack_h2(u, v);
-                    if constexpr (NS == 2) s[2 * k] = __float_as_uint(u), s[2 * k + 1] = __float_as_uint(v);
+                if (NS == 2 && j > 0 && j % kFlush == 0) {
+                    ok = __all_sync(0xffffffffu, wait(&pvdone[x], (step - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    flush<DP>(to, sums(), pend, j > kFlush);
+                    pend = 1.f;
                 }
-                tmem_st16(ts + 32 * b, ph);
-                if constexpr (NS == 2) {
+                if (__any_sync(0xffffffffu, mn > m + kLazy)) {
+                    const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
+                    m = mn;
+                    l *= alpha;
+                    pend *= alpha;
+                    if (NS == 2 ? j % kFlush != 0 : j > 0) {
+                        ok = __all_sync(0xffffffffu, wait(&pvdone[x], (step - 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < DP; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(to + d, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st16(to + d, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float mu = (m == -INFINITY ? 0.f : m) - kTileShift;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t (&t)[32] = s[kHold ? b : b & 1];
+                    if constexpr (!kHold) {
+                        if (b % 2 == 0) {
+                            tmem_ld32(ts + 32 * b, s[0]);
+                            tmem_ld32(ts + 32 * b + 32, s[1]);
+                            tmem_ld_wait();
+                        }
+                        if (edge) hide(t, seen[b]);
+                    }
+                    const uint64_t k2 = f2(bk[b], bk[b]), off = f2(es[b] - mu, es[b] - mu);
+                    uint64_t sum[2] = {0, 0};
+                    uint32_t ph[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 h = unpack_h2(ph[k]);
-                        ph[k] = pack_h2(__uint_as_float(s[2 * k]) - h.x, __uint_as_float(s[2 * k + 1]) - h.y);
+                        float u, v;
+                        f2_split(f2_fma(f2(__uint_as_float(t[2 * k]), __uint_as_float(t[2 * k + 1])), k2, off), u, v);
+                        u = exp2_fast(u);
+                        v = exp2_fast(v);
+                        sum[k & 1] = f2_add(sum[k & 1], f2(u, v));
+                        ph[k] = pack_h2(u, v);
+                        if constexpr (NS == 2) t[2 * k] = __float_as_uint(u), t[2 * k + 1] = __float_as_uint(v);
                     }
-                    tmem_st16(ts + 32 * b + 16, ph);
+                    tmem_st16(ts + 32 * b, ph);
+                    if constexpr (NS == 2) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 h = unpack_h2(ph[k]);
+                            ph[k] = pack_h2(__uint_as_float(t[2 * k]) - h.x, __uint_as_float(t[2 * k + 1]) - h.y);
+                        }
+                        tmem_st16(ts + 32 * b + 16, ph);
+                    }
+                    float u, v;
+                    f2_split(f2_add(sum[0], sum[1]), u, v);
+                    l = fmaf(u + v, is[b], l);
                 }
-                float u, v;
-                f2_split(f2_add(sum[0], sum[1]), u, v);
-                l = fmaf(u + v, is[b], l);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pready[x]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pready[x]);
-        }
-        if (nx > 0) ok = __all_sync(0xffffffffu, wait(&pvdone[x], (nx - 1) & 1)) && ok;
-        // A row's sum is its halves'.
-        s_row[x][half][i] = l;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * x + (warp & 3)) : "memory");
-        l = s_row[x][0][i] + s_row[x][1][i];
-        if (ok) {
+            if (ok && nx > 0) ok = __all_sync(0xffffffffu, wait(&pvdone[x], (step - 1) & 1));
+            if (!ok) break;
             tc_fence_after();
-            const int h = head * a.group + ht * p.hpt + hi, D = a.c.head_dim;
+            const int tok = w.tok + x * p.tqt + ti, h = w.head * a.group + w.ht * p.hpt + hi, D = a.c.head_dim;
             const bool none = m == -INFINITY;
-            if (NS == 2 && nx > kFlush) flush<DP / 2>(to, sums, pend, true, true);
+            if (NS == 2 && nx > kFlush) flush<DP>(to, sums(), pend, true, true);
             float inv = 0.f;
-            const int64_t prow = ((int64_t)tok * a.n_heads + h) * a.splits + part;
+            const int64_t prow = ((int64_t)tok * a.n_heads + h) * a.splits + w.part;
             if (a.splits > 1) {
                 // in the join's convention: weights 2^(x - M + kWShift)
-                if (row_ok && half == 0) a.part_ml[prow] = make_float2(none ? m : m + (kWShift - kTileShift), l);
+                if (row_ok) a.part_ml[prow] = make_float2(none ? m : m + (kWShift - kTileShift), l);
                 inv = 1.f;
             } else if (!none) {
                 if (a.sinks && row_ok) l += exp2_fast(fmaf(a.sinks[h], kLog2e, kTileShift - m));
                 inv = 1.f / l;
             }
 #pragma unroll 1
-            for (int c = 0; c < DP / 2; c += 32) {
+            for (int c = 0; c < DP; c += 32) {
                 uint32_t o[32];
                 if (nx > 0) {
                     tmem_ld32(to + c, o);
@@ -704,7 +845,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                 if (row_ok) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
-                        const int d = DP / 2 * half + c + k;
+                        const int d = c + k;
                         if (d >= D) break;
                         float v[4];
 #pragma unroll
@@ -717,6 +858,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                     }
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&iempty[slot]);
         }
     }
     tc_fence_before();
@@ -773,8 +917,8 @@ Layout layout(const AttnParams &p, const TileParams &t, int dtype, int64_t max_l
     };
     const size_t slot = (size_t)kTile * dp * 2;
     L.plan = take(sizeof(TilePlan));
-    L.q_tiles = take(L.cap_q * sizeof(int2));
-    L.kv_base = take((p.b.n_seq + 1) * sizeof(int32_t));
+    L.q_tiles = take(L.cap_q * sizeof(QTile));
+    L.kv_base = take(p.b.n_seq * sizeof(int32_t));
     L.kv_first = take(p.b.n_seq * sizeof(int32_t));
     L.q_img = take(L.cap_q * kvh * t.head_tiles * 2 * ns * slot);
     L.q_unit = take(L.cap_q * kvh * t.head_tiles * 2 * kTile * sizeof(float));
@@ -796,7 +940,7 @@ template <typename T, int DP>
 rf_status launch_tiles(const TileParams &t, cudaStream_t s, bool chain)
 {
     constexpr int NS = sizeof(T) == 4 ? 2 : 1;
-    static_assert(tile_smem<DP, NS>() + 4 * 4 * kTile + 64 <= 232448, "tiles exceed the 227 KB of shared memory");
+    static_assert(tile_smem<DP, NS>() + 3072 <= 232448, "tiles exceed the 227 KB of shared memory");
     static std::once_flag once[64];
     static bool okd[64];
     int dev = 0;
@@ -817,7 +961,7 @@ rf_status launch_tiles(const TileParams &t, cudaStream_t s, bool chain)
     if (const rf_status st = launch_kernel(tile_plan_kernel, dim3(1), dim3(1024), 0, s, chain, t)) return st;
     if (const rf_status st = launch_kernel(tile_stage_kernel<T, DP>, dim3((unsigned)stage), dim3(256), 0, s, true, t))
         return st;
-    return launch_kernel(attn_tile_kernel<T, DP>, dim3((unsigned)(ctas * a.splits)), dim3(kMainThreads),
+    return launch_kernel(attn_tile_kernel<T, DP>, dim3((unsigned)std::min<int64_t>(ctas * a.splits, num_sms())), dim3(kMainThreads),
                          tile_smem<DP, NS>(), s, true, t);
 }
 
@@ -851,7 +995,7 @@ rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *works
     t.a = p;
     t.cap_q = (int)L.cap_q, t.cap_kv = (int)L.cap_kv;
     t.plan = reinterpret_cast<TilePlan *>(ws + L.plan);
-    t.q_tiles = reinterpret_cast<int2 *>(ws + L.q_tiles);
+    t.q_tiles = reinterpret_cast<QTile *>(ws + L.q_tiles);
     t.kv_base = reinterpret_cast<int32_t *>(ws + L.kv_base);
     t.kv_first = reinterpret_cast<int32_t *>(ws + L.kv_first);
     t.q_img = ws + L.q_img;

@@ -21,6 +21,18 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t sbo)
     return d;
 }
 
+// True in one thread of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols)
 {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
