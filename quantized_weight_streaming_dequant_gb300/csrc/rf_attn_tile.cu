@@ -899,15 +899,23 @@ Layout layout(const AttnParams &p, const TileParams &t, int dtype, int64_t max_l
     if (p.window > 0)
         L.cap_kv = std::min<int64_t>(L.cap_kv, (p.b.n_seq * std::min(p.window, max_len) + p.b.n_tok) / kTile + 3LL * p.b.n_seq);
     const int64_t kvh = p.c.n_kv_heads;
-    // Parts of the position tiles: enough CTAs to fill the SMs about twice,
-    // at least four tiles to a part.
+    // Parts of the position tiles: the number for which the items' rounds over
+    // the SMs take the least time, in steps of one position tile (about 2 us,
+    // twice that for fp32): a round is its part's tiles and about two more to
+    // start and to write, and parts cost their write and read in the join.
     const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(L.cap_q, (p.b.n_tok + ctt - 1) / ctt) * kvh * t.head_tiles);
     int64_t seen = (max_len + kTile - 1) / kTile;
     if (p.window > 0) seen = std::min<int64_t>(seen, (p.window + ctt) / kTile + 2);
-    int64_t splits = std::max<int64_t>(1, 2LL * num_sms() / ctas);
-    splits = std::min<int64_t>(splits, std::max<int64_t>(1, seen / 4));
-    splits = std::min<int64_t>(splits, 64);
-    L.split_tiles = (int)((seen + splits - 1) / splits);
+    const double join = (double)p.b.n_tok * p.n_heads * p.c.head_dim * 8 / (6.0e6 * 2.0 * ns);
+    double best = 0;
+    for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, seen / 4)); ++s) {
+        const int64_t per = (seen + s - 1) / s, rounds = (ctas * s + num_sms() - 1) / num_sms();
+        const double cost = (double)rounds * (per + 2) + (s > 1 ? s * join + 3 : 0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            L.split_tiles = (int)per;
+        }
+    }
     L.splits = (int)((seen + L.split_tiles - 1) / L.split_tiles);
     size_t at = 0;
     auto take = [&at](size_t n) {
