@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
     const int kvh = u % p.c.n_kv_heads, t = u / p.c.n_kv_heads;
     pdl_launch_dependents();
     pdl_wait();
-    const int seq = find_seq(p.b.q_start, p.b.n_seq, t);
+    const int seq = find_seq_warp(p.b.q_start, p.b.n_seq, t);
     int n_here = 1;
     int64_t pos0 = -1;
     if (seq >= 0) {
@@ -129,6 +129,52 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
         const int to = part == p.splits - 1 ? b_hi : (int)min((int64_t)b_hi, from + p.split_blocks);
         b_lo = (int)min(from, (int64_t)b_hi);
         b_hi = to;
+    }
+
+    // Ring of this warp: stage s holds K then V of one block.  The first
+    // copies go out before the queries are read.
+    const int stage_bytes = 64 * D;
+    uint8_t *ring = smem + (size_t)warp * ST * stage_bytes;
+    const int n_it = b_hi - b_lo > warp ? (b_hi - b_lo - warp + kWarps - 1) / kWarps : 0;
+    const int per_page = p.c.page_size / kKvBlock;
+    int64_t pg_block = -1;    // lane i: block index in the cache of iteration (it & ~31) + i
+    int pg_meta = 0;          // its scale bytes, bit 16: valid
+    auto issue = [&](int it) {
+        if ((it & 31) == 0) {
+            const int blk = b_lo + warp + kWarps * (it + lane);
+            pg_block = -1;
+            pg_meta = 0;
+            if (it + lane < n_it) {
+                const int page = page_of(p.b, p.c, seq, (int64_t)blk * kKvBlock);
+                if (page >= 0) {
+                    pg_block = ((int64_t)page * p.c.n_kv_heads + kvh) * per_page + blk % per_page;
+                    pg_meta = (int)p.c.k_scale[pg_block] | (int)p.c.v_scale[pg_block] << 8 | 1 << 16;
+                } else {
+                    record_status(&g_attn_status, RF_ERR_INVALID_ARG);
+                }
+            }
+        }
+        const int64_t blk = __shfl_sync(0xffffffffu, pg_block, it & 31);
+        const int st = it % ST;
+        if (lane == (it & 31)) s_meta[warp][st] = pg_meta;
+        if (blk >= 0) {
+            uint8_t *kd = ring + st * stage_bytes, *vd = kd + 32 * D;
+            const int8_t *ks = p.c.k + blk * kKvBlock * D, *vs = p.c.v + blk * kKvBlock * D;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                const int w = i * 32 + lane;          // 16-byte run of the block
+                if (SWZ || w < 2 * D) {
+                    const int row = SWZ ? w / (DP / 16) : 0, run = SWZ ? w % (DP / 16) : w;
+                    cp_async16(kd + (SWZ ? k_off<SWZ>(row, run, DP) : 16 * w), ks + 16 * w);
+                    cp_async16(vd + (SWZ ? v_off<SWZ>(row, 16 * run, DP) : 16 * w), vs + 16 * w);
+                }
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+        if (i < n_it) issue(i);
+        cp_async_commit();
     }
 
     // Query fragments (columns of S^T): lane (g, c) holds row 8r + g, elements
@@ -195,50 +241,6 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
         l[r][0] = l[r][1] = 0.f;
     }
 
-    // Ring of this warp: stage s holds K then V of one block.
-    const int stage_bytes = 64 * D;
-    uint8_t *ring = smem + (size_t)warp * ST * stage_bytes;
-    const int n_it = b_hi - b_lo > warp ? (b_hi - b_lo - warp + kWarps - 1) / kWarps : 0;
-    const int per_page = p.c.page_size / kKvBlock;
-    int64_t pg_block = -1;    // lane i: block index in the cache of iteration (it & ~31) + i
-    int pg_meta = 0;          // its scale bytes, bit 16: valid
-    auto issue = [&](int it) {
-        if ((it & 31) == 0) {
-            const int blk = b_lo + warp + kWarps * (it + lane);
-            pg_block = -1;
-            pg_meta = 0;
-            if (it + lane < n_it) {
-                const int page = page_of(p.b, p.c, seq, (int64_t)blk * kKvBlock);
-                if (page >= 0) {
-                    pg_block = ((int64_t)page * p.c.n_kv_heads + kvh) * per_page + blk % per_page;
-                    pg_meta = (int)p.c.k_scale[pg_block] | (int)p.c.v_scale[pg_block] << 8 | 1 << 16;
-                } else {
-                    record_status(&g_attn_status, RF_ERR_INVALID_ARG);
-                }
-            }
-        }
-        const int64_t blk = __shfl_sync(0xffffffffu, pg_block, it & 31);
-        const int st = it % ST;
-        if (lane == (it & 31)) s_meta[warp][st] = pg_meta;
-        if (blk >= 0) {
-            uint8_t *kd = ring + st * stage_bytes, *vd = kd + 32 * D;
-            const int8_t *ks = p.c.k + blk * kKvBlock * D, *vs = p.c.v + blk * kKvBlock * D;
-#pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-                const int w = i * 32 + lane;          // 16-byte run of the block
-                if (SWZ || w < 2 * D) {
-                    const int row = SWZ ? w / (DP / 16) : 0, run = SWZ ? w % (DP / 16) : w;
-                    cp_async16(kd + (SWZ ? k_off<SWZ>(row, run, DP) : 16 * w), ks + 16 * w);
-                    cp_async16(vd + (SWZ ? v_off<SWZ>(row, 16 * run, DP) : 16 * w), vs + 16 * w);
-                }
-            }
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) {
-        if (i < n_it) issue(i);
-        cp_async_commit();
-    }
     for (int it = 0; it < n_it; ++it) {
         __syncwarp();                                 // the stage written next was read by all
         if (it + ST - 1 < n_it) issue(it + ST - 1);
@@ -462,16 +464,22 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
     }
 }
 
-// One warp per (token, head): the parts of a row, in their order.
-template <typename T>
+// Joins the parts of a row in their order.  WPR: warps per (token, head) row:
+// one where a row has few parts, eight (a CTA) where it has more, since a
+// part is a dependent round trip to memory (38 parts of 32 rows: 24 us with
+// one warp each, 5 with eight).
+template <typename T, int WPR>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p)
 {
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, D = p.c.head_dim;
+    __shared__ __align__(16) float s_o[WPR > 1 ? 8 : 1][256];
+    __shared__ float s_l[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = p.c.head_dim;
+    const int64_t row = WPR > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
     pdl_launch_dependents();
     pdl_wait();
     if (row >= (int64_t)p.b.n_tok * p.n_heads) return;
     const int64_t tok = row / p.n_heads;
+    const int h = (int)(row % p.n_heads);
     const float2 *ml = p.part_ml + row * p.splits;
     float M = -INFINITY;
     // a token that belongs to no sequence may have no parts
@@ -479,12 +487,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         for (int k = lane; k < p.splits; k += 32) M = fmaxf(M, ml[k].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const int h = (int)(row % p.n_heads);
-    T *out = static_cast<T *>(p.out) + tok * p.o_lt + (int64_t)h * p.o_lh;
     float L = 0.f, a[2][4] = {};
     if (M != -INFINITY) {
-        if (p.sinks) L = exp2_fast(fmaf(p.sinks[h], kLog2e, kWShift - M));
-        for (int k = 0; k < p.splits; ++k) {
+#pragma unroll 4
+        for (int k = WPR > 1 ? warp : 0; k < p.splits; k += WPR) {
             const float2 v = ml[k];
             if (v.x == -INFINITY && v.y == 0.f) continue;      // an empty part wrote no sums
             const float f = exp2_fast(v.x - M);
@@ -502,6 +508,27 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
             }
         }
     }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float4 *>(&s_o[warp][128 * i + 4 * lane]) = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+        if (lane == 0) s_l[warp] = L;
+        __syncthreads();
+        if (warp > 0) return;
+        L = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) L += s_l[k];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[i][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) a[i][e] += s_o[k][128 * i + 4 * lane + e];
+            }
+    }
+    if (p.sinks && M != -INFINITY) L += exp2_fast(fmaf(p.sinks[h], kLog2e, kWShift - M));
+    T *out = static_cast<T *>(p.out) + tok * p.o_lt + (int64_t)h * p.o_lh;
     const float inv = M == -INFINITY ? 0.f : 1.f / L;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -622,8 +649,11 @@ rf_status plan(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype, in
 rf_status launch_attn_join(const AttnParams &p, int dtype, cudaStream_t s)
 {
     const int64_t rows = (int64_t)p.b.n_tok * p.n_heads;
+    if (rows > 0x7fffffffLL) return RF_ERR_TOO_LARGE;
     return with_dtype(dtype, [&](auto t) {
-        return launch_kernel(attn_join_kernel<decltype(t)>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, p);
+        using T = decltype(t);
+        if (p.splits > 8) return launch_kernel(attn_join_kernel<T, 8>, dim3((unsigned)rows), dim3(256), 0, s, true, p);
+        return launch_kernel(attn_join_kernel<T, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, true, p);
     });
 }
 

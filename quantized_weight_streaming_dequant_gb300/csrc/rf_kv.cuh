@@ -114,6 +114,25 @@ __device__ __forceinline__ int find_seq(const int32_t *q_start, int n_seq, int t
     return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
+// find_seq by a converged warp, in fewer round trips to memory: sequence t
+// is tried first (a decode batch has one token each), then 32 entries at a
+// time are compared.
+__device__ __forceinline__ int find_seq_warp(const int32_t *q_start, int n_seq, int t)
+{
+    if (t < n_seq && q_start[t] == t && q_start[t + 1] == t + 1) return t;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = n_seq;                 // q_start[lo .. lo + n] brackets t, if anything does
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + lane * step;
+        const bool below = lane * step < n && (lane == 0 || q_start[at] <= t);
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, below));   // the last one not after t
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
+}
+
 // The page of position `pos` of sequence s, or -1 if it has none.
 __device__ __forceinline__ int page_of(const rf_kv_batch &b, const rf_kv_cache &c, int s, int64_t pos)
 {
