@@ -70,7 +70,7 @@ template <bool SWZ> __device__ __forceinline__ int v_off(int row, int byte, int 
     return SWZ ? o ^ (((row >> 1) & 3) << 5) : o;
 }
 
-template <int DP> __host__ __device__ constexpr int ring_stages() { return DP == 256 ? 2 : DP == 128 ? 3 : 4; }
+template <int DP> __host__ __device__ constexpr int ring_stages() { return DP == 256 ? 2 : 3; }
 template <int DP> size_t rows_smem(int D)
 {
     return (size_t)kWarps * ring_stages<DP>() * 64 * D + 256;
@@ -83,7 +83,7 @@ struct RowTiling {
 // DP: head_dim rounded up to 64, 128 or 256.  NR: query rows / 8.  SPLIT:
 // queries and weights as two fp16 terms (fp32 activations).
 template <typename T, int DP, int NR, bool SPLIT, bool SWZ>
-__global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
+__global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : DP == 128 ? 2 : NR == 1 ? 4 : 2)
     attn_rows_kernel(const __grid_constant__ AttnParams p, const RowTiling tl)
 {
     constexpr int ST = ring_stages<DP>();
@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
         const bool edge = p_lo + kKvBlock - 1 > pos0 || (p.window > 0 && p_lo <= pos_last - p.window);
         float w[2][NR][4];
         bool grew = false;
-        float alpha[NR][2];
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -308,39 +307,52 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
                         w[mt][r][2 * y + e] = x;
                         best = fmaxf(best, x);
                     }
-                best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 4));
-                best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 8));
-                best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 16));
-                const float mn = fmaxf(m[r][e], best);
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                alpha[r][e] = exp2_fast(m[r][e] - mu);
-                grew |= mn != m[r][e];
-                m[r][e] = mn;
+                grew |= best > m[r][e] + w_lazy<SPLIT>();
+            }
+        // The maximum that the weights go by is raised only when some lane
+        // has outgrown it by w_lazy (the weights' range allows that much),
+        // so most blocks need one vote and no exchange between lanes.
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mn = m[r][e];
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) mn = fmaxf(mn, fmaxf(w[mt][r][e], w[mt][r][2 + e]));
+                    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 4));
+                    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 8));
+                    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
+                    const float alpha = exp2_fast(m[r][e] - (mn == -INFINITY ? 0.f : mn));
+                    m[r][e] = mn;
+                    l[r][e] *= alpha;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) o[r][i][e] *= alpha, o[r][i][2 + e] *= alpha;
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mu = (m[r][e] == -INFINITY ? 0.f : m[r][e]) - w_shift<SPLIT>();
                 float sum = 0.f;
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         float &x = w[mt][r][2 * y + e];
-                        const bool out = edge && x == -INFINITY;
-                        x = exp2_fast(x - (mu - kWShift));
-                        sum = out ? sum : fmaf(x, iv, sum);   // a hidden position adds no NaN unit
+                        x = exp2_fast(x - mu);
+                        sum += x;
                     }
-                l[r][e] = fmaf(l[r][e], alpha[r][e], sum);
+                // the sum's unit; a lane that sees nothing of the block adds no NaN unit
+                const bool none = edge && w[0][r][e] == 0.f && w[0][r][2 + e] == 0.f && w[1][r][e] == 0.f && w[1][r][2 + e] == 0.f;
+                l[r][e] = none ? l[r][e] : fmaf(sum, iv, l[r][e]);
             }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[r][i][e] *= alpha[r][e & 1];
-        }
 
-        // O^T += V^T P^T.  The tensor core truncates its fp32 sums, so a
-        // block's product starts from zero and is added with rounding: over
-        // thousands of blocks the truncations would drift (1e-5 relative at
-        // 32,768 positions).
+        // O^T += V^T P^T.  The tensor core truncates its fp32 sums, so for
+        // fp32 a block's product starts from zero and is added with rounding:
+        // over thousands of blocks the truncations would drift (1e-5 relative
+        // at 32,768 positions, which 16-bit outputs do not see).
         uint32_t pf[2][NR][NS][2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -377,6 +389,7 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
             for (int k = 0; k < VB / 4; ++k)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {         // bytes 2x, 2x+1 of the words: one 16-row tile
+                    const int i = half * (MT / (DP == 256 ? 2 : 1)) + 2 * k + x;
                     float acc[NR][4] = {};
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
@@ -388,13 +401,14 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
                         for (int r = 0; r < NR; ++r)
 #pragma unroll
                             for (int n = NS - 1; n >= 0; --n)
-                                mma_16816(acc[r], a0, a1, a2, a3, pf[mt][r][n][0], pf[mt][r][n][1]);
+                                mma_16816(SPLIT ? acc[r] : o[r][i], a0, a1, a2, a3, pf[mt][r][n][0], pf[mt][r][n][1]);
                     }
-                    const int i = half * (MT / (DP == 256 ? 2 : 1)) + 2 * k + x;
+                    if constexpr (SPLIT) {
 #pragma unroll
-                    for (int r = 0; r < NR; ++r)
+                        for (int r = 0; r < NR; ++r)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[r][i][e] += acc[r][e];
+                            for (int e = 0; e < 4; ++e) o[r][i][e] += acc[r][e];
+                    }
                 }
         }
     }
@@ -455,7 +469,7 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : 2)
             *reinterpret_cast<float4 *>(p.part_o + at * D + d) = make_float4(a[0], a[1], a[2], a[3]);
             if (d == 0) p.part_ml[at] = make_float2(M, L);
         } else {
-            if (p.sinks && M != -INFINITY) L += exp2_fast(fmaf(p.sinks[h], kLog2e, kWShift - M));
+            if (p.sinks && M != -INFINITY) L += exp2_fast(fmaf(p.sinks[h], kLog2e, w_shift<SPLIT>() - M));
             const float inv = M == -INFINITY ? 0.f : 1.f / L;
 #pragma unroll
             for (int e = 0; e < 4; ++e) a[e] *= inv;
@@ -527,7 +541,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
                 for (int k = 0; k < 8; ++k) a[i][e] += s_o[k][128 * i + 4 * lane + e];
             }
     }
-    if (p.sinks && M != -INFINITY) L += exp2_fast(fmaf(p.sinks[h], kLog2e, kWShift - M));
+    if (p.sinks && M != -INFINITY) L += exp2_fast(fmaf(p.sinks[h], kLog2e, w_shift<sizeof(T) == 4>() - M));
     T *out = static_cast<T *>(p.out) + tok * p.o_lt + (int64_t)h * p.o_lh;
     const float inv = M == -INFINITY ? 0.f : 1.f / L;
 #pragma unroll
@@ -567,7 +581,7 @@ void choose_splits(AttnParams *p, const RowTiling &tl, int64_t max_len)
     const int64_t per_seq = (p->b.n_tok + p->b.n_seq - 1) / p->b.n_seq;
     const int64_t tiles = std::min<int64_t>(p->b.n_tok, (per_seq + tl.tq - 1) / tl.tq * p->b.n_seq) *
                           p->c.n_kv_heads * tl.head_tiles;
-    const int occ = p->c.head_dim > 128 ? 1 : p->c.head_dim > 64 ? 2 : 3;
+    const int occ = p->c.head_dim > 128 ? 1 : p->c.head_dim > 64 ? 2 : 4;
     // One sequence: its parts fill the SMs once.  Several: parts of equal
     // size, about four waves of them, so that long sequences do not leave
     // the others' SMs idle.  A part has a block for each warp at least.

@@ -18,8 +18,8 @@
 //          One thread issues the products of the two tiles alternately, so
 //          that one tile's exponentials run under the other's products; O
 //          stays in tensor memory and is rescaled only when a row's maximum
-//          has grown by more than 2^7 (the weights' exponent range allows it;
-//          the factor cancels).
+//          has grown by more than w_lazy (the weights' exponent range allows
+//          it; the factor cancels).
 // Bound: the tensor pipe for long rows: 4 * 128 * 128 * head_dim flops per
 // step and tile (twice that for fp32, whose queries and weights are two fp16
 // terms), against 16,384 exponentials.
@@ -48,8 +48,6 @@ constexpr int kMainThreads = 32 * (kSoftWarps + 4);   // ... and a warpgroup of 
 constexpr int kRegsSoftmax = 232, kRegsOther = 40;
 constexpr int kFlush = 16;          // position tiles that fp32 sums stay in tensor memory
 constexpr int kPadParts = 8;        // CTAs that zero the rows of no sequence
-constexpr float kTileShift = 8.f;   // weights are 2^(x - m + 8) <= 2^15
-constexpr float kLazy = 7.f;        // growth of a maximum that is not yet applied
 
 // What the plan kernel leaves for the others.
 struct TilePlan {
@@ -755,7 +753,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                     flush<DP>(to, sums(), pend, j > kFlush);
                     pend = 1.f;
                 }
-                if (__any_sync(0xffffffffu, mn > m + kLazy)) {
+                if (__any_sync(0xffffffffu, mn > m + w_lazy<NS == 2>())) {
                     const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
                     m = mn;
                     l *= alpha;
@@ -776,7 +774,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                         tmem_st_wait();
                     }
                 }
-                const float mu = (m == -INFINITY ? 0.f : m) - kTileShift;
+                const float mu = (m == -INFINITY ? 0.f : m) - w_shift<NS == 2>();
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     uint32_t (&t)[32] = s[kHold ? b : b & 1];
@@ -828,11 +826,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             float inv = 0.f;
             const int64_t prow = ((int64_t)tok * a.n_heads + h) * a.splits + w.part;
             if (a.splits > 1) {
-                // in the join's convention: weights 2^(x - M + kWShift)
-                if (row_ok) a.part_ml[prow] = make_float2(none ? m : m + (kWShift - kTileShift), l);
+                if (row_ok) a.part_ml[prow] = make_float2(m, l);
                 inv = 1.f;
             } else if (!none) {
-                if (a.sinks && row_ok) l += exp2_fast(fmaf(a.sinks[h], kLog2e, kTileShift - m));
+                if (a.sinks && row_ok) l += exp2_fast(fmaf(a.sinks[h], kLog2e, w_shift<NS == 2>() - m));
                 inv = 1.f / l;
             }
 #pragma unroll 1

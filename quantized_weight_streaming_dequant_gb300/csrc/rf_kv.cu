@@ -95,7 +95,10 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int half, in
                                              int page, int64_t pos, uint32_t *s_max)
 {
     const int tid = (int)threadIdx.x & 127;
-    const int D = p.c.head_dim, upr = D / 8;           // units per token
+    // Unit tid % upr of tokens tid / upr, + per, + 2 per, ... (threads that
+    // are left over idle).
+    const int D = p.c.head_dim, upr = D / 8, per = 128 / upr;
+    const int j0 = tid / upr, j1 = j0 < per ? n : 0;
     const int in_page = (int)(pos & (p.c.page_size - 1));
     const int r = in_page & (kKvBlock - 1);            // tokens of the block held before
     const T *src = static_cast<const T *>(half ? p.v : p.k) + head * (half ? p.v_lh : p.k_lh);
@@ -107,13 +110,13 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int half, in
     uint8_t *scale = (half ? p.c.v_scale : p.c.k_scale) + ph * (p.c.page_size / kKvBlock) + in_page / kKvBlock;
     const int E_old = r > 0 ? *scale : 0;
 
+    const Unit un = unit_at(tid - j0 * upr, rot, p.style);
     float x[UPT][4], y[UPT][4];
     uint32_t amax = 0;
 #pragma unroll
     for (int k = 0; k < UPT; ++k) {
-        const int w = tid + 128 * k, j = w / upr;      // token of the call's part of the block
-        if (j < n) {
-            const Unit un = unit_at(w - j * upr, rot, p.style);
+        const int j = j0 + k * per;                    // token of the call's part of the block
+        if (j < j1) {
             const T *row = src + (int64_t)(t0 + j) * lt;
             load4<T>(row + un.a, vec, x[k]);
             load4<T>(row + un.b, vec, y[k]);
@@ -141,9 +144,8 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int half, in
         };
 #pragma unroll
         for (int k = 0; k < UPT; ++k) {
-            const int w = tid + 128 * k, j = w / upr;
-            if (j < n) {
-                const Unit un = unit_at(w - j * upr, rot, p.style);
+            const int j = j0 + k * per;
+            if (j < j1) {
                 int8_t *row = codes + (int64_t)(r + j) * D;
                 *reinterpret_cast<uint32_t *>(row + un.a) = word(x[k]);
                 *reinterpret_cast<uint32_t *>(row + un.b) = word(y[k]);
@@ -221,22 +223,24 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     } else {
         const int h0 = ((int)blockIdx.y - p.c.n_kv_heads) * kQHeads;
         const int nh = min(kQHeads, p.n_heads - h0), upr = p.c.head_dim / 8;
-        for (int w = tid; w < t_n * nh * upr; w += kAppendThreads) {
-            const int j = w / (nh * upr), v = w - j * nh * upr, h = h0 + v / upr;
+        const int upt = nh * upr, per = kAppendThreads / upt;    // units per token (128 at most), tokens per pass
+        const int j0 = tid / upt, v = tid - j0 * upt, h = h0 + v / upr;
+        if (j0 >= per) return;
+        const Unit un = unit_at(v % upr, p.rot, p.style);
+        const T *src = static_cast<const T *>(p.q) + (int64_t)t_lo * p.q_lt + h * p.q_lh;
+        T *dst = static_cast<T *>(p.q_out) + (int64_t)t_lo * p.qo_lt + h * p.qo_lh;
+#pragma unroll 4
+        for (int j = j0; j < t_n; j += per) {
             if (s_pos[j] < 0) continue;
-            const Unit un = unit_at(v % upr, p.rot, p.style);
-            const int64_t t = t_lo + j;
-            const T *row = static_cast<const T *>(p.q) + t * p.q_lt + h * p.q_lh;
-            T *out = static_cast<T *>(p.q_out) + t * p.qo_lt + h * p.qo_lh;
             float x[4], y[4];
-            load4<T>(row + un.a, p.q_vec, x);
-            load4<T>(row + un.b, p.q_vec, y);
+            load4<T>(src + j * p.q_lt + un.a, p.q_vec, x);
+            load4<T>(src + j * p.q_lt + un.b, p.q_vec, y);
             if (p.rot) {
                 const int64_t at = (int64_t)s_pos[j] * (p.rot / 2);
                 rotate_unit(x, y, un, p.style, p.cos_tab + at, p.sin_tab + at);
             }
-            store4<T>(out + un.a, p.qo_vec, x);
-            store4<T>(out + un.b, p.qo_vec, y);
+            store4<T>(dst + j * p.qo_lt + un.a, p.qo_vec, x);
+            store4<T>(dst + j * p.qo_lt + un.b, p.qo_vec, y);
         }
     }
 }
