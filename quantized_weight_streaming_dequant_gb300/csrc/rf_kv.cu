@@ -13,9 +13,11 @@
 //
 // Bound: HBM bytes for a prompt (q, k, v read once, codes and rotated q
 // written once); for one token the chain launch - position - page - load -
-// reduce - store.  A CTA owns one block of one head, K on its first four
-// warps and V on its last four, values in registers between the maximum and
-// the rounding; other CTAs of the same grid rotate the queries.
+// reduce - store.  A CTA owns the K or the V block of one head, with at most
+// 32 values per thread (16 up to head_dim 128) in registers between the
+// maximum and the rounding: the chain of dependent reads is long, so many
+// small CTAs per SM hide it better than fewer with more values a thread.
+// Other CTAs of the same grid rotate the queries.
 #include <algorithm>
 
 #include "rf_kv.cuh"
@@ -37,6 +39,7 @@ struct AppendParams {
     const float *cos_tab, *sin_tab;
     int64_t n_pos;
     int n_heads, rot, style, chunk;
+    unsigned parts;          // CTAs per chunk
     bool k_vec, v_vec, q_vec, qo_vec;
 };
 
@@ -84,20 +87,15 @@ __device__ __forceinline__ int scale_for(uint32_t amax_bits)
     return E > kScaleMax ? kScaleNan : E < kScaleMin ? kScaleMin : E;
 }
 
-__device__ __forceinline__ void bar_half(int half)
-{
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-}
-
-// One block of one head, K or V, by 128 threads.  UPT: units per thread.
+// One block of one head, K or V, by the CTA.  UPT: units per thread.
 template <typename T, int UPT>
 __device__ __forceinline__ void append_block(const AppendParams &p, int half, int head, int t0, int n,
                                              int page, int64_t pos, uint32_t *s_max)
 {
-    const int tid = (int)threadIdx.x & 127;
+    const int tid = (int)threadIdx.x;
     // Unit tid % upr of tokens tid / upr, + per, + 2 per, ... (threads that
     // are left over idle).
-    const int D = p.c.head_dim, upr = D / 8, per = 128 / upr;
+    const int D = p.c.head_dim, upr = D / 8, per = kAppendThreads / upr;
     const int j0 = tid / upr, j1 = j0 < per ? n : 0;
     const int in_page = (int)(pos & (p.c.page_size - 1));
     const int r = in_page & (kKvBlock - 1);            // tokens of the block held before
@@ -132,8 +130,8 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int half, in
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
     if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-    bar_half(half);
-    amax = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+    __syncthreads();
+    amax = __reduce_max_sync(0xffffffffu, s_max[tid & 7]);
     int E = scale_for(amax);
     if (r > 0) E = max(E, E_old);                      // kScaleNan stays
     if (E != kScaleNan) {
@@ -155,7 +153,7 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int half, in
             // Held codes in the larger unit; |code| <= 128 and the factor is
             // 2^-1 at most, so the product is exact before rint.
             const float f = E_old == 0 || E - E_old > 100 ? 0.f : __uint_as_float((uint32_t)(127 + E_old - E) << 23);
-            for (int w = tid; w < r * D / 4; w += 128) {
+            for (int w = tid; w < r * D / 4; w += kAppendThreads) {
                 const uint32_t old = reinterpret_cast<const uint32_t *>(codes)[w];
                 uint32_t now = 0;
 #pragma unroll
@@ -166,36 +164,38 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int half, in
         }
     }
     if (tid == 0) *scale = (uint8_t)E;
-    bar_half(half);                                    // s_max is used again
+    __syncthreads();                                   // s_max is used again
 }
 
-// grid.x: chunks of p.chunk tokens; grid.y: K/V heads, then groups of
-// kQHeads query heads.  The K/V part of a chunk handles the blocks whose
+// grid: chunks of p.chunk tokens x (K and V of each head, then groups of
+// kQHeads query heads), the heads of a chunk next to one another: they share
+// its rows and tables, and the light K and V CTAs run beside the queries'.  The K/V part of a chunk handles the blocks whose
 // first token of this call lies in the chunk (a block starts at a position
 // that is a multiple of 32, or at its sequence's first token of the call).
 template <typename T, int UPT>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(kAppendThreads, UPT <= 2 ? 6 : 3) append_kernel(const __grid_constant__ AppendParams p)
 {
-    __shared__ uint32_t s_max[2][4];
+    __shared__ uint32_t s_max[8];
     __shared__ int s_pos[32], s_n[32], s_page[32];
     const int tid = threadIdx.x;
-    const int t_lo = (int)blockIdx.x * p.chunk, t_n = min(p.chunk, p.b.n_tok - t_lo);
-    const bool kv_part = (int)blockIdx.y < p.c.n_kv_heads;
+    const int part = (int)(blockIdx.x % p.parts);
+    const int t_lo = (int)(blockIdx.x / p.parts) * p.chunk, t_n = min(p.chunk, p.b.n_tok - t_lo);
+    const bool kv_part = part < 2 * p.c.n_kv_heads;
     pdl_launch_dependents();
     pdl_wait();
     // One thread per token of the chunk: its position, whether it has one,
     // and (K/V part) whether it opens a block and how many tokens follow.
     if (tid < t_n) {
         const int t = t_lo + tid;
-        const int s = find_seq(p.b.q_start, p.b.n_seq, t);
+        const int s = last_start(p.b.q_start, p.b.n_seq, t);
+        const int first = p.b.q_start[s], next = p.b.q_start[s + 1], past = p.b.past[s];   // in flight together
         int n = 0, page = -1;
         int64_t pos = -1;
-        if (s >= 0) {
-            const int first = p.b.q_start[s];
-            pos = (int64_t)p.b.past[s] + (t - first);
+        if (first <= t && t < next) {
+            pos = (int64_t)past + (t - first);
             if (kv_part) {
                 if (t == first || (pos & (kKvBlock - 1)) == 0) {
-                    const int end = min(p.b.q_start[s + 1], p.b.n_tok);
+                    const int end = min(next, p.b.n_tok);
                     n = min(kKvBlock - (int)(pos & (kKvBlock - 1)), end - t);
                     page = page_of(p.b, p.c, s, pos);
                     const bool turns = p.rot == 0 || pos + n <= p.n_pos;
@@ -215,13 +215,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
     __syncthreads();
     if (kv_part) {
-        const int half = tid >> 7;
         for (int j = 0; j < t_n; ++j)
             if (s_n[j] > 0)
-                append_block<T, UPT>(p, half, (int)blockIdx.y, t_lo + j, s_n[j], s_page[j], s_pos[j],
-                                     s_max[half]);
+                append_block<T, UPT>(p, part & 1, part >> 1, t_lo + j, s_n[j], s_page[j], s_pos[j], s_max);
     } else {
-        const int h0 = ((int)blockIdx.y - p.c.n_kv_heads) * kQHeads;
+        const int h0 = (part - 2 * p.c.n_kv_heads) * kQHeads;
         const int nh = min(kQHeads, p.n_heads - h0), upr = p.c.head_dim / 8;
         const int upt = nh * upr, per = kAppendThreads / upt;    // units per token (128 at most), tokens per pass
         const int j0 = tid / upt, v = tid - j0 * upt, h = h0 + v / upr;
@@ -269,24 +267,39 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ rf_kv
         s_off[threadIdx.x] = off;
     }
     __syncthreads();
-    const int cpr = c.head_dim / 16, per = c.n_kv_heads * cpr;   // 16-code runs per token
-    for (int w = (int)threadIdx.x; w < 2 * t_n * per; w += blockDim.x) {
-        const int side = w >= t_n * per, u = w - side * t_n * per;
-        const int j = u / per, h = (u - j * per) / cpr, i = (u - j * per) % cpr;
-        float *out = (side ? v_out : k_out) + ((int64_t)(t_lo + j) * c.n_kv_heads + h) * c.head_dim + 16 * i;
-        uint4 w4 = make_uint4(0u, 0u, 0u, 0u);
-        float unit = 0.f;
-        if (s_page[j] >= 0) {
-            const int64_t ph = (int64_t)s_page[j] * c.n_kv_heads + h;
-            w4 = *reinterpret_cast<const uint4 *>((side ? c.v : c.k) + (ph * c.page_size + s_off[j]) * c.head_dim + 16 * i);
-            unit = scale_value((side ? c.v_scale : c.k_scale)[ph * (c.page_size / kKvBlock) + s_off[j] / kKvBlock]);
-        }
-        const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+    // Four runs of 16 codes at a time, so that their reads overlap.
+    const int cpr = c.head_dim / 16, per = c.n_kv_heads * cpr, total = 2 * t_n * per;
+    for (int w0 = (int)threadIdx.x; w0 < total; w0 += 4 * 256) {
+        uint4 code[4];
+        float unit[4];
+        float *out[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-            reinterpret_cast<float4 *>(out)[m] =
-                make_float4((float)(int8_t)ws[m] * unit, (float)(int8_t)(ws[m] >> 8) * unit,
-                            (float)(int8_t)(ws[m] >> 16) * unit, (float)(int8_t)(ws[m] >> 24) * unit);
+        for (int r = 0; r < 4; ++r) {
+            const int w = w0 + 256 * r;
+            code[r] = make_uint4(0u, 0u, 0u, 0u);
+            unit[r] = 0.f;
+            out[r] = nullptr;
+            if (w < total) {
+                const int side = w >= t_n * per, u = w - side * t_n * per;
+                const int j = u / per, h = (u - j * per) / cpr, i = (u - j * per) % cpr;
+                out[r] = (side ? v_out : k_out) + ((int64_t)(t_lo + j) * c.n_kv_heads + h) * c.head_dim + 16 * i;
+                if (s_page[j] >= 0) {
+                    const int64_t ph = (int64_t)s_page[j] * c.n_kv_heads + h;
+                    code[r] = *reinterpret_cast<const uint4 *>((side ? c.v : c.k) + (ph * c.page_size + s_off[j]) * c.head_dim + 16 * i);
+                    unit[r] = scale_value((side ? c.v_scale : c.k_scale)[ph * (c.page_size / kKvBlock) + s_off[j] / kKvBlock]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (!out[r]) continue;
+            const uint32_t ws[4] = {code[r].x, code[r].y, code[r].z, code[r].w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                reinterpret_cast<float4 *>(out[r])[m] =
+                    make_float4((float)(int8_t)ws[m] * unit[r], (float)(int8_t)(ws[m] >> 8) * unit[r],
+                                (float)(int8_t)(ws[m] >> 16) * unit[r], (float)(int8_t)(ws[m] >> 24) * unit[r]);
+        }
     }
 }
 
@@ -370,14 +383,17 @@ rf_status rf_kv_append(const rf_kv_cache *cache, const rf_kv_batch *batch, int d
     // block in 32 tokens, so a chunk of 32 holds about one.
     p.chunk = (int64_t)batch->n_tok >= 16LL * batch->n_seq ? 32 : 1;
     const int q_groups = q ? (n_heads + kQHeads - 1) / kQHeads : 0;
-    const dim3 grid((unsigned)((batch->n_tok + p.chunk - 1) / p.chunk), (unsigned)(cache->n_kv_heads + q_groups));
+    p.parts = (unsigned)(2 * cache->n_kv_heads + q_groups);
+    const int64_t ctas = (((int64_t)batch->n_tok + p.chunk - 1) / p.chunk) * p.parts;
+    if (ctas > 0x7fffffffLL) return RF_ERR_TOO_LARGE;
+    const dim3 grid((unsigned)ctas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chain = (flags & RF_CHAIN) != 0;
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        if (D <= 64) return launch_kernel(append_kernel<T, 2>, grid, dim3(kAppendThreads), 0, s, chain, p);
-        if (D <= 128) return launch_kernel(append_kernel<T, 4>, grid, dim3(kAppendThreads), 0, s, chain, p);
-        return launch_kernel(append_kernel<T, 8>, grid, dim3(kAppendThreads), 0, s, chain, p);
+        if (D <= 64) return launch_kernel(append_kernel<T, 1>, grid, dim3(kAppendThreads), 0, s, chain, p);
+        if (D <= 128) return launch_kernel(append_kernel<T, 2>, grid, dim3(kAppendThreads), 0, s, chain, p);
+        return launch_kernel(append_kernel<T, 4>, grid, dim3(kAppendThreads), 0, s, chain, p);
     });
 }
 

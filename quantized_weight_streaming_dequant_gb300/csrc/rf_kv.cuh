@@ -101,16 +101,22 @@ __device__ __forceinline__ float exp2_fast(float x)
 }
 
 // ------------------------------------------------------------------- batch
-// The sequence that owns token t, or -1: the last s with q_start[s] <= t,
-// if t < q_start[s+1].  Reads only q_start[0 .. n_seq].
-__device__ __forceinline__ int find_seq(const int32_t *q_start, int n_seq, int t)
+// The last sequence s with q_start[s] <= t, or 0 if there is none.
+__device__ __forceinline__ int last_start(const int32_t *q_start, int n_seq, int t)
 {
-    int lo = 0, hi = n_seq;   // q_start[lo] <= t (checked below); q_start[hi] > t or hi == n_seq
+    int lo = 0, hi = n_seq;   // q_start[lo] <= t or lo == 0; q_start[hi] > t or hi == n_seq
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (q_start[mid] <= t) lo = mid;
         else hi = mid;
     }
+    return lo;
+}
+
+// The sequence that owns token t, or -1.  Reads only q_start[0 .. n_seq].
+__device__ __forceinline__ int find_seq(const int32_t *q_start, int n_seq, int t)
+{
+    const int lo = last_start(q_start, n_seq, t);
     return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
