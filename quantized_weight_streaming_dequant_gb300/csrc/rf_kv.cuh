@@ -72,6 +72,21 @@ __device__ __forceinline__ void store4(T *p, bool vec, const float (&f)[4])
     }
 }
 
+// 32 bytes in one store (a whole memory sector); p is aligned to them.
+__device__ __forceinline__ void store_sector(void *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+// Two elements as T, packed.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    union { T t[2]; uint32_t u; } v;
+    v.t[0] = from_f32<T>(a), v.t[1] = from_f32<T>(b);
+    return v.u;
+}
+
 // ------------------------------------------------------------------- codes
 // Codes 0, 1 / 2, 3 of a word, their sign bits flipped, as an fp16 pair:
 // 0x6400 | u is 1024 + code + 128, so subtracting 1152 is exact.
