@@ -245,17 +245,17 @@ __device__ __forceinline__ void stage_kv(const TileParams &p, int tile, int head
             v[i] = blk >= 0 && d < D
                        ? *reinterpret_cast<const uint32_t *>(c.v + (blk * kKvBlock + (8 * t + i) % 32) * D + d) ^ 0x80808080u
                        : 0x80808080u;
-        uint4 o[4];
+        uint32_t o[2][8];                            // two elements (16 bytes each) to a sector
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             const uint32_t a = prmt(v[i], v[i + 1], 0x5140u), b = prmt(v[i], v[i + 1], 0x7362u);
             const uint32_t x[4] = {codes_lo(a), codes_hi(a), codes_lo(b), codes_hi(b)};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t *>(&o[e])[i / 2] = x[e];
+            for (int e = 0; e < 4; ++e) o[e >> 1][4 * (e & 1) + i / 2] = x[e];
         }
         uint8_t *dst = vi + (d / 8) * 2048 + t * 128 + (d % 8) * 16;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + 16 * e) = o[e];
+        store_sector(dst, o[0]);
+        store_sector(dst + 32, o[1]);
     }
 }
 
