@@ -156,11 +156,18 @@ def _check(code: int, what: str) -> None:
         raise RFError(code, what)
 
 
+_raw_stream = _current_device = None
+
+
 def _stream(stream):
+    global _raw_stream, _current_device
     if stream is None:
-        # The handle alone: building a torch.cuda.Stream costs 3 us a call.
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _raw_stream is None:
+            # The handle alone: building a torch.cuda.Stream costs 3 us a call.
+            import torch
+            torch.cuda.init()
+            _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -529,15 +536,15 @@ def moe_workspace_views(workspace, top_k: int, n_ff: int):
     return idx, w, h
 
 
-_DTYPES = None
+_DTYPES = _empty = None
 
 
 def _dtype(t) -> int:
     """The activation type of a tensor."""
-    global _DTYPES
-    if _DTYPES is None:
+    global _DTYPES, _empty
+    if _DTYPES is None:   # torch is looked up once: an import statement costs each call 0.5 us
         import torch
-        _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        _DTYPES, _empty = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}, torch.empty
     d = _DTYPES.get(t.dtype)   # F32 is 0
     if d is None:
         raise ValueError(f"activations are float32, float16 or bfloat16, not {t.dtype}")
@@ -572,7 +579,6 @@ def norm_residual(residual, x=None, *, post_weight=None, gate=None, scale: float
     either may be None); gate is (n,) or (n_tok, n) float32.  Returns
     (residual + scale * gate * post_norm(x), its norm); the norm is None with
     norm=False."""
-    import torch
     like = residual if residual is not None else x
     if like is None or like.dim() != 2:
         raise ValueError("residual or x must be given, (n_tok, n)")
@@ -581,12 +587,12 @@ def norm_residual(residual, x=None, *, post_weight=None, gate=None, scale: float
     px, ldx = _rows(x, n_tok, n, dt, "x")
     pr, ldr = _rows(residual, n_tok, n, dt, "residual")
     if residual_out is None:
-        residual_out = torch.empty((n_tok, n), dtype=like.dtype, device=like.device)
+        residual_out = _empty((n_tok, n), dtype=like.dtype, device=like.device)
         po, ldo = residual_out.data_ptr(), n
     else:
         po, ldo = _rows(residual_out, n_tok, n, dt, "residual_out")
     if y is None and norm:
-        y = torch.empty((n_tok, n), dtype=like.dtype, device=like.device)
+        y = _empty((n_tok, n), dtype=like.dtype, device=like.device)
         py, ldy = y.data_ptr(), n
     else:
         py, ldy = _rows(y, n_tok, n, dt, "y")
@@ -678,11 +684,12 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None
     if q is not None:
         pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
         if q_out is None:
-            import torch
-            q_out = torch.empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
-        po, olt, olh, oh = _heads(q_out, n_tok, dim, dt, "q_out")
-        if oh != nh:
-            raise ValueError("q_out must be like q")
+            q_out = _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+            po, olt, olh = q_out.data_ptr(), nh * dim, dim
+        else:
+            po, olt, olh, oh = _heads(q_out, n_tok, dim, dt, "q_out")
+            if oh != nh:
+                raise ValueError("q_out must be like q")
     pc = ps = None
     n_pos = rot = 0
     if cos is not None or sin is not None:
@@ -728,11 +735,12 @@ def attention(cache: KVCache, batch: KVBatch, q, out=None, scale: float | None =
     n_tok, dim, dt = batch.n_tok, cache.head_dim, _dtype(q)
     pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
     if out is None:
-        import torch
-        out = torch.empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
-    po, olt, olh, oh = _heads(out, n_tok, dim, dt, "out")
-    if oh != nh:
-        raise ValueError("out must be like q")
+        out = _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+        po, olt, olh = out.data_ptr(), nh * dim, dim
+    else:
+        po, olt, olh, oh = _heads(out, n_tok, dim, dt, "out")
+        if oh != nh:
+            raise ValueError("out must be like q")
     if workspace is None:
         workspace = attention_workspace(cache, batch, q, max_len, window)
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
