@@ -717,7 +717,8 @@ RF_API rf_status rf_kv_read(const rf_kv_cache *cache, const rf_kv_batch *batch, 
  * then enter the tensor cores as two fp16 terms (22 bits); for 16-bit
  * dtypes the weights are rounded once to fp16, and queries exactly
  * representable in fp16 after scaling by a power of two are not rounded.
- * Results do not depend on the other sequences' contents or on timing.
+ * Results do not depend on the other sequences or on timing (n_seq, n_tok and
+ * max_len choose how a row's sums are shared out).
  * q, out: n_tok x n_heads x head_dim with token and head strides; out may
  * not overlap q.  workspace: device, 256-byte aligned, at least
  * rf_attention_workspace_bytes(...) bytes (NULL if that is 0), overwritten.

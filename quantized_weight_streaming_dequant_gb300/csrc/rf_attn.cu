@@ -24,6 +24,7 @@
 // private ring of cp.async copies (no CTA barrier in the loop); warps and
 // CTAs are joined at the end.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <mutex>
 
@@ -124,6 +125,12 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : DP == 128 ? 2 : N
     int64_t lo = 0;
     if (p.window > 0) lo = max((int64_t)0, pos0 - p.window + 1);
     int b_lo = (int)(lo / kKvBlock), b_hi = seq >= 0 && pos_last >= 0 ? (int)(pos_last / kKvBlock) + 1 : 0;
+    // (positions past the table have no page, however many there are)
+    const int b_cap = (int)min((int64_t)INT_MAX, (int64_t)p.b.table_width * (p.c.page_size / kKvBlock));
+    if (b_hi > b_cap) {
+        if (threadIdx.x == 0) record_status(&g_attn_status, RF_ERR_INVALID_ARG);
+        b_hi = b_cap;
+    }
     {
         const int64_t from = b_lo + (int64_t)part * p.split_blocks;
         const int to = part == p.splits - 1 ? b_hi : (int)min((int64_t)b_hi, from + p.split_blocks);
@@ -469,8 +476,9 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : DP == 128 ? 2 : N
             *reinterpret_cast<float4 *>(p.part_o + at * D + d) = make_float4(a[0], a[1], a[2], a[3]);
             if (d == 0) p.part_ml[at] = make_float2(M, L);
         } else {
-            if (p.sinks && M != -INFINITY) L += exp2_fast(fmaf(p.sinks[h], kLog2e, w_shift<SPLIT>() - M));
-            const float inv = M == -INFINITY ? 0.f : 1.f / L;
+            const bool none = M == -INFINITY && L == 0.f;   // (NaN scores are seen, and raise no maximum)
+            if (p.sinks && !none) L += exp2_fast(fmaf(p.sinks[h], kLog2e, w_shift<SPLIT>() - mu));
+            const float inv = none ? 0.f : 1.f / L;
 #pragma unroll
             for (int e = 0; e < 4; ++e) a[e] *= inv;
             store4<T>(static_cast<T *>(p.out) + tok * p.o_lt + (int64_t)h * p.o_lh + d, p.o_vec, a);
@@ -496,18 +504,25 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const int h = (int)(row % p.n_heads);
     const float2 *ml = p.part_ml + row * p.splits;
     float M = -INFINITY;
+    bool any = false;                              // a part that saw something, were it only NaN scores
     // a token that belongs to no sequence may have no parts
-    if (find_seq(p.b.q_start, p.b.n_seq, (int)tok) >= 0)
-        for (int k = lane; k < p.splits; k += 32) M = fmaxf(M, ml[k].x);
+    if (find_seq_warp(p.b.q_start, p.b.n_seq, (int)tok) >= 0)
+        for (int k = lane; k < p.splits; k += 32) {
+            const float2 v = ml[k];
+            M = fmaxf(M, v.x);
+            any |= !(v.x == -INFINITY && v.y == 0.f);
+        }
+    any = __any_sync(0xffffffffu, any);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.f, a[2][4] = {};
-    if (M != -INFINITY) {
+    const float mu = M == -INFINITY ? 0.f : M;
+    if (any) {
 #pragma unroll 4
         for (int k = WPR > 1 ? warp : 0; k < p.splits; k += WPR) {
             const float2 v = ml[k];
             if (v.x == -INFINITY && v.y == 0.f) continue;      // an empty part wrote no sums
-            const float f = exp2_fast(v.x - M);
+            const float f = exp2_fast(v.x - mu);
             L = fmaf(f, v.y, L);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -541,9 +556,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
                 for (int k = 0; k < 8; ++k) a[i][e] += s_o[k][128 * i + 4 * lane + e];
             }
     }
-    if (p.sinks && M != -INFINITY) L += exp2_fast(fmaf(p.sinks[h], kLog2e, w_shift<sizeof(T) == 4>() - M));
+    if (p.sinks && any) L += exp2_fast(fmaf(p.sinks[h], kLog2e, w_shift<sizeof(T) == 4>() - mu));
     T *out = static_cast<T *>(p.out) + tok * p.o_lt + (int64_t)h * p.o_lh;
-    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    const float inv = any ? 1.f / L : 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int d = 128 * i + 4 * lane;
@@ -693,7 +708,7 @@ size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv_batch 
 {
     AttnParams p = {};
     if (plan(cache, batch, dtype, n_heads, window, &max_len, &p) != RF_OK || batch->n_tok == 0) return 0;
-    if (attn_tile_takes(p)) return attn_tile_workspace(p, dtype, max_len);
+    if (attn_tile_takes(p, max_len)) return attn_tile_workspace(p, dtype, max_len);
     RowTiling tl;
     rows_tiling(p, &tl);
     choose_splits(&p, tl, max_len);
@@ -723,7 +738,7 @@ rf_status rf_attention(const rf_kv_cache *cache, const rf_kv_batch *batch, int d
     p.o_sector = aligned_to(out, 32) && (out_ld_tok * (int64_t)b) % 32 == 0 && (out_ld_head * (int64_t)b) % 32 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chain = (flags & RF_CHAIN) != 0;
-    if (attn_tile_takes(p)) {
+    if (attn_tile_takes(p, max_len)) {
         if (!workspace || workspace_bytes < attn_tile_workspace(p, dtype, max_len)) return RF_ERR_INVALID_ARG;
         return launch_attn_tile(p, dtype, max_len, workspace, s, chain);
     }

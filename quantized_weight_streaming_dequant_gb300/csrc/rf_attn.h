@@ -38,7 +38,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // The path for long chunks (128-row tiles on tcgen05), its workspace and
 // whether it takes the call.
-bool attn_tile_takes(const AttnParams &p);
+bool attn_tile_takes(const AttnParams &p, int64_t max_len);
 size_t attn_tile_workspace(const AttnParams &p, int dtype, int64_t max_len);
 rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *workspace, cudaStream_t s,
                            bool chain);

@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             if (!ok) break;
             tc_fence_after();
             const int tok = w.tok + x * p.tqt + ti, h = w.head * a.group + w.ht * p.hpt + hi, D = a.c.head_dim;
-            const bool none = m == -INFINITY;
+            const bool none = m == -INFINITY && l == 0.f;   // (NaN scores are seen, and raise no maximum)
             if (NS == 2 && nx > kFlush) flush<DP>(to, sums(), pend, true, true);
             float inv = 0.f;
             const int64_t prow = ((int64_t)tok * a.n_heads + h) * a.splits + w.part;
@@ -995,11 +995,19 @@ rf_status launch_tiles(const TileParams &t, cudaStream_t s, bool chain)
 
 }  // namespace
 
-bool attn_tile_takes(const AttnParams &p)
+bool attn_tile_takes(const AttnParams &p, int64_t max_len)
 {
-    // Tiles of 128 rows are worth their staging where a sequence's new rows
-    // (tokens x heads of a group) fill about half of one.
-    return p.c.head_dim <= 128 && (int64_t)p.b.n_tok * p.group >= 64LL * p.b.n_seq;
+    // Rows (tokens x heads of a group) per sequence and the work in all.
+    // Measured in us, rows kernel / tiles, one sequence, bf16, four heads of
+    // 128 to a K/V head, against 30,000 positions: 64 rows 58 / 67, 128 rows
+    // 108 / 71, 256 rows 201 / 85; against 1,000: 64 rows 16 / 24, 256 rows
+    // 21 / 32; 16 sequences against 8,000: 64 rows 235 / 247, 128 rows 397 /
+    // 250 (fp32: 324 / 326, 572 / 342).  Tiles pay from about 96 rows, once
+    // the work outweighs two more launches and the staging.
+    if (p.c.head_dim > 128) return false;
+    const int64_t per_seq = (p.b.n_tok + p.b.n_seq - 1) / p.b.n_seq, rows = per_seq * p.group;
+    const int64_t seen = p.window > 0 ? std::min(max_len, p.window + per_seq) : max_len;
+    return rows >= 96 && (double)rows * seen * p.b.n_seq >= 5e5;
 }
 
 size_t attn_tile_workspace(const AttnParams &p, int dtype, int64_t max_len)
@@ -1017,7 +1025,6 @@ rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *works
     if (L.cap_q > 0x3fffffffLL || L.cap_kv > 0x3fffffffLL) return RF_ERR_TOO_LARGE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.splits = L.splits;
-    p.split_blocks = 0;
     p.part_o = reinterpret_cast<float *>(ws + L.part_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + L.part_ml);
     t.a = p;

@@ -90,3 +90,12 @@ def check_attention(su, q, q64, dtype, scale=None, window=0, sinks=None, max_len
     worst = np.nanmax(err / bound) if err.size else 0.0
     assert worst <= 1.0, (worst, np.argwhere(err > bound)[:5].tolist())
     return out
+
+
+def by_tiles(su, heads, window=0, max_len=0):
+    """Whether the call goes through the 128-row tiles: 96 rows (tokens x heads
+    of a group) a sequence and half a million row-position pairs."""
+    per = -(-su.n_tok // len(su.past))
+    rows = per * heads // su.ref.heads
+    seen = max_len or su.table.shape[1] * su.ref.page
+    return su.ref.dim <= 128 and rows >= 96 and rows * min(seen, window + per if window else seen) * len(su.past) >= 5e5

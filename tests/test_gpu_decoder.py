@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import quantized_weight_streaming_dequant_gb300 as rf
-from decoder_helpers import DTYPES, TORCH, Setup, check_attention, i32, randn, strided
+from decoder_helpers import DTYPES, TORCH, Setup, by_tiles, check_attention, i32, randn, strided
 from oracle import decoder as od
 
 pytestmark = pytest.mark.gpu
@@ -392,13 +392,13 @@ def test_many_pages_pass_32_bit_offsets():
 # ------------------------------------------------------------- long chunks
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("dim,heads,kv,page,past,new", [
-    (128, 4, 1, 64, [0], [300]), (64, 8, 1, 32, [0, 77, 3], [129, 200, 64]), (128, 2, 2, 128, [515], [257]),
-    (80, 5, 1, 256, [130, 0], [90, 31]), (16, 3, 1, 32, [0], [130]), (112, 7, 1, 64, [40], [75]),
-    (64, 130, 1, 64, [33], [3]), (128, 20, 1, 32, [0, 500], [40, 1]), (64, 64, 2, 64, [0, 10, 700, 0], [0, 5, 2, 30])])
+    (128, 4, 1, 64, [0], [400]), (64, 8, 1, 32, [0, 77, 3], [129, 200, 64]), (128, 2, 2, 128, [900], [600]),
+    (80, 5, 1, 256, [130, 0], [190, 331]), (16, 3, 1, 32, [0], [430]), (112, 7, 1, 64, [440], [175]),
+    (64, 130, 1, 64, [1400], [3]), (128, 20, 1, 32, [0, 900], [40, 7]), (64, 64, 2, 64, [0, 10, 700, 0], [0, 5, 2, 60])])
 def test_attention_long_chunks(dtype, dim, heads, kv, page, past, new):
     rng = np.random.default_rng([dim, heads, sum(new)])
     su = Setup(rng, past, new, kv, dim, page, pad_tokens=3)
-    assert su.n_tok * heads // kv >= 64 * len(past)              # rows enough for the 128-row tiles
+    assert by_tiles(su, heads)
     q, q64 = randn(rng, (su.n_tok, heads, dim), dtype, 2.0)
     out = check_attention(su, q, q64, dtype)
     assert not out[-3:].any()
@@ -412,6 +412,7 @@ def test_attention_long_chunks(dtype, dim, heads, kv, page, past, new):
 def test_attention_long_chunks_split_and_joined(dtype, dim):
     rng = np.random.default_rng(dim)
     su = Setup(rng, [4000], [40], 1, dim, 64, pad_tokens=1)
+    assert by_tiles(su, 4, max_len=4040) and not by_tiles(su, 4, window=1000)
     q, q64 = randn(rng, (su.n_tok, 4, dim), dtype, 2.0)
     a = check_attention(su, q, q64, dtype, max_len=4040)
     assert torch.equal(a, rf.attention(su.cache, su.batch, q, max_len=4040))
@@ -421,7 +422,8 @@ def test_attention_long_chunks_split_and_joined(dtype, dim):
 
 def test_attention_long_chunks_hide_missing_pages_and_nan_blocks():
     rng = np.random.default_rng(18)
-    su = Setup(rng, [200], [100], 2, 64, 32)
+    su = Setup(rng, [600], [500], 2, 64, 32)
+    assert by_tiles(su, 4) and by_tiles(su, 4, window=150)
     su.table[0, 3] = -1                                         # positions 96..127 have no page
     su.ref.scales[1][su.table[0, 0], 1] = 255                   # values 0..31, head 1
     su.upload()
@@ -429,13 +431,14 @@ def test_attention_long_chunks_hide_missing_pages_and_nan_blocks():
     out = check_attention(su, q, q64, "float32")
     assert torch.isnan(out[:, 2:]).all() and torch.isfinite(out[:, :2]).all()
     assert rf.device_status() == 1
-    out = check_attention(su, q, q64, "float32", window=150)    # the first row sees positions 51..
+    out = check_attention(su, q, q64, "float32", window=150)    # the first row sees positions 451..
     assert torch.isfinite(out).all()
 
 
 def test_attention_long_chunks_strides_streams_and_chains():
     rng = np.random.default_rng(19)
-    su = Setup(rng, [64, 300], [90, 70], 2, 128, 64)
+    su = Setup(rng, [64, 600], [290, 270], 2, 128, 64)
+    assert by_tiles(su, 8)
     for dtype in DTYPES:
         q, q64 = randn(rng, (su.n_tok, 8, 128), dtype)
         want = check_attention(su, q, q64, dtype)
@@ -455,10 +458,40 @@ def test_attention_long_chunks_strides_streams_and_chains():
 def test_attention_tiles_and_rows_agree_on_one_token_at_a_time():
     """A chunk gives each token what it gets alone (within both paths' bounds)."""
     rng = np.random.default_rng(20)
-    su = Setup(rng, [150], [64], 1, 128, 64)
-    q, q64 = randn(rng, (64, 4, 128))
+    su = Setup(rng, [1500], [100], 1, 128, 64)
+    assert by_tiles(su, 4)
+    q, q64 = randn(rng, (100, 4, 128))
     whole = check_attention(su, q, q64, "float32")
     for t in (0, 31, 63):
-        one = rf.KVBatch(i32(su.table), i32([150 + t]), i32([0, 1]), 1)
+        one = rf.KVBatch(i32(su.table), i32([1500 + t]), i32([0, 1]), 1)
         alone = rf.attention(su.cache, one, q[t:t + 1].contiguous())
         assert torch.allclose(alone[0], whole[t], rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("past,new", [(5, 1), (3000, 1), (150, 40), (4000, 40)])
+def test_nan_and_infinite_queries_stay_in_their_rows(dtype, past, new):
+    """Single tokens and chunks, one part and several."""
+    rng = np.random.default_rng([past, new])
+    su = Setup(rng, [past], [new], 1, 64, 64)
+    q, q64 = randn(rng, (new, 4, 64), dtype)
+    clean = check_attention(su, q, q64, dtype)
+    q[0, 1, 5] = float("nan")
+    q[new - 1, 2, 7] = float("inf")
+    out = rf.attention(su.cache, su.batch, q)
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(out[new - 1, 2]).all()
+    hit = torch.zeros((new, 4), dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[new - 1, 2] = True
+    assert torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim,heads,window,past,new", [(64, 8, 1, [500], [600]), (64, 8, 128, [300, 0, 9], [300, 257, 31]),
+                                                       (128, 4, 200, [40, 1000], [400, 301])])
+def test_attention_long_chunks_under_a_window(dtype, dim, heads, window, past, new):
+    rng = np.random.default_rng([dim, window])
+    su = Setup(rng, past, new, 1, dim, 64)
+    assert by_tiles(su, heads, window)
+    q, q64 = randn(rng, (su.n_tok, heads, dim), dtype, 2.0)
+    check_attention(su, q, q64, dtype, window=window, sinks=rng.standard_normal(heads).astype(np.float32))
+    assert rf.device_status() == rf.OK
