@@ -714,9 +714,10 @@ RF_API rf_status rf_kv_read(const rf_kv_cache *cache, const rf_kv_batch *batch, 
  * launch shape and the workspace (0: the table's capacity); the rows of a
  * longer sequence are undefined.
  * Scores and softmax sums are fp32.  fp32 queries and the softmax weights
- * then enter the tensor cores as two fp16 terms (22 bits); for 16-bit
- * dtypes the weights are rounded once to fp16, and queries exactly
- * representable in fp16 after scaling by a power of two are not rounded.
+ * then enter the tensor cores as two fp16 terms (22 bits; weights below
+ * 2^-17 of a row's largest: to 2^-39 of it); for 16-bit dtypes the weights
+ * are rounded once to fp16 (below 2^-22 of the largest: to 2^-33 of it), and
+ * queries, scaled by a power of two, are not rounded.
  * Results do not depend on the other sequences or on timing (n_seq, n_tok and
  * max_len choose how a row's sums are shared out).
  * q, out: n_tok x n_heads x head_dim with token and head strides; out may

@@ -37,7 +37,10 @@
 namespace rf {
 namespace {
 
-__device__ int g_tile_status = 0;
+__device__ int g_tile_status = 0;    // bounded waits that gave up
+// Positions or pages that do not exist: a word of its own, since waits end
+// early while theirs is set.
+__device__ int g_tile_invalid = 0;
 
 constexpr int kTile = 128;          // query rows, and positions, per tile
 constexpr int kSoftWarps = 8;       // four per tile: a thread per row
@@ -135,14 +138,14 @@ __global__ void __launch_bounds__(1024) tile_plan_kernel(const __grid_constant__
                 first = lo / kTile;
                 nt = max((int64_t)0, min(last / kTile + 1, (int64_t)b.table_width * p.a.c.page_size / kTile + 1) - first);
             }
-            if (past < 0 && nq > 0) record_status(&g_tile_status, RF_ERR_INVALID_ARG);
+            if (past < 0 && nq > 0) record_status(&g_tile_invalid, RF_ERR_INVALID_ARG);
         }
         int64_t total_kv, total_q;
         const int64_t kv0 = kv_at + scan1024(nt, part, &total_kv);
         const int64_t at = q_at + scan1024((nq + ctt - 1) / ctt, part, &total_q);
         // past the capacity (a sequence longer than max_len): not staged
         const int64_t kvn = max((int64_t)0, min(nt, (int64_t)p.cap_kv - kv0));
-        if (kvn < nt) record_status(&g_tile_status, RF_ERR_INVALID_ARG);
+        if (kvn < nt) record_status(&g_tile_invalid, RF_ERR_INVALID_ARG);
         if (s < b.n_seq) {
             p.kv_base[s] = (int)min(kv0, (int64_t)p.cap_kv);
             p.kv_first[s] = (int)first;
@@ -207,7 +210,7 @@ __device__ __forceinline__ void stage_kv(const TileParams &p, int tile, int head
             const int page = page_of(p.a.b, c, lo, pos);
             const int per = c.page_size / kKvBlock;
             if (page >= 0) blk = ((int64_t)page * c.n_kv_heads + head) * per + (pos / kKvBlock) % per;
-            else record_status(&g_tile_status, RF_ERR_INVALID_ARG);
+            else record_status(&g_tile_invalid, RF_ERR_INVALID_ARG);
         }
         s_blk[tid] = blk;
         // a block that does not exist has unit 0 and exponent -inf: weight 0
@@ -1053,13 +1056,15 @@ rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *works
 
 rf_status read_and_clear_attn_tile_status()
 {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_tile_status, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
-    if (v != 0) {
-        const int zero = 0;
-        if (cudaMemcpyToSymbol(g_tile_status, &zero, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
-    }
-    return static_cast<rf_status>(v);
+    int v[2] = {0, 0};
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&v[0], g_tile_status, sizeof(int)) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&v[1], g_tile_invalid, sizeof(int)) != cudaSuccess)
+        return RF_ERR_CUDA;
+    if ((v[0] != 0 && cudaMemcpyToSymbol(g_tile_status, &zero, sizeof(int)) != cudaSuccess) ||
+        (v[1] != 0 && cudaMemcpyToSymbol(g_tile_invalid, &zero, sizeof(int)) != cudaSuccess))
+        return RF_ERR_CUDA;
+    return static_cast<rf_status>(v[0] != 0 ? v[0] : v[1]);
 }
 
 }  // namespace rf
