@@ -66,15 +66,24 @@ struct __align__(16) QTile {
     int64_t pos, pad;
 };
 
+// head_dim rounded up (DP) is walked in SUB pieces of DW elements, each an
+// operand image of its own: 64, 128 or two times 128.
+template <int DP> struct Dims {
+    static constexpr int SUB = DP > 128 ? 2 : 1, DW = DP / SUB;
+    static constexpr int NT = DP > 128 ? 1 : 2;   // query tiles per item (tensor memory holds S and O of each)
+    static constexpr int IMG = kTile * DW * 2;    // bytes of an image
+};
+
 struct TileParams {
     AttnParams a;
     int hpt, head_tiles, tqt;       // heads per tile, tiles per K/V head, tokens per 128-row tile
+    int nt;                         // query tiles per item: 2, or 1 for head_dim above 128
     int cap_q, cap_kv;              // capacities of the lists below
     TilePlan *plan;
     QTile *q_tiles;                 // [cap_q]
     int32_t *kv_base;               // [n_seq]: first position tile of a sequence
     int32_t *kv_first;              // [n_seq]: its position / 128 (window)
-    uint8_t *q_img;                 // [cap_q][kv head][head tile][2][NS][128 x DP] fp16
+    uint8_t *q_img;                 // [cap_q][kv head][head tile][tile][NS][128 x DP] fp16
     float *q_unit;                  // [cap_q][kv head][head tile][2][128]
     uint8_t *k_img, *v_img;         // [kv head][cap_kv][128 x DP] fp16
     float *units;                   // [kv head][cap_kv][12]: 2^ek, ev, 2^-ev of four blocks
@@ -122,7 +131,7 @@ __global__ void __launch_bounds__(1024) tile_plan_kernel(const __grid_constant__
     pdl_launch_dependents();
     pdl_wait();
     const rf_kv_batch &b = p.a.b;
-    const int ctt = 2 * p.tqt, tid = (int)threadIdx.x;
+    const int ctt = p.nt * p.tqt, tid = (int)threadIdx.x;
     int64_t kv_at = 0, q_at = 0;
     for (int s0 = 0; s0 < b.n_seq; s0 += 1024) {
         const int s = s0 + tid;
@@ -173,7 +182,7 @@ __global__ void __launch_bounds__(1024) tile_plan_kernel(const __grid_constant__
             q.t_lo = p.a.window > 0 ? max(0, (int)(max((int64_t)0, q.pos - p.a.window + 1) / kTile) - q.kvf) : 0;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int toks = min(p.tqt, q.end - (q.tok + x * p.tqt));
+                const int toks = x < p.nt ? min(p.tqt, q.end - (q.tok + x * p.tqt)) : 0;
                 const int64_t last = q.pos + x * p.tqt + toks - 1;
                 q.t_hi[x] = toks > 0 && last >= 0 ? (int)min((int64_t)s_kvn[lo], last / kTile + 1 - q.kvf) : 0;
             }
@@ -222,11 +231,13 @@ __device__ __forceinline__ void stage_kv(const TileParams &p, int tile, int head
         u[8 + tid] = blk < 0 ? 0.f : ev == 255u ? nan : scale_value(254u - ev);
     }
     __syncthreads();
+    constexpr int DW = Dims<DP>::DW;
     const int64_t img = ((int64_t)head * p.cap_kv + tile) * (kTile * DP * 2);
-    // K: 16-byte unit (row n, elements 8k..) at (n/8) * 16 DP + k * 128 + (n%8) * 16.
+    // K: 16-byte unit (row n, elements 8k..) of a piece at (n/8) * 16 DW + k * 128 + (n%8) * 16.
     uint8_t *ki = p.k_img + img;
     for (int w = tid; w < kTile * DP / 8; w += 256) {
-        const int n8 = w & 7, k = (w >> 3) % (DP / 8), n = (w >> 3) / (DP / 8) * 8 + n8;
+        const int piece = w / (kTile * DW / 8), v8 = w % (kTile * DW / 8);
+        const int n8 = v8 & 7, k = (v8 >> 3) % (DW / 8) + piece * (DW / 8), n = (v8 >> 3) / (DW / 8) * 8 + n8;
         uint4 o = make_uint4(0u, 0u, 0u, 0u);
         const int64_t blk = s_blk[n >> 5];
         if (blk >= 0 && 8 * k < D) {
@@ -267,16 +278,16 @@ __device__ __forceinline__ void stage_kv(const TileParams &p, int tile, int head
 template <typename T, int DP>
 __device__ __forceinline__ void stage_q(const TileParams &p, int qt, int head, int ht)
 {
-    constexpr int NS = sizeof(T) == 4 ? 2 : 1, LPR = DP / 8, RPW = 32 / LPR;
+    constexpr int NS = sizeof(T) == 4 ? 2 : 1, LPR = DP / 8, RPW = 32 / LPR, NT = Dims<DP>::NT, DW = Dims<DP>::DW;
     const AttnParams &a = p.a;
     const QTile q = p.q_tiles[qt];
     const int end = q.end, D = a.c.head_dim;
     const int h0 = head * a.group + ht * p.hpt, nh = min(p.hpt, a.group - ht * p.hpt);
     const int64_t at = ((int64_t)qt * a.c.n_kv_heads + head) * p.head_tiles + ht;
-    uint8_t *img = p.q_img + at * (2 * NS * kTile * DP * 2);
+    uint8_t *img = p.q_img + at * (NT * NS * kTile * DP * 2);
     float *unit = p.q_unit + at * (2 * kTile);
     const int lane = threadIdx.x & 31, k = lane % LPR;
-    for (int r = (int)(threadIdx.x >> 5) * RPW + lane / LPR; r < 2 * kTile; r += 8 * RPW) {
+    for (int r = (int)(threadIdx.x >> 5) * RPW + lane / LPR; r < NT * kTile; r += 8 * RPW) {
         const int x = r / kTile, n = r % kTile, ti = n / p.hpt, hi = n % p.hpt;
         const int tok = q.tok + x * p.tqt + ti;
         const bool ok = ti < p.tqt && hi < nh && tok < end;
@@ -307,7 +318,7 @@ __device__ __forceinline__ void stage_q(const TileParams &p, int qt, int head, i
             const float2 h = unpack_h2(ph[i]);
             pl[i] = pack_h2(u - h.x, v - h.y);
         }
-        uint8_t *dst = img + x * (NS * kTile * DP * 2) + (n / 8) * (16 * DP) + k * 128 + (n % 8) * 16;
+        uint8_t *dst = img + x * (NS * kTile * DP * 2) + k / (DW / 8) * Dims<DP>::IMG + (n / 8) * (16 * DW) + k % (DW / 8) * 128 + (n % 8) * 16;
         *reinterpret_cast<uint4 *>(dst) = hi4;
         if constexpr (NS == 2) *reinterpret_cast<uint4 *>(dst + kTile * DP * 2) = lo4;
     }
@@ -354,10 +365,12 @@ __global__ void __launch_bounds__(256) tile_stage_kernel(const __grid_constant__
 }
 
 // --------------------------------------------------------------------- tiles
-template <int DP, int NS> __host__ __device__ constexpr int ring_slots() { return (DP == 128 ? 7 : 14) - (DP == 128 ? 2 : 4) * NS; }
+// Slots of the ring, each an image of a piece of K or V; the queries take as
+// many bytes as 2 NS of them.
+template <int DP, int NS> __host__ __device__ constexpr int ring_slots() { return DP >= 128 ? 7 - 2 * NS : 14 - 4 * NS; }
 template <int DP, int NS> __host__ __device__ constexpr size_t tile_smem()
 {
-    return (size_t)kTile * DP * 2 * (2 * NS + ring_slots<DP, NS>());
+    return (size_t)Dims<DP>::IMG * (2 * NS + ring_slots<DP, NS>());
 }
 
 __host__ __device__ constexpr uint32_t tile_idesc(int n)
@@ -437,11 +450,12 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
 {
     constexpr int NS = sizeof(T) == 4 ? 2 : 1;
     constexpr int R = ring_slots<DP, NS>();
-    constexpr int SLOT = kTile * DP * 2;
+    constexpr int SLOT = Dims<DP>::IMG, SUB = Dims<DP>::SUB, DW = Dims<DP>::DW, NT = Dims<DP>::NT;
+    static_assert(NT * SUB == 2, "the queries of an item take 2 NS slots");
     constexpr int kItems = 4;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *q_s = smem;                          // [2][NS][SLOT]
-    uint8_t *ring = smem + 2 * NS * SLOT;         // [R][SLOT]: K0 V0 K1 V1 ...
+    uint8_t *q_s = smem;                          // [NT][NS][SUB][SLOT]
+    uint8_t *ring = smem + 2 * NS * SLOT;         // [R][SLOT]: the pieces of K0, V0, K1, V1, ...
     __shared__ uint64_t full[R], empty[R], qfull[1], qempty[1], sfull[2], pready[2], pvdone[2], drained[1];
     __shared__ uint64_t ifull[kItems], iempty[kItems];
     __shared__ Item items[kItems];
@@ -529,7 +543,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                 for (int x = 0; x < 2; ++x) w.n[x] = n[x] = max(0, min(q.t_hi[x], from + p.split_tiles) - from);
                 w.kv = q.kv0 + from;
                 w.base = (int64_t)(q.kvf + from) * kTile;
-                const int64_t q_at = w.q_at, img = ((int64_t)w.head * p.cap_kv + w.kv) * SLOT;
+                const int64_t q_at = w.q_at, img = ((int64_t)w.head * p.cap_kv + w.kv) * (SUB * SLOT);
                 mbar_arrive(&ifull[slot]);
                 const int nmax = max(n[0], n[1]);
                 if (nmax == 0) continue;
@@ -539,11 +553,11 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                 const uint8_t *src = p.q_img + q_at * (2 * NS * SLOT);
 #pragma unroll
                 for (int i = 0; i < 2 * NS; ++i) bulk_g2s(q_s + i * SLOT, src + i * SLOT, SLOT, qfull);
-                for (int i = 0; i < 2 * nmax; ++i) {
-                    const int s = ikv % R;
+                for (int i = 0; i < 2 * SUB * nmax; ++i) {
+                    const int s = ikv % R, kv = i % (2 * SUB), sub = kv % SUB;
                     if (!(ok = wait(&empty[s], ((ikv / R) & 1) ^ 1))) break;
                     mbar_arrive_expect_tx(&full[s], SLOT);
-                    bulk_g2s(ring + s * SLOT, (i & 1 ? p.v_img : p.k_img) + img + (int64_t)(i >> 1) * SLOT, SLOT, &full[s]);
+                    bulk_g2s(ring + s * SLOT, (kv >= SUB ? p.v_img : p.k_img) + img + ((int64_t)(i / (2 * SUB)) * SUB + sub) * SLOT, SLOT, &full[s]);
                     ++ikv;
                 }
             }
@@ -558,31 +572,36 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
         // 256 + DP x.  All in one thread's order, which is what lets a tile's
         // next scores follow its values over the same columns.  The warp runs
         // as one; `leader` is the thread that issues.
-        const uint64_t qd = smem_desc(smem_addr(q_s), 16 * DP), kd = smem_desc(smem_addr(ring), 16 * DP);
+        const uint64_t qd = smem_desc(smem_addr(q_s), 16 * DW), kd = smem_desc(smem_addr(ring), 16 * DW);
         const uint64_t vd = smem_desc(smem_addr(ring), 2048);
         const bool leader = elect_one();
         bool ok = true, any = false;
         uint32_t iq = 0, steps[2] = {0, 0};
-        int ks = 0;                                // ring slot of the next K tile, and its phase
-        uint32_t kph = 0;
+        int rs = 0;                                // ring slot of the next piece, and its phase
+        uint32_t rph = 0;
         auto waits = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
         auto commit = [&](uint64_t *bar) {
             if (leader) tc_commit(bar);
         };
-        auto scores = [&](int x, int slot) {
+        auto next = [&] {
+            if (++rs == R) rs = 0, rph ^= 1u;
+        };
+        // Scores of tile x from piece `sub` of K in `slot`; the last piece
+        // hands S over.
+        auto scores = [&](int x, int slot, int sub) {
             tc_fence_after();
-            const uint64_t q0 = qd + (uint64_t)((x * NS * SLOT) >> 4), k0 = kd + (uint64_t)((slot * SLOT) >> 4);
+            const uint64_t q0 = qd + (uint64_t)(((x * NS * SUB + sub) * SLOT) >> 4), k0 = kd + (uint64_t)((slot * SLOT) >> 4);
             if (leader) {
 #pragma unroll 1
                 for (int t = NS - 1; t >= 0; --t)
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        tc_mma(tmem + 128 * x, q0 + ((t * SLOT + k * 256) >> 4), k0 + 16 * k, tile_idesc(kTile),
-                               !(t == NS - 1 && k == 0));
-                tc_commit(&sfull[x]);
+                    for (int k = 0; k < DW / 16; ++k)
+                        tc_mma(tmem + 128 * x, q0 + ((t * SUB * SLOT + k * 256) >> 4), k0 + 16 * k, tile_idesc(kTile),
+                               !(sub == 0 && t == NS - 1 && k == 0));
+                if (sub == SUB - 1) tc_commit(&sfull[x]);
             }
         };
-        auto values = [&](int x, int slot, bool add) {
+        auto values = [&](int x, int slot, int sub, bool add) {
             tc_fence_after();
             const uint64_t v0 = vd + (uint64_t)((slot * SLOT) >> 4);
             if (leader) {
@@ -590,9 +609,9 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
                 for (int t = NS - 1; t >= 0; --t)
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_ts(tmem + 256 + DP * x, tmem + 128 * x + 32 * (k >> 1) + 16 * t + 8 * (k & 1), v0 + 16 * k,
-                                  tile_idesc(DP), add || !(t == NS - 1 && k == 0));
-                tc_commit(&pvdone[x]);
+                        tc_mma_ts(tmem + 256 + DP * x + DW * sub, tmem + 128 * x + 32 * (k >> 1) + 16 * t + 8 * (k & 1), v0 + 16 * k,
+                                  tile_idesc(DW), add || !(t == NS - 1 && k == 0));
+                if (sub == SUB - 1) tc_commit(&pvdone[x]);
             }
         };
         for (uint32_t it = 0; ok; ++it) {
@@ -607,38 +626,57 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             if (nmax == 0) continue;
             if (!waits(qfull, iq & 1)) break;
             ++iq;
-            if (!waits(&full[ks], kph)) break;
-            any = true;
-            if (n0 > 0) scores(0, ks);
-            if (n1 > 0) scores(1, ks);
-            commit(&empty[ks]);
+#pragma unroll
+            for (int sub = 0; sub < SUB; ++sub) {
+                if (!(ok = ok && waits(&full[rs], rph))) break;
+                any = true;
+                if (n0 > 0) scores(0, rs, sub);
+                if (n1 > 0) scores(1, rs, sub);
+                commit(&empty[rs]);
+                next();
+            }
+            if (!ok) break;
             if (nmax == 1) commit(qempty);
             for (int j = 0; ok && j < nmax; ++j) {
-                const int vs = ks + 1 == R ? 0 : ks + 1, ns = vs + 1 == R ? 0 : vs + 1;
-                const uint32_t vph = vs ? kph : kph ^ 1u, nph = ns ? vph : vph ^ 1u;
-                const bool more = j + 1 < nmax;
-                if (!(ok = waits(&full[vs], vph))) break;
-                if (more && !(ok = waits(&full[ns], nph))) break;
-                const bool add = NS == 2 ? j % kFlush != 0 : j > 0;
-                if (j < n0) {
+                const bool more = j + 1 < nmax, add = NS == 2 ? j % kFlush != 0 : j > 0;
+                if constexpr (SUB == 1) {
+                    // Two tiles in turn: each one's values, then its next scores.
+                    const int vs = rs;
+                    if (!(ok = waits(&full[vs], rph))) break;
+                    next();
+                    const int ns = rs;
+                    if (more && !(ok = waits(&full[ns], rph))) break;
+                    if (j < n0) {
+                        if (!(ok = waits(&pready[0], steps[0] & 1))) break;
+                        ++steps[0];
+                        values(0, vs, 0, add);
+                        if (j + 1 < n0) scores(0, ns, 0);
+                    }
+                    if (j < n1) {
+                        if (!(ok = waits(&pready[1], steps[1] & 1))) break;
+                        ++steps[1];
+                        values(1, vs, 0, add);
+                    }
+                    commit(&empty[vs]);
+                    if (j + 1 < n1) scores(1, ns, 0);
+                    if (more) {
+                        commit(&empty[ns]);
+                        next();
+                    }
+                } else {
                     if (!(ok = waits(&pready[0], steps[0] & 1))) break;
                     ++steps[0];
-                    values(0, vs, add);
-                    if (j + 1 < n0) scores(0, ns);
+#pragma unroll
+                    for (int i = 0; i < 2 * SUB; ++i) {
+                        if (i >= SUB && !more) break;
+                        if (!(ok = waits(&full[rs], rph))) break;
+                        if (i < SUB) values(0, rs, i, add);
+                        else scores(0, rs, i - SUB);
+                        commit(&empty[rs]);
+                        next();
+                    }
                 }
-                if (j < n1) {
-                    if (!(ok = waits(&pready[1], steps[1] & 1))) break;
-                    ++steps[1];
-                    values(1, vs, add);
-                }
-                commit(&empty[vs]);
-                if (j + 1 < n1) scores(1, ns);
-                if (more) {
-                    commit(&empty[ns]);
-                    if (j + 2 == nmax) commit(qempty);
-                }
-                ks = ns;
-                kph = nph;
+                if (ok && j + 2 == nmax) commit(qempty);
             }
         }
         // Every issued product completes before tensor memory is freed.
@@ -665,7 +703,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
             const Item &w = items[slot];           // given back after the output
             if (w.stop) break;
             const int nx = w.n[x];
-            const bool row_ok = ti < p.tqt && hi < min(p.hpt, a.group - w.ht * p.hpt) && w.tok + x * p.tqt + ti < w.end;
+            const bool row_ok = x < NT && ti < p.tqt && hi < min(p.hpt, a.group - w.ht * p.hpt) && w.tok + x * p.tqt + ti < w.end;
             // The visible positions [first, top] of the row, counted from the
             // first tile's first.
             const int top = row_ok ? (int)(w.pos - w.base) + x * p.tqt + ti : INT_MIN / 2;
@@ -908,13 +946,14 @@ void tile_shape(const AttnParams &p, TileParams *t)
     t->hpt = std::min(p.group, kTile);
     t->head_tiles = (p.group + t->hpt - 1) / t->hpt;
     t->tqt = kTile / t->hpt;
+    t->nt = p.c.head_dim > 128 ? 1 : 2;
 }
 
 Layout layout(const AttnParams &p, const TileParams &t, int dtype, int64_t max_len)
 {
     Layout L = {};
-    const int ns = dtype == RF_F32 ? 2 : 1, dp = p.c.head_dim > 64 ? 128 : 64;
-    const int64_t ctt = 2 * t.tqt;
+    const int ns = dtype == RF_F32 ? 2 : 1, dp = p.c.head_dim > 128 ? 256 : p.c.head_dim > 64 ? 128 : 64;
+    const int64_t ctt = t.nt * t.tqt;
     L.cap_q = p.b.n_tok / ctt + std::min<int64_t>(p.b.n_seq, p.b.n_tok);
     // No sequence's position tiles exceed max_len's; with a window, all of
     // them together do not exceed the windows' and the new tokens'.
@@ -951,7 +990,7 @@ Layout layout(const AttnParams &p, const TileParams &t, int dtype, int64_t max_l
     L.q_tiles = take(L.cap_q * sizeof(QTile));
     L.kv_base = take(p.b.n_seq * sizeof(int32_t));
     L.kv_first = take(p.b.n_seq * sizeof(int32_t));
-    L.q_img = take(L.cap_q * kvh * t.head_tiles * 2 * ns * slot);
+    L.q_img = take(L.cap_q * kvh * t.head_tiles * t.nt * ns * slot);
     L.q_unit = take(L.cap_q * kvh * t.head_tiles * 2 * kTile * sizeof(float));
     L.k_img = take(L.cap_kv * kvh * slot);
     L.v_img = take(L.cap_kv * kvh * slot);
@@ -1007,7 +1046,6 @@ bool attn_tile_takes(const AttnParams &p, int64_t max_len)
     // 21 / 32; 16 sequences against 8,000: 64 rows 235 / 247, 128 rows 397 /
     // 250 (fp32: 324 / 326, 572 / 342).  Tiles pay from about 96 rows, once
     // the work outweighs two more launches and the staging.
-    if (p.c.head_dim > 128) return false;
     const int64_t per_seq = (p.b.n_tok + p.b.n_seq - 1) / p.b.n_seq, rows = per_seq * p.group;
     const int64_t seen = p.window > 0 ? std::min(max_len, p.window + per_seq) : max_len;
     return rows >= 96 && (double)rows * seen * p.b.n_seq >= 5e5;
@@ -1045,10 +1083,11 @@ rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *works
     t.qk_abs = p.qk_scale < 0.f ? -p.qk_scale : p.qk_scale;
     t.negate = p.qk_scale < 0.f;
     t.limit = kWaitLimitNs;
-    const bool small = p.c.head_dim <= 64;
+    const int D = p.c.head_dim;
     rf_status st = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
-        return small ? launch_tiles<T, 64>(t, s, chain) : launch_tiles<T, 128>(t, s, chain);
+        if (D > 128) return launch_tiles<T, 256>(t, s, chain);
+        return D > 64 ? launch_tiles<T, 128>(t, s, chain) : launch_tiles<T, 64>(t, s, chain);
     });
     if (st != RF_OK) return st;
     return p.splits > 1 ? launch_attn_join(p, dtype, s) : RF_OK;

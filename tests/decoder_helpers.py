@@ -98,4 +98,4 @@ def by_tiles(su, heads, window=0, max_len=0):
     per = -(-su.n_tok // len(su.past))
     rows = per * heads // su.ref.heads
     seen = max_len or su.table.shape[1] * su.ref.page
-    return su.ref.dim <= 128 and rows >= 96 and rows * min(seen, window + per if window else seen) * len(su.past) >= 5e5
+    return rows >= 96 and rows * min(seen, window + per if window else seen) * len(su.past) >= 5e5

@@ -394,7 +394,8 @@ def test_many_pages_pass_32_bit_offsets():
 @pytest.mark.parametrize("dim,heads,kv,page,past,new", [
     (128, 4, 1, 64, [0], [400]), (64, 8, 1, 32, [0, 77, 3], [129, 200, 64]), (128, 2, 2, 128, [900], [600]),
     (80, 5, 1, 256, [130, 0], [190, 331]), (16, 3, 1, 32, [0], [430]), (112, 7, 1, 64, [440], [175]),
-    (64, 130, 1, 64, [1400], [3]), (128, 20, 1, 32, [0, 900], [40, 7]), (64, 64, 2, 64, [0, 10, 700, 0], [0, 5, 2, 60])])
+    (64, 130, 1, 64, [1400], [3]), (128, 20, 1, 32, [0, 900], [40, 7]), (64, 64, 2, 64, [0, 10, 700, 0], [0, 5, 2, 60]),
+    (256, 4, 1, 64, [0, 30], [290, 270]), (144, 6, 2, 32, [100], [430]), (240, 5, 1, 128, [900, 0], [40, 150])])
 def test_attention_long_chunks(dtype, dim, heads, kv, page, past, new):
     rng = np.random.default_rng([dim, heads, sum(new)])
     su = Setup(rng, past, new, kv, dim, page, pad_tokens=3)
@@ -408,7 +409,7 @@ def test_attention_long_chunks(dtype, dim, heads, kv, page, past, new):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dim", [64, 128, 256])
 def test_attention_long_chunks_split_and_joined(dtype, dim):
     rng = np.random.default_rng(dim)
     su = Setup(rng, [4000], [40], 1, dim, 64, pad_tokens=1)
