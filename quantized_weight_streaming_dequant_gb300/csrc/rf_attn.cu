@@ -740,6 +740,7 @@ rf_status rf_attention(const rf_kv_cache *cache, const rf_kv_batch *batch, int d
     p.qk_scale = (float)((double)scale * 1.4426950408889634);
     p.q_vec = aligned_to(q, 4 * b) && q_ld_tok % 4 == 0 && q_ld_head % 4 == 0;
     p.o_vec = aligned_to(out, 4 * b) && out_ld_tok % 4 == 0 && out_ld_head % 4 == 0;
+    p.q_vec8 = aligned_to(q, 8 * b) && q_ld_tok % 8 == 0 && q_ld_head % 8 == 0;
     p.o_sector = aligned_to(out, 32) && (out_ld_tok * (int64_t)b) % 32 == 0 && (out_ld_head * (int64_t)b) % 32 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chain = (flags & RF_CHAIN) != 0;

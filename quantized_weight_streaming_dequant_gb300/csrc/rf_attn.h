@@ -18,6 +18,7 @@ struct AttnParams {
     float qk_scale;          // scale * log2(e): scores are powers of two
     int n_heads, group;      // query heads; query heads per K/V head
     bool q_vec, o_vec;       // aligned for four elements at a time
+    bool q_vec8;             // queries aligned for eight
     bool o_sector;           // every 32 bytes of an output row are aligned to them
     int splits;              // parts of a row's positions, joined by a second launch
     int split_blocks;        // 32-token blocks per part

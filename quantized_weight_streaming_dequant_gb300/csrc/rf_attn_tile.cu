@@ -235,17 +235,22 @@ __device__ __forceinline__ void stage_kv(const TileParams &p, int tile, int head
     const int64_t img = ((int64_t)head * p.cap_kv + tile) * (kTile * DP * 2);
     // K: 16-byte unit (row n, elements 8k..) of a piece at (n/8) * 16 DW + k * 128 + (n%8) * 16.
     uint8_t *ki = p.k_img + img;
-    for (int w = tid; w < kTile * DP / 8; w += 256) {
-        const int piece = w / (kTile * DW / 8), v8 = w % (kTile * DW / 8);
-        const int n8 = v8 & 7, k = (v8 >> 3) % (DW / 8) + piece * (DW / 8), n = (v8 >> 3) / (DW / 8) * 8 + n8;
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    // A thread turns 16 elements (the load-store pipe, not memory, bounds this
+    // kernel: wide reads, and stores that fill whole lines).
+    for (int w = tid; w < kTile * DP / 16; w += 256) {
+        const int piece = w / (kTile * DW / 16), v16 = w % (kTile * DW / 16);
+        const int n = (v16 >> 3) / (DW / 16) * 8 + (v16 & 7), k = (v16 >> 3) % (DW / 16);   // elements 16 k.. of the piece
+        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
         const int64_t blk = s_blk[n >> 5];
-        if (blk >= 0 && 8 * k < D) {
-            uint2 v = *reinterpret_cast<const uint2 *>(c.k + (blk * kKvBlock + (n & 31)) * D + 8 * k);
-            v.x ^= 0x80808080u, v.y ^= 0x80808080u;
-            o = make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y));
+        if (blk >= 0 && piece * DW + 16 * k < D) {
+            uint4 v = *reinterpret_cast<const uint4 *>(c.k + (blk * kKvBlock + (n & 31)) * D + piece * DW + 16 * k);
+            v.x ^= 0x80808080u, v.y ^= 0x80808080u, v.z ^= 0x80808080u, v.w ^= 0x80808080u;
+            lo = make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y));
+            hi = make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w));
         }
-        *reinterpret_cast<uint4 *>(ki + (int64_t)w * 16) = o;
+        uint8_t *dst = ki + piece * Dims<DP>::IMG + (n / 8) * (16 * DW) + k * 256 + (n % 8) * 16;
+        *reinterpret_cast<uint4 *>(dst) = lo;
+        *reinterpret_cast<uint4 *>(dst + 128) = hi;
     }
     // V transposed: unit (row d, positions 8t..) at (d/8) * 2048 + t * 128 + (d%8) * 16;
     // a thread turns 8 positions x 4 elements.
@@ -294,11 +299,7 @@ __device__ __forceinline__ void stage_q(const TileParams &p, int qt, int head, i
         float f[8] = {};
         if (ok && 8 * k < D) {
             const T *src = static_cast<const T *>(a.q) + (int64_t)tok * a.q_lt + (int64_t)(h0 + hi) * a.q_lh + 8 * k;
-            float u[4], v[4];
-            load4<T>(src, a.q_vec, u);
-            load4<T>(src + 4, a.q_vec, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = u[i], f[4 + i] = v[i];
+            load8<T>(src, a.q_vec8, a.q_vec, f);
         }
         float amax = 0.f;
 #pragma unroll

@@ -54,6 +54,30 @@ __device__ __forceinline__ void load4(const T *p, bool vec, float (&f)[4])
         for (int i = 0; i < 4; ++i) f[i] = to_f32<T>(p[i]);
     }
 }
+// Eight; vec8: the address is aligned to all of them (16 or 32 bytes).
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec8, bool vec4, float (&f)[8])
+{
+    if (vec8) {
+        if constexpr (sizeof(T) == 4) {
+            asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                         : "l"(p)
+                         : "memory");
+        } else {
+            union { uint4 u; T t[8]; } a;
+            a.u = *reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = to_f32<T>(a.t[i]);
+        }
+    } else {
+        float u[4], v[4];
+        load4<T>(p, vec4, u);
+        load4<T>(p + 4, vec4, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = u[i], f[4 + i] = v[i];
+    }
+}
 template <typename T>
 __device__ __forceinline__ void store4(T *p, bool vec, const float (&f)[4])
 {
