@@ -28,6 +28,7 @@ namespace {
 __device__ int g_kv_status = 0;   // positions or pages that do not exist (read by rf_device_status)
 
 constexpr int kAppendThreads = 256;
+constexpr int kReadTokens = 8;    // tokens per CTA of the read kernel, at most
 constexpr int kQHeads = 4;        // query heads per CTA of the rotation part
 
 struct AppendParams {
@@ -243,13 +244,15 @@ __global__ void __launch_bounds__(kAppendThreads, UPT <= 2 ? 6 : 3) append_kerne
     }
 }
 
-// Values at the batch's positions; a CTA per p.chunk tokens, a thread per 16
-// codes.
+// Values at the batch's positions; a CTA per p.chunk tokens (at most eight).
+// A thread turns eight codes of a head into 32 bytes, neighbouring threads
+// neighbouring ones, for all tokens of the chunk at once.
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ rf_kv_cache c,
                                                    const __grid_constant__ rf_kv_batch b, int chunk,
-                                                   float *__restrict__ k_out, float *__restrict__ v_out)
+                                                   float *__restrict__ k_out, float *__restrict__ v_out,
+                                                   bool sectors)
 {
-    __shared__ int s_page[32], s_off[32];
+    __shared__ int s_page[kReadTokens], s_off[kReadTokens];
     const int t_lo = (int)blockIdx.x * chunk, t_n = min(chunk, b.n_tok - t_lo);
     pdl_launch_dependents();
     pdl_wait();
@@ -267,38 +270,39 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ rf_kv
         s_off[threadIdx.x] = off;
     }
     __syncthreads();
-    // Four runs of 16 codes at a time, so that their reads overlap.
-    const int cpr = c.head_dim / 16, per = c.n_kv_heads * cpr, total = 2 * t_n * per;
-    for (int w0 = (int)threadIdx.x; w0 < total; w0 += 4 * 256) {
-        uint4 code[4];
-        float unit[4];
-        float *out[4];
+    const int cpr = c.head_dim / 8, per = c.n_kv_heads * cpr;    // runs of eight codes per token
+    for (int u = (int)threadIdx.x; u < 2 * per; u += 256) {
+        const int side = u >= per, w = u - side * per, h = w / cpr, i = w - h * cpr;
+        const int8_t *codes = (side ? c.v : c.k) + 8 * i;
+        const uint8_t *scales = side ? c.v_scale : c.k_scale;
+        float *out = (side ? v_out : k_out) + (int64_t)t_lo * per * 8 + 8 * w;
+        uint2 code[kReadTokens];
+        float unit[kReadTokens];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int w = w0 + 256 * r;
-            code[r] = make_uint4(0u, 0u, 0u, 0u);
-            unit[r] = 0.f;
-            out[r] = nullptr;
-            if (w < total) {
-                const int side = w >= t_n * per, u = w - side * t_n * per;
-                const int j = u / per, h = (u - j * per) / cpr, i = (u - j * per) % cpr;
-                out[r] = (side ? v_out : k_out) + ((int64_t)(t_lo + j) * c.n_kv_heads + h) * c.head_dim + 16 * i;
-                if (s_page[j] >= 0) {
-                    const int64_t ph = (int64_t)s_page[j] * c.n_kv_heads + h;
-                    code[r] = *reinterpret_cast<const uint4 *>((side ? c.v : c.k) + (ph * c.page_size + s_off[j]) * c.head_dim + 16 * i);
-                    unit[r] = scale_value((side ? c.v_scale : c.k_scale)[ph * (c.page_size / kKvBlock) + s_off[j] / kKvBlock]);
-                }
+        for (int j = 0; j < kReadTokens; ++j) {
+            code[j] = make_uint2(0u, 0u);
+            unit[j] = 0.f;
+            if (j < t_n && s_page[j] >= 0) {
+                const int64_t ph = (int64_t)s_page[j] * c.n_kv_heads + h;
+                code[j] = *reinterpret_cast<const uint2 *>(codes + (ph * c.page_size + s_off[j]) * c.head_dim);
+                unit[j] = scale_value(scales[ph * (c.page_size / kKvBlock) + s_off[j] / kKvBlock]);
             }
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (!out[r]) continue;
-            const uint32_t ws[4] = {code[r].x, code[r].y, code[r].z, code[r].w};
+        for (int j = 0; j < kReadTokens; ++j) {
+            if (j >= t_n) break;
+            uint32_t v[8];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-                reinterpret_cast<float4 *>(out[r])[m] =
-                    make_float4((float)(int8_t)ws[m] * unit[r], (float)(int8_t)(ws[m] >> 8) * unit[r],
-                                (float)(int8_t)(ws[m] >> 16) * unit[r], (float)(int8_t)(ws[m] >> 24) * unit[r]);
+            for (int m = 0; m < 8; ++m)
+                v[m] = __float_as_uint((float)(int8_t)((m < 4 ? code[j].x : code[j].y) >> (8 * (m & 3))) * unit[j]);
+            float *dst = out + (int64_t)j * per * 8;
+            if (sectors) {
+                store_sector(dst, v);
+            } else {
+#pragma unroll
+                for (int m = 0; m < 8; m += 4)
+                    *reinterpret_cast<uint4 *>(dst + m) = make_uint4(v[m], v[m + 1], v[m + 2], v[m + 3]);
+            }
         }
     }
 }
@@ -405,10 +409,10 @@ rf_status rf_kv_read(const rf_kv_cache *cache, const rf_kv_batch *batch, float *
     if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16)) return RF_ERR_MISALIGNED;
     if (batch->n_tok == 0) return RF_OK;
     // Few tokens: one per CTA; many: eight share the lookup.
-    const int chunk = batch->n_tok > 8 * num_sms() ? 8 : 1;
+    const int chunk = batch->n_tok > 8 * num_sms() ? kReadTokens : 1;
     return launch_kernel(read_kernel, dim3((unsigned)((batch->n_tok + chunk - 1) / chunk)), dim3(256), 0,
                          static_cast<cudaStream_t>(stream), (flags & RF_CHAIN) != 0, *cache, *batch, chunk,
-                         k_out, v_out);
+                         k_out, v_out, aligned_to(k_out, 32) && aligned_to(v_out, 32));
 }
 
 }  // extern "C"
