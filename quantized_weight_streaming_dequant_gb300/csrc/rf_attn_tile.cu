@@ -10,8 +10,10 @@
 //          scaled by a power of two per row, and the blocks' units.  It moves
 //          3 bytes per code (and 2 to 4 per query element), which 128-row
 //          tiles read back many times.
-//   tiles  a CTA owns two tiles of 128 query rows (tokens x heads of one K/V
-//          head) and walks the visible positions, 128 at a time:
+//   tiles  persistent CTAs draw items: two tiles of 128 query rows (tokens x
+//          heads of one K/V head; one tile above head_dim 128, whose S and O
+//          fill tensor memory) and part of their positions.  A CTA walks the
+//          visible ones, 128 at a time:
 //              S = Q K^T (tcgen05.mma from shared memory, fp32 in tensor
 //              memory) -> weights by one thread per row (no shuffles) -> P in
 //              fp16 over S's own columns -> O += P V (P from tensor memory).
@@ -23,6 +25,21 @@
 // Bound: the tensor pipe for long rows: 4 * 128 * 128 * head_dim flops per
 // step and tile (twice that for fp32, whose queries and weights are two fp16
 // terms), against 16,384 exponentials.
+// Measured (plan / stage / tiles / join, us): 8192-token bf16 prompt, 32 / 8
+// heads of 128: 5 / 36 / 386 / - (1.42 PFLOP/s in the tiles, 0.73 of the
+// measured bf16 rate); fp32, 511 tokens against 32,768 positions: 5 / 48 /
+// 361 / 21 (1.51 PFLOP/s with both terms); fp16, ragged prompts of 8193 tokens
+// in all under a window of 128, 64 / 8 heads of 64: 5 / 31 / 85 / -.  The same
+// tiles without the softmax's work take 322, 308 and 46 us, so the products
+// bound the long ones: a step's operands (Q and K for S, V for O, and the
+// copies) are 256 KB of shared-memory traffic for 2,048 tensor cycles, which
+// is all that 128 bytes a cycle allow (a pair of CTAs that share B would halve
+// half of it).  Tried and not kept: two threads per row (16 softmax warps,
+// 462 us for the prompt's call against 454), handing over the first half of P
+// early (465 against 466), products issued by one lane from per-thread
+// registers (576 against 454; fp32 chunk 1,343 against 620: operands in
+// uniform registers let one warp keep the pipe busy), maxima applied at once
+// beyond 2^1.5 instead of 2^7 for 16-bit types (486 against 466).
 //
 // Every wait is bounded; after a failure every role stops, copies and
 // products already issued are waited for, and tensor memory is freed.
