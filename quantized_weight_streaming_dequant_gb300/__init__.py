@@ -536,15 +536,21 @@ def moe_workspace_views(workspace, top_k: int, n_ff: int):
     return idx, w, h
 
 
-_DTYPES = _empty = None
+_DTYPES = _empty = _empty_like = _F32_TYPE = None
+
+
+def _look_up() -> None:
+    """torch's names, once: an import statement in a function costs each call 0.5 us."""
+    global _DTYPES, _empty, _empty_like, _F32_TYPE
+    import torch
+    _empty, _empty_like, _F32_TYPE = torch.empty, torch.empty_like, torch.float32
+    _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _dtype(t) -> int:
     """The activation type of a tensor."""
-    global _DTYPES, _empty
-    if _DTYPES is None:   # torch is looked up once: an import statement costs each call 0.5 us
-        import torch
-        _DTYPES, _empty = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}, torch.empty
+    if _DTYPES is None:
+        _look_up()
     d = _DTYPES.get(t.dtype)   # F32 is 0
     if d is None:
         raise ValueError(f"activations are float32, float16 or bfloat16, not {t.dtype}")
@@ -586,13 +592,14 @@ def norm_residual(residual, x=None, *, post_weight=None, gate=None, scale: float
     dt = _dtype(like)
     px, ldx = _rows(x, n_tok, n, dt, "x")
     pr, ldr = _rows(residual, n_tok, n, dt, "residual")
+    dense = like.is_contiguous()
     if residual_out is None:
-        residual_out = _empty((n_tok, n), dtype=like.dtype, device=like.device)
+        residual_out = _empty_like(like) if dense else _empty((n_tok, n), dtype=like.dtype, device=like.device)
         po, ldo = residual_out.data_ptr(), n
     else:
         po, ldo = _rows(residual_out, n_tok, n, dt, "residual_out")
     if y is None and norm:
-        y = _empty((n_tok, n), dtype=like.dtype, device=like.device)
+        y = _empty_like(like) if dense else _empty((n_tok, n), dtype=like.dtype, device=like.device)
         py, ldy = y.data_ptr(), n
     else:
         py, ldy = _rows(y, n_tok, n, dt, "y")
@@ -612,6 +619,7 @@ class KVCache:
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
+        _look_up()
         if k.dim() != 4 or v.shape != k.shape or k.dtype != torch.int8 or v.dtype != torch.int8:
             raise ValueError("k and v must be int8, (n_pages, n_kv_heads, page_size, head_dim)")
         n_pages, n_kv, page, dim = k.shape
@@ -620,6 +628,7 @@ class KVCache:
                 raise ValueError(f"{what} must be uint8, (n_pages, n_kv_heads, page_size / {KV_BLOCK})")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, n_kv, page, dim
+        self.device = k.device
         self.struct = KVCacheStruct(_dev_ptr(k, "k"), _dev_ptr(v, "v"), _dev_ptr(k_scale, "k_scale"),
                                     _dev_ptr(v_scale, "v_scale"), n_pages, page, n_kv, dim, 0)
         self.ref = ctypes.addressof(self.struct)
@@ -684,7 +693,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None
     if q is not None:
         pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
         if q_out is None:
-            q_out = _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+            q_out = _empty_like(q) if q.is_contiguous() else _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
             po, olt, olh = q_out.data_ptr(), nh * dim, dim
         else:
             po, olt, olh, oh = _heads(q_out, n_tok, dim, dt, "q_out")
@@ -706,16 +715,13 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None
 def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None, flags: int = 0):
     """rf_kv_read: the cache's values at the batch's positions, two float32
     tensors (n_tok, n_kv_heads, head_dim)."""
-    import torch
     shape = (batch.n_tok, cache.n_kv_heads, cache.head_dim)
-    n, out = shape[0] * shape[1] * shape[2], []
-    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.float32, device=cache.k.device)
-            out += [t, t.data_ptr()]
-        else:
-            out += [t, _f32_ptr(t, n, what)]
-    k_out, pk, v_out, pv = out
+    n = shape[0] * shape[1] * shape[2]
+    if k_out is None:
+        k_out = _empty(shape, dtype=_F32_TYPE, device=cache.device)
+    if v_out is None:
+        v_out = _empty(shape, dtype=_F32_TYPE, device=cache.device)
+    pk, pv = _f32_ptr(k_out, n, "k_out"), _f32_ptr(v_out, n, "v_out")
     _check(lib().rf_kv_read(cache.ref, batch.ref, pk, pv, flags, _stream(stream)), "rf_kv_read")
     return k_out, v_out
 
@@ -735,7 +741,7 @@ def attention(cache: KVCache, batch: KVBatch, q, out=None, scale: float | None =
     n_tok, dim, dt = batch.n_tok, cache.head_dim, _dtype(q)
     pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
     if out is None:
-        out = _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+        out = _empty_like(q) if q.is_contiguous() else _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
         po, olt, olh = out.data_ptr(), nh * dim, dim
     else:
         po, olt, olh, oh = _heads(out, n_tok, dim, dt, "out")
