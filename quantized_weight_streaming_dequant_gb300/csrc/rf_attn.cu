@@ -26,14 +26,15 @@
 // Measured: fp32, one token against 131,072 positions of 8 heads of 128 (four
 // query heads each): 48 us (5.6 TB/s, 0.82 of the measured copy rate) and 7
 // for the join; bf16, 48 ragged sequences of up to 16,001 positions, 8 heads
-// of 64 (eight each): 80 us (4.9 TB/s) and 8.  Both issue 2.0 to 2.6
+// of 64 (eight each): 78 us (5.1 TB/s) and 8.  Both issue 2.0 to 2.6
 // instructions a cycle and SM from 8 to 16 warps: turning codes into fp16
 // (five instructions for four codes, and two more to pair V's) is what keeps
 // them from the memory's pace.  Tried and not kept: equal shares of all blocks
 // over one wave of CTAs (62 and 104 us against 54 and 88 for the calls: SMs
 // differ in speed, and the shares' state costs registers), three CTAs an SM
 // for head_dim 128 (66 against 54: spills), two and six waves of parts
-// instead of four (106 and 101 against 88).
+// instead of four (106 and 95 against 86), keys as fp16 subnormals, which
+// saves them the subtraction (86 against 87 before empty parts left early).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -147,6 +148,14 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : DP == 128 ? 2 : N
         const int to = part == p.splits - 1 ? b_hi : (int)min((int64_t)b_hi, from + p.split_blocks);
         b_lo = (int)min(from, (int64_t)b_hi);
         b_hi = to;
+    }
+
+    // A part past the end of its sequence sees nothing.
+    if (p.splits > 1 && b_hi <= b_lo) {
+        const int row = (int)threadIdx.x, ti = row / tl.hpt, hi = row % tl.hpt;
+        if (row < ROWS && ti < n_here && hi < nh)
+            p.part_ml[((int64_t)(t + ti) * p.n_heads + h0 + hi) * p.splits + part] = make_float2(-INFINITY, 0.f);
+        return;
     }
 
     // Ring of this warp: stage s holds K then V of one block.  The first
