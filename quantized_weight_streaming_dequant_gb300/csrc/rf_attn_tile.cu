@@ -96,6 +96,7 @@ struct TileParams {
     int hpt, head_tiles, tqt;       // heads per tile, tiles per K/V head, tokens per 128-row tile
     int nt;                         // query tiles per item: 2, or 1 for head_dim above 128
     int cap_q, cap_kv;              // capacities of the lists below
+    int cap_seq;                    // position tiles of one sequence, at most: its share of cap_kv
     TilePlan *plan;
     QTile *q_tiles;                 // [cap_q]
     int32_t *kv_base;               // [n_seq]: first position tile of a sequence
@@ -162,14 +163,18 @@ __global__ void __launch_bounds__(1024) tile_plan_kernel(const __grid_constant__
             if (nq > 0 && last >= 0) {
                 const int64_t lo = p.a.window > 0 ? max((int64_t)0, past - p.a.window + 1) : 0;
                 first = lo / kTile;
-                nt = max((int64_t)0, min(last / kTile + 1, (int64_t)b.table_width * p.a.c.page_size / kTile + 1) - first);
+                // A sequence that is longer than max_len (or its table) keeps to
+                // its share: the staged tiles of the others are not its own.
+                const int64_t tiles = last / kTile + 1;
+                if (tiles > p.cap_seq) record_status(&g_tile_invalid, RF_ERR_INVALID_ARG);
+                nt = max((int64_t)0, min(tiles, (int64_t)p.cap_seq) - first);
             }
             if (past < 0 && nq > 0) record_status(&g_tile_invalid, RF_ERR_INVALID_ARG);
         }
         int64_t total_kv, total_q;
         const int64_t kv0 = kv_at + scan1024(nt, part, &total_kv);
         const int64_t at = q_at + scan1024((nq + ctt - 1) / ctt, part, &total_q);
-        // past the capacity (a sequence longer than max_len): not staged
+        // past the capacity (only where q_start decreases): not staged
         const int64_t kvn = max((int64_t)0, min(nt, (int64_t)p.cap_kv - kv0));
         if (kvn < nt) record_status(&g_tile_invalid, RF_ERR_INVALID_ARG);
         if (s < b.n_seq) {
@@ -952,7 +957,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) attn_tile_kernel(const __grid
 
 // ------------------------------------------------------------------ host side
 struct Layout {
-    int64_t cap_q, cap_kv;
+    int64_t cap_q, cap_kv, cap_seq;
     int splits, split_tiles;
     size_t plan, q_tiles, kv_base, kv_first, q_img, q_unit, k_img, v_img, units, sums, part_o, part_ml, total;
 };
@@ -974,10 +979,18 @@ Layout layout(const AttnParams &p, const TileParams &t, int dtype, int64_t max_l
     const int64_t ctt = t.nt * t.tqt;
     L.cap_q = p.b.n_tok / ctt + std::min<int64_t>(p.b.n_seq, p.b.n_tok);
     // No sequence's position tiles exceed max_len's; with a window, all of
-    // them together do not exceed the windows' and the new tokens'.
-    L.cap_kv = p.b.n_seq * ((max_len + kTile - 1) / kTile);
-    if (p.window > 0)
-        L.cap_kv = std::min<int64_t>(L.cap_kv, (p.b.n_seq * std::min(p.window, max_len) + p.b.n_tok) / kTile + 3LL * p.b.n_seq);
+    // them together do not exceed the windows' and the new tokens', however
+    // long the sequences are (positions are below 2^31).
+    auto tiles_of = [](int64_t len) { return std::min<int64_t>((len + kTile - 1) / kTile, 1 << 24); };
+    L.cap_seq = tiles_of(max_len);
+    L.cap_kv = p.b.n_seq * L.cap_seq;
+    if (p.window > 0) {
+        const int64_t windows = (p.b.n_seq * std::min(p.window, max_len) + p.b.n_tok) / kTile + 3LL * p.b.n_seq;
+        if (windows < L.cap_kv) {
+            L.cap_kv = windows;
+            L.cap_seq = tiles_of((int64_t)p.b.table_width * p.c.page_size);
+        }
+    }
     const int64_t kvh = p.c.n_kv_heads;
     // Parts of the position tiles: the number for which the items' rounds over
     // the SMs take the least time, in steps of one position tile (about 2 us,
@@ -1087,7 +1100,7 @@ rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *works
     p.part_o = reinterpret_cast<float *>(ws + L.part_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + L.part_ml);
     t.a = p;
-    t.cap_q = (int)L.cap_q, t.cap_kv = (int)L.cap_kv;
+    t.cap_q = (int)L.cap_q, t.cap_kv = (int)L.cap_kv, t.cap_seq = (int)L.cap_seq;
     t.plan = reinterpret_cast<TilePlan *>(ws + L.plan);
     t.q_tiles = reinterpret_cast<QTile *>(ws + L.q_tiles);
     t.kv_base = reinterpret_cast<int32_t *>(ws + L.kv_base);

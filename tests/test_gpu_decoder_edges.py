@@ -1,0 +1,59 @@
+"""GPU tests of what unusual sequences, positions and queries may do in the
+cache and the attention over it."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_weight_streaming_dequant_gb300 as rf
+from decoder_helpers import Setup, by_tiles, i32, randn
+from oracle import decoder as od
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    rf.device_status()
+    yield
+    rf.device_status()
+
+
+def check_sequences(su, q, q64, dtype, which, window=0, max_len=0):
+    """The rows of sequences `which` against the oracle, within its bound."""
+    out = rf.attention(su.cache, su.batch, q, window=window, max_len=max_len).double().cpu().numpy()
+    dim = q.shape[2]
+    for s in which:
+        a, b = int(su.q_start[s]), int(su.q_start[s + 1])
+        ref, mag, xmag = od.attention(su.ref, su.table[s:s + 1], [su.past[s]], [0, b - a], b - a, q64[a:b], dim ** -0.5, window)
+        bound = od.attention_bound(dtype, dim, su.past[s] + b - a, ref, mag, xmag)
+        worst = (np.abs(out[a:b] - ref) / bound).max()
+        assert worst <= 1.0, (s, worst)
+
+
+# Sequences before, between and after the one that is too long; 16 heads of one
+# K/V head, so that the call goes through the 128-row tiles.
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("long_at", [0, 1, 2])
+def test_a_sequence_past_its_table_takes_nothing_from_the_others(dtype, window, long_at):
+    rng = np.random.default_rng([21, window, long_at])
+    su = Setup(rng, [192, 130, 192], [64, 64, 64], 1, 64, 64, width=4)
+    assert su.table.shape[1] == 4 and by_tiles(su, 16, window)
+    su.past[long_at] = 4096
+    su.batch = rf.KVBatch(i32(su.table), i32(su.past), i32(su.q_start), su.n_tok)
+    q, q64 = randn(rng, (su.n_tok, 16, 64), dtype, 2.0)
+    check_sequences(su, q, q64, dtype, [s for s in range(3) if s != long_at], window)
+    assert rf.device_status() == 1                              # the long one is reported
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("long_at", [0, 1, 2])
+def test_a_sequence_longer_than_max_len_takes_nothing_from_the_others(dtype, window, long_at):
+    rng = np.random.default_rng([22, window, long_at])
+    past = [192, 130, 192]
+    past[long_at] = 900
+    su = Setup(rng, past, [64, 64, 64], 1, 64, 64)
+    assert by_tiles(su, 16, window, max_len=256)
+    q, q64 = randn(rng, (su.n_tok, 16, 64), dtype, 2.0)
+    check_sequences(su, q, q64, dtype, [s for s in range(3) if s != long_at], window, max_len=256)
