@@ -642,14 +642,14 @@ typedef struct rf_kv_cache {
 
 /* The tokens of one call, sequence after sequence: sequence s owns tokens
  * [q_start[s], q_start[s+1]) of the call's n_tok, at positions past[s],
- * past[s] + 1, ...; position p of sequence s lies in page
+ * past[s] + 1, ...; position p of sequence s (below 2^31) lies in page
  * page_table[s * table_stride + p / page_size].  The three arrays are device
  * int32 (q_start: n_seq + 1, not decreasing; past: n_seq; n_seq 1..65536),
  * read by the kernels, so that a captured step can be replayed with other
  * lengths.  table_width: entries per sequence that may be read.  Tokens that
  * belong to no sequence are allowed (a padded batch) and are skipped.  A
- * token whose position has no page (a negative past, a position past the
- * table, an entry outside [0, n_pages)), or none in the rotation's tables,
+ * token whose position has no page (a negative past, a position of 2^31 or
+ * past the table, an entry outside [0, n_pages)), or none in the rotation's tables,
  * is skipped too, and rf_device_status reports RF_ERR_INVALID_ARG. */
 typedef struct rf_kv_batch {
     const int32_t *page_table;
@@ -685,7 +685,8 @@ typedef struct rf_kv_batch {
  * unknown style or flag, strides below head_dim, n_heads < 1 with q);
  * RF_ERR_MISALIGNED (codes not 16-byte aligned, other pointers not to their
  * element); RF_ERR_TOO_LARGE (n_heads > 4096).  n_tok 0 is a no-op.  (A query is
- * rotated, and q_out written, whenever its position lies in the tables.) */
+ * rotated, and q_out written, whenever its position is one and lies in the
+ * tables.) */
 RF_API rf_status rf_kv_append(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype,
                               const void *k, int64_t k_ld_tok, int64_t k_ld_head, const void *v,
                               int64_t v_ld_tok, int64_t v_ld_head, const void *q,

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kAppendThreads, UPT <= 2 ? 6 : 3) append_kerne
         int n = 0, page = -1;
         int64_t pos = -1;
         if (first <= t && t < next) {
-            pos = (int64_t)past + (t - first);
+            pos = (int64_t)past + t - first;
             if (kv_part) {
                 if (t == first || (pos & (kKvBlock - 1)) == 0) {
                     const int end = min(next, p.b.n_tok);
@@ -209,12 +209,12 @@ __global__ void __launch_bounds__(kAppendThreads, UPT <= 2 ? 6 : 3) append_kerne
                     if (page < 0 || !turns) record_status(&g_kv_status, RF_ERR_INVALID_ARG);
                     if (page < 0) n = 0;
                 }
-            } else if (pos < 0 || (p.rot != 0 && pos >= p.n_pos)) {
+            } else if (pos < 0 || pos > 0x7fffffffLL || (p.rot != 0 && pos >= p.n_pos)) {
                 pos = -1;
                 record_status(&g_kv_status, RF_ERR_INVALID_ARG);
             }
         }
-        s_pos[tid] = (int)(pos < 0x7fffffffLL ? pos : -1);
+        s_pos[tid] = (int)pos;   // below 2^31 where there is something to do
         s_n[tid] = n;
         s_page[tid] = page;
     }

@@ -178,11 +178,12 @@ __device__ __forceinline__ int find_seq_warp(const int32_t *q_start, int n_seq, 
     return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
-// The page of position `pos` of sequence s, or -1 if it has none.
+// The page of position `pos` of sequence s, or -1 if it has none (positions
+// from 2^31 on have none: kernels hold them in 32 bits).
 __device__ __forceinline__ int page_of(const rf_kv_batch &b, const rf_kv_cache &c, int s, int64_t pos)
 {
     const int64_t i = pos >> (31 - __clz(c.page_size));   // a power of two
-    if (pos < 0 || i >= b.table_width) return -1;
+    if (pos < 0 || pos > 0x7fffffffLL || i >= b.table_width) return -1;
     const int page = b.page_table[(int64_t)s * b.table_stride + i];
     return page >= 0 && page < c.n_pages ? page : -1;
 }

@@ -57,3 +57,37 @@ def test_a_sequence_longer_than_max_len_takes_nothing_from_the_others(dtype, win
     assert by_tiles(su, 16, window, max_len=256)
     q, q64 = randn(rng, (su.n_tok, 16, 64), dtype, 2.0)
     check_sequences(su, q, q64, dtype, [s for s in range(3) if s != long_at], window, max_len=256)
+
+
+@pytest.mark.parametrize("with_q", [True, False])
+def test_positions_end_at_two_to_the_31(with_q):
+    """The last three positions that there are, and one that is none: it is
+    skipped and reported, although the table has a page for it."""
+    rng = np.random.default_rng(24)
+    page, dim, width = 256, 64, 2 ** 23 + 1
+    table = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    table[0, -2], table[0, -1] = 1, 2
+    small = od.Cache(rng.integers(-127, 128, (3, 2, page, dim)).astype(np.int8), rng.integers(-127, 128, (3, 2, page, dim)).astype(np.int8),
+                     rng.integers(118, 123, (3, 2, 8)).astype(np.uint8), rng.integers(118, 123, (3, 2, 8)).astype(np.uint8))
+    cache = rf.KVCache(*(torch.from_numpy(a).cuda() for a in (*small.codes, *small.scales)))
+    batch = rf.KVBatch(table, i32([2 ** 31 - 3]), i32([0, 4]), 4)
+    k, v = randn(rng, (4, 2, dim))[0], randn(rng, (4, 2, dim))[0]
+    q, q64 = randn(rng, (4, 4, dim))
+    out = torch.full_like(q, 7.0)
+    rf.kv_append(cache, batch, k, v, **(dict(q=q, q_out=out) if with_q else {}))
+    assert rf.device_status() == 1 and rf.device_status() == rf.OK
+    if with_q:
+        assert torch.equal(out[:3], q[:3]) and (out[3] == 7.0).all()
+    small.append(np.array([[1]]), [page - 3], [0, 3], k.cpu().numpy(), v.cpu().numpy())
+    for got, want in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), small.codes + small.scales):
+        assert np.array_equal(got.cpu().numpy(), want)
+    kr, vr = rf.kv_read(cache, batch)
+    assert rf.device_status() == 1
+    for t in range(3):
+        assert np.array_equal(kr[t].double().cpu().numpy(), small.values([1], page - 3 + t, 0))
+        assert np.array_equal(vr[t].double().cpu().numpy(), small.values([1], page - 3 + t, 1))
+    assert not kr[3].any() and not vr[3].any()
+    got = rf.attention(cache, batch, q, window=8).double().cpu().numpy()
+    assert rf.device_status() == 1
+    ref, mag, xmag = od.attention(small, np.array([[1]]), [page - 3], [0, 3], 3, q64[:3], dim ** -0.5, 8)
+    assert (np.abs(got[:3] - ref) <= od.attention_bound("float32", dim, 8, ref, mag, xmag)).all()
