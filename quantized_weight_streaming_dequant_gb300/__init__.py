@@ -173,6 +173,55 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_DTYPES = _empty = _empty_like = _F32_TYPE = _U8_TYPE = None
+
+
+def _look_up() -> None:
+    """torch's names, once: an import statement in a function costs each call 0.5 us."""
+    global _DTYPES, _empty, _empty_like, _F32_TYPE, _U8_TYPE
+    import torch
+    _empty, _empty_like, _F32_TYPE, _U8_TYPE = torch.empty, torch.empty_like, torch.float32, torch.uint8
+    _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+def _new(stream, size, dtype, device, out: bool = True):
+    """A device tensor for a call on `stream` (None: the current stream), from
+    that stream's own memory, as torch's operators take theirs: memory of
+    another stream may still be in use there, and may be handed on there while
+    this call's kernels run.  out: the caller may also use it, and then drop it,
+    on the current stream."""
+    if _empty is None:
+        _look_up()
+    if stream is None or _stream(stream) == _stream(None):
+        return _empty(size, dtype=dtype, device=device)
+    import torch
+    current = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = _empty(size, dtype=dtype, device=device)
+    if out:
+        t.record_stream(current)
+    return t
+
+
+def _new_f32(stream, size, like):
+    """_new: float32, on the device of `like`."""
+    if _empty is None:
+        _look_up()
+    return _new(stream, size, _F32_TYPE, like.device)
+
+
+def _new_like(stream, like):
+    """_new: contiguous, of the shape and type of `like`."""
+    if _empty is None:
+        _look_up()
+    if stream is None and like.is_contiguous():
+        return _empty_like(like)
+    return _new(stream, like.shape, like.dtype, like.device)
+
+
 def _dev_ptr(t, what: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
@@ -198,11 +247,10 @@ def max_in_dim(fmt: int, n_x: int = 1) -> int:
 
 
 def dequantize(fmt: int, W, n_blocks: int | None = None, out=None, stream=None):
-    import torch
     if n_blocks is None:
         n_blocks = W.numel() // BLOCK_BYTES[fmt]
     if out is None:
-        out = torch.empty(BLOCK_ELEMS[fmt] * n_blocks, dtype=torch.float32, device=W.device)
+        out = _new_f32(stream, BLOCK_ELEMS[fmt] * n_blocks, W)
     _check(lib().rf_dequantize(fmt, _dev_ptr(W, "W"), n_blocks, _dev_ptr(out, "out"),
                                _stream(stream)), "rf_dequantize")
     return out
@@ -210,9 +258,8 @@ def dequantize(fmt: int, W, n_blocks: int | None = None, out=None, stream=None):
 
 def gemv(fmt: int, W, row_start: int, row_end: int, in_dim: int, x, y=None, stream=None,
          flags: int = 0):
-    import torch
     if y is None:
-        y = torch.empty(max(row_end - row_start, 0), dtype=torch.float32, device=x.device)
+        y = _new_f32(stream, max(row_end - row_start, 0), x)
     _check(lib().rf_gemv_ex(fmt, _dev_ptr(W, "W"), row_start, row_end, in_dim, _dev_ptr(x, "x"),
                             _dev_ptr(y, "y") if y.numel() else 1, flags, _stream(stream)),
            "rf_gemv")
@@ -223,12 +270,11 @@ def gemv_multi(fmt: int, W, row_start: int, row_end: int, in_dim: int, X, Y=None
                flags: int = 0):
     """rf_gemv_multi: X is (n_tok, in_dim) float32 on the device (rows may be
     strided); returns Y (n_tok, row_end - row_start)."""
-    import torch
     if X.dim() != 2 or X.stride(1) != 1:
         raise ValueError("X must be 2-D with unit stride along in_dim")
     n_tok = X.shape[0]
     if Y is None:
-        Y = torch.empty(n_tok, max(row_end - row_start, 0), dtype=torch.float32, device=X.device)
+        Y = _new_f32(stream, (n_tok, max(row_end - row_start, 0)), X)
     if Y.dim() != 2 or Y.stride(1) != 1:
         raise ValueError("Y must be 2-D with unit stride along the rows")
     _check(lib().rf_gemv_multi(fmt, _dev_ptr(W, "W"), row_start, row_end, in_dim, n_tok,
@@ -246,17 +292,16 @@ def gemm(fmt: int, W, row_start: int, row_end: int, in_dim: int, X, Y=None, work
     """rf_gemm (tensor cores): X is (n_tok, in_dim) float32 on the device
     (rows may be strided); returns Y (n_tok, row_end - row_start).  The
     workspace (a uint8 device tensor) is allocated when not given."""
-    import torch
     if X.dim() != 2 or X.stride(1) != 1:
         raise ValueError("X must be 2-D with unit stride along in_dim")
     n_tok = X.shape[0]
     if Y is None:
-        Y = torch.empty(n_tok, max(row_end - row_start, 0), dtype=torch.float32, device=X.device)
+        Y = _new_f32(stream, (n_tok, max(row_end - row_start, 0)), X)
     if Y.dim() != 2 or Y.stride(1) != 1:
         raise ValueError("Y must be 2-D with unit stride along the rows")
     need = gemm_workspace_bytes(fmt, in_dim, n_tok)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = _new(stream, need, _U8_TYPE, X.device, out=False)
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
     _check(lib().rf_gemm(fmt, _dev_ptr(W, "W"), row_start, row_end, in_dim, n_tok,
@@ -275,16 +320,14 @@ def gemv_batch(fmt: int, in_dim: int, windows, stream=None, flags: int = 0):
 
 
 def swiglu(g, u, h=None, stream=None):
-    import torch
-    h = torch.empty_like(g) if h is None else h
+    h = _new_like(stream, g) if h is None else h
     _check(lib().rf_swiglu(_dev_ptr(g, "g"), _dev_ptr(u, "u"), _dev_ptr(h, "h"), g.numel(),
                            _stream(stream)), "rf_swiglu")
     return h
 
 
 def gelu(z, h=None, stream=None):
-    import torch
-    h = torch.empty_like(z) if h is None else h
+    h = _new_like(stream, z) if h is None else h
     _check(lib().rf_gelu(_dev_ptr(z, "z"), _dev_ptr(h, "h"), z.numel(), _stream(stream)),
            "rf_gelu")
     return h
@@ -293,11 +336,10 @@ def gelu(z, h=None, stream=None):
 def gemv_host(fmt: int, host_W, row_start: int, row_end: int, in_dim: int, x, y=None,
               stream=None):
     """rf_gemv_host: host_W is a page-locked CPU tensor (uint8) read in place."""
-    import torch
     if host_W.is_cuda or not host_W.is_contiguous():
         raise ValueError("host_W must be a contiguous CPU tensor")
     if y is None:
-        y = torch.empty(max(row_end - row_start, 0), dtype=torch.float32, device=x.device)
+        y = _new_f32(stream, max(row_end - row_start, 0), x)
     _check(lib().rf_gemv_host(fmt, host_W.data_ptr(), row_start, row_end, in_dim,
                               _dev_ptr(x, "x"), _dev_ptr(y, "y") if y.numel() else 1,
                               _stream(stream)), "rf_gemv_host")
@@ -313,9 +355,8 @@ def ffn_workspace(n_ff: int, device):
 def ffn_swiglu(fmt: int, gate, up, down, n_ff: int, n_embd: int, x, y=None, h=None,
                stream=None, flags: int = 0, workspace=None):
     """rf_ffn_swiglu_ws (workspace: from ffn_workspace, or None)."""
-    import torch
-    y = torch.empty(n_embd, dtype=torch.float32, device=x.device) if y is None else y
-    h = torch.empty(n_ff, dtype=torch.float32, device=x.device) if h is None else h
+    y = _new_f32(stream, n_embd, x) if y is None else y
+    h = _new_f32(stream, n_ff, x) if h is None else h
     _check(lib().rf_ffn_swiglu_ws(fmt, _dev_ptr(gate, "gate"), _dev_ptr(up, "up"),
                                   _dev_ptr(down, "down"), n_ff, n_embd, _dev_ptr(x, "x"),
                                   _dev_ptr(y, "y"), _dev_ptr(h, "h"),
@@ -379,11 +420,10 @@ class Arena:
     def stream_linear(self, fmt: int, host_W, in_dim: int, row_start: int, row_end: int,
                       block_rows: int, depth: int, x, y=None, stream=None):
         """host_W: page-locked CPU tensor (uint8) holding row 0 onwards."""
-        import torch
         if host_W.is_cuda or not host_W.is_contiguous():
             raise ValueError("host_W must be a contiguous CPU tensor")
         if y is None:
-            y = torch.empty(max(row_end - row_start, 0), dtype=torch.float32, device=x.device)
+            y = _new_f32(stream, max(row_end - row_start, 0), x)
         _check(lib().rf_stream_linear(fmt, host_W.data_ptr(), in_dim, row_start, row_end,
                                       block_rows, depth, self.handle, _dev_ptr(x, "x"),
                                       _dev_ptr(y, "y") if y.numel() else 1, _stream(stream)),
@@ -428,13 +468,12 @@ def moe_ffn_streamed(fmt: int, logits, top_k: int, host_gate, host_up, host_down
                      y=None, workspace=None, stream=None):
     """rf_moe_ffn_streamed: experts in page-locked CPU tensors, one layer-wide
     prefetch plan through `arena`, an optional ExpertCache."""
-    import torch
     for t, nm in ((host_gate, "host_gate"), (host_up, "host_up"), (host_down, "host_down")):
         if t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{nm} must be a contiguous CPU tensor")
-    y = torch.empty(n_embd, dtype=torch.float32, device=x.device) if y is None else y
+    y = _new_f32(stream, n_embd, x) if y is None else y
     if workspace is None:
-        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device)
+        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device, stream)
     _check(lib().rf_moe_ffn_streamed(fmt, _dev_ptr(logits, "logits"), logits.numel(), top_k,
                                      host_gate.data_ptr(), host_up.data_ptr(),
                                      host_down.data_ptr(), n_ff, n_embd, block_rows, depth,
@@ -447,8 +486,8 @@ def moe_ffn_streamed(fmt: int, logits, top_k: int, host_gate, host_up, host_down
 
 def moe_route(logits, top_k: int, stream=None):
     import torch
-    idx = torch.empty(top_k, dtype=torch.int32, device=logits.device)
-    w = torch.empty(top_k, dtype=torch.float32, device=logits.device)
+    idx = _new(stream, top_k, torch.int32, logits.device)
+    w = _new_f32(stream, top_k, logits)
     _check(lib().rf_moe_route(_dev_ptr(logits, "logits"), logits.numel(), top_k,
                               _dev_ptr(idx, "idx"), _dev_ptr(w, "w"), _stream(stream)),
            "rf_moe_route")
@@ -459,18 +498,17 @@ def moe_workspace_bytes(top_k: int, n_ff: int, n_embd: int, block_rows: int) -> 
     return lib().rf_moe_workspace_bytes(top_k, n_ff, n_embd, block_rows)
 
 
-def moe_workspace(top_k: int, n_ff: int, n_embd: int, block_rows: int, device):
-    import torch
-    n = moe_workspace_bytes(top_k, n_ff, n_embd, block_rows)
-    return torch.empty(n, dtype=torch.uint8, device=device)
+def moe_workspace(top_k: int, n_ff: int, n_embd: int, block_rows: int, device, stream=None):
+    if _empty is None:
+        _look_up()
+    return _new(stream, moe_workspace_bytes(top_k, n_ff, n_embd, block_rows), _U8_TYPE, device)
 
 
 def moe_ffn(fmt: int, logits, top_k: int, gate, up, down, n_ff: int, n_embd: int,
             block_rows: int, x, y=None, workspace=None, stream=None):
-    import torch
-    y = torch.empty(n_embd, dtype=torch.float32, device=x.device) if y is None else y
+    y = _new_f32(stream, n_embd, x) if y is None else y
     if workspace is None:
-        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device)
+        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device, stream)
     _check(lib().rf_moe_ffn(fmt, _dev_ptr(logits, "logits"), logits.numel(), top_k,
                             _dev_ptr(gate, "gate"), _dev_ptr(up, "up"), _dev_ptr(down, "down"),
                             n_ff, n_embd, block_rows, _dev_ptr(x, "x"), _dev_ptr(y, "y"),
@@ -482,10 +520,9 @@ def moe_ffn_biased(fmt: int, logits, top_k: int, gate, up, down, gate_bias, up_b
                    alpha: float, limit: float, n_ff: int, n_embd: int, block_rows: int, x,
                    y=None, workspace=None, stream=None):
     """rf_moe_ffn_biased: biases are device float32 tensors (or None)."""
-    import torch
-    y = torch.empty(n_embd, dtype=torch.float32, device=x.device) if y is None else y
+    y = _new_f32(stream, n_embd, x) if y is None else y
     if workspace is None:
-        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device)
+        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device, stream)
     opt = lambda t, nm: None if t is None else _dev_ptr(t, nm)   # noqa: E731
     _check(lib().rf_moe_ffn_biased(fmt, _dev_ptr(logits, "logits"), logits.numel(), top_k,
                                    _dev_ptr(gate, "gate"), _dev_ptr(up, "up"),
@@ -512,13 +549,12 @@ def moe_ffn_noalloc(fmt: int, logits, top_k: int, gate, up, down, n_ff: int, n_e
 def moe_ffn_host(fmt: int, logits, top_k: int, gate, up, down, n_ff: int, n_embd: int,
                  block_rows: int, x, y=None, workspace=None, stream=None):
     """rf_moe_ffn_host: gate/up/down are page-locked CPU tensors read in place."""
-    import torch
     for t in (gate, up, down):
         if t.is_cuda or not t.is_contiguous():
             raise ValueError("expert tensors must be contiguous CPU tensors")
-    y = torch.empty(n_embd, dtype=torch.float32, device=x.device) if y is None else y
+    y = _new_f32(stream, n_embd, x) if y is None else y
     if workspace is None:
-        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device)
+        workspace = moe_workspace(top_k, n_ff, n_embd, block_rows, x.device, stream)
     _check(lib().rf_moe_ffn_host(fmt, _dev_ptr(logits, "logits"), logits.numel(), top_k,
                                  gate.data_ptr(), up.data_ptr(), down.data_ptr(), n_ff, n_embd,
                                  block_rows, _dev_ptr(x, "x"), _dev_ptr(y, "y"),
@@ -534,17 +570,6 @@ def moe_workspace_views(workspace, top_k: int, n_ff: int):
     w = workspace[256:288].view(torch.float32)[:top_k]
     h = workspace[512:512 + 4 * top_k * n_ff].view(torch.float32).view(top_k, n_ff)
     return idx, w, h
-
-
-_DTYPES = _empty = _empty_like = _F32_TYPE = None
-
-
-def _look_up() -> None:
-    """torch's names, once: an import statement in a function costs each call 0.5 us."""
-    global _DTYPES, _empty, _empty_like, _F32_TYPE
-    import torch
-    _empty, _empty_like, _F32_TYPE = torch.empty, torch.empty_like, torch.float32
-    _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _dtype(t) -> int:
@@ -592,14 +617,13 @@ def norm_residual(residual, x=None, *, post_weight=None, gate=None, scale: float
     dt = _dtype(like)
     px, ldx = _rows(x, n_tok, n, dt, "x")
     pr, ldr = _rows(residual, n_tok, n, dt, "residual")
-    dense = like.is_contiguous()
     if residual_out is None:
-        residual_out = _empty_like(like) if dense else _empty((n_tok, n), dtype=like.dtype, device=like.device)
+        residual_out = _new_like(stream, like)
         po, ldo = residual_out.data_ptr(), n
     else:
         po, ldo = _rows(residual_out, n_tok, n, dt, "residual_out")
     if y is None and norm:
-        y = _empty_like(like) if dense else _empty((n_tok, n), dtype=like.dtype, device=like.device)
+        y = _new_like(stream, like)
         py, ldy = y.data_ptr(), n
     else:
         py, ldy = _rows(y, n_tok, n, dt, "y")
@@ -693,7 +717,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, cos=None
     if q is not None:
         pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
         if q_out is None:
-            q_out = _empty_like(q) if q.is_contiguous() else _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+            q_out = _new_like(stream, q)
             po, olt, olh = q_out.data_ptr(), nh * dim, dim
         else:
             po, olt, olh, oh = _heads(q_out, n_tok, dim, dt, "q_out")
@@ -718,19 +742,18 @@ def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None,
     shape = (batch.n_tok, cache.n_kv_heads, cache.head_dim)
     n = shape[0] * shape[1] * shape[2]
     if k_out is None:
-        k_out = _empty(shape, dtype=_F32_TYPE, device=cache.device)
+        k_out = _new(stream, shape, _F32_TYPE, cache.device)
     if v_out is None:
-        v_out = _empty(shape, dtype=_F32_TYPE, device=cache.device)
+        v_out = _new(stream, shape, _F32_TYPE, cache.device)
     pk, pv = _f32_ptr(k_out, n, "k_out"), _f32_ptr(v_out, n, "v_out")
     _check(lib().rf_kv_read(cache.ref, batch.ref, pk, pv, flags, _stream(stream)), "rf_kv_read")
     return k_out, v_out
 
 
-def attention_workspace(cache: KVCache, batch: KVBatch, q, max_len: int = 0, window: int = 0):
-    """Device workspace for attention() with these arguments, or None."""
-    import torch
+def attention_workspace(cache: KVCache, batch: KVBatch, q, max_len: int = 0, window: int = 0, stream=None):
+    """Device workspace for attention() with these arguments on `stream`, or None."""
     n = lib().rf_attention_workspace_bytes(cache.ref, batch.ref, _dtype(q), q.shape[1], window, max_len)
-    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    return _new(stream, n, _U8_TYPE, q.device, out=False) if n else None
 
 
 def attention(cache: KVCache, batch: KVBatch, q, out=None, scale: float | None = None, window: int = 0,
@@ -741,14 +764,14 @@ def attention(cache: KVCache, batch: KVBatch, q, out=None, scale: float | None =
     n_tok, dim, dt = batch.n_tok, cache.head_dim, _dtype(q)
     pq, qlt, qlh, nh = _heads(q, n_tok, dim, dt, "q")
     if out is None:
-        out = _empty_like(q) if q.is_contiguous() else _empty((n_tok, nh, dim), dtype=q.dtype, device=q.device)
+        out = _new_like(stream, q)
         po, olt, olh = out.data_ptr(), nh * dim, dim
     else:
         po, olt, olh, oh = _heads(out, n_tok, dim, dt, "out")
         if oh != nh:
             raise ValueError("out must be like q")
     if workspace is None:
-        workspace = attention_workspace(cache, batch, q, max_len, window)
+        workspace = attention_workspace(cache, batch, q, max_len, window, stream)
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
     _check(lib().rf_attention(cache.ref, batch.ref, dt, pq, qlt, qlh, nh,

@@ -96,8 +96,7 @@ class DecoderLayer:
         if n_tok <= 8:
             return rf.gemv_multi(self.fmt, W, 0, rows, in_dim, x, stream=stream)
         if self.fmt == rf.Q6_K:
-            import torch
-            y = torch.empty((n_tok, rows), dtype=torch.float32, device=x.device)
+            y = rf._new_f32(stream, (n_tok, rows), x)
             for t in range(0, n_tok, 8):
                 rf.gemv_multi(self.fmt, W, 0, rows, in_dim, x[t:t + 8], y[t:t + 8], stream=stream)
             return y
@@ -116,9 +115,7 @@ class DecoderLayer:
         o["in"], o["x"] = rf.norm_residual(residual, delta, post_weight=prev_post, scale=alpha,
                                            weight=self.norm_attn, eps=self.eps, stream=s)
         if n_tok == 1:
-            import torch
-            q, k, v = (torch.empty(n, dtype=torch.float32, device=residual.device)
-                       for n in (nh * hd, nk * hd, nk * hd))
+            q, k, v = (rf._new_f32(s, n, residual) for n in (nh * hd, nk * hd, nk * hd))
             x = o["x"].view(-1)
             rf.gemv_batch(self.fmt, d, [(self.wq, 0, nh * hd, x, q), (self.wk, 0, nk * hd, x, k),
                                         (self.wv, 0, nk * hd, x, v)], stream=s)

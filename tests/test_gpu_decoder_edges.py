@@ -91,3 +91,26 @@ def test_positions_end_at_two_to_the_31(with_q):
     assert rf.device_status() == 1
     ref, mag, xmag = od.attention(small, np.array([[1]]), [page - 3], [0, 3], 3, q64[:3], dim ** -0.5, 8)
     assert (np.abs(got[:3] - ref) <= od.attention_bound("float32", dim, 8, ref, mag, xmag)).all()
+
+
+@pytest.mark.parametrize("past,new,heads", [(6000, 1, 4), (4000, 40, 4), (300, 60, 32)])
+def test_attention_on_a_busy_stream_keeps_its_workspace(past, new, heads):
+    """The current stream allocates and fills blocks of the workspace's size
+    while the calls still wait on a stream of their own."""
+    rng = np.random.default_rng([25, past])
+    su = Setup(rng, [past], [new], 1, 64, 64)
+    q, _ = randn(rng, (new, heads, 64))
+    want = rf.attention(su.cache, su.batch, q)
+    size = rf.attention_workspace(su.cache, su.batch, q)
+    size = 0 if size is None else size.numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = [rf.attention(su.cache, su.batch, q, stream=handle) for _ in range(3)]
+        fill = [torch.full((max(size, 1),), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        fill += [torch.full_like(q, 7.0) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want) for g in got)
+        assert all((f == f.flatten()[0]).all() for f in fill)
