@@ -708,7 +708,8 @@ RF_API rf_status rf_kv_read(const rf_kv_cache *cache, const rf_kv_batch *batch, 
  *     out = sum_j w_j v_j / (sum_j w_j + exp(sink_h - m)),
  *     w_j = exp(scale * q.k_j - m)
  * (sinks: n_heads floats, or NULL: no such term).  A row that sees nothing
- * (its token belongs to no sequence or has no page) is 0.  Positions on
+ * (its token belongs to no sequence or has no page) is 0; one whose query
+ * holds a NaN or an infinity, and that sees something, is NaN.  Positions on
  * invalid pages are not seen (and are reported, see rf_kv_batch); what lies
  * beyond a sequence's last position in its pages is never used.
  * max_len: an upper bound of past + new tokens over the sequences, for the

@@ -229,9 +229,7 @@ __global__ void __launch_bounds__(32 * kWarps, DP == 256 ? 1 : DP == 128 ? 2 : N
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int ex = min(max(263 - (int)(__float_as_uint(amax) >> 23), 1), 253);
-        const float up = __uint_as_float((uint32_t)ex << 23);
-        qs[r] = p.qk_scale * __uint_as_float((uint32_t)(254 - ex) << 23);
+        const float up = row_power(amax, p.qk_scale, &qs[r]);
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll

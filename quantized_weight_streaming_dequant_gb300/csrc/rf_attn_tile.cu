@@ -328,10 +328,9 @@ __device__ __forceinline__ void stage_q(const TileParams &p, int qt, int head, i
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // the row's maximum comes to [512, 1024)
-        const int ex = min(max(263 - (int)(__float_as_uint(amax) >> 23), 1), 253);
-        const float up = __uint_as_float((uint32_t)ex << 23) * (p.negate ? -1.f : 1.f);
-        if (k == 0) unit[r] = p.qk_abs * __uint_as_float((uint32_t)(254 - ex) << 23);
+        float factor;
+        const float up = row_power(amax, p.qk_abs, &factor) * (p.negate ? -1.f : 1.f);
+        if (k == 0) unit[r] = factor;
         uint4 hi4, lo4;
         uint32_t *ph = reinterpret_cast<uint32_t *>(&hi4), *pl = reinterpret_cast<uint32_t *>(&lo4);
 #pragma unroll

@@ -194,6 +194,19 @@ __device__ __forceinline__ float scale_value(uint32_t E)
     return __uint_as_float(E == 255u ? 0x7fc00000u : E == 0u ? 0x00400000u : E << 23);
 }
 
+// Attention: what a query row is multiplied by, a power of two that brings
+// its maximum (amax) to [512, 1024), and the factor of its scores that takes
+// it back, times `scale`.  A row that holds an infinity has NaN for a factor:
+// its scores are all infinite or NaN, and where all of them are minus
+// infinity it would pass for one that sees nothing.
+__device__ __forceinline__ float row_power(float amax, float scale, float *unit)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    const int ex = min(max(263 - (int)(bits >> 23), 1), 253);
+    *unit = bits == 0x7f800000u ? __uint_as_float(0x7fc00000u) : scale * __uint_as_float((uint32_t)(254 - ex) << 23);
+    return __uint_as_float((uint32_t)ex << 23);
+}
+
 // ---------------------------------------------------------------- host side
 inline bool dtype_ok(int dtype) { return dtype == RF_F32 || dtype == RF_F16 || dtype == RF_BF16; }
 inline int dtype_bytes(int dtype) { return dtype == RF_F32 ? 4 : 2; }

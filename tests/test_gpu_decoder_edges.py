@@ -114,3 +114,25 @@ def test_attention_on_a_busy_stream_keeps_its_workspace(past, new, heads):
         torch.cuda.synchronize()
         assert all(torch.equal(g, want) for g in got)
         assert all((f == f.flatten()[0]).all() for f in fill)
+
+
+# One token and a chunk in one part (rows), rows in several parts, tiles in one
+# part and in several.
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("past,new,heads", [(0, 1, 4), (150, 3, 4), (6000, 1, 4), (300, 60, 32), (4000, 40, 4)])
+def test_an_infinite_query_gives_nan_whatever_the_signs_of_its_scores(dtype, past, new, heads):
+    """Scores that are all minus infinity are seen all the same: such a row is
+    not one that sees nothing."""
+    rng = np.random.default_rng([23, past, new])
+    su = Setup(rng, [past], [new], 1, 64, 64)
+    su.ref.codes[0][..., 7] = -np.abs(su.ref.codes[0][..., 7]) - (su.ref.codes[0][..., 7] == 0)
+    su.upload()
+    q, q64 = randn(rng, (new, heads, 64), dtype)
+    clean = rf.attention(su.cache, su.batch, q)
+    q[0, 1, 7] = float("inf")
+    q[new - 1, 2, 7] = float("-inf")
+    out = rf.attention(su.cache, su.batch, q)
+    hit = torch.zeros((new, heads), dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[new - 1, 2] = True
+    assert torch.isnan(out[hit]).all()
+    assert torch.equal(out[~hit], clean[~hit])
