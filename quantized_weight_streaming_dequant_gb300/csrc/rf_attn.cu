@@ -692,7 +692,7 @@ rf_status plan(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype, in
     if (*max_len == 0 || *max_len > cap) *max_len = cap;
     p->c = *cache, p->b = *batch;
     p->n_heads = n_heads, p->group = n_heads / cache->n_kv_heads;
-    p->window = window;
+    p->window = window <= INT_MAX ? window : 0;   // positions are below 2^31: it hides none
     return RF_OK;
 }
 
