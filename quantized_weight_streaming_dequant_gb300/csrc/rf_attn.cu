@@ -698,10 +698,11 @@ rf_status plan(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype, in
 
 }  // namespace
 
+bool attn_join_takes(const AttnParams &p) { return (int64_t)p.b.n_tok * p.n_heads <= INT_MAX; }
+
 rf_status launch_attn_join(const AttnParams &p, int dtype, cudaStream_t s)
 {
     const int64_t rows = (int64_t)p.b.n_tok * p.n_heads;
-    if (rows > 0x7fffffffLL) return RF_ERR_TOO_LARGE;
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         if (p.splits > 8) return launch_kernel(attn_join_kernel<T, 8>, dim3((unsigned)rows), dim3(256), 0, s, true, p);
@@ -771,6 +772,7 @@ rf_status rf_attention(const rf_kv_cache *cache, const rf_kv_batch *batch, int d
     choose_splits(&p, tl, max_len);
     const size_t need = parts_bytes(p);
     if (need > 0 && (!workspace || workspace_bytes < need)) return RF_ERR_INVALID_ARG;
+    if (p.splits > 1 && !attn_join_takes(p)) return RF_ERR_TOO_LARGE;
     if (need > 0) {
         p.part_o = static_cast<float *>(workspace);
         p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)p.b.n_tok * p.n_heads * p.splits * D);

@@ -44,7 +44,9 @@ size_t attn_tile_workspace(const AttnParams &p, int dtype, int64_t max_len);
 rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *workspace, cudaStream_t s,
                            bool chain);
 
-// Joins the parts of each row (part_o, part_ml) into out.
+// Joins the parts of each row (part_o, part_ml) into out.  Whether it takes
+// the rows is asked before anything is enqueued.
+bool attn_join_takes(const AttnParams &p);
 rf_status launch_attn_join(const AttnParams &p, int dtype, cudaStream_t s);
 
 }  // namespace rf

@@ -1093,7 +1093,7 @@ rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *works
     TileParams t;
     tile_shape(p, &t);
     const Layout L = layout(p, t, dtype, max_len);
-    if (L.cap_q > 0x3fffffffLL || L.cap_kv > 0x3fffffffLL) return RF_ERR_TOO_LARGE;
+    if (L.cap_q > 0x3fffffffLL || L.cap_kv > 0x3fffffffLL || (L.splits > 1 && !attn_join_takes(p))) return RF_ERR_TOO_LARGE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.splits = L.splits;
     p.part_o = reinterpret_cast<float *>(ws + L.part_o);
