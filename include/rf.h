@@ -766,6 +766,21 @@ RF_API rf_status rf_device_status(void);
  * 2,000,000. */
 RF_API rf_status rf_debug_arm_wait_fault(uint32_t limit_us);
 
+/* Test hook: how rf_attention lays out a call on the current device, from
+ * its host arguments alone (nothing is enqueued).  Errors: as rf_attention. */
+typedef struct rf_attention_plan {
+    int64_t part_positions; /* positions per part, at most */
+    int32_t tiles;          /* 1: tiles of 128 query rows, 0: rows */
+    int32_t parts;          /* parts of a row's positions */
+    int32_t item_tokens;    /* tokens of one work item */
+    int32_t head_tiles;     /* work items per K/V head, item_tokens and part */
+    int32_t sms;            /* SMs: as many items run at once in the tiles */
+    int32_t reserved;       /* 0 */
+} rf_attention_plan;
+RF_API rf_status rf_debug_attention_plan(const rf_kv_cache *cache, const rf_kv_batch *batch,
+                                         int dtype, int n_heads, int64_t window, int64_t max_len,
+                                         rf_attention_plan *out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -169,5 +169,5 @@ def attention_bound(dtype, dim, n_pos, out, mag, xmag):
     ew = 0.6932 * ex + 2.0 ** -21 + (n_pos / 8 + 64) * 2.0 ** -23
     bound = 2.0 * ew * mag
     if dtype != "float32":
-        bound = bound + 2.0 ** -11 * mag + (2.0 ** -8 if dtype == "bfloat16" else 2.0 ** -10) * np.abs(out) + 2.0 ** -24
+        bound = bound + 2.0 ** -11 * mag + (2.0 ** -8 if dtype == "bfloat16" else 2.0 ** -10) * abs(out) + 2.0 ** -24
     return bound + 1e-30

@@ -72,6 +72,12 @@ class KVBatchStruct(ctypes.Structure):
                 ("n_tok", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class AttentionPlan(ctypes.Structure):
+    _fields_ = [("part_positions", ctypes.c_int64), ("tiles", ctypes.c_int32), ("parts", ctypes.c_int32),
+                ("item_tokens", ctypes.c_int32), ("head_tiles", ctypes.c_int32), ("sms", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _SIGS = {
     "rf_status_str": ([_I], ctypes.c_char_p),
@@ -125,6 +131,7 @@ _SIGS = {
     "rf_attention_workspace_bytes": ([_P, _P, _I, _I, _I64, _I64], _SZ),
     "rf_device_status": ([], _I),
     "rf_debug_arm_wait_fault": ([ctypes.c_uint32], _I),
+    "rf_debug_attention_plan": ([_P, _P, _I, _I, _I64, _I64, ctypes.POINTER(AttentionPlan)], _I),
 }
 
 _lib = None
@@ -790,3 +797,12 @@ def debug_arm_wait_fault(limit_us: int) -> None:
     """rf_debug_arm_wait_fault (test hook): the next tensor-copy GEMV launch
     withholds one stage's copy and gives up its wait after limit_us."""
     _check(lib().rf_debug_arm_wait_fault(limit_us), "rf_debug_arm_wait_fault")
+
+
+def debug_attention_plan(cache: KVCache, batch: KVBatch, q, window: int = 0, max_len: int = 0) -> dict:
+    """rf_debug_attention_plan (test hook): how attention() lays out a call
+    with these arguments."""
+    p = AttentionPlan()
+    _check(lib().rf_debug_attention_plan(cache.ref, batch.ref, _dtype(q), q.shape[1], window, max_len,
+                                         ctypes.byref(p)), "rf_debug_attention_plan")
+    return {k: getattr(p, k) for k, _ in AttentionPlan._fields_ if k != "reserved"}

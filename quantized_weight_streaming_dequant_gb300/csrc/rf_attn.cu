@@ -739,6 +739,27 @@ size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv_batch 
     return parts_bytes(p);
 }
 
+rf_status rf_debug_attention_plan(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype, int n_heads,
+                                  int64_t window, int64_t max_len, rf_attention_plan *out)
+{
+    AttnParams p = {};
+    if (!out) return RF_ERR_INVALID_ARG;
+    if (const rf_status st = plan(cache, batch, dtype, n_heads, window, &max_len, &p)) return st;
+    *out = rf_attention_plan{};
+    out->sms = num_sms();
+    if (batch->n_tok == 0) return RF_OK;
+    if (attn_tile_takes(p, max_len)) {
+        attn_tile_plan(p, dtype, max_len, out);
+        return RF_OK;
+    }
+    RowTiling tl;
+    rows_tiling(p, &tl);
+    choose_splits(&p, tl, max_len);
+    out->parts = p.splits, out->part_positions = (int64_t)p.split_blocks * kKvBlock;
+    out->item_tokens = tl.tq, out->head_tiles = tl.head_tiles;
+    return RF_OK;
+}
+
 rf_status rf_attention(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype, const void *q,
                        int64_t q_ld_tok, int64_t q_ld_head, int n_heads, float scale, int64_t window,
                        const float *sinks, void *out, int64_t out_ld_tok, int64_t out_ld_head, int64_t max_len,

@@ -41,6 +41,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // whether it takes the call.
 bool attn_tile_takes(const AttnParams &p, int64_t max_len);
 size_t attn_tile_workspace(const AttnParams &p, int dtype, int64_t max_len);
+void attn_tile_plan(const AttnParams &p, int dtype, int64_t max_len, rf_attention_plan *out);
 rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *workspace, cudaStream_t s,
                            bool chain);
 

@@ -1088,6 +1088,15 @@ size_t attn_tile_workspace(const AttnParams &p, int dtype, int64_t max_len)
     return layout(p, t, dtype, max_len).total;
 }
 
+void attn_tile_plan(const AttnParams &p, int dtype, int64_t max_len, rf_attention_plan *out)
+{
+    TileParams t;
+    tile_shape(p, &t);
+    const Layout L = layout(p, t, dtype, max_len);
+    out->tiles = 1, out->parts = L.splits, out->part_positions = (int64_t)L.split_tiles * kTile;
+    out->item_tokens = t.nt * t.tqt, out->head_tiles = t.head_tiles;
+}
+
 rf_status launch_attn_tile(AttnParams p, int dtype, int64_t max_len, void *workspace, cudaStream_t s, bool chain)
 {
     TileParams t;
