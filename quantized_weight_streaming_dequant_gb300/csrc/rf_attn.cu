@@ -593,7 +593,7 @@ int rows_tiling(const AttnParams &p, RowTiling *tl)
 {
     // Eight rows hold one token of a group of up to eight heads; sixteen are
     // taken where they are filled (head_dim above 128 leaves no registers).
-    const int64_t rows = (int64_t)p.group * ((p.b.n_tok + p.b.n_seq - 1) / p.b.n_seq);
+    const int64_t rows = (int64_t)p.group * tokens_per_seq(p);
     const int nr = rows > 8 && p.c.head_dim <= 128 ? 2 : 1;
     tl->hpt = std::min(p.group, 8 * nr);
     tl->head_tiles = (p.group + tl->hpt - 1) / tl->hpt;
@@ -611,7 +611,7 @@ int64_t visible_blocks(const AttnParams &p, int64_t max_len, int tq)
 void choose_splits(AttnParams *p, const RowTiling &tl, int64_t max_len)
 {
     const int64_t blocks = visible_blocks(*p, max_len, tl.tq);
-    const int64_t per_seq = (p->b.n_tok + p->b.n_seq - 1) / p->b.n_seq;
+    const int64_t per_seq = tokens_per_seq(*p);
     const int64_t tiles = std::min<int64_t>(p->b.n_tok, (per_seq + tl.tq - 1) / tl.tq * p->b.n_seq) *
                           p->c.n_kv_heads * tl.head_tiles;
     const int occ = p->c.head_dim > 128 ? 1 : p->c.head_dim > 64 ? 2 : 4;

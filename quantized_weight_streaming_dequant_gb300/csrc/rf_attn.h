@@ -26,6 +26,9 @@ struct AttnParams {
     float2 *part_ml;         // [token][head][split]: maximum, sum
 };
 
+// Tokens of a sequence, on average and rounded up.
+inline int64_t tokens_per_seq(const AttnParams &p) { return ((int64_t)p.b.n_tok + p.b.n_seq - 1) / p.b.n_seq; }
+
 // Softmax weights are 2^(x - m + w_shift), where m is the row's maximum or up
 // to w_lazy below it: at most 2^15 (2^15.5), the top of fp16's range.  The
 // factor cancels between numerator and denominator.  SPLIT (fp32, two terms):

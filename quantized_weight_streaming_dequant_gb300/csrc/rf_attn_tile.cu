@@ -1057,7 +1057,8 @@ rf_status launch_tiles(const TileParams &t, cudaStream_t s, bool chain)
     const AttnParams &a = t.a;
     const int64_t kvh = a.c.n_kv_heads, ctas = (int64_t)t.cap_q * kvh * t.head_tiles;
     const int64_t stage = (int64_t)t.cap_kv * kvh + ctas + kPadParts;
-    if (stage > 0x7fffffffLL || ctas * a.splits > 0x7fffffffLL) return RF_ERR_TOO_LARGE;
+    // (CTAs draw items until they get one past the last: that count is an int too)
+    if (stage > 0x7fffffffLL || ctas * a.splits > 0x7fffffffLL - 65536) return RF_ERR_TOO_LARGE;
     if (const rf_status st = launch_kernel(tile_plan_kernel, dim3(1), dim3(1024), 0, s, chain, t)) return st;
     if (const rf_status st = launch_kernel(tile_stage_kernel<T, DP>, dim3((unsigned)stage), dim3(256), 0, s, true, t))
         return st;
@@ -1076,7 +1077,7 @@ bool attn_tile_takes(const AttnParams &p, int64_t max_len)
     // 21 / 32; 16 sequences against 8,000: 64 rows 235 / 247, 128 rows 397 /
     // 250 (fp32: 324 / 326, 572 / 342).  Tiles pay from about 96 rows, once
     // the work outweighs two more launches and the staging.
-    const int64_t per_seq = (p.b.n_tok + p.b.n_seq - 1) / p.b.n_seq, rows = per_seq * p.group;
+    const int64_t per_seq = tokens_per_seq(p), rows = per_seq * p.group;
     const int64_t seen = p.window > 0 ? std::min(max_len, p.window + per_seq) : max_len;
     return rows >= 96 && (double)rows * seen * p.b.n_seq >= 5e5;
 }

@@ -414,7 +414,7 @@ rf_status rf_kv_read(const rf_kv_cache *cache, const rf_kv_batch *batch, float *
     if (batch->n_tok == 0) return RF_OK;
     // Few tokens: one per CTA; many: eight share the lookup.
     const int chunk = batch->n_tok > 8 * num_sms() ? kReadTokens : 1;
-    return launch_kernel(read_kernel, dim3((unsigned)((batch->n_tok + chunk - 1) / chunk)), dim3(256), 0,
+    return launch_kernel(read_kernel, dim3((unsigned)(((int64_t)batch->n_tok + chunk - 1) / chunk)), dim3(256), 0,
                          static_cast<cudaStream_t>(stream), (flags & RF_CHAIN) != 0, *cache, *batch, chunk,
                          k_out, v_out, aligned_to(k_out, 32) && aligned_to(v_out, 32));
 }

@@ -76,3 +76,10 @@ def test_the_tests_rule_of_the_path_is_the_librarys(L, heads, kv, window):
                     assert bool(p.tiles) == by_tiles(su, heads, window, capped), (n_tok, n_seq, width, max_len)
                     took.add(p.tiles)
     assert took == {0, 1}
+
+
+def test_the_most_tokens_of_a_call_are_counted_in_64_bits(L):
+    p = rf.AttentionPlan()
+    c, b = cache(), batch(2 ** 31 - 1, 4, 65536)
+    assert L.rf_debug_attention_plan(ctypes.byref(c), ctypes.byref(b), rf.F32, 1, 0, 0, ctypes.byref(p)) == OK
+    assert p.tiles == 1                                         # 32,768 tokens a sequence
