@@ -588,7 +588,8 @@ RF_API rf_status rf_moe_ffn_noalloc(int fmt, const float *router_logits, int n_e
  * tables are fp32.  All arithmetic is in fp32 or wider sums; a 16-bit output
  * is rounded once.  Innermost dimensions are contiguous; other strides are
  * arguments, in elements.  Wide accesses are used where pointers and strides
- * are 16-byte aligned, and narrow ones (with equal results) where not.
+ * are 16-byte aligned, and narrow ones where not, with equal results (but for
+ * rf_norm_residual, whose sums of squares then add in another order).
  * flags: 0 or RF_CHAIN (weights and tables are static; the launch may be
  * set up while the previous kernel on `stream` drains). */
 #define RF_F32 0
@@ -623,7 +624,8 @@ RF_API rf_status rf_norm_residual(int dtype, int64_t n_tok, int64_t n, const voi
 /* Paged KV cache of 8-bit codes.  Keys and values of one head are held in
  * blocks of 32 tokens; a block has one scale byte E and
  * value = code * 2^(E-127), so every value is exact in fp32 (and a held code
- * is re-rounded, never recomputed, when its block's scale grows).
+ * is re-rounded, never recomputed, when its block's scale grows: however
+ * often that is, a value stays within one unit of the last scale).
  *   k, v            int8  [n_pages][n_kv_heads][page_size][head_dim]
  *   k_scale, v_scale uint8 [n_pages][n_kv_heads][page_size / 32]
  * All device memory of the caller, 16-byte aligned (the scales: any
@@ -631,7 +633,9 @@ RF_API rf_status rf_norm_residual(int dtype, int64_t n_tok, int64_t n, const voi
  * to 256; n_kv_heads: 1..1024.  E = 255 marks a block that holds a value
  * that is not a number, infinite or above 127 * 2^40: all of it reads as
  * NaN.  Otherwise 87 <= E <= 167 when written by rf_kv_append; values below
- * 2^-41 become 0. */
+ * 2^-41 become 0.  rf_kv_read takes every E; rf_attention takes those that
+ * rf_kv_append writes (its weights carry the units of the values, and more
+ * than 2^100 between the units of a row would leave fp32's range). */
 typedef struct rf_kv_cache {
     int8_t *k, *v;
     uint8_t *k_scale, *v_scale;
@@ -644,13 +648,14 @@ typedef struct rf_kv_cache {
  * [q_start[s], q_start[s+1]) of the call's n_tok, at positions past[s],
  * past[s] + 1, ...; position p of sequence s (below 2^31) lies in page
  * page_table[s * table_stride + p / page_size].  The three arrays are device
- * int32 (q_start: n_seq + 1, not decreasing; past: n_seq; n_seq 1..65536),
- * read by the kernels, so that a captured step can be replayed with other
- * lengths.  table_width: entries per sequence that may be read.  Tokens that
- * belong to no sequence are allowed (a padded batch) and are skipped.  A
- * token whose position has no page (a negative past, a position of 2^31 or
- * past the table, an entry outside [0, n_pages)), or none in the rotation's tables,
- * is skipped too, and rf_device_status reports RF_ERR_INVALID_ARG. */
+ * int32 (q_start: n_seq + 1, from 0 or more, not decreasing; past: n_seq;
+ * n_seq 1..65536), read by the kernels, so that a captured step can be
+ * replayed with other lengths.  table_width: entries per sequence that may be
+ * read.  Tokens that belong to no sequence are allowed (a padded batch) and
+ * are skipped.  A token whose position has no page (a negative past, a
+ * position of 2^31 or past the table, an entry outside [0, n_pages)), or none
+ * in the rotation's tables, is neither appended nor read back, and
+ * rf_device_status reports RF_ERR_INVALID_ARG. */
 typedef struct rf_kv_batch {
     const int32_t *page_table;
     const int32_t *past;
@@ -683,10 +688,10 @@ typedef struct rf_kv_batch {
  * Errors: RF_ERR_UNSUPPORTED_FMT (dtype); RF_ERR_INVALID_ARG (a null pointer
  * or a field out of range, rot not a multiple of 8 in [0, head_dim], an
  * unknown style or flag, strides below head_dim, n_heads < 1 with q);
- * RF_ERR_MISALIGNED (codes not 16-byte aligned, other pointers not to their
- * element); RF_ERR_TOO_LARGE (n_heads > 4096).  n_tok 0 is a no-op.  (A query is
- * rotated, and q_out written, whenever its position is one and lies in the
- * tables.) */
+ * RF_ERR_MISALIGNED (codes or rotation tables not 16-byte aligned, other
+ * pointers not to their element); RF_ERR_TOO_LARGE (n_heads > 4096).
+ * n_tok 0 is a no-op.  (A query is rotated, and q_out written, whenever its
+ * position is in [0, 2^31) and in the tables.) */
 RF_API rf_status rf_kv_append(const rf_kv_cache *cache, const rf_kv_batch *batch, int dtype,
                               const void *k, int64_t k_ld_tok, int64_t k_ld_head, const void *v,
                               int64_t v_ld_tok, int64_t v_ld_head, const void *q,
@@ -708,18 +713,25 @@ RF_API rf_status rf_kv_read(const rf_kv_cache *cache, const rf_kv_batch *batch, 
  *     out = sum_j w_j v_j / (sum_j w_j + exp(sink_h - m)),
  *     w_j = exp(scale * q.k_j - m)
  * (sinks: n_heads floats, or NULL: no such term).  A row that sees nothing
- * (its token belongs to no sequence or has no page) is 0; one whose query
- * holds a NaN or an infinity, and that sees something, is NaN.  Positions on
- * invalid pages are not seen (and are reported, see rf_kv_batch); what lies
- * beyond a sequence's last position in its pages is never used.
+ * (its token belongs to no sequence, or none of its positions has a page) is
+ * 0; one whose query holds a NaN or an infinity, and that sees something, is
+ * NaN.  Positions without a page are not seen (and are reported, see
+ * rf_kv_batch); what lies beyond a sequence's last position in its pages is
+ * never used.
  * max_len: an upper bound of past + new tokens over the sequences, for the
  * launch shape and the workspace (0: the table's capacity); the rows of a
- * longer sequence are undefined.
- * Scores and softmax sums are fp32.  fp32 queries and the softmax weights
- * then enter the tensor cores as two fp16 terms (22 bits; weights below
- * 2^-17 of a row's largest: to 2^-39 of it); for 16-bit dtypes the weights
- * are rounded once to fp16 (below 2^-22 of the largest: to 2^-33 of it), and
- * queries, scaled by a power of two, are not rounded.
+ * longer sequence are undefined (and may be reported), the others' are not
+ * touched by it.  The parts of a long row follow max_len, not its length, so
+ * a loose bound costs time.
+ * Scores (scale * q.k, which have to lie in fp32's range) and softmax sums
+ * are fp32.  Queries enter the tensor cores scaled by a power of two per row:
+ * fp32 ones as two fp16 terms (22 bits; elements below 2^-12 of their row's
+ * largest: to 2^-34 of it), 16-bit ones as they are (bf16 elements below
+ * 2^-26 of the largest and fp16 ones below 2^-23: to 2^-34 of it).  So do the
+ * softmax weights, each times the unit of its values: for fp32 as two fp16
+ * terms (22 bits; products below 2^-17 of a row's largest: to 2^-39 of it),
+ * for 16-bit dtypes rounded once to fp16 (11 bits; below 2^-22: to 2^-33).
+ * The sum of the weights is not rounded.
  * Results do not depend on the other sequences or on timing (n_seq, n_tok and
  * max_len choose how a row's sums are shared out).
  * q, out: n_tok x n_heads x head_dim with token and head strides; out may

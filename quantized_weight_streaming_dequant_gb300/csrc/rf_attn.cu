@@ -26,10 +26,11 @@
 // Measured: fp32, one token against 131,072 positions of 8 heads of 128 (four
 // query heads each): 48 us (5.6 TB/s, 0.82 of the measured copy rate) and 7
 // for the join; bf16, 48 ragged sequences of up to 16,001 positions, 8 heads
-// of 64 (eight each): 78 us (5.1 TB/s) and 8.  Both issue 2.0 to 2.6
-// instructions a cycle and SM from 8 to 16 warps: turning codes into fp16
-// (five instructions for four codes, and two more to pair V's) is what keeps
-// them from the memory's pace.  Tried and not kept: equal shares of all blocks
+// of 64 (eight each): 78 us (5.1 TB/s) and 8.  Neither memory nor issue is
+// full (0.82 and 0.75 of the copy rate, 50 and 65 % of the issue slots): the
+// registers of queries and O leave 8 and 16 warps an SM, too few to hide the
+// chains that turn codes into fp16 (five instructions for four codes, and two
+// more to pair V's) and into weights.  Tried and not kept: equal shares of all blocks
 // over one wave of CTAs (62 and 104 us against 54 and 88 for the calls: SMs
 // differ in speed, and the shares' state costs registers), three CTAs an SM
 // for head_dim 128 (66 against 54: spills), two and six waves of parts

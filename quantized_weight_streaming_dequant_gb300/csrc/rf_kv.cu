@@ -5,8 +5,10 @@
 // One power-of-two scale per 32 tokens of a head.  A power of two makes every
 // held value exact in fp32 (and in fp16 products of the attention kernels),
 // and lets a block grow its scale by re-rounding held codes (a right shift to
-// nearest even) without the original values: a block's scale doubles a few
-// times at most, and each re-rounding errs by at most half a new unit.
+// nearest even) without the original values.  Each of the 31 later tokens may
+// make it grow, by 80 doublings in all; a re-rounding errs by at most half its
+// new unit and units at least double, so the errors of a value, its first
+// rounding among them, sum to less than one unit of the last scale.
 //
 // The rotation rounds each product and the sum on its own, so that the codes
 // do not depend on how a compiler contracts them.
