@@ -75,9 +75,24 @@ def test_prompt_and_tokens(fmt):
     rng = np.random.default_rng([fmt, 1])
     c = Checked(fmt, rng, [[5, 2, 7, 0]], window=48 if fmt == rf.Q4_0 else 0)
     past = 0
-    for n in (130, 1, 5, 1, 20):                                # tiles, rows, rows in a chunk
+    for n in (130, 1, 5, 1, 20):                                # the GEMM, the GEMV and its batched form
         batch = rf.KVBatch(i32(c.table), i32([past]), i32([0, n]), n)
         o = c.layer.step(residual(rng, n), residual(rng, n), c.cache, batch, prev_post=c.layer.post_ffn, max_len=past + n)
+        c.check(o, [past], [n])
+        past += n
+    assert rf.device_status() == rf.OK
+
+
+@pytest.mark.parametrize("window", [0, 300])
+def test_a_prompt_through_the_tiles(window):
+    rng = np.random.default_rng([31, window])
+    c = Checked(rf.Q8_0, rng, [[4, 0, 7, 2, 6, 1, 5, 3]], window=window)
+    past = 0
+    for n in (500, 1, 9):
+        batch = rf.KVBatch(i32(c.table), i32([past]), i32([0, n]), n)
+        o = c.layer.step(residual(rng, n), residual(rng, n), c.cache, batch, max_len=past + n)
+        plan = rf.debug_attention_plan(c.cache, batch, o["q_rot"], window=window, max_len=past + n)
+        assert plan["tiles"] == (n == 500)
         c.check(o, [past], [n])
         past += n
     assert rf.device_status() == rf.OK
