@@ -56,7 +56,7 @@ def listed():
         # a projection of its own for each of many groups, few rows in most and none in some
         _grouped("grouped_few", "Q8_0", "f32", 45, 64, 1408, 2048, False),
         # ragged groups of a prompt, with a bias for each group
-        _grouped("grouped_prompt", "Q4_0", "bf16", 5000, 24, 4000, 2080, True),
+        _grouped("grouped_prompt", "Q4_0", "f16", 5000, 24, 4000, 2080, True),
         # a decode batch through the 128-expert layer of the benchmark: nearly all weights for few rows
         _moe("moe_few", "MXFP4", "f32", 6, 128, 4, 2880, 2880, True, False),
         # a short chunk of odd length through the same layer
@@ -64,7 +64,7 @@ def listed():
         # a prompt through the same layer
         _moe("moe_prompt", "MXFP4", "bf16", 2048, 128, 4, 2880, 2880, True, False),
         # few large experts of the dense layer's sizes
-        _moe("moe_large", "Q4_0", "f16", 1001, 8, 2, 4096, 11008, False, True),
+        _moe("moe_large", "Q4_0", "bf16", 1001, 8, 2, 4096, 11008, False, True),
         # just more tokens than the multi-token GEMV takes: gate and up of the dense layer
         _fused("fused_few", "Q4_0", "f32", 9, 11008, 4096, "swiglu", False, False),
         # a chunk of odd length through a biased projection
