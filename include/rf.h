@@ -756,6 +756,151 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
                                            int dtype, int n_heads, int64_t window,
                                            int64_t max_len);
 
+/* ------------------------------------------- chunks of tokens, typed */
+/* Quantized weights times a chunk of tokens with everything around the product
+ * in the same pass: bias, activation (of one projection, or of a gate and an
+ * up projection) and residual, for one matrix or for a stack of matrices that
+ * each multiply their own rows (experts).  (neurostream, "What the numbers
+ * taught us", names the chunked prefill and "GPT-OSS-120B" the biased experts;
+ * the pages print no form for chunks, so each is defined here.)
+ *
+ * Formats: RF_Q4_0, RF_Q8_0, RF_MXFP4, RF_Q4_K (others:
+ * RF_ERR_UNSUPPORTED_FMT).  X, Y and residual are of one `dtype` (RF_F32,
+ * RF_F16, RF_BF16); biases are fp32.  Y is computed in fp32 and rounded once.
+ * Precision, from the operands of the tensor cores (products are exact, sums
+ * fp32).  Each row of X is scaled by a power of two that puts its largest
+ * finite value at [2^14, 2^15); its values enter
+ *   RF_F32        as two fp16 terms (22 bits; below 2^-28 of the row's largest:
+ *                 to 2^-50 of it),
+ *   RF_F16, BF16  as they are (below 2^-28 of the largest, 2^-25 for RF_F16: to
+ *                 2^-39 of it).
+ * Weights (below 65504 in magnitude) enter
+ *   MXFP4         as they are (below 2^-24: to 2^-25),
+ *   others        RF_F32 and RF_F16: as two fp16 terms (22 bits, small ones to
+ *                 2^-36); RF_BF16: rounded once to fp16, as rf_gemm's (2^-12
+ *                 relative, a sixteenth of half a step of bf16).
+ * A row of X that holds an infinity or a NaN has products that are infinite or
+ * NaN (the activations clamp infinities, NaN stays); other rows do not see it.  Results do not depend on the other rows' values or on
+ * timing (the number of rows chooses how sums are shared out).
+ * Weight tensors: 16-byte aligned, rows of rf_row_bytes each; all bytes of the
+ * tensors given may be read.  Workspaces: device, 256-byte aligned, at least
+ * the stated bytes, overwritten, used by one call at a time. */
+#define RF_ACT_NONE 0           /* z */
+#define RF_ACT_SILU 1           /* z / (1 + exp(-z)) */
+#define RF_ACT_GELU 2           /* z / 2 * (1 + erf(z / sqrt(2))) */
+#define RF_ACT_SWIGLU 3         /* z / (1 + exp(-z)) * u */
+#define RF_ACT_SWIGLU_CLAMPED 4 /* z' / (1 + exp(-alpha z')) * (u' + 1), z' = min(z, limit),
+                                 * u' = min(max(u, -limit), limit) (rf_moe_ffn_biased's) */
+
+/* What follows a product z = W x: y = residual + act(z + bias, U x + up_bias).
+ * bias, up_bias: one float per output row of each matrix (stacked like the
+ * matrices), or NULL; up_bias only with the gated activations (SWIGLU,
+ * SWIGLU_CLAMPED), which take a second matrix U.  residual: rows of the
+ * call's dtype ld_residual elements apart, one for each row of Y, or NULL.
+ * alpha, limit: SWIGLU_CLAMPED's, as rf_moe_ffn_biased's. */
+typedef struct rf_epilogue {
+    const float *bias, *up_bias;
+    const void *residual;
+    int64_t ld_residual;
+    int32_t act;
+    float alpha, limit;
+    int32_t reserved;   /* 0 */
+} rf_epilogue;
+
+/* Y[t] = residual[t] + act(W X[t] + bias, U X[t] + up_bias) for t < n_tok, over
+ * the rows [row_start, row_end) of W (and of `up`, U, with a gated
+ * activation; NULL without).  X: n_tok rows of in_dim, ldx apart; Y and
+ * residual: n_tok rows of row_end - row_start; biases: row_end - row_start.
+ * epi NULL: no bias, activation or residual.  Y may be residual (with equal
+ * strides); other overlaps are not allowed.
+ * Errors: RF_ERR_UNSUPPORTED_FMT (format or dtype); RF_ERR_INVALID_ARG (null
+ * pointer, in_dim not a positive multiple of the format's block, bad window,
+ * n_tok < 0, a row stride below the row, an unknown activation, `up` with an
+ * activation that is not gated or missing with one that is, up_bias without
+ * `up`, alpha NaN or infinite or limit not positive with SWIGLU_CLAMPED,
+ * workspace missing or too small); RF_ERR_MISALIGNED (weights not to 16
+ * bytes, workspace not to 256, others not to their element);
+ * RF_ERR_TOO_LARGE (in_dim above 2^20, more than 2^31 - 1 rows, or more than
+ * 2^30 pieces of 16 tokens or of 64 rows x 64 tokens).  Empty work is a
+ * no-op. */
+RF_API rf_status rf_gemm_fused(int fmt, const void *W, const void *up, int64_t row_start,
+                               int64_t row_end, int64_t in_dim, int dtype, int64_t n_tok,
+                               const void *X, int64_t ldx, const rf_epilogue *epi, void *Y,
+                               int64_t ldy, void *workspace, size_t workspace_bytes,
+                               void *stream);
+/* Bytes of workspace rf_gemm_fused needs; 0 when the arguments are invalid. */
+RF_API size_t rf_gemm_fused_workspace_bytes(int fmt, int64_t rows, int64_t in_dim, int dtype,
+                                            int64_t n_tok);
+
+/* The same for a stack of n_group matrices (n_group, rows, in_dim) that each
+ * multiply rows of their own: row r of Y belongs to the group g with
+ * offsets[g] <= r < offsets[g + 1] and is
+ *     Y[r] = residual[r] + act(W_g x_r + bias_g, U_g x_r + up_bias_g),
+ * x_r = X[r] without `order`, X[order[r] / per] with it (rf_moe_route_tokens:
+ * per = top_k).  offsets: device int32, n_group + 1, not decreasing, within
+ * [0, n_row]; order: device int32, n_row, or NULL; both are read by the
+ * kernels, so a captured call can be replayed with other sizes.  n_row: rows
+ * of Y at most (for the launch shape and the workspace); rows of Y that
+ * belong to no group are left as they were.  n_x: rows of X (without `order`
+ * at least n_row).  biases: (n_group, rows).  A group whose offsets decrease
+ * or leave [0, n_row] is skipped, a row whose order entry leaves X counts as
+ * zero (its Y is what zeros give), and rf_device_status reports
+ * RF_ERR_INVALID_ARG.
+ * Errors: as rf_gemm_fused; RF_ERR_INVALID_ARG for n_group < 1, per < 1,
+ * n_x < 0 or too few rows of X; RF_ERR_TOO_LARGE for n_group > 65536. */
+RF_API rf_status rf_gemm_grouped(int fmt, const void *W, const void *up, int n_group, int64_t rows,
+                                 int64_t in_dim, int dtype, const void *X, int64_t ldx, int64_t n_x,
+                                 const int32_t *offsets, const int32_t *order, int per,
+                                 int64_t n_row, const rf_epilogue *epi, void *Y, int64_t ldy,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+RF_API size_t rf_gemm_grouped_workspace_bytes(int fmt, int n_group, int64_t rows, int64_t in_dim,
+                                              int dtype, int64_t n_row);
+
+/* Routing of a chunk: for each of n_tok rows of n_expert logits (of `dtype`,
+ * ld apart) what rf_moe_route gives, and the chunk's rows in the order of
+ * their experts.
+ *   idx, w   n_tok x top_k: the experts, best first (ties to the lower
+ *            index, a NaN logit counts as -inf), and the softmax over them;
+ *   offsets  n_expert + 1: offsets[e] rows go to experts below e;
+ *   order    n_tok * top_k: the flat index token * top_k + slot of each row,
+ *            by expert, then by flat index;
+ *   place    n_tok * top_k: the row of each flat index (order's inverse).
+ * (A token whose selected logits are all -inf has NaN weights, one with a
+ * +inf logit too, as the softmax gives.)  workspace:
+ * rf_moe_route_tokens_workspace_bytes (NULL if that is 0).
+ * Errors: RF_ERR_UNSUPPORTED_FMT (dtype); RF_ERR_INVALID_ARG (null pointer,
+ * n_expert not in 1..1024, top_k not in 1..min(n_expert, 8), ld < n_expert,
+ * n_tok < 0, workspace missing or too small); RF_ERR_MISALIGNED;
+ * RF_ERR_TOO_LARGE (n_tok * top_k above 2^30).  n_tok 0 sets offsets to 0. */
+RF_API rf_status rf_moe_route_tokens(int dtype, const void *logits, int64_t ld, int64_t n_tok,
+                                     int n_expert, int top_k, int32_t *idx, float *w,
+                                     int32_t *offsets, int32_t *order, int32_t *place,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+RF_API size_t rf_moe_route_tokens_workspace_bytes(int64_t n_tok, int n_expert, int top_k);
+
+/* Routed FFN of a chunk over stacked experts, gate and up (n_expert, n_ff,
+ * n_embd), down (n_expert, n_embd, n_ff):
+ *     y_t = residual_t + sum_k w_tk (D_e h_tk + down_bias_e),
+ *     h_tk = act(G_e x_t + gate_bias_e, U_e x_t + up_bias_e),  e = idx_tk,
+ * with the routing of rf_moe_route_tokens over `logits` (n_tok rows of
+ * n_expert, of logits_dtype, ld_logits apart), act RF_ACT_SWIGLU or
+ * RF_ACT_SWIGLU_CLAMPED (alpha, limit), the sum in selection order.  The h
+ * are kept in fp32 and enter the second product like rows of X (16-bit
+ * dtypes: rounded once to fp16).  Biases and residual may be NULL; Y may be
+ * residual (with equal strides), other overlaps are not allowed.  No host
+ * synchronisation; the call can be captured.
+ * Errors: as rf_gemm_grouped and rf_moe_route_tokens. */
+RF_API rf_status rf_moe_ffn_tokens(int fmt, int dtype, int logits_dtype, const void *logits,
+                                   int64_t ld_logits, int n_expert, int top_k, int64_t n_tok,
+                                   const void *gate, const void *up, const void *down,
+                                   const float *gate_bias, const float *up_bias,
+                                   const float *down_bias, int act, float alpha, float limit,
+                                   int64_t n_ff, int64_t n_embd, const void *X, int64_t ldx,
+                                   const void *residual, int64_t ld_residual, void *Y, int64_t ldy,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+RF_API size_t rf_moe_tokens_workspace_bytes(int fmt, int n_expert, int top_k, int64_t n_ff,
+                                            int64_t n_embd, int dtype, int64_t n_tok);
+
 /* --------------------------------------------------------------- status */
 /* Synchronizes the current device, then reports and clears the device status
  * word that kernels set when a bounded wait times out, or RF_ERR_INVALID_ARG

@@ -23,6 +23,7 @@ BLOCK_ELEMS = {Q4_0: 32, Q8_0: 32, Q4_K: 256, Q6_K: 256, MXFP4: 32}
 
 F32, F16, BF16 = 0, 1, 30           # activation types
 ROPE_HALF, ROPE_PAIRS = 0, 1        # rotation styles
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU, ACT_SWIGLU_CLAMPED = 0, 1, 2, 3, 4   # activations of rf_epilogue
 KV_BLOCK = 32                       # tokens that share a scale byte of the KV cache
 
 OK = 0
@@ -78,6 +79,12 @@ class AttentionPlan(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("up_bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("act", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("limit", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _SIGS = {
     "rf_status_str": ([_I], ctypes.c_char_p),
@@ -129,6 +136,16 @@ _SIGS = {
     "rf_attention": ([_P, _P, _I, _P, _I64, _I64, _I, ctypes.c_float, _I64, _P, _P, _I64, _I64,
                       _I64, _P, _SZ, ctypes.c_uint, _P], _I),
     "rf_attention_workspace_bytes": ([_P, _P, _I, _I, _I64, _I64], _SZ),
+    "rf_gemm_fused": ([_I, _P, _P, _I64, _I64, _I64, _I, _I64, _P, _I64, _P, _P, _I64, _P, _SZ, _P], _I),
+    "rf_gemm_fused_workspace_bytes": ([_I, _I64, _I64, _I, _I64], _SZ),
+    "rf_gemm_grouped": ([_I, _P, _P, _I, _I64, _I64, _I, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _I64, _P,
+                         _SZ, _P], _I),
+    "rf_gemm_grouped_workspace_bytes": ([_I, _I, _I64, _I64, _I, _I64], _SZ),
+    "rf_moe_route_tokens": ([_I, _P, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "rf_moe_route_tokens_workspace_bytes": ([_I64, _I, _I], _SZ),
+    "rf_moe_ffn_tokens": ([_I, _I, _I, _P, _I64, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _I, ctypes.c_float,
+                           ctypes.c_float, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P], _I),
+    "rf_moe_tokens_workspace_bytes": ([_I, _I, _I, _I64, _I64, _I, _I64], _SZ),
     "rf_device_status": ([], _I),
     "rf_debug_arm_wait_fault": ([ctypes.c_uint32], _I),
     "rf_debug_attention_plan": ([_P, _P, _I, _I, _I64, _I64, ctypes.POINTER(AttentionPlan)], _I),
@@ -786,6 +803,204 @@ def attention(cache: KVCache, batch: KVBatch, q, out=None, scale: float | None =
                               _f32_ptr(sinks, nh, "sinks"), po, olt, olh, max_len, ws, ws_bytes, flags,
                               _stream(stream)), "rf_attention")
     return out
+
+
+def _matrix_rows(t, what: str):
+    """(pointer, row stride, rows, columns, type) of a 2-D CUDA tensor with contiguous rows."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    n_tok, n = t.shape
+    ld, one = t.stride()
+    if one != 1 and n > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.data_ptr(), ld if n_tok > 1 or ld > n else n, n_tok, n, _dtype(t)
+
+
+def _weights(t, rows: int, fmt: int, in_dim: int, what: str) -> int:
+    """Data pointer of a stack of `rows` quantized rows (uint8, contiguous)."""
+    p = _dev_ptr(t, what)
+    if t.numel() * t.element_size() < rows * (in_dim // BLOCK_ELEMS[fmt]) * BLOCK_BYTES[fmt]:
+        raise ValueError(f"{what} is shorter than its {rows} rows")
+    return p
+
+
+def _known_fmt(fmt: int) -> int:
+    if fmt not in BLOCK_BYTES:
+        raise RFError(2, "weight format")
+    return fmt
+
+
+def _epilogue(n_bias, n_tok, rows, dt, act, up, bias, up_bias, alpha, limit, residual):
+    pr, ldr = _rows(residual, n_tok, rows, dt, "residual")
+    return Epilogue(_f32_ptr(bias, n_bias, "bias"), _f32_ptr(up_bias, n_bias, "up_bias"), pr, ldr, act, alpha, limit, 0)
+
+
+def _space(workspace, need: int, stream, device):
+    """(tensor, pointer, bytes) of a workspace, allocated when not given."""
+    if workspace is None and need > 0:
+        if _empty is None:
+            _look_up()
+        workspace = _new(stream, need, _U8_TYPE, device, out=False)
+    if workspace is None:
+        return None, None, 0
+    return workspace, _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def gemm_fused_workspace(fmt: int, rows: int, in_dim: int, X, stream=None):
+    """Device workspace for gemm_fused() of X on `stream`, or None."""
+    n = lib().rf_gemm_fused_workspace_bytes(fmt, rows, in_dim, _dtype(X), X.shape[0])
+    return _new(stream, n, _U8_TYPE, X.device, out=False) if n else None
+
+
+def gemm_fused(fmt: int, W, row_start: int, row_end: int, in_dim: int, X, Y=None, *, act: int = ACT_NONE, up=None,
+               bias=None, up_bias=None, alpha: float = 1.702, limit: float = 7.0, residual=None, workspace=None,
+               stream=None):
+    """rf_gemm_fused: residual + act(W X + bias, up X + up_bias) for the rows
+    [row_start, row_end).  X (n_tok, in_dim) and residual (n_tok, rows) are of
+    one type (rows may be strided); biases are float32, one per row of the
+    window.  Returns Y (n_tok, rows), of X's type."""
+    _known_fmt(fmt)
+    px, ldx, n_tok, n, dt = _matrix_rows(X, "X")
+    if n != in_dim:
+        raise ValueError(f"X must be (n_tok, {in_dim})")
+    rows = max(row_end - row_start, 0)
+    if Y is None:
+        Y = _new(stream, (n_tok, rows), X.dtype, X.device)
+    py, ldy = _rows(Y, n_tok, rows, dt, "Y")
+    e = _epilogue(rows, n_tok, rows, dt, act, up, bias, up_bias, alpha, limit, residual)
+    if workspace is None:
+        need = lib().rf_gemm_fused_workspace_bytes(fmt, rows, in_dim, dt, n_tok)
+    workspace, ws, ws_bytes = _space(workspace, need if workspace is None else 0, stream, X.device)
+    _check(lib().rf_gemm_fused(fmt, _weights(W, max(row_end, 0), fmt, in_dim, "W"),
+                               None if up is None else _weights(up, max(row_end, 0), fmt, in_dim, "up"), row_start,
+                               row_end, in_dim, dt, n_tok, px, ldx, ctypes.byref(e), py, ldy, ws, ws_bytes,
+                               _stream(stream)), "rf_gemm_fused")
+    return Y
+
+
+def gemm_grouped_workspace(fmt: int, n_group: int, rows: int, in_dim: int, X, n_row: int, stream=None):
+    """Device workspace for gemm_grouped() of n_row rows on `stream`, or None."""
+    n = lib().rf_gemm_grouped_workspace_bytes(fmt, n_group, rows, in_dim, _dtype(X), n_row)
+    return _new(stream, n, _U8_TYPE, X.device, out=False) if n else None
+
+
+def gemm_grouped(fmt: int, W, rows: int, in_dim: int, X, offsets, order=None, per: int = 1, Y=None, *,
+                 act: int = ACT_NONE, up=None, bias=None, up_bias=None, alpha: float = 1.702, limit: float = 7.0,
+                 residual=None, workspace=None, stream=None):
+    """rf_gemm_grouped: row r of Y, in group g (offsets[g] <= r < offsets[g +
+    1]), is residual + act(W_g x + bias_g, up_g x + up_bias_g), where x is row
+    r of X, or row order[r] // per.  W and up are (n_group, rows, in_dim)
+    quantized, offsets (n_group + 1,) and order (n_row,) int32 device tensors,
+    biases (n_group, rows) float32.  Rows of no group are left as they were (a
+    Y made here holds anything there)."""
+    _known_fmt(fmt)
+    px, ldx, n_x, n, dt = _matrix_rows(X, "X")
+    if n != in_dim:
+        raise ValueError(f"X must be (n, {in_dim})")
+    for t, what in ((offsets, "offsets"), (order, "order")):
+        if t is not None and (not t.is_cuda or t.element_size() != 4 or t.is_floating_point() or t.dim() != 1 or
+                              not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous int32 CUDA tensor")
+    n_group, n_row = offsets.numel() - 1, n_x if order is None else order.numel()
+    if Y is None:
+        Y = _new(stream, (n_row, rows), X.dtype, X.device)
+    py, ldy = _rows(Y, n_row, rows, dt, "Y")
+    e = _epilogue(max(n_group, 0) * rows, n_row, rows, dt, act, up, bias, up_bias, alpha, limit, residual)
+    if workspace is None:
+        need = lib().rf_gemm_grouped_workspace_bytes(fmt, n_group, rows, in_dim, dt, n_row)
+    workspace, ws, ws_bytes = _space(workspace, need if workspace is None else 0, stream, X.device)
+    _check(lib().rf_gemm_grouped(fmt, _weights(W, max(n_group, 0) * rows, fmt, in_dim, "W"),
+                                 None if up is None else _weights(up, max(n_group, 0) * rows, fmt, in_dim, "up"),
+                                 n_group, rows, in_dim, dt, px, ldx, n_x, offsets.data_ptr(),
+                                 None if order is None else order.data_ptr(), per, n_row, ctypes.byref(e), py, ldy, ws,
+                                 ws_bytes, _stream(stream)), "rf_gemm_grouped")
+    return Y
+
+
+class MoERouting:
+    """What rf_moe_route_tokens gives, over one int32 device tensor: idx and
+    w (n_tok, top_k), offsets (n_expert + 1,), order and place (n_tok * top_k,)."""
+
+    def __init__(self, n_tok: int, n_expert: int, top_k: int, device, stream=None):
+        import torch
+        n = n_tok * top_k
+        self.n_tok, self.n_expert, self.top_k, self.n_row = n_tok, n_expert, top_k, n
+        self.memory = _new(stream, 4 * n + n_expert + 1, torch.int32, device)
+
+    @property
+    def idx(self):
+        return self.memory[:self.n_row].view(self.n_tok, self.top_k)
+
+    @property
+    def w(self):
+        return self.memory[self.n_row:2 * self.n_row].view(_F32_TYPE).view(self.n_tok, self.top_k)
+
+    @property
+    def order(self):
+        return self.memory[2 * self.n_row:3 * self.n_row]
+
+    @property
+    def place(self):
+        return self.memory[3 * self.n_row:4 * self.n_row]
+
+    @property
+    def offsets(self):
+        return self.memory[4 * self.n_row:]
+
+
+def moe_route_tokens(logits, top_k: int, workspace=None, stream=None) -> MoERouting:
+    """rf_moe_route_tokens: logits (n_tok, n_expert) float32, float16 or
+    bfloat16 (rows may be strided)."""
+    pl, ld, n_tok, n_expert, dt = _matrix_rows(logits, "logits")
+    r = MoERouting(n_tok, n_expert, max(top_k, 0), logits.device, stream)
+    if workspace is None:
+        need = lib().rf_moe_route_tokens_workspace_bytes(n_tok, n_expert, top_k)
+    workspace, ws, ws_bytes = _space(workspace, need if workspace is None else 0, stream, logits.device)
+    at, n = r.memory.data_ptr(), 4 * r.n_row
+    _check(lib().rf_moe_route_tokens(dt, pl, ld, n_tok, n_expert, top_k, at, at + n, at + 4 * n, at + 2 * n, at + 3 * n,
+                                     ws, ws_bytes, _stream(stream)), "rf_moe_route_tokens")
+    return r
+
+
+def moe_tokens_workspace(fmt: int, n_expert: int, top_k: int, n_ff: int, n_embd: int, X, stream=None):
+    """Device workspace for moe_ffn_tokens() of X on `stream`, or None."""
+    n = lib().rf_moe_tokens_workspace_bytes(fmt, n_expert, top_k, n_ff, n_embd, _dtype(X), X.shape[0])
+    return _new(stream, n, _U8_TYPE, X.device, out=False) if n else None
+
+
+def moe_ffn_tokens(fmt: int, logits, top_k: int, gate, up, down, n_ff: int, n_embd: int, X, Y=None, *, gate_bias=None,
+                   up_bias=None, down_bias=None, alpha: float | None = None, limit: float | None = None, residual=None,
+                   workspace=None, stream=None):
+    """rf_moe_ffn_tokens: the routed FFN of a chunk X (n_tok, n_embd) over
+    stacked experts, with the clamped SwiGLU when alpha and limit are given and
+    the plain one without.  logits (n_tok, n_expert) may be of another type
+    than X; biases are float32.  Returns Y (n_tok, n_embd), of X's type."""
+    _known_fmt(fmt)
+    px, ldx, n_tok, n, dt = _matrix_rows(X, "X")
+    pl, ldl, nl, n_expert, ldt = _matrix_rows(logits, "logits")
+    if n != n_embd or nl != n_tok:
+        raise ValueError(f"X must be (n_tok, {n_embd}), logits (n_tok, n_expert)")
+    if (alpha is None) != (limit is None):
+        raise ValueError("alpha and limit belong together")
+    if Y is None:
+        Y = _new(stream, (n_tok, n_embd), X.dtype, X.device)
+    py, ldy = _rows(Y, n_tok, n_embd, dt, "Y")
+    pr, ldr = _rows(residual, n_tok, n_embd, dt, "residual")
+    if workspace is None:
+        need = lib().rf_moe_tokens_workspace_bytes(fmt, n_expert, top_k, n_ff, n_embd, dt, n_tok)
+    workspace, ws, ws_bytes = _space(workspace, need if workspace is None else 0, stream, X.device)
+    clamped = alpha is not None
+    _check(lib().rf_moe_ffn_tokens(fmt, dt, ldt, pl, ldl, n_expert, top_k, n_tok,
+                                   _weights(gate, n_expert * n_ff, fmt, n_embd, "gate"),
+                                   _weights(up, n_expert * n_ff, fmt, n_embd, "up"),
+                                   _weights(down, n_expert * n_embd, fmt, n_ff, "down"),
+                                   _f32_ptr(gate_bias, n_expert * n_ff, "gate_bias"),
+                                   _f32_ptr(up_bias, n_expert * n_ff, "up_bias"),
+                                   _f32_ptr(down_bias, n_expert * n_embd, "down_bias"),
+                                   ACT_SWIGLU_CLAMPED if clamped else ACT_SWIGLU, alpha if clamped else 0.0,
+                                   limit if clamped else 0.0, n_ff, n_embd, px, ldx, pr, ldr, py, ldy, ws, ws_bytes,
+                                   _stream(stream)), "rf_moe_ffn_tokens")
+    return Y
 
 
 def device_status() -> int:

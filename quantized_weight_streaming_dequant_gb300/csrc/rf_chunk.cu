@@ -1,0 +1,639 @@
+// rf_chunk.cu -- entry points of the chunk operators and the kernels around
+// their product (rf_chunk_mma.cu): the token tiles and operand images before
+// it, the sum over a token's experts after it.
+//
+// prep_kernel, one launch:
+//   * its last CTA lists the token tiles: up to T rows of one group each.
+//   * the others write the images.  A granule is 16 operand rows (16 tokens,
+//     or 8 tokens of two terms) of a group; granule q of group g is granule
+//     offsets[g] / GT + g + q of the images: no two groups meet, and no scan
+//     over the groups is needed to find a place.  A CTA takes a granule, or a
+//     share of its slices: the rows' largest values give their powers of two,
+//     then the rows are rounded to fp16 in the layout of the MMA's operand
+//     (K-major core matrices, 2 KB a granule and slice, written whole).
+// It reads X once from memory (the second pass over a row finds it in cache)
+// and writes 2 bytes an element (4 with two terms).  At most a few percent of
+// a prompt's time; with few rows, its latency.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "rf_chunk.h"
+#include "rf_device.cuh"
+#include "rf_half.cuh"
+
+namespace rf {
+namespace {
+
+__device__ int g_chunk_invalid = 0;   // offsets or order entries out of range
+
+constexpr int kPrepThreads = 256;
+constexpr int64_t kMaxPieces = 1LL << 30;
+
+template <int DT> struct Elem;
+template <> struct Elem<RF_F32> { using T = float; };
+template <> struct Elem<RF_F16> { using T = __half; };
+template <> struct Elem<RF_BF16> { using T = __nv_bfloat16; };
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Four consecutive elements (vec: aligned to them all).
+__device__ __forceinline__ void load4(const float *x, bool vec, float (&f)[4])
+{
+    if (vec) {
+        const float4 v = *reinterpret_cast<const float4 *>(x);
+        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = x[e];
+    }
+}
+template <class T>
+__device__ __forceinline__ void load4(const T *x, bool vec, float (&f)[4])
+{
+    T t[4];
+    if (vec) *reinterpret_cast<uint2 *>(t) = *reinterpret_cast<const uint2 *>(x);
+    else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = x[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = to_f32(t[e]);
+}
+
+struct PrepParams {
+    const void *X;
+    int64_t ldx, n_x;
+    const int32_t *offsets;   // NULL: one group of all rows
+    const int32_t *order;
+    int32_t per, n_row, n_group;
+    int32_t in_dim, nst, order8;   // order8: which inputs a 16-byte unit holds
+    int32_t tile_tokens, cap_tiles, cap_gran, parts, vec;
+    ChunkPlan *plan;
+    ChunkTile *tiles;
+    float *inv;               // by place in the granules
+    uint8_t *img;
+};
+
+// Rows [a, b) of group g; none when its offsets are not in order.
+__device__ __forceinline__ bool group_rows(const PrepParams &p, int g, int &a, int &b)
+{
+    a = p.offsets ? p.offsets[g] : 0;
+    b = p.offsets ? p.offsets[g + 1] : p.n_row;
+    const bool ok = a >= 0 && b >= a && b <= p.n_row;
+    if (!ok) a = b = 0;
+    return ok;
+}
+
+// Exclusive prefix sum over the CTA, and the total.
+__device__ __forceinline__ int scan_block(int v, int *part, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int base = 0, sum = 0;
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+        if (w < warp) base += part[w];
+        sum += part[w];
+    }
+    __syncthreads();
+    *total = sum;
+    return base + x - v;
+}
+
+template <int GT>
+__device__ void list_tiles(const PrepParams &p)
+{
+    __shared__ int part[kPrepThreads / 32];
+    int next = 0;
+    for (int g0 = 0; g0 < p.n_group; g0 += kPrepThreads) {
+        const int g = g0 + (int)threadIdx.x;
+        int a = 0, b = 0;
+        if (g < p.n_group && !group_rows(p, g, a, b)) record_status(&g_chunk_invalid, RF_ERR_INVALID_ARG);
+        const int n = (b - a + p.tile_tokens - 1) / p.tile_tokens;
+        int total;
+        const int at = next + scan_block(n, part, &total);
+        for (int t = 0; t < n && at + t < p.cap_tiles; ++t) {
+            ChunkTile w;
+            w.group = g;
+            w.row0 = a + t * p.tile_tokens;
+            w.cnt = min(p.tile_tokens, b - w.row0);
+            w.gran = a / GT + g + t * (p.tile_tokens / GT);
+            p.tiles[at + t] = w;
+        }
+        next += total;
+    }
+    if (threadIdx.x == 0) {
+        p.plan->n_tiles = min(next, p.cap_tiles);   // (more only when groups overlap)
+        p.plan->next = 0;
+    }
+}
+
+// Which inputs the 16-byte units of a 32-input block hold, as the decoders
+// of rf_chunk_mma.cu order a block's weights: unit u is made of a =
+// inputs 4u.. and b = 16 + 4u.. (kOrderPairs, kOrderSpread), or 8u.. and
+// 8u + 4.. (kOrderPlain).
+constexpr int kOrderPlain = 0, kOrderPairs = 1, kOrderSpread = 2;
+__device__ __forceinline__ void slice_order(int order, const float (&a)[4], const float (&b)[4], float (&f)[8])
+{
+    if (order == kOrderPairs) {          // MXFP4: the two nibbles of a byte
+        f[0] = a[0], f[1] = b[0], f[2] = a[1], f[3] = b[1], f[4] = a[2], f[5] = b[2], f[6] = a[3], f[7] = b[3];
+    } else if (order == kOrderSpread) {  // Q4_0: nibbles four apart in a word
+        f[0] = a[0], f[1] = a[2], f[2] = b[0], f[3] = b[2], f[4] = a[1], f[5] = a[3], f[6] = b[1], f[7] = b[3];
+    } else {
+        f[0] = a[0], f[1] = a[1], f[2] = a[2], f[3] = a[3], f[4] = b[0], f[5] = b[1], f[6] = b[2], f[7] = b[3];
+    }
+}
+
+template <int DT, int XT>
+__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ PrepParams p)
+{
+    using T = typename Elem<DT>::T;
+    constexpr int GT = kGranRows / XT;
+    if (blockIdx.x == gridDim.x - 1) {
+        list_tiles<GT>(p);
+        return;
+    }
+    const int gran = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int s_group, s_row, s_cnt, s_n, s_at;
+    __shared__ float s_scale[GT];
+    __shared__ int64_t s_src[GT];
+    if (tid == 0) s_group = -1;
+    __syncthreads();
+    for (int g = tid; g < p.n_group; g += kPrepThreads) {
+        int a, b;
+        if (!group_rows(p, g, a, b)) continue;
+        const int q = gran - (a / GT + g);
+        if (q < 0 || q >= (b - a + GT - 1) / GT) continue;
+        const int tt = p.tile_tokens / GT;   // granules per whole tile
+        s_group = g;
+        s_row = a + q * GT;
+        s_cnt = min(GT, b - s_row);
+        s_at = gran - q + q / tt * tt;       // the tile's first granule
+        s_n = min(tt, (b - a - q / tt * p.tile_tokens + GT - 1) / GT);
+    }
+    __syncthreads();
+    if (s_group < 0) return;
+    const int cnt = s_cnt;
+    // Scales: a warp per row.
+    for (int r = warp; r < GT; r += kPrepThreads / 32) {
+        int64_t src = -1;
+        if (r < cnt) {
+            const int row = s_row + r;
+            src = p.order ? p.order[row] / p.per : row;
+            if (p.order && (p.order[row] < 0 || src >= p.n_x)) {
+                src = -1;
+                if (lane == 0) record_status(&g_chunk_invalid, RF_ERR_INVALID_ARG);
+            }
+        }
+        float m = 0.f;
+        if (src >= 0) {
+            const T *x = static_cast<const T *>(p.X) + src * p.ldx;
+            for (int k = 4 * lane; k < p.in_dim; k += 128) {
+                float f[4];
+                load4(x + k, p.vec, f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = fabsf(f[e]);
+                    if (v < INFINITY) m = fmaxf(m, v);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // The largest value to [2^14, 2^15), by a factor within fp32's normal
+        // numbers (so is its inverse).
+        const int e = (int)(__float_as_uint(m) >> 23) - 127;
+        const int k = m == 0.f ? 0 : max(-126, min(126, 14 - e));
+        if (lane == 0) {
+            s_scale[r] = __uint_as_float((uint32_t)(k + 127) << 23);
+            s_src[r] = src;
+            if (part == 0) p.inv[(int64_t)gran * GT + r] = __uint_as_float((uint32_t)(127 - k) << 23);
+        }
+    }
+    __syncthreads();
+    // Units: thread (r, c) writes inputs 8c.. of a slice of token r (its high
+    // and its low term).
+    constexpr int kUnits = GT * 8;
+    const int r = (tid & 7) + (GT == 16 ? ((tid >> 6) & 1) * 8 : 0), c = (tid >> 3) & 7;
+    const float scale = s_scale[r];
+    const int64_t src = s_src[r];
+    const T *x = static_cast<const T *>(p.X) + (src >= 0 ? src * p.ldx : 0);
+    const int first = c >> 2, u = c & 3;
+    const int ka = 32 * first + (p.order8 == kOrderPlain ? 8 * u : 4 * u);
+    const int kb = ka + (p.order8 == kOrderPlain ? 4 : 16);
+    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * kGranBytes +
+                   (GT == 16 ? (r >> 3) * 1024 : 0) + c * 128 + (r & 7) * 16;
+    const int64_t step = (int64_t)s_n * kGranBytes;
+    for (int s = part * (kPrepThreads / kUnits) + tid / kUnits; s < p.nst; s += p.parts * (kPrepThreads / kUnits)) {
+        float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f}, f[8];
+        const int k0 = s * kSliceK;
+        if (src >= 0 && k0 + 32 * first < p.in_dim) {   // (whole blocks)
+            load4(x + k0 + ka, p.vec, a);
+            load4(x + k0 + kb, p.vec, b);
+        }
+        slice_order(p.order8, a, b, f);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f0 = f[2 * e] * scale, f1 = f[2 * e + 1] * scale;
+            const __half2 v = __floats2half2_rn(f0, f1);
+            h[e] = h2_bits(v);
+            if constexpr (XT == 2) {
+                const float2 w = __half22float2(v);
+                l[e] = h2_bits(__floats2half2_rn(fabsf(w.x) < INFINITY ? (f0 - w.x) * 2048.f : 0.f,
+                                                 fabsf(w.y) < INFINITY ? (f1 - w.y) * 2048.f : 0.f));
+            }
+        }
+        *reinterpret_cast<uint4 *>(out + s * step) = make_uint4(h[0], h[1], h[2], h[3]);
+        if constexpr (XT == 2) *reinterpret_cast<uint4 *>(out + s * step + 1024) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+// y_t = residual_t + sum_k w_tk d[place_tk], in selection order; four columns a
+// thread.
+struct JoinParams {
+    const float *d, *w;
+    const int32_t *place;
+    const void *residual;
+    void *Y;
+    int64_t ldr, ldy, n_tok, n, ldd;
+    int32_t top_k, nb, vec;
+};
+template <int DT>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p)
+{
+    using T = typename Elem<DT>::T;
+    const int64_t t = blockIdx.x / p.nb;
+    const int64_t c = 4 * ((int64_t)(blockIdx.x % p.nb) * 256 + threadIdx.x);
+    if (c >= p.n) return;   // (a multiple of 32)
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < p.top_k; ++k) {
+        const float w = p.w[t * p.top_k + k];
+        const float4 v = *reinterpret_cast<const float4 *>(p.d + (int64_t)p.place[t * p.top_k + k] * p.ldd + c);
+        y[0] = fmaf(w, v.x, y[0]), y[1] = fmaf(w, v.y, y[1]), y[2] = fmaf(w, v.z, y[2]), y[3] = fmaf(w, v.w, y[3]);
+    }
+    if (p.residual) {
+        float f[4];
+        load4(static_cast<const T *>(p.residual) + t * p.ldr + c, p.vec, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += f[e];
+    }
+    T o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (DT == RF_F32) o[e] = y[e];
+        else if constexpr (DT == RF_F16) o[e] = __float2half_rn(y[e]);
+        else o[e] = __float2bfloat16_rn(y[e]);
+    }
+    T *out = static_cast<T *>(p.Y) + t * p.ldy + c;
+    if (p.vec) {
+        if constexpr (DT == RF_F32) *reinterpret_cast<float4 *>(out) = *reinterpret_cast<float4 *>(o);
+        else *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<uint2 *>(o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = o[e];
+    }
+}
+
+bool fmt_has_chunks(int fmt) { return fmt == RF_Q4_0 || fmt == RF_Q8_0 || fmt == RF_MXFP4 || fmt == RF_Q4_K; }
+bool dtype_ok(int d) { return d == RF_F32 || d == RF_F16 || d == RF_BF16; }
+int dtype_size(int d) { return d == RF_F32 ? 4 : 2; }
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// The operands of a product of n_row rows shared by n_group groups.  Tiles of
+// 256 operand rows where the groups fill them: a weight slice is decoded once
+// per tile, and 256 rows of products (512 cycles) cover the decoding, 128 do
+// not quite.  Smaller groups take tiles of 128, whose sums fit tensor memory
+// twice, so that an item's epilogue runs beside the next one's products.
+ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row)
+{
+    ChunkShape sh;
+    sh.fmt = fmt;
+    sh.xt = dtype == RF_F32 ? 2 : 1;
+    sh.wt = dtype != RF_BF16 && fmt != RF_MXFP4 ? 2 : 1;
+    sh.n_row = n_row, sh.n_group = n_group, sh.rows = rows, sh.in_dim = in_dim;
+    sh.nst = (int)((in_dim + kSliceK - 1) / kSliceK);
+    const int64_t each = (n_row + n_group - 1) / n_group * sh.xt;   // operand rows of a group
+    sh.nt = sh.wt == 1 && sh.xt == 1 && each > 128 ? 256 : 128;
+    const int64_t T = sh.tile_tokens(), GT = sh.gran_tokens();
+    sh.cap_tiles = std::min<int64_t>(n_row, n_row / T + n_group);
+    sh.cap_gran = n_row / GT + n_group;
+    size_t at = sizeof(ChunkPlan);
+    sh.at_tiles = at, at = up256(at + (size_t)sh.cap_tiles * sizeof(ChunkTile));
+    sh.at_inv = at, at = up256(at + (size_t)sh.cap_gran * GT * sizeof(float));
+    sh.at_img = at, at = up256(at + (size_t)sh.cap_gran * sh.nst * kGranBytes);
+    sh.bytes = at;
+    return sh;
+}
+
+// Sizes that a product takes, for the entry points and the workspace.
+rf_status check_sizes(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row)
+{
+    if (!fmt_has_chunks(fmt) || !dtype_ok(dtype)) return RF_ERR_UNSUPPORTED_FMT;
+    if (n_group < 1 || rows < 0 || n_row < 0 || in_dim <= 0 || in_dim % block_elems_of(fmt) != 0) return RF_ERR_INVALID_ARG;
+    if (in_dim > (1 << 20) || rows > 0x7fffffffLL || n_group > 65536 || n_row > kMaxPieces) return RF_ERR_TOO_LARGE;
+    const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row);
+    if (sh.cap_gran > kMaxPieces || sh.cap_tiles * ((rows + 63) / 64) > kMaxPieces) return RF_ERR_TOO_LARGE;
+    return RF_OK;
+}
+
+bool gated_act(int act) { return act == RF_ACT_SWIGLU || act == RF_ACT_SWIGLU_CLAMPED; }
+
+rf_status check_epilogue(const rf_epilogue &e, const void *up, int dtype, int64_t rows)
+{
+    if (e.act < RF_ACT_NONE || e.act > RF_ACT_SWIGLU_CLAMPED || e.reserved != 0) return RF_ERR_INVALID_ARG;
+    if (gated_act(e.act) != (up != nullptr) || (e.up_bias && !up)) return RF_ERR_INVALID_ARG;
+    if (e.act == RF_ACT_SWIGLU_CLAMPED && (!(e.alpha > -INFINITY && e.alpha < INFINITY) || !(e.limit > 0.f)))
+        return RF_ERR_INVALID_ARG;
+    if (e.residual && e.ld_residual < rows) return RF_ERR_INVALID_ARG;
+    return RF_OK;
+}
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+struct Source {
+    int dtype;
+    const void *X;
+    int64_t ldx, n_x;
+    const int32_t *offsets, *order;
+    int per;
+};
+
+template <int DT, int XT>
+rf_status launch_prep_t(const PrepParams &p, int64_t blocks, cudaStream_t s)
+{
+    prep_kernel<DT, XT><<<(unsigned)(blocks + 1), kPrepThreads, 0, s>>>(p);
+    return last_cuda_error();
+}
+
+// The token tiles and the images of one product's rows.
+rf_status launch_prep(const ChunkShape &sh, const Source &x, uint8_t *ws, cudaStream_t s)
+{
+    PrepParams p;
+    p.X = x.X, p.ldx = x.ldx, p.n_x = x.n_x;
+    p.offsets = x.offsets, p.order = x.order, p.per = x.per;
+    p.n_row = (int32_t)sh.n_row, p.n_group = (int32_t)sh.n_group;
+    p.in_dim = (int32_t)sh.in_dim, p.nst = sh.nst;
+    p.order8 = sh.fmt == RF_MXFP4 ? kOrderPairs : (sh.fmt == RF_Q4_0 ? kOrderSpread : kOrderPlain);
+    p.tile_tokens = sh.tile_tokens();
+    p.cap_tiles = (int32_t)sh.cap_tiles, p.cap_gran = (int32_t)sh.cap_gran;
+    const int size = dtype_size(x.dtype);
+    p.vec = aligned(x.X, 4 * size) && (x.ldx * size) % (4 * size) == 0;
+    p.plan = reinterpret_cast<ChunkPlan *>(ws);
+    p.tiles = reinterpret_cast<ChunkTile *>(ws + sh.at_tiles);
+    p.inv = reinterpret_cast<float *>(ws + sh.at_inv);
+    p.img = ws + sh.at_img;
+    // A granule's slices are shared out while there are few granules (each
+    // share finds the rows' maxima again).
+    const int64_t busy = std::min<int64_t>(sh.cap_gran, sh.n_row);   // granules with rows, at most
+    p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((sh.nst + 3) / 4, 2 * num_sms() / std::max<int64_t>(1, busy)));
+    const int64_t blocks = sh.cap_gran * p.parts;
+    if (blocks > 0x7ffffffeLL) return RF_ERR_TOO_LARGE;
+    if (x.dtype == RF_F32)
+        return sh.xt == 2 ? launch_prep_t<RF_F32, 2>(p, blocks, s) : launch_prep_t<RF_F32, 1>(p, blocks, s);
+    return x.dtype == RF_F16 ? launch_prep_t<RF_F16, 1>(p, blocks, s) : launch_prep_t<RF_BF16, 1>(p, blocks, s);
+}
+
+// Prepared and multiplied.  `total_rows`: rows of the weight tensors.
+rf_status run_product(const ChunkShape &sh, const Source &x, const void *W, const void *up, int64_t row0, int64_t group_rows,
+                      int64_t total_rows, const rf_epilogue &epi, int dtype, void *Y, int64_t ldy, void *ws, cudaStream_t s)
+{
+    rf_status st = launch_prep(sh, x, static_cast<uint8_t *>(ws), s);
+    if (st != RF_OK) return st;
+    ChunkGemm g;
+    g.sh = sh;
+    g.W = static_cast<const uint8_t *>(W);
+    g.up = static_cast<const uint8_t *>(up);
+    g.row0 = row0, g.group_rows = group_rows, g.total_rows = total_rows;
+    g.epi = epi;
+    g.dtype = dtype;
+    g.Y = Y, g.ldy = ldy;
+    g.ws = static_cast<uint8_t *>(ws);
+    return launch_chunk_mma(g, s);
+}
+
+rf_status check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (need == 0) return RF_OK;
+    if (!ws || have < need) return RF_ERR_INVALID_ARG;
+    return aligned(ws, 256) ? RF_OK : RF_ERR_MISALIGNED;
+}
+
+const rf_epilogue kNoEpilogue = {nullptr, nullptr, nullptr, 0, RF_ACT_NONE, 0.f, 0.f, 0};
+
+// The routed FFN's workspace.
+struct MoeLayout {
+    ChunkShape up, down;
+    size_t at_idx, at_w, at_offsets, at_order, at_place, at_route, at_product, at_h, bytes;
+    int64_t ldd;   // row stride of the experts' outputs
+};
+MoeLayout moe_layout(int fmt, int n_expert, int top_k, int64_t n_ff, int64_t n_embd, int dtype, int64_t n_tok)
+{
+    MoeLayout m;
+    const int64_t n_row = n_tok * top_k;
+    m.up = chunk_shape(fmt, dtype, n_expert, n_ff, n_embd, n_row);
+    m.down = chunk_shape(fmt, dtype, n_expert, n_embd, n_ff, n_row);
+    m.ldd = n_embd;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at = up256(at + n);
+        return here;
+    };
+    m.at_idx = take(4 * n_row), m.at_w = take(4 * n_row), m.at_offsets = take(4 * ((size_t)n_expert + 1));
+    m.at_order = take(4 * n_row), m.at_place = take(4 * n_row);
+    m.at_route = take(route_workspace(n_tok, n_expert, top_k));
+    m.at_product = take(std::max(m.up.bytes, m.down.bytes));   // the second product prepares after the first has run
+    m.at_h = take(4 * (size_t)n_row * std::max(n_ff, n_embd)); // h, read before the experts' outputs are written
+    m.bytes = at;
+    return m;
+}
+
+rf_status check_route(int dtype, const void *logits, int64_t ld, int64_t n_tok, int n_expert, int top_k)
+{
+    if (!dtype_ok(dtype)) return RF_ERR_UNSUPPORTED_FMT;
+    if (n_expert < 1 || n_expert > 1024 || top_k < 1 || top_k > 8 || top_k > n_expert || n_tok < 0 || ld < n_expert ||
+        (!logits && n_tok > 0))
+        return RF_ERR_INVALID_ARG;
+    if (!aligned(logits, dtype_size(dtype))) return RF_ERR_MISALIGNED;
+    if (n_tok > kMaxPieces / top_k) return RF_ERR_TOO_LARGE;
+    return RF_OK;
+}
+
+}  // namespace
+
+rf_status read_and_clear_chunk_invalid()
+{
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_chunk_invalid, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
+    if (v != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_chunk_invalid, &zero, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
+    }
+    return static_cast<rf_status>(v);
+}
+
+}  // namespace rf
+
+using namespace rf;
+
+extern "C" {
+
+size_t rf_gemm_grouped_workspace_bytes(int fmt, int n_group, int64_t rows, int64_t in_dim, int dtype, int64_t n_row)
+{
+    if (check_sizes(fmt, dtype, n_group, rows, in_dim, n_row) != RF_OK || rows == 0 || n_row == 0) return 0;
+    return chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row).bytes;
+}
+
+size_t rf_gemm_fused_workspace_bytes(int fmt, int64_t rows, int64_t in_dim, int dtype, int64_t n_tok)
+{
+    return rf_gemm_grouped_workspace_bytes(fmt, 1, rows, in_dim, dtype, n_tok);
+}
+
+rf_status rf_gemm_fused(int fmt, const void *W, const void *up, int64_t row_start, int64_t row_end, int64_t in_dim, int dtype,
+                        int64_t n_tok, const void *X, int64_t ldx, const rf_epilogue *epi, void *Y, int64_t ldy,
+                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    const rf_epilogue e = epi ? *epi : kNoEpilogue;
+    const int64_t rows = row_end - row_start;
+    if (row_start < 0 || row_end < row_start) return RF_ERR_INVALID_ARG;
+    rf_status st = check_sizes(fmt, dtype, 1, rows, in_dim, n_tok);
+    if (st != RF_OK) return st;
+    if (!W || (n_tok > 0 && (!X || !Y)) || ldx < in_dim || ldy < rows) return RF_ERR_INVALID_ARG;
+    if ((st = check_epilogue(e, up, dtype, rows)) != RF_OK) return st;
+    const int size = dtype_size(dtype);
+    if (!aligned(W, 16) || !aligned(up, 16) || !aligned(X, size) || !aligned(Y, size) || !aligned(e.residual, size) ||
+        !aligned(e.bias, 4) || !aligned(e.up_bias, 4))
+        return RF_ERR_MISALIGNED;
+    if (rows == 0 || n_tok == 0) return RF_OK;
+    const ChunkShape sh = chunk_shape(fmt, dtype, 1, rows, in_dim, n_tok);
+    if ((st = check_workspace(workspace, workspace_bytes, sh.bytes)) != RF_OK) return st;
+    const Source x = {dtype, X, ldx, n_tok, nullptr, nullptr, 1};
+    return run_product(sh, x, W, up, row_start, rows, row_end, e, dtype, Y, ldy, workspace, static_cast<cudaStream_t>(stream));
+}
+
+rf_status rf_gemm_grouped(int fmt, const void *W, const void *up, int n_group, int64_t rows, int64_t in_dim, int dtype,
+                          const void *X, int64_t ldx, int64_t n_x, const int32_t *offsets, const int32_t *order, int per,
+                          int64_t n_row, const rf_epilogue *epi, void *Y, int64_t ldy, void *workspace,
+                          size_t workspace_bytes, void *stream)
+{
+    const rf_epilogue e = epi ? *epi : kNoEpilogue;
+    rf_status st = check_sizes(fmt, dtype, n_group, rows, in_dim, n_row);
+    if (st != RF_OK) return st;
+    if (!W || !offsets || (n_row > 0 && !Y) || (n_x > 0 && !X) || n_x < 0 || ldx < in_dim || ldy < rows || per < 1 ||
+        (!order && n_x < n_row))
+        return RF_ERR_INVALID_ARG;
+    if ((st = check_epilogue(e, up, dtype, rows)) != RF_OK) return st;
+    const int size = dtype_size(dtype);
+    if (!aligned(W, 16) || !aligned(up, 16) || !aligned(X, size) || !aligned(Y, size) || !aligned(e.residual, size) ||
+        !aligned(e.bias, 4) || !aligned(e.up_bias, 4) || !aligned(offsets, 4) || !aligned(order, 4))
+        return RF_ERR_MISALIGNED;
+    if (rows == 0 || n_row == 0) return RF_OK;
+    const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row);
+    if ((st = check_workspace(workspace, workspace_bytes, sh.bytes)) != RF_OK) return st;
+    const Source x = {dtype, X, ldx, n_x, offsets, order, per};
+    return run_product(sh, x, W, up, 0, rows, (int64_t)n_group * rows, e, dtype, Y, ldy, workspace,
+                       static_cast<cudaStream_t>(stream));
+}
+
+size_t rf_moe_route_tokens_workspace_bytes(int64_t n_tok, int n_expert, int top_k)
+{
+    if (n_tok <= 0 || n_expert < 1 || n_expert > 1024 || top_k < 1 || top_k > 8 || top_k > n_expert ||
+        n_tok > kMaxPieces / top_k)
+        return 0;
+    return route_workspace(n_tok, n_expert, top_k);
+}
+
+rf_status rf_moe_route_tokens(int dtype, const void *logits, int64_t ld, int64_t n_tok, int n_expert, int top_k, int32_t *idx,
+                              float *w, int32_t *offsets, int32_t *order, int32_t *place, void *workspace,
+                              size_t workspace_bytes, void *stream)
+{
+    rf_status st = check_route(dtype, logits, ld, n_tok, n_expert, top_k);
+    if (st != RF_OK) return st;
+    if (!offsets || (n_tok > 0 && (!idx || !w || !order || !place))) return RF_ERR_INVALID_ARG;
+    if (!aligned(idx, 4) || !aligned(w, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(place, 4))
+        return RF_ERR_MISALIGNED;
+    if ((st = check_workspace(workspace, workspace_bytes, n_tok > 0 ? route_workspace(n_tok, n_expert, top_k) : 0)) != RF_OK)
+        return st;
+    return launch_route_tokens(dtype, logits, ld, n_tok, n_expert, top_k, idx, w, offsets, order, place, workspace,
+                               static_cast<cudaStream_t>(stream));
+}
+
+size_t rf_moe_tokens_workspace_bytes(int fmt, int n_expert, int top_k, int64_t n_ff, int64_t n_embd, int dtype, int64_t n_tok)
+{
+    if (n_tok <= 0 || n_expert < 1 || n_expert > 1024 || top_k < 1 || top_k > 8 || top_k > n_expert ||
+        n_tok > kMaxPieces / top_k || n_ff <= 0 || n_embd <= 0)
+        return 0;
+    if (check_sizes(fmt, dtype, n_expert, n_ff, n_embd, n_tok * top_k) != RF_OK ||
+        check_sizes(fmt, dtype, n_expert, n_embd, n_ff, n_tok * top_k) != RF_OK)
+        return 0;
+    return moe_layout(fmt, n_expert, top_k, n_ff, n_embd, dtype, n_tok).bytes;
+}
+
+rf_status rf_moe_ffn_tokens(int fmt, int dtype, int logits_dtype, const void *logits, int64_t ld_logits, int n_expert,
+                            int top_k, int64_t n_tok, const void *gate, const void *up, const void *down,
+                            const float *gate_bias, const float *up_bias, const float *down_bias, int act, float alpha,
+                            float limit, int64_t n_ff, int64_t n_embd, const void *X, int64_t ldx, const void *residual,
+                            int64_t ld_residual, void *Y, int64_t ldy, void *workspace, size_t workspace_bytes, void *stream)
+{
+    rf_status st = check_route(logits_dtype, logits, ld_logits, n_tok, n_expert, top_k);
+    if (st != RF_OK) return st;
+    if (n_ff <= 0 || n_embd <= 0) return RF_ERR_INVALID_ARG;
+    if ((st = check_sizes(fmt, dtype, n_expert, n_ff, n_embd, n_tok * top_k)) != RF_OK ||
+        (st = check_sizes(fmt, dtype, n_expert, n_embd, n_ff, n_tok * top_k)) != RF_OK)
+        return st;
+    if (!gate || !up || !down || (n_tok > 0 && (!X || !Y)) || ldx < n_embd || ldy < n_embd ||
+        (residual && ld_residual < n_embd) || !gated_act(act))
+        return RF_ERR_INVALID_ARG;
+    const rf_epilogue first = {gate_bias, up_bias, nullptr, 0, act, alpha, limit, 0};
+    if ((st = check_epilogue(first, up, dtype, n_ff)) != RF_OK) return st;
+    const int size = dtype_size(dtype);
+    if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(down, 16) || !aligned(X, size) || !aligned(Y, size) ||
+        !aligned(residual, size) || !aligned(gate_bias, 4) || !aligned(up_bias, 4) || !aligned(down_bias, 4))
+        return RF_ERR_MISALIGNED;
+    if (n_tok == 0) return RF_OK;
+    const int64_t nb = (n_embd / 4 + 255) / 256;
+    if (n_tok * nb > 0x7fffffffLL) return RF_ERR_TOO_LARGE;
+    const MoeLayout m = moe_layout(fmt, n_expert, top_k, n_ff, n_embd, dtype, n_tok);
+    if ((st = check_workspace(workspace, workspace_bytes, m.bytes)) != RF_OK) return st;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int32_t *idx = reinterpret_cast<int32_t *>(ws + m.at_idx), *offsets = reinterpret_cast<int32_t *>(ws + m.at_offsets);
+    int32_t *order = reinterpret_cast<int32_t *>(ws + m.at_order), *place = reinterpret_cast<int32_t *>(ws + m.at_place);
+    float *w = reinterpret_cast<float *>(ws + m.at_w), *h = reinterpret_cast<float *>(ws + m.at_h);
+    st = launch_route_tokens(logits_dtype, logits, ld_logits, n_tok, n_expert, top_k, idx, w, offsets, order, place,
+                             ws + m.at_route, s);
+    if (st != RF_OK) return st;
+    const int64_t n_row = n_tok * top_k;
+    const Source x = {dtype, X, ldx, n_tok, offsets, order, top_k};
+    st = run_product(m.up, x, gate, up, 0, n_ff, n_expert * n_ff, first, RF_F32, h, n_ff, ws + m.at_product, s);
+    if (st != RF_OK) return st;
+    const Source hs = {RF_F32, h, n_ff, n_row, offsets, nullptr, 1};
+    rf_epilogue second = kNoEpilogue;
+    second.bias = down_bias;
+    st = run_product(m.down, hs, down, nullptr, 0, n_embd, n_expert * n_embd, second, RF_F32, h, m.ldd, ws + m.at_product, s);
+    if (st != RF_OK) return st;
+    JoinParams j;
+    j.d = h, j.w = w, j.place = place;
+    j.residual = residual, j.Y = Y;
+    j.ldr = ld_residual, j.ldy = ldy, j.n_tok = n_tok, j.n = n_embd, j.ldd = m.ldd;
+    j.top_k = top_k, j.nb = (int32_t)nb;
+    j.vec = aligned(Y, 4 * size) && ldy % 4 == 0 && (!residual || (aligned(residual, 4 * size) && ld_residual % 4 == 0));
+    const unsigned grid = (unsigned)(n_tok * nb);
+    if (dtype == RF_F32) join_kernel<RF_F32><<<grid, 256, 0, s>>>(j);
+    else if (dtype == RF_F16) join_kernel<RF_F16><<<grid, 256, 0, s>>>(j);
+    else join_kernel<RF_BF16><<<grid, 256, 0, s>>>(j);
+    return last_cuda_error();
+}
+
+}  // extern "C"
