@@ -776,9 +776,10 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  *                 2^-39 of it).
  * Weights (below 65504 in magnitude) enter
  *   MXFP4         as they are (below 2^-24: to 2^-25),
- *   others        RF_F32 and RF_F16: as two fp16 terms (22 bits, small ones to
- *                 2^-36); RF_BF16: rounded once to fp16, as rf_gemm's (2^-12
- *                 relative, a sixteenth of half a step of bf16).
+ *   others        RF_F32: as two fp16 terms (22 bits, small ones to 2^-36);
+ *                 RF_F16: as two fp16 terms (to 2^-22 or 2^-25, whichever is
+ *                 more); RF_BF16: rounded once to fp16, as rf_gemm's (2^-11 or
+ *                 2^-25: an eighth of half a step of bf16).
  * A row of X that holds an infinity or a NaN has products that are infinite or
  * NaN (the activations clamp infinities, NaN stays); other rows do not see it.  Results do not depend on the other rows' values or on
  * timing (the number of rows chooses how sums are shared out).

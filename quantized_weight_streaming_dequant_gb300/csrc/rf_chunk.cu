@@ -312,10 +312,9 @@ int dtype_size(int d) { return d == RF_F32 ? 4 : 2; }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The operands of a product of n_row rows shared by n_group groups.  Tiles of
-// 256 operand rows where the groups fill them: a weight slice is decoded once
-// per tile, and 256 rows of products (512 cycles) cover the decoding, 128 do
-// not quite.  Smaller groups take tiles of 128, whose sums fit tensor memory
-// twice, so that an item's epilogue runs beside the next one's products.
+// 192 operand rows where the groups fill them (a weight slice is decoded once
+// per tile), of 128 where they do not; both let tensor memory hold two items'
+// sums, so that an epilogue runs beside the next item's products.
 ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row)
 {
     ChunkShape sh;
@@ -324,8 +323,9 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     sh.wt = dtype != RF_BF16 && fmt != RF_MXFP4 ? 2 : 1;
     sh.n_row = n_row, sh.n_group = n_group, sh.rows = rows, sh.in_dim = in_dim;
     sh.nst = (int)((in_dim + kSliceK - 1) / kSliceK);
-    const int64_t each = (n_row + n_group - 1) / n_group * sh.xt;   // operand rows of a group
-    sh.nt = sh.wt == 1 && sh.xt == 1 && each > 128 ? 256 : 128;
+    // Twice the average, so that most groups have one tile.
+    const int64_t each = 2 * sh.xt * ((n_row + n_group - 1) / n_group);   // operand rows
+    sh.nt = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : sh.wt == 1 && sh.xt == 1 && each > 256 ? 192 : 128;
     const int64_t T = sh.tile_tokens(), GT = sh.gran_tokens();
     sh.cap_tiles = std::min<int64_t>(n_row, n_row / T + n_group);
     sh.cap_gran = n_row / GT + n_group;

@@ -14,7 +14,7 @@
 //   warp 1       copies the operand slices of the token tile (1-D bulk);
 //   warp 2       issues the products;
 //   warp 3       draws the items;
-//   decoders     three groups of four warps: each takes every third 64-input
+//   decoders     four groups of four warps: each takes every fourth 64-input
 //                slice, a thread its row, turns the raw bytes into fp16 pairs
 //                and stores them to tensor memory, from where tcgen05.mma reads
 //                the weights: they cost no shared-memory bandwidth, which is
@@ -37,8 +37,8 @@
 //
 // Precision: see rf.h.  Two fp16 terms of an activation are two rows of the
 // operand (8 high, 8 low) with sums of their own; the low terms are scaled by
-// 2^11.  Low terms of weights multiply the high terms of activations into a
-// third sum (the product of two low terms is below 2^-22 of the result).
+// 2^11.  Low terms of weights multiply the high terms of activations (the
+// product of two low terms is below 2^-22 of the result).
 //
 // Every wait is bounded; after a failure every role stops, copies and products
 // already issued are waited for, and tensor memory is freed.
@@ -58,15 +58,9 @@ namespace {
 __device__ int g_chunk_status = 0;   // bounded waits that gave up
 
 constexpr int kM = 128;              // matrix rows per item (MMA M)
-constexpr int kGroups = 3;           // decoder groups of four warps
-constexpr int kDec0 = 4, kEpi0 = kDec0 + 4 * kGroups;
-constexpr int kThreads = 32 * (kEpi0 + 4);
-// fp32 calls hold 64 sums a thread in the epilogue, whose warpgroup takes
-// registers from that of the copies and the issue (96 a thread at launch:
-// 40 + 152 + 3 * 96 = 5 * 96).
-constexpr int kRegsRoles = 40, kRegsSums = 152;
+constexpr int kDec0 = 4;             // first decoder warp; the epilogue's four follow the decoders
 constexpr int kItems = 4;            // items drawn ahead
-constexpr int kItemUsers = 3 + 4 * kGroups + 4;
+constexpr int kInFlight = 16;        // stages of activations in flight at most
 
 // Raw chunk: BPC blocks (of BE weights, BS bytes) of each row.
 template <int FMT> struct Raw;
@@ -75,7 +69,17 @@ template <> struct Raw<RF_Q8_0> { static constexpr int BS = 34, BE = 32, BPC = 8
 template <> struct Raw<RF_MXFP4> { static constexpr int BS = 17, BE = 32, BPC = 16; };
 template <> struct Raw<RF_Q4_K> { static constexpr int BS = 144, BE = 256, BPC = 1; };
 
-// NT: operand rows per token tile; XT, WT: fp16 terms per activation, weight.
+// Box bytes: the chunk's, with what rounding its first byte down takes, as an
+// odd number of 16-byte units (see Win::load); with 16 matrix rows to a
+// super-row an even one, which keeps the boxes 128 bytes aligned.
+__host__ __device__ constexpr int box_bytes(int fmt, int P)
+{
+    const int cb = fmt == RF_Q4_0 || fmt == RF_Q4_K ? 144 : 272;
+    const int n = fmt == RF_Q4_K ? cb : cb + (P > 1 ? 16 : 0);
+    return P < 16 && n / 16 % 2 == 0 ? n + 16 : n;
+}
+
+// NT: operand rows per token tile at most; XT, WT: fp16 terms per activation, weight.
 // A stage is KS slices of weights (tensor memory) and activations (shared
 // memory): two where a slice's products are short, so that the issuing warp's
 // chain of wait, issue and commit is paid half as often.
@@ -83,29 +87,43 @@ template <int FMT, int NT, int XT, int WT>
 struct Cfg {
     static constexpr int CB = Raw<FMT>::BPC * Raw<FMT>::BS;            // chunk bytes per row
     static constexpr int QPC = Raw<FMT>::BPC * Raw<FMT>::BE / kSliceK; // slices per chunk
-    static constexpr int BW = CB + (FMT == RF_Q4_K ? 0 : 16);          // box bytes at most
+    static constexpr int BW = box_bytes(FMT, 8);                       // box bytes at most
     static constexpr int T = NT / XT;                                  // tokens
     static constexpr int KS = NT == 128 && WT == 1 ? 2 : 1;
-    static constexpr int S = 4;                                        // stages
-    static constexpr int BT = NT * kSliceK * 2;                        // activation bytes per slice
+    static constexpr int S = 4;                                        // stages of weights
+    static constexpr int G = 4;                                        // decoder groups of four warps
+    static constexpr int EPI0 = kDec0 + 4 * G, THREADS = 32 * (EPI0 + 4);
+    static constexpr int USERS = 3 + 4 * G + 4;                        // warps that take an item
+    // Registers a thread: what a launch gives every warp, and what the roles
+    // trade among them (fp32 calls hold 64 sums a thread in the epilogue).
+    static constexpr int REGS = 65536 / THREADS / 8 * 8, RROLES = 40, RDEC = REGS - 8;
+    static constexpr int REPI = (G + 2) * REGS - RROLES - G * RDEC;
+    static constexpr int BT = NT * kSliceK * 2;                        // activation bytes per slice at most
     static constexpr int RAW = kM * BW;
-    static constexpr int R = RAW > 32768 ? 2 : 4;                      // raw chunks in flight
-    // Columns of one item's sums: one region of NT, or (two terms of both) T
-    // of high products and T of the others.  With two terms of weights alone,
-    // a second region for the low ones.
-    static constexpr int ACC = WT == 2 && XT == 1 ? 2 * NT : NT;
-    static constexpr int NBUF = 2 * ACC <= 256 ? 2 : 1;
-    static constexpr int ACOL = 256;                                   // first column of the weights
+    static constexpr int R = RAW > 32768 ? 2 : 3;                      // raw chunks in flight
+    static constexpr int RING = (230000 - R * RAW) / 2048 * 2048;      // bytes of activations in flight
+    static constexpr int LOW = WT == 1 ? 0 : (XT == 1 ? 1 : 2);        // Low
+    // Columns of one item's sums (with two terms of both: T of high products,
+    // T of the others).
+    static constexpr int ACC = NT;
     static constexpr int ASLICE = 32 * WT, ASTAGE = KS * ASLICE;
-    // Sums of fp32 calls leave tensor memory every FLUSH slices: the tensor cores truncate each addition (about 1e-8 of the
-    // sum, always towards zero), rounded additions in registers do not drift.
+    static constexpr int ACOL = 512 - S * ASTAGE;                      // first column of the weights
+    static constexpr int NBUF = 2 * ACC <= ACOL ? 2 : 1;
+    // Sums of fp32 calls leave tensor memory every FLUSH slices: the tensor
+    // cores truncate each addition (about 1e-8 of the sum, always towards
+    // zero), rounded additions in registers do not drift.
     static constexpr int FLUSH = XT == 2 ? 4 : 1 << 30;                // slices
-    static constexpr size_t SMEM = (size_t)S * KS * BT + (size_t)R * RAW + 16;
-    static_assert(ACC * NBUF <= 256 && S * ASTAGE <= 256, "tensor memory");
+    static constexpr size_t SMEM = (size_t)RING + (size_t)R * RAW + 16;
+    // Barriers, by number.
+    static constexpr int FULL = 0, ADONE = FULL + S, BFULL = ADONE + S, BDONE = BFULL + kInFlight, RFULL = BDONE + kInFlight,
+                         REMPTY = RFULL + R, ACCF = REMPTY + R, ACCE = ACCF + NBUF, IFULL = ACCE + NBUF, IEMPTY = IFULL + kItems,
+                         DRAIN = IEMPTY + kItems, BARS = DRAIN + 1;
+    static_assert(ACC * NBUF <= ACOL, "tensor memory");
     static_assert(QPC % KS == 0 && FLUSH % KS == 0, "a stage lies in one chunk and between two flushes");
     static_assert(T % 16 == 0, "the epilogue takes 16 tokens at a time");
-    static_assert(kGroups <= S, "groups wait within one phase of a stage");
-    static_assert(SMEM <= 231000, "shared memory");
+    static_assert((G + KS - 1) / KS <= S, "groups wait within one phase of a stage");
+    static_assert(REPI <= 248 && REPI % 8 == 0 && RROLES < REGS, "registers");
+    static_assert(KS * BT <= RING && S <= kInFlight, "a stage fits the ring");
 };
 
 struct Item {
@@ -123,6 +141,8 @@ struct Params {
     int32_t P, logP;          // matrix rows per super-row
     int32_t bw;               // box bytes: chunk bytes, 16 more when P > 1
     int32_t copies;           // 0: every row is behind the last super-row
+    int32_t slots;            // stages of activations in shared memory,
+    uint32_t slot;            // and the bytes of a slice of one
     int32_t rows, nst, nch, nb, nrt, gated;   // rows of Y; slices, chunks, blocks of a row; row tiles
     int32_t act, dtype;
     float alpha, limit;
@@ -134,17 +154,22 @@ struct Params {
     unsigned long long limit_ns;
 };
 
+// Row of a half of the tile for each of its 64 threads (tensor-memory lanes):
+// neighbours take rows at the same position of successive super-rows, which
+// lie box_bytes apart.
+__device__ __forceinline__ int lane_row(int e, int logP) { return ((e & ((64 >> logP) - 1)) << logP) + (e >> (6 - logP)); }
+
 __host__ __device__ constexpr uint32_t idesc_n(int n)
 {
     return (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
 }
 
 // ------------------------------------------------------------------ decoding
-// A slice's bytes as words from its first byte; word<B>, byte<B>, half<B> at
-// byte B.
-template <int SBYTES>
+// A slice's bytes (two blocks of 32 weights) as words from its first byte;
+// word<B>, byte<B>, half<B> at byte B.
+template <int BYTES>
 struct Win {
-    static constexpr int NO = (SBYTES + 3) / 4;
+    static constexpr int NO = (BYTES + 3) / 4, NU = (15 + BYTES + 15) / 16;
     uint32_t w[NO];
     template <int B> __device__ __forceinline__ uint32_t word() const
     {
@@ -157,56 +182,37 @@ struct Win {
         static_assert(B % 2 == 0, "fp16 scale at an odd byte");
         return (w[B / 4] >> (8 * (B % 4))) & 0xFFFFu;
     }
-    // From shared memory at any byte: 8-byte loads (rows are multiples of 16
-    // bytes apart, so 32 lanes' 4-byte loads would hit 8 banks four times),
-    // then a word's and a byte's shift.
+    // From shared memory at any byte: the 16-byte units that hold them (eight
+    // lanes' rows are an odd number of units apart, so their loads meet no
+    // bank twice), then words' and bytes' shifts.
     __device__ __forceinline__ void load(const uint8_t *raw, uint32_t off)
     {
-        constexpr int ND = (NO + 3) / 2;
-        uint32_t x[2 * ND];
-        const uint2 *s = reinterpret_cast<const uint2 *>(raw + (off & ~7u));
+        uint32_t x[4 * NU];
+        const uint4 *s = reinterpret_cast<const uint4 *>(raw + (off & ~15u));
 #pragma unroll
-        for (int i = 0; i < ND; ++i) {
-            const uint2 v = s[i];
-            x[2 * i] = v.x;
-            x[2 * i + 1] = v.y;
+        for (int i = 0; i < NU; ++i) {
+            const uint4 v = s[i];
+            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
         }
-        const bool odd = (off & 4u) != 0;
+        const bool two = (off & 8u) != 0, one = (off & 4u) != 0;
         const uint32_t sh = 8u * (off & 3u);
 #pragma unroll
-        for (int i = 0; i < NO + 1; ++i) x[i] = odd ? x[i + 1] : x[i];
+        for (int i = 0; i < NO + 2; ++i) x[i] = two ? x[i + 2] : x[i];
+#pragma unroll
+        for (int i = 0; i < NO + 1; ++i) x[i] = one ? x[i + 1] : x[i];
 #pragma unroll
         for (int i = 0; i < NO; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], sh);
     }
-    // From global memory, `n` bytes of a row (the rest read as 0): aligned
-    // words, none that holds no byte of them.
-    __device__ __forceinline__ void load_global(const uint8_t *a, int n)
+    // From global memory, n bytes one by one (the rest reads as 0).
+    __device__ __forceinline__ void load_bytes(const uint8_t *a, int n)
     {
-        const uintptr_t ua = reinterpret_cast<uintptr_t>(a);
-        const uint32_t *a4 = reinterpret_cast<const uint32_t *>(ua & ~(uintptr_t)3);
-        const uint32_t sh = 8u * (uint32_t)(ua & 3);
-        const int end = (int)(ua & 3) + n;
-        uint32_t x[NO + 1];
 #pragma unroll
-        for (int i = 0; i < NO + 1; ++i) {
-            const int rem = end - 4 * i;
-            const uint32_t v = rem > 0 ? __ldg(a4 + i) : 0u;
-            x[i] = rem >= 4 ? v : v & ((1u << (8 * (rem > 0 ? rem : 0))) - 1u);
-        }
+        for (int i = 0; i < NO; ++i) w[i] = 0u;
 #pragma unroll
-        for (int i = 0; i < NO; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], sh);
+        for (int i = 0; i < BYTES; ++i)
+            if (i < n) w[i / 4] |= (uint32_t)__ldg(a + i) << (8 * (i % 4));
     }
 };
-
-// fp32 weights as a pair of fp16 values and the pair of what they leave,
-// scaled by 2^11.
-__device__ __forceinline__ void two_terms(float w0, float w1, uint32_t &hi, uint32_t &lo)
-{
-    const __half2 h = __floats2half2_rn(w0, w1);
-    const float2 f = __half22float2(h);
-    hi = h2_bits(h);
-    lo = h2_bits(__floats2half2_rn((w0 - f.x) * 2048.f, (w1 - f.y) * 2048.f));
-}
 
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
 {
@@ -215,80 +221,115 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
     return r;
 }
 
-// Q4_0, d and its four quant words: pair s of word m holds nibbles s and s + 4.
-// 0x6400 | n is the fp16 value 1024 + n (and 0x6400 | 16 n is 1024 + 16 n), so
-// n - 8 is exact; one multiply by d rounds the weight once.
-template <int WT>
-__device__ __forceinline__ void q4_0_block(uint32_t d, const uint32_t (&q)[4], uint32_t (&hi)[16], uint32_t (&lo)[16])
+// How low terms are kept.  kOne: none.  kPlain: as they are (16-bit
+// activations: their products join the high ones' sums; a weight is then off
+// by 2^-25 at most).  kScaled: times 2^11 (fp32: 22 bits of the weight).
+enum Low { kOne, kPlain, kScaled };
+
+// fp32 weights as a pair of fp16 values and the pair of what they leave.
+template <int L>
+__device__ __forceinline__ void two_terms(float w0, float w1, uint32_t &hi, uint32_t &lo)
 {
-    const uint32_t dd = d | (d << 16);
-    const float df = __half2float(__ushort_as_half((unsigned short)d));
+    const __half2 h = __floats2half2_rn(w0, w1);
+    hi = h2_bits(h);
+    if constexpr (L != kOne) {
+        const float2 f = __half22float2(h);
+        const float m = L == kScaled ? 2048.f : 1.f;
+        lo = h2_bits(__floats2half2_rn((w0 - f.x) * m, (w1 - f.y) * m));
+    }
+}
+// The same for products n * d of small integers (|n| <= N, fp16 pairs that
+// number(j) gives) and an fp16 scale, in fp16: hi rounds the product, and what
+// it leaves has at most 11 bits, so that one fused multiply-add gives it
+// exactly.  Scaled: n * (2^11 d) - 2^11 hi, in fp32 where that might overflow
+// (N |d| >= 32).
+template <int L, int N, class F>
+__device__ __forceinline__ void products(uint32_t d, F number, uint32_t (&hi)[16], uint32_t (&lo)[16])
+{
+    const uint32_t dd = d * 0x00010001u, dl = L == kScaled ? hmul2(dd, 0x68006800u) : dd;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const uint32_t v[2] = {q[m], q[m] >> 8};
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t n = number(j);
+        hi[j] = hmul2(n, dd);
+        if constexpr (L != kOne) lo[j] = hfma2(n, dl, L == kScaled ? hmul2(hi[j], 0xE800E800u) : hi[j] ^ 0x80008000u);
+    }
+    if constexpr (L == kScaled) {
+        const float f = __half2float(__ushort_as_half((unsigned short)d));
+        if (!(fabsf(f) * N < 32.f)) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint32_t t = v[s >> 1];
-            if constexpr (WT == 1) {
-                const uint32_t n = (s & 1) ? hfma2((t & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u)   // x / 16 - 72
-                                           : hsub2((t & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-                hi[4 * m + s] = hmul2(n, dd);
-            } else {
-                const uint32_t u = (t >> (4 * (s & 1))) & 0x000F000Fu;
-                const float a = __uint_as_float(0x4B000000u | (u & 15u)) - 8388616.f;   // 2^23 + n - (2^23 + 8)
-                const float b = __uint_as_float(0x4B000000u | (u >> 16)) - 8388616.f;
-                two_terms(df * a, df * b, hi[4 * m + s], lo[4 * m + s]);
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t n = number(j);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&n));
+                two_terms<L>(v.x * f, v.y * f, hi[j], lo[j]);
             }
         }
     }
 }
+
+// Q4_0, d and its four quant words: pair 4 m + s holds nibbles s and s + 4 of
+// word m.  0x6400 | n is the fp16 value 1024 + n (and 0x6400 | 16 n is 1024 +
+// 16 n), so n - 8 is exact; one multiply by d rounds the weight once.
+template <int L>
+__device__ __forceinline__ void q4_0_block(uint32_t d, const uint32_t (&q)[4], uint32_t (&hi)[16], uint32_t (&lo)[16])
+{
+    products<L, 8>(d, [&](int j) {
+        const uint32_t t = (j & 2) ? q[j >> 2] >> 8 : q[j >> 2];
+        return (j & 1) ? hfma2((t & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u)   // x / 16 - 72
+                       : hsub2((t & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+    }, hi, lo);
+}
 // Q8_0: with the sign bit flipped, 0x6400 | u is 1024 + q + 128.
-template <int WT>
+template <int L>
 __device__ __forceinline__ void q8_0_block(uint32_t d, const uint32_t (&q)[8], uint32_t (&hi)[16], uint32_t (&lo)[16])
 {
-    const uint32_t dd = d | (d << 16);
-    const float df = __half2float(__ushort_as_half((unsigned short)d));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t v = q[j] ^ 0x80808080u;
-        if constexpr (WT == 1) {
-            hi[2 * j] = hmul2(hsub2(prmt(v, 0x64646464u, 0x5140u), 0x64806480u), dd);
-            hi[2 * j + 1] = hmul2(hsub2(prmt(v, 0x64646464u, 0x7362u), 0x64806480u), dd);
-        } else {
-            float f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                f[e] = df * (__uint_as_float(prmt(v, 0x4B000000u, 0x7440u + e)) - 8388736.f);   // 2^23 + 128 + q
-            two_terms(f[0], f[1], hi[2 * j], lo[2 * j]);
-            two_terms(f[2], f[3], hi[2 * j + 1], lo[2 * j + 1]);
-        }
-    }
+    products<L, 128>(d, [&](int j) {
+        return hsub2(prmt(q[j >> 1] ^ 0x80808080u, 0x64646464u, (j & 1) ? 0x7362u : 0x5140u), 0x64806480u);
+    }, hi, lo);
+}
+// Four bytes of two E2M1 codes each as four fp16 pairs (low nibble, high).
+__device__ __forceinline__ void e2m1x8(uint32_t q, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(q));
 }
 // MXFP4: pair j holds byte j's two codes, scaled by 2^(E - 127): exact whenever
 // the product is representable, in two steps outside fp16's exponents (one
 // rounding).
 __device__ __forceinline__ void mxfp4_block(uint32_t E, const uint32_t (&q)[4], uint32_t (&hi)[16])
 {
-    const int k = (int)E - 127;
-    uint32_t s1, s2 = 0u;
-    if (E == 255u) s1 = 0x7E00u;                       // NaN scale
-    else if (k >= -14 && k <= 15) s1 = (uint32_t)(k + 15) << 10;
-    else if (k > 15) s1 = 0x7800u, s2 = pow2_h(min(k - 15, 15));
-    else if (k >= -24) s1 = pow2_h(k);
-    else s1 = 0x0C00u, s2 = k + 12 >= -24 ? pow2_h(k + 12) : 0u;
-    const uint32_t ss = s1 | (s1 << 16);
+    const bool normal = E - 113u < 30u;                     // 2^-14 .. 2^15
+    uint32_t s1 = E * 0x04000400u - 112u * 0x04000400u, s2 = 0u;
+    if (!normal) {
+        const int k = (int)E - 127;
+        uint32_t t = 0x0C00u;                               // 2^-12
+        if (E == 255u) t = 0x7E00u;                         // NaN scale
+        else if (k > 15) t = 0x7800u, s2 = pow2_h(min(k - 15, 15));
+        else if (k >= -24) t = pow2_h(k), s2 = 0x3C00u;
+        else s2 = k + 12 >= -24 ? pow2_h(k + 12) : 0u;
+        s1 = t * 0x00010001u, s2 *= 0x00010001u;
+    }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) hi[j] = hmul2(e2m1x2_h2(q[j >> 2] >> (8 * (j & 3))), ss);
-    if (E != 255u && (k < -24 || k > 15)) {
-        const uint32_t s22 = s2 | (s2 << 16);
+    for (int m = 0; m < 4; ++m) {
+        uint32_t h[4];
+        e2m1x8(q[m], h);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) hi[j] = hmul2(hi[j], s22);
+        for (int e = 0; e < 4; ++e) hi[4 * m + e] = hmul2(h[e], s1);
+    }
+    if (!normal && E != 255u) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) hi[j] = hmul2(hi[j], s2);
     }
 }
 // Half T (0: low nibbles, 1: high) of slice Q of a Q4_K super-block at `s`
 // (16-byte aligned): sub-block 2 Q + T, d * sc * q - dmin * m by one fused
 // multiply-add in fp32 (its products are exact).
-template <int WT>
+template <int L>
 __device__ __forceinline__ void q4k_block(const uint8_t *s, int Q, int T, uint32_t (&hi)[16], uint32_t (&lo)[16])
 {
     const uint4 h = *reinterpret_cast<const uint4 *>(s);
@@ -314,29 +355,25 @@ __device__ __forceinline__ void q4k_block(const uint8_t *s, int Q, int T, uint32
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             f[e] = fmaf(ds, __uint_as_float(prmt(v, 0x4B000000u, 0x7440u + e)) - 8388608.f, -dm);
-        if constexpr (WT == 1) {
-            hi[2 * k] = h2_bits(__floats2half2_rn(f[0], f[1]));
-            hi[2 * k + 1] = h2_bits(__floats2half2_rn(f[2], f[3]));
-        } else {
-            two_terms(f[0], f[1], hi[2 * k], lo[2 * k]);
-            two_terms(f[2], f[3], hi[2 * k + 1], lo[2 * k + 1]);
-        }
+        two_terms<L>(f[0], f[1], hi[2 * k], lo[2 * k]);
+        two_terms<L>(f[2], f[3], hi[2 * k + 1], lo[2 * k + 1]);
     }
 }
 
-template <int FMT, int WT, int BLK, class W>
-__device__ __forceinline__ void win_block(const W &win, uint32_t (&hi)[16], uint32_t (&lo)[16])
+// Block BLK of a slice.
+template <int FMT, int L, int BLK, class W>
+__device__ __forceinline__ void block_pairs(const W &win, uint32_t (&hi)[16], uint32_t (&lo)[16])
 {
     constexpr int O = BLK * Raw<FMT>::BS;
     if constexpr (FMT == RF_Q4_0) {
         const uint32_t q[4] = {win.template word<O + 2>(), win.template word<O + 6>(), win.template word<O + 10>(),
                                win.template word<O + 14>()};
-        q4_0_block<WT>(win.template half<O>(), q, hi, lo);
+        q4_0_block<L>(win.template half<O>(), q, hi, lo);
     } else if constexpr (FMT == RF_Q8_0) {
         const uint32_t q[8] = {win.template word<O + 2>(),  win.template word<O + 6>(),  win.template word<O + 10>(),
                                win.template word<O + 14>(), win.template word<O + 18>(), win.template word<O + 22>(),
                                win.template word<O + 26>(), win.template word<O + 30>()};
-        q8_0_block<WT>(win.template half<O>(), q, hi, lo);
+        q8_0_block<L>(win.template half<O>(), q, hi, lo);
     } else {
         const uint32_t q[4] = {win.template word<O + 1>(), win.template word<O + 5>(), win.template word<O + 9>(),
                                win.template word<O + 13>()};
@@ -449,19 +486,78 @@ __device__ __forceinline__ void load_inv(const float *inv, float (&f)[16])
     }
 }
 
+// Barriers and copies by shared-memory address: the roles' loops are chains of
+// a few instructions, and a generic pointer's conversion would be among them.
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// Whether phase `parity` has completed: at once (test), within the hardware's
+// own time (try), or within `ns` nanoseconds, the thread set aside meanwhile.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_try_ns(uint32_t bar, uint32_t parity, uint32_t ns)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(ns) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void bar_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+                     "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+// A copy that was issued lands whatever else failed: wait for it (bounded,
+// ignoring the status word), so that none is under way when the CTA exits.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
+{
+    const unsigned long long t0 = globaltimer_ns();
+    while (!bar_try_ns(bar, parity, 20000u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    }
+}
+
 template <int FMT, int NT, int XT, int WT>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<FMT, NT, XT, WT>;
     constexpr int S = C::S, KS = C::KS, R = C::R, QPC = C::QPC, NBUF = C::NBUF, GT = kGranRows / XT;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *b_t = smem;                       // [S][KS slices]
-    uint8_t *raw = b_t + S * KS * C::BT;       // [R][RAW], then 16 bytes that a last load may touch
-    // bfull: a stage's activations have landed; full: so have they, and its
-    // weights are decoded (an arrival per decoder warp and slice); done: its
-    // products are through.
-    __shared__ uint64_t full[S], bfull[S], done[S], rfull[R], rempty[R], accfull[NBUF], accempty[NBUF], ifull[kItems], iempty[kItems],
-        drained;
+    constexpr int G = C::G, kEpi0 = C::EPI0;
+    extern __shared__ __align__(1024) uint8_t smem[];   // [RING], [R][RAW], 16 bytes that a last load may touch
+    uint8_t *raw = smem + C::RING;
+    // FULL: a stage's weights are decoded (an arrival per decoder warp and
+    // slice); BFULL: its activations have landed; ADONE, BDONE: its products
+    // are through; RFULL, REMPTY: raw chunks; ACCF, ACCE: sums; IFULL, IEMPTY:
+    // items.
+    __shared__ uint64_t bars[C::BARS];
     __shared__ Item items[kItems];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
@@ -469,11 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&full[i], 4 * KS), mbar_init(&bfull[i], 1), mbar_init(&done[i], 1);
-        for (int i = 0; i < R; ++i) mbar_init(&rfull[i], 1), mbar_init(&rempty[i], 4 * kGroups);
-        for (int i = 0; i < NBUF; ++i) mbar_init(&accfull[i], 1), mbar_init(&accempty[i], 4);
-        for (int i = 0; i < kItems; ++i) mbar_init(&ifull[i], 1), mbar_init(&iempty[i], kItemUsers);
-        mbar_init(&drained, 1);
+        for (int i = 0; i < C::BARS; ++i) {
+            uint32_t n = 1;
+            if (i < C::ADONE) n = 4 * KS;
+            else if (i >= C::REMPTY && i < C::ACCF) n = 4 * G;
+            else if (i >= C::ACCE && i < C::IFULL) n = 4;
+            else if (i >= C::IEMPTY && i < C::DRAIN) n = C::USERS;
+            mbar_init(&bars[i], n);
+        }
         s_stop = 0;
         fence_barrier_init();
     }
@@ -485,36 +584,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*stop) return false;
-        if (mbar_wait_bounded(bar, parity, &g_chunk_status, p.limit_ns)) return true;
-        *stop = 1;
+    const uint32_t bar0 = smem_addr(bars);
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
+    auto wait = [&](uint32_t at, uint32_t parity) -> bool {
+        // (The timer is read only after a long wait: it takes as long as a
+        // stage's products.)
+        if (bar_try(at, parity) || bar_try_ns(at, parity, 20000u)) return true;
+        const unsigned long long t0 = globaltimer_ns();
+        while (!*stop) {
+            if (bar_try_ns(at, parity, 20000u)) return true;
+            const unsigned long long dt = globaltimer_ns() - t0;
+            if (dt > p.limit_ns) {
+                record_status(&g_chunk_status, RF_ERR_TIMEOUT);
+                *stop = 1;
+            } else if (dt > 20000ull && *reinterpret_cast<volatile int *>(&g_chunk_status) != 0) {
+                *stop = 1;   // another CTA's wait has given up
+            }
+        }
         return false;
     };
     // A warp's waits; the next item, copied from its slot (one arrival a warp).
-    auto waits = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    auto waits = [&](uint32_t at, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(at, parity)); };
     auto take = [&](uint32_t it, Item &w) -> bool {
         const int slot = it % kItems;
-        if (!waits(&ifull[slot], (it / kItems) & 1)) return false;
+        if (!waits(bar(C::IFULL + slot), (it / kItems) & 1)) return false;
         const int32_t *src = reinterpret_cast<const int32_t *>(&items[slot]);
         w.group = __shfl_sync(0xffffffffu, src[0], 0), w.row0 = __shfl_sync(0xffffffffu, src[1], 0);
         w.cnt = __shfl_sync(0xffffffffu, src[2], 0), w.gran = __shfl_sync(0xffffffffu, src[3], 0);
         w.rt = __shfl_sync(0xffffffffu, src[4], 0), w.stop = __shfl_sync(0xffffffffu, src[5], 0);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&iempty[slot]);
+        if (lane == 0) bar_arrive(bar(C::IEMPTY + slot));
         return w.stop == 0;
     };
 
     // (Registers are traded for good: the roles do not join again before the end.)
     if (warp < kDec0) {
-    if constexpr (XT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RROLES));
     if (warp == 3) {
         if (lane == 0) {
             const int total = p.plan->n_tiles * p.nrt;   // at most 2^30
             for (uint32_t it = 0;; ++it) {
                 const int slot = it % kItems;
-                if (!wait(&iempty[slot], ((it / kItems) & 1) ^ 1)) break;
+                if (!wait(bar(C::IEMPTY + slot), ((it / kItems) & 1) ^ 1)) break;
                 Item &w = items[slot];
                 const int index = atomicAdd(&p.plan->next, 1);
                 w.stop = index >= total;
@@ -524,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     w.rt = index % p.nrt;
                 }
                 const bool end = w.stop != 0;
-                mbar_arrive(&ifull[slot]);
+                bar_arrive(bar(C::IFULL + slot));
                 if (end) break;
             }
         }
@@ -533,127 +644,153 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         // Raw rows: lane l copies box l of a chunk (half l / P, position l % P).
         const int half = lane >> p.logP, j = lane & (p.P - 1);
         const bool copies = half < 2 && p.copies;
-        const uint32_t box = (uint32_t)((64 >> p.logP) * p.bw);
+        const uint32_t dst = smem_addr(raw) + (uint32_t)lane * (uint32_t)((64 >> p.logP) * p.bw);
         const int xj = (int)((int64_t)j * p.rb);
-        uint32_t rc = 0;
+        const CUtensorMap *map = &p.map[p.gated ? half & 1 : 0];
+        uint32_t rc = 0, r = 0, ph = 1;
         Item w;
         for (uint32_t it = 0; take(it, w); ++it) {
             const int64_t first = p.row0 + (int64_t)w.group * p.group_rows +
                                   (p.gated ? (int64_t)w.rt * 64 : (int64_t)w.rt * 128 + 64 * half);
             const int y = (int)((first - j + p.P - 1) >> p.logP);   // first super-row with position j in the tile
-            const CUtensorMap *map = &p.map[p.gated ? half & 1 : 0];
             bool ok = true;
-            for (int c = 0; c < p.nch; ++c, ++rc) {
-                const int r = rc % R;
-                if (!(ok = waits(&rempty[r], ((rc / R) & 1) ^ 1))) break;
+            for (int c = 0; c < p.nch; ++c) {
+                if (!(ok = waits(bar(C::REMPTY + r), ph))) break;
                 if (lane == 0) {
-                    if (p.copies) mbar_arrive_expect_tx(&rfull[r], (uint32_t)(kM * p.bw));
-                    else mbar_arrive(&rfull[r]);
+                    if (p.copies) bar_expect(bar(C::RFULL + r), (uint32_t)(kM * p.bw));
+                    else bar_arrive(bar(C::RFULL + r));
                 }
                 __syncwarp();
-                if (copies)
-                    tma_2d_g2s(raw + r * C::RAW + lane * box, map, ((xj + c * C::CB) & ~15) >> 1, y, &rfull[r]);
+                if (copies) copy_box(dst + r * C::RAW, map, ((xj + c * C::CB) & ~15) >> 1, y, bar(C::RFULL + r));
+                ++rc;
+                if (++r == R) r = 0, ph ^= 1u;
             }
             if (!ok) break;
         }
         // Every copy issued lands before the CTA can exit.
         if (lane == 0)
-            for (uint32_t i = rc > R ? rc - R : 0; i < rc; ++i) mbar_drain(&rfull[i % R], (i / R) & 1);
+            for (uint32_t i = rc > R ? rc - R : 0; i < rc; ++i) bar_drain(bar(C::RFULL + i % R), (i / R) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        uint32_t n = 0;          // stages so far
-        uint32_t skipped = 0xffffffffu;
-        Item w;
-        for (uint32_t it = 0; take(it, w); ++it) {
+        // Activations, a stage at a time.
+        if (lane == 0) {
+            const uint32_t ring = smem_addr(smem);
+            uint32_t n = 0, ib = 0, ph = 1;   // stages copied; place in the ring and phase
+            uint32_t skipped = 0xffffffffu;
             bool ok = true;
-            if (lane == 0) {
-                const uint32_t bytes = (uint32_t)((w.cnt + GT - 1) / GT) * kGranBytes;   // of a slice
-                const uint8_t *src = p.img + (int64_t)w.gran * p.nst * kGranBytes;
+            for (uint32_t it = 0; ok; ++it) {
+                const int slot = it % kItems;
+                if (!wait(bar(C::IFULL + slot), (it / kItems) & 1)) break;
+                const int grans = (items[slot].cnt + GT - 1) / GT, gran = items[slot].gran, end = items[slot].stop;
+                bar_arrive(bar(C::IEMPTY + slot));
+                if (end) break;
+                const uint32_t slice = (uint32_t)grans * kGranBytes;
+                const uint8_t *src = p.img + (int64_t)gran * p.nst * kGranBytes;
                 for (int b = 0; b < p.nst; b += KS, ++n) {
-                    const int st = n % S;
-                    if (!(ok = wait(&done[st], ((n / S) & 1) ^ 1))) break;
+                    if (!(ok = wait(bar(C::BDONE + ib), ph))) break;
                     if (blockIdx.x == 0 && n == (uint32_t)p.withhold) {
                         skipped = n;
-                        continue;
+                    } else {
+                        const int slices = KS > 1 && b + 1 < p.nst ? KS : 1;
+                        bar_expect(bar(C::BFULL + ib), slices * slice);
+                        for (int i = 0; i < slices; ++i)
+                            copy_bulk(ring + (ib * KS + i) * p.slot, src + i * slice, slice, bar(C::BFULL + ib));
                     }
-                    const int slices = min(KS, p.nst - b);
-                    mbar_arrive_expect_tx(&bfull[st], slices * bytes);
-                    for (int i = 0; i < slices; ++i)
-                        bulk_g2s(b_t + (st * KS + i) * C::BT, src + (int64_t)(b + i) * bytes, bytes, &bfull[st]);
+                    src += KS * slice;
+                    if (++ib == (uint32_t)p.slots) ib = 0, ph ^= 1u;
                 }
             }
-            if (!__shfl_sync(0xffffffffu, (int)ok, 0)) break;
+            // Every copy issued lands before the CTA can exit.
+            const uint32_t slots = (uint32_t)p.slots;
+            for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i)
+                if (i != skipped) bar_drain(bar(C::BFULL + i % slots), (i / slots) & 1);
         }
-        // Every copy issued lands before the CTA can exit.
-        if (lane == 0)
-            for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
-                if (i != skipped) mbar_drain(&bfull[i % S], (i / S) & 1);
         __syncwarp();
     } else if (warp == 2) {
-        const uint64_t bd0 = smem_desc(smem_addr(b_t), 1024);
-        const uint64_t bd1 = smem_desc(smem_addr(b_t), 2048);   // every other 8 rows: the high (or low) terms
-        const bool leader = elect_one();
-        uint32_t n = 0, seg = 0;   // stages, sums
-        bool any = false, ok = true;
-        Item w;
-        for (uint32_t it = 0; ok && take(it, w); ++it) {
-            const int grans = (w.cnt + GT - 1) / GT;
-            const uint32_t id = WT == 2 && XT == 2 ? idesc_n((grans + 1) / 2 * 16) : idesc_n(kGranRows * grans);
-            for (int b = 0; b < p.nst; ++n) {
-                const bool fresh = b % C::FLUSH == 0;
-                const uint32_t acc = tmem + (seg % NBUF) * C::ACC;
-                if (fresh) {
-                    if (!(ok = waits(&accempty[seg % NBUF], ((seg / NBUF) & 1) ^ 1))) break;
-                }
-                const int st = n % S;
-                if (!(ok = waits(&full[st], (n / S) & 1))) break;
-                tc_fence_after();
-                any = true;
-                if (leader) {
+        // Products, the whole role in one elected thread (a warp that waits
+        // as one and elects per stage is as fast, but then how often the
+        // election runs is the compiler's choice; lane 0 by its number keeps
+        // the operands out of uniform registers: 388 against 300 us for 2048
+        // tokens through 2 x 11008 x 4096 Q4_0).
+        if (elect_one()) {
+            const uint64_t bd0 = smem_desc(smem_addr(smem), 1024);
+            const uint64_t bd1 = smem_desc(smem_addr(smem), 2048);   // every other 8 rows: the high (or low) terms
+            uint32_t sa = 0, pa = 0;           // stage of weights and its phase
+            uint32_t ib = 0, pb = 0;           // stage of activations and its phase
+            uint32_t seg = 0;                  // sums
+            bool any = false, ok = true, ready = false;
+            for (uint32_t it = 0; ok; ++it) {
+                const int slot = it % kItems;
+                if (!wait(bar(C::IFULL + slot), (it / kItems) & 1)) break;
+                const int grans = (items[slot].cnt + GT - 1) / GT, end = items[slot].stop;
+                bar_arrive(bar(C::IEMPTY + slot));
+                if (end) break;
+                const uint32_t id = WT == 2 && XT == 2 ? idesc_n((grans + 1) / 2 * 16) : idesc_n(kGranRows * grans);
+                for (int b = 0; b < p.nst;) {
+                    const bool fresh = b % C::FLUSH == 0;
+                    const uint32_t acc = tmem + (seg % NBUF) * C::ACC;
+                    if (fresh) {
+                        if (!(ok = wait(bar(C::ACCE + seg % NBUF), ((seg / NBUF) & 1) ^ 1))) break;
+                    }
+                    if (!ready && !(ok = wait(bar(C::BFULL + ib), pb) && wait(bar(C::FULL + sa), pa))) break;
+                    const uint32_t a_done = bar(C::ADONE + sa), b_done = bar(C::BDONE + ib);
+                    const uint32_t a0 = tmem + C::ACOL + sa * C::ASTAGE, at = (ib * KS * p.slot) >> 4;
+                    const bool two = KS > 1 && b + 1 < p.nst;
+                    // The next stage's barriers are read (about 130 cycles
+                    // each) beside this one's products.
+                    if (++sa == S) sa = 0, pa ^= 1u;
+                    if (++ib == (uint32_t)p.slots) ib = 0, pb ^= 1u;
+                    const bool b_next = bar_test(bar(C::BFULL + ib), pb), f_next = bar_test(bar(C::FULL + sa), pa);
+                    tc_fence_after();
+                    any = true;
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
-                        if (i > 0 && b + i >= p.nst) break;
-                        const uint32_t a = tmem + C::ACOL + (uint32_t)(st * C::ASTAGE + i * C::ASLICE);
-                        const uint64_t slot = (uint64_t)(((st * KS + i) * C::BT) >> 4);
+                        if (i > 0 && !two) break;
+                        const uint32_t a = a0 + (uint32_t)(i * C::ASLICE);
+                        const uint64_t at_i = at + i * (p.slot >> 4);
 #pragma unroll
                         for (int k = 0; k < kSliceK / 16; ++k) {
                             const uint32_t add = !fresh || i > 0 || k > 0;
                             if constexpr (WT == 2 && XT == 2) {
-                                tc_mma_ts(acc, a + 8 * k, bd1 + slot + 16 * k, id, add);
-                                tc_mma_ts(acc + C::T, a + 8 * k, bd1 + slot + 64 + 16 * k, id, add);
-                                tc_mma_ts(acc + C::T, a + 32 + 8 * k, bd1 + slot + 16 * k, id, 1u);
+                                tc_mma_ts(acc, a + 8 * k, bd1 + at_i + 16 * k, id, add);
+                                tc_mma_ts(acc + C::T, a + 8 * k, bd1 + at_i + 64 + 16 * k, id, add);
+                                tc_mma_ts(acc + C::T, a + 32 + 8 * k, bd1 + at_i + 16 * k, id, 1u);
                             } else {
-                                tc_mma_ts(acc, a + 8 * k, bd0 + slot + 16 * k, id, add);
-                                if constexpr (WT == 2) tc_mma_ts(acc + NT, a + 32 + 8 * k, bd0 + slot + 16 * k, id, add);
+                                tc_mma_ts(acc, a + 8 * k, bd0 + at_i + 16 * k, id, add);
+                                if constexpr (WT == 2) tc_mma_ts(acc, a + 32 + 8 * k, bd0 + at_i + 16 * k, id, 1u);
                             }
                         }
                     }
-                    tc_commit(&done[st]);
-                }
-                b += KS;
-                if (b >= p.nst || b % C::FLUSH == 0) {
-                    if (leader) tc_commit(&accfull[seg % NBUF]);
-                    ++seg;
+                    bar_commit(a_done);
+                    bar_commit(b_done);
+                    ready = b_next && f_next;
+                    b += KS;
+                    if (b >= p.nst || b % C::FLUSH == 0) {
+                        bar_commit(bar(C::ACCF + seg % NBUF));
+                        ++seg;
+                    }
                 }
             }
-        }
-        // Every issued product completes before tensor memory is freed.
-        if (any) {
-            if (leader) tc_commit(&drained);
-            mbar_drain(&drained, 0);
+            // Every issued product completes before tensor memory is freed.
+            if (any) {
+                bar_commit(bar(C::DRAIN));
+                bar_drain(bar(C::DRAIN), 0);
+            }
         }
         __syncwarp();
     }
     } else if (warp < kEpi0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RDEC));
         // Decoders: lane's half of the tile (lanes 16 apart hold the same row
         // of both) and row in it.
         const int grp = (warp - kDec0) >> 2, w4 = warp & 3;
-        const int half = lane >> 4, i = 16 * w4 + (lane & 15);
+        const int half = lane >> 4, i = lane_row(16 * w4 + (lane & 15), p.logP);
         const uint32_t a0 = tmem + C::ACOL + ((uint32_t)(32 * w4) << 16);
         const int64_t copied = p.copies ? p.total_rows & ~(int64_t)(p.P - 1) : 0;   // rows in whole super-rows
         const int nst = (p.nst + KS - 1) / KS * KS;   // with the slice that fills the last stage
-        uint32_t n0 = 0, rc = 0;       // slices and chunks before this chunk
-        int turn = 0;                  // n0 % kGroups
+        uint32_t n0 = 0;               // slices before this chunk
+        uint32_t r = 0, ph = 0;        // raw chunk and its phase
+        int turn = 0;                  // n0 % G
         bool ok = true;
         Item w;
         for (uint32_t it = 0; ok && take(it, w); ++it) {
@@ -666,62 +803,72 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                 ((uint32_t)(j * p.rb) & 15u);
             const bool tail = row >= copied && row < p.total_rows;
             const uint8_t *direct = p.W[p.gated ? half : 0] + (tail ? row : 0) * p.rb;
-            for (int c = 0; ok && c < p.nch; ++c, ++rc) {
-                const int r = rc % R, nq = min(QPC, nst - c * QPC);
-                if (!(ok = waits(&rfull[r], (rc / R) & 1))) break;
+            for (int c = 0; ok && c < p.nch; ++c) {
+                const int nq = min(QPC, nst - c * QPC);
+                if (!(ok = waits(bar(C::RFULL + r), ph))) break;
                 const uint8_t *src = raw + r * C::RAW;
                 int q = grp - turn;
-                if (q < 0) q += kGroups;
-                for (; q < nq; q += kGroups) {
+                if (q < 0) q += G;
+                for (; q < nq; q += G) {
                     const uint32_t n = n0 + q;
-                    const int st = n / KS % S;
-                    if (!(ok = waits(&done[st], ((n / (KS * S)) & 1) ^ 1))) break;
+                    const uint32_t m = n / KS, st = m % S;   // its stage
+                    const uint32_t a = a0 + st * C::ASTAGE + n % KS * C::ASLICE;
+                    auto free = [&]() -> bool { return waits(bar(C::ADONE + st), ((m / S) & 1) ^ 1); };
                     const bool none = KS > 1 && c * QPC + q >= p.nst;   // (nothing of this slice is read)
-                    tc_fence_after();
-                    const uint32_t a = a0 + (uint32_t)(st * C::ASTAGE + n % KS * C::ASLICE);
                     uint32_t hi[16], lo[16];
-                    if (none) {
-                    } else if constexpr (FMT == RF_Q4_K) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            q4k_block<WT>(src + at, q, t, hi, lo);
-                            tmem_st16(a + 16 * t, hi);
-                            if constexpr (WT == 2) tmem_st16(a + 32 + 16 * t, lo);
+                    auto store = [&](int t) {
+                        tmem_st16(a + 16 * t, hi);
+                        if constexpr (WT == 2) tmem_st16(a + 32 + 16 * t, lo);
+                    };
+                    // The first block's pairs are ready when the stage is free.
+                    if constexpr (FMT == RF_Q4_K) {
+                        if (!none) q4k_block<C::LOW>(src + at, q, 0, hi, lo);
+                        if (!(ok = free())) break;
+                        tc_fence_after();
+                        if (!none) {
+                            store(0);
+                            q4k_block<C::LOW>(src + at, q, 1, hi, lo);
+                            store(1);
                         }
                     } else {
-                        constexpr int SBYTES = 2 * Raw<FMT>::BS;
-                        Win<SBYTES> win;
+                        constexpr int BS = Raw<FMT>::BS;
                         const int b0 = 2 * (c * QPC + q);
-                        if (tail) win.load_global(direct + (int64_t)b0 * Raw<FMT>::BS, min(2, p.nb - b0) * Raw<FMT>::BS);
-                        else win.load(src, at + (uint32_t)(q * SBYTES));
-                        win_block<FMT, WT, 0>(win, hi, lo);
-                        tmem_st16(a, hi);
-                        if constexpr (WT == 2) tmem_st16(a + 32, lo);
-                        if (b0 + 1 < p.nb) {
-                            win_block<FMT, WT, 1>(win, hi, lo);
-                        } else {   // behind the last block: the next row's bytes
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0u;
+                        const bool second = b0 + 1 < p.nb;   // behind the last block: the next row's bytes
+                        Win<2 * BS> win;
+                        if (!none) {
+                            if (tail) win.load_bytes(direct + (int64_t)b0 * BS, second ? 2 * BS : BS);
+                            else win.load(src, at + (uint32_t)(q * 2 * BS));
+                            block_pairs<FMT, C::LOW, 0>(win, hi, lo);
                         }
-                        tmem_st16(a + 16, hi);
-                        if constexpr (WT == 2) tmem_st16(a + 48, lo);
+                        if (!(ok = free())) break;
+                        tc_fence_after();
+                        if (!none) {
+                            store(0);
+                            if (second) block_pairs<FMT, C::LOW, 1>(win, hi, lo);
+                            else {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0u;
+                            }
+                            store(1);
+                        }
                     }
                     tmem_st_wait();
                     tc_fence_before();
-                    if (!(ok = waits(&bfull[st], (n / (KS * S)) & 1))) break;
-                    if (lane == 0) mbar_arrive(&full[st]);
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(C::FULL + st));
                 }
                 if (!ok) break;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&rempty[r]);
+                if (lane == 0) bar_arrive(bar(C::REMPTY + r));
+                if (++r == R) r = 0, ph ^= 1u;
                 n0 += nq;
-                turn = (turn + nq) % kGroups;
+                turn = (turn + nq) % G;
             }
         }
     } else {
-        if constexpr (XT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REPI));
         // Epilogue: lane's row as the decoders have it.
-        const int w4 = warp & 3, half = lane >> 4, i = 16 * w4 + (lane & 15);
+        const int w4 = warp & 3, half = lane >> 4, i = lane_row(16 * w4 + (lane & 15), p.logP);
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         uint32_t seg = 0;
         Item w;
@@ -734,28 +881,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             auto release = [&] {   // the sums are read: others may overwrite them
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&accempty[seg % NBUF]);
+                if (lane == 0) bar_arrive(bar(C::ACCE + seg % NBUF));
                 ++seg;
             };
             if constexpr (XT == 1) {
                 float next[16];
                 load_inv(inv, next);
-                if (!waits(&accfull[seg % NBUF], (seg / NBUF) & 1)) break;
+                if (!waits(bar(C::ACCF + seg % NBUF), (seg / NBUF) & 1)) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + lanes + (seg % NBUF) * C::ACC;
 #pragma unroll 1
                 for (int t0 = 0; t0 < w.cnt; t0 += 16) {
                     float z[16], f[16];
-                    uint32_t v[16], l[16];
+                    uint32_t v[16];
                     tmem_ld16(acc + t0, v);
-                    if constexpr (WT == 2) tmem_ld16(acc + NT + t0, l);
 #pragma unroll
                     for (int u = 0; u < 16; ++u) f[u] = next[u];
                     if (t0 + 16 < w.cnt) load_inv(inv + t0 + 16, next);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        z[u] = WT == 2 ? fmaf(__uint_as_float(l[u]), 1.f / 2048.f, __uint_as_float(v[u])) : __uint_as_float(v[u]);
+                    for (int u = 0; u < 16; ++u) z[u] = __uint_as_float(v[u]);
                     if (t0 + 16 >= w.cnt) release();
                     finish_typed(p, z, f, b, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
                 }
@@ -767,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int u = 0; u < C::T; ++u) sum[u] = 0.f;
 #pragma unroll 1
                 for (int b0 = 0; b0 < p.nst; b0 += C::FLUSH) {
-                    if (!(ok = waits(&accfull[seg % NBUF], (seg / NBUF) & 1))) break;
+                    if (!(ok = waits(bar(C::ACCF + seg % NBUF), (seg / NBUF) & 1))) break;
                     tc_fence_after();
                     const uint32_t acc = tmem + lanes + (seg % NBUF) * C::ACC;
 #pragma unroll
@@ -808,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 }
 
 template <int FMT, int NT, int XT, int WT>
-rf_status launch(const Params &p, int grid, cudaStream_t s)
+rf_status launch(Params &p, int grid, cudaStream_t s)
 {
     using C = Cfg<FMT, NT, XT, WT>;
     static std::once_flag once[64];
@@ -824,19 +969,20 @@ rf_status launch(const Params &p, int grid, cudaStream_t s)
         cudaGetLastError();
     });
     if (!ok[dev & 63]) return RF_ERR_CUDA;
-    chunk_kernel<FMT, NT, XT, WT><<<grid, kThreads, C::SMEM, s>>>(p);
+    p.slots = std::min<int>(kInFlight, C::RING / (C::KS * p.slot));
+    chunk_kernel<FMT, NT, XT, WT><<<grid, C::THREADS, C::SMEM, s>>>(p);
     return last_cuda_error();
 }
 
 template <int FMT>
-rf_status launch_fmt(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
+rf_status launch_fmt(const ChunkShape &sh, Params &p, int grid, cudaStream_t s)
 {
     if constexpr (FMT != RF_MXFP4) {
         if (sh.wt == 2) return sh.xt == 2 ? launch<FMT, 128, 2, 2>(p, grid, s) : launch<FMT, 128, 1, 2>(p, grid, s);
     } else {
         if (sh.xt == 2) return launch<FMT, 128, 2, 1>(p, grid, s);
     }
-    return sh.nt == 256 ? launch<FMT, 256, 1, 1>(p, grid, s) : launch<FMT, 128, 1, 1>(p, grid, s);
+    return sh.nt > 128 ? launch<FMT, 192, 1, 1>(p, grid, s) : launch<FMT, 128, 1, 1>(p, grid, s);
 }
 
 }  // namespace
@@ -864,7 +1010,7 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
     p.P = P;
     while ((1 << p.logP) < P) ++p.logP;
     const int cb = sh.fmt == RF_Q4_0 || sh.fmt == RF_Q4_K ? 144 : 272;
-    p.bw = cb + (P > 1 ? 16 : 0);
+    p.bw = box_bytes(sh.fmt, P);
     p.gated = g.up != nullptr;
     p.W[0] = g.W;
     p.W[1] = g.up;
@@ -902,6 +1048,7 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
         p.limit_ns = lim;
         p.withhold = sh.nst > 1 ? 1 : 0;
     }
+    p.slot = (uint32_t)sh.nt * kSliceK * 2;
     const int grid = (int)std::min<int64_t>(num_sms(), sh.cap_tiles * p.nrt);
     switch (sh.fmt) {
     case RF_Q4_0: return launch_fmt<RF_Q4_0>(sh, p, grid, s);
