@@ -14,8 +14,8 @@
 //   warp 1       copies the operand slices of the token tile (1-D bulk);
 //   warp 2       issues the products;
 //   warp 3       draws the items;
-//   decoders     four groups of four warps: each takes every fourth 64-input
-//                slice, a thread its row, turns the raw bytes into fp16 pairs
+//   decoders     four groups of four warps: each takes every fourth stage (one
+//                or two 64-input slices), a thread its row, turns the raw bytes into fp16 pairs
 //                and stores them to tensor memory, from where tcgen05.mma reads
 //                the weights: they cost no shared-memory bandwidth, which is
 //                what bounds tiles whose operands both lie there;
@@ -28,7 +28,7 @@
 // chunk of 64 matrix rows is P boxes, one for each position j in the
 // super-row, whose first byte j * rb + c * (chunk bytes) is rounded down to 16;
 // a thread skips the remainder.  Rows behind the last whole super-row (fewer
-// than 16 of a tensor) are read by their threads directly.
+// than 16 of a tensor) are copied by their threads.
 //
 // Order of the inputs.  A product does not care in which order its inputs are
 // summed, so a slice's inputs are in the order in which the decoder finds them
@@ -121,7 +121,7 @@ struct Cfg {
     static_assert(ACC * NBUF <= ACOL, "tensor memory");
     static_assert(QPC % KS == 0 && FLUSH % KS == 0, "a stage lies in one chunk and between two flushes");
     static_assert(T % 16 == 0, "the epilogue takes 16 tokens at a time");
-    static_assert((G + KS - 1) / KS <= S, "groups wait within one phase of a stage");
+    static_assert(G == S && (G & (G - 1)) == 0, "each group has a stage of its own");
     static_assert(REPI <= 248 && REPI % 8 == 0 && RROLES < REGS, "registers");
     static_assert(KS * BT <= RING && S <= kInFlight, "a stage fits the ring");
 };
@@ -185,10 +185,11 @@ struct Win {
     // From shared memory at any byte: the 16-byte units that hold them (eight
     // lanes' rows are an odd number of units apart, so their loads meet no
     // bank twice), then words' and bytes' shifts.
-    __device__ __forceinline__ void load(const uint8_t *raw, uint32_t off)
+    __device__ __forceinline__ void load(const uint8_t *row, int at)
     {
         uint32_t x[4 * NU];
-        const uint4 *s = reinterpret_cast<const uint4 *>(raw + (off & ~15u));
+        const uint32_t off = smem_addr(row) + (uint32_t)at;
+        const uint4 *s = reinterpret_cast<const uint4 *>(row + at - (off & 15u));
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
             const uint4 v = s[i];
@@ -202,15 +203,6 @@ struct Win {
         for (int i = 0; i < NO + 1; ++i) x[i] = one ? x[i + 1] : x[i];
 #pragma unroll
         for (int i = 0; i < NO; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], sh);
-    }
-    // From global memory, n bytes one by one (the rest reads as 0).
-    __device__ __forceinline__ void load_bytes(const uint8_t *a, int n)
-    {
-#pragma unroll
-        for (int i = 0; i < NO; ++i) w[i] = 0u;
-#pragma unroll
-        for (int i = 0; i < BYTES; ++i)
-            if (i < n) w[i / 4] |= (uint32_t)__ldg(a + i) << (8 * (i % 4));
     }
 };
 
@@ -553,8 +545,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
     constexpr int G = C::G, kEpi0 = C::EPI0;
     extern __shared__ __align__(1024) uint8_t smem[];   // [RING], [R][RAW], 16 bytes that a last load may touch
     uint8_t *raw = smem + C::RING;
-    // FULL: a stage's weights are decoded (an arrival per decoder warp and
-    // slice); BFULL: its activations have landed; ADONE, BDONE: its products
+    // FULL: a stage's weights are decoded (an arrival per decoder warp); BFULL: its activations have landed; ADONE, BDONE: its products
     // are through; RFULL, REMPTY: raw chunks; ACCF, ACCE: sums; IFULL, IEMPTY:
     // items.
     __shared__ uint64_t bars[C::BARS];
@@ -567,7 +558,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::BARS; ++i) {
             uint32_t n = 1;
-            if (i < C::ADONE) n = 4 * KS;
+            if (i < C::ADONE) n = 4;
             else if (i >= C::REMPTY && i < C::ACCF) n = 4 * G;
             else if (i >= C::ACCE && i < C::IFULL) n = 4;
             else if (i >= C::IEMPTY && i < C::DRAIN) n = C::USERS;
@@ -787,10 +778,9 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
         const int half = lane >> 4, i = lane_row(16 * w4 + (lane & 15), p.logP);
         const uint32_t a0 = tmem + C::ACOL + ((uint32_t)(32 * w4) << 16);
         const int64_t copied = p.copies ? p.total_rows & ~(int64_t)(p.P - 1) : 0;   // rows in whole super-rows
-        const int nst = (p.nst + KS - 1) / KS * KS;   // with the slice that fills the last stage
-        uint32_t n0 = 0;               // slices before this chunk
+        const uint32_t a = a0 + (uint32_t)grp * C::ASTAGE;   // (as many stages as groups: each group has its own)
+        uint32_t m = 0;                // stages before this chunk
         uint32_t r = 0, ph = 0;        // raw chunk and its phase
-        int turn = 0;                  // n0 % G
         bool ok = true;
         Item w;
         for (uint32_t it = 0; ok && take(it, w); ++it) {
@@ -802,67 +792,66 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
             const uint32_t at = (uint32_t)((half << p.logP) + j) * (uint32_t)((64 >> p.logP) * p.bw) + (uint32_t)(s * p.bw) +
                                 ((uint32_t)(j * p.rb) & 15u);
             const bool tail = row >= copied && row < p.total_rows;
-            const uint8_t *direct = p.W[p.gated ? half : 0] + (tail ? row : 0) * p.rb;
             for (int c = 0; ok && c < p.nch; ++c) {
-                const int nq = min(QPC, nst - c * QPC);
+                const int nq = min(QPC, p.nst - c * QPC), ns = (nq + KS - 1) / KS;   // its slices and stages
                 if (!(ok = waits(bar(C::RFULL + r), ph))) break;
-                const uint8_t *src = raw + r * C::RAW;
-                int q = grp - turn;
-                if (q < 0) q += G;
-                for (; q < nq; q += G) {
-                    const uint32_t n = n0 + q;
-                    const uint32_t m = n / KS, st = m % S;   // its stage
-                    const uint32_t a = a0 + st * C::ASTAGE + n % KS * C::ASLICE;
-                    auto free = [&]() -> bool { return waits(bar(C::ADONE + st), ((m / S) & 1) ^ 1); };
-                    const bool none = KS > 1 && c * QPC + q >= p.nst;   // (nothing of this slice is read)
+                uint8_t *src = raw + r * C::RAW + at;
+                if (tail) {
+                    // A row that the boxes do not reach, copied to where they
+                    // would put it (by every group, each for itself).
+                    const uint8_t *g = p.W[p.gated ? half : 0] + row * p.rb + (int64_t)c * C::CB;
+                    const int n = (int)min((int64_t)C::CB, p.rb - (int64_t)c * C::CB);
+#pragma unroll 1
+                    for (int k = 0; k < n; ++k) src[k] = __ldg(g + k);
+                }
+                for (int q = (grp - (int)m) & (G - 1); q < ns; q += G) {
                     uint32_t hi[16], lo[16];
-                    auto store = [&](int t) {
-                        tmem_st16(a + 16 * t, hi);
-                        if constexpr (WT == 2) tmem_st16(a + 32 + 16 * t, lo);
+                    bool open = false;   // the stage is known to be free
+                    auto store = [&](int at_col) -> bool {
+                        if (!open) {
+                            if (!waits(bar(C::ADONE + grp), (((m + (uint32_t)q) / G) & 1) ^ 1)) return false;
+                            tc_fence_after();
+                            open = true;
+                        }
+                        tmem_st16(a + at_col, hi);
+                        if constexpr (WT == 2) tmem_st16(a + 32 + at_col, lo);
+                        return true;
                     };
-                    // The first block's pairs are ready when the stage is free.
-                    if constexpr (FMT == RF_Q4_K) {
-                        if (!none) q4k_block<C::LOW>(src + at, q, 0, hi, lo);
-                        if (!(ok = free())) break;
-                        tc_fence_after();
-                        if (!none) {
-                            store(0);
-                            q4k_block<C::LOW>(src + at, q, 1, hi, lo);
-                            store(1);
-                        }
-                    } else {
-                        constexpr int BS = Raw<FMT>::BS;
-                        const int b0 = 2 * (c * QPC + q);
-                        const bool second = b0 + 1 < p.nb;   // behind the last block: the next row's bytes
-                        Win<2 * BS> win;
-                        if (!none) {
-                            if (tail) win.load_bytes(direct + (int64_t)b0 * BS, second ? 2 * BS : BS);
-                            else win.load(src, at + (uint32_t)(q * 2 * BS));
+#pragma unroll
+                    for (int e = 0; e < KS; ++e) {
+                        const int sl = q * KS + e;   // slice of the chunk
+                        if (e > 0 && sl >= nq) break;
+                        if constexpr (FMT == RF_Q4_K) {
+                            q4k_block<C::LOW>(src, sl, 0, hi, lo);
+                            if (!(ok = store(C::ASLICE * e))) break;
+                            q4k_block<C::LOW>(src, sl, 1, hi, lo);
+                            store(C::ASLICE * e + 16);
+                        } else {
+                            constexpr int BS = Raw<FMT>::BS;
+                            Win<2 * BS> win;
+                            win.load(src, sl * 2 * BS);
                             block_pairs<FMT, C::LOW, 0>(win, hi, lo);
-                        }
-                        if (!(ok = free())) break;
-                        tc_fence_after();
-                        if (!none) {
-                            store(0);
-                            if (second) block_pairs<FMT, C::LOW, 1>(win, hi, lo);
-                            else {
+                            if (!(ok = store(C::ASLICE * e))) break;
+                            block_pairs<FMT, C::LOW, 1>(win, hi, lo);
+                            if (2 * (c * QPC + sl) + 1 >= p.nb) {   // behind the last block: the next row's bytes
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0u;
                             }
-                            store(1);
+                            store(C::ASLICE * e + 16);
                         }
                     }
+                    if (!ok) break;
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(bar(C::FULL + st));
+                    if (lane == 0) bar_arrive(bar(C::FULL + grp));
                 }
                 if (!ok) break;
+                if (tail) fence_async_smem();   // the next copy follows these stores
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(C::REMPTY + r));
                 if (++r == R) r = 0, ph ^= 1u;
-                n0 += nq;
-                turn = (turn + nq) % G;
+                m += ns;
             }
         }
     } else {
