@@ -29,6 +29,7 @@ namespace {
 __device__ int g_chunk_invalid = 0;   // offsets or order entries out of range
 
 constexpr int kPrepThreads = 256;
+constexpr int kPrepRows = 8;         // tokens per CTA of the pre-pass
 constexpr int64_t kMaxPieces = 1LL << 30;
 
 template <int DT> struct Elem;
@@ -158,16 +159,16 @@ template <int DT, int XT>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ PrepParams p)
 {
     using T = typename Elem<DT>::T;
-    constexpr int GT = kGranRows / XT;
+    constexpr int GT = kGranRows / XT, H = GT / kPrepRows;   // tokens of a granule, CTAs that share it
     if (blockIdx.x == gridDim.x - 1) {
         list_tiles<GT>(p);
         return;
     }
-    const int gran = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+    const int part = blockIdx.x % p.parts, gran = blockIdx.x / p.parts / H, sub = blockIdx.x / p.parts % H;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __shared__ int s_group, s_row, s_cnt, s_n, s_at;
-    __shared__ float s_scale[GT];
-    __shared__ int64_t s_src[GT];
+    __shared__ float s_scale[kPrepRows];
+    __shared__ int64_t s_src[kPrepRows];
     if (tid == 0) s_group = -1;
     __syncthreads();
     for (int g = tid; g < p.n_group; g += kPrepThreads) {
@@ -177,19 +178,19 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         if (q < 0 || q >= (b - a + GT - 1) / GT) continue;
         const int tt = p.tile_tokens / GT;   // granules per whole tile
         s_group = g;
-        s_row = a + q * GT;
-        s_cnt = min(GT, b - s_row);
+        s_row = a + q * GT + sub * kPrepRows;
+        s_cnt = min(kPrepRows, b - s_row);
         s_at = gran - q + q / tt * tt;       // the tile's first granule
         s_n = min(tt, (b - a - q / tt * p.tile_tokens + GT - 1) / GT);
     }
     __syncthreads();
     if (s_group < 0) return;
-    const int cnt = s_cnt;
     // Scales: a warp per row.
-    for (int r = warp; r < GT; r += kPrepThreads / 32) {
+    {
+        static_assert(kPrepRows == kPrepThreads / 32, "a warp per row");
         int64_t src = -1;
-        if (r < cnt) {
-            const int row = s_row + r;
+        if (warp < s_cnt) {
+            const int row = s_row + warp;
             src = p.order ? p.order[row] / p.per : row;
             if (p.order && (p.order[row] < 0 || src >= p.n_x)) {
                 src = -1;
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         float m = 0.f;
         if (src >= 0) {
             const T *x = static_cast<const T *>(p.X) + src * p.ldx;
+#pragma unroll 8
             for (int k = 4 * lane; k < p.in_dim; k += 128) {
                 float f[4];
                 load4(x + k, p.vec, f);
@@ -216,26 +218,26 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         const int e = (int)(__float_as_uint(m) >> 23) - 127;
         const int k = m == 0.f ? 0 : max(-126, min(126, 14 - e));
         if (lane == 0) {
-            s_scale[r] = __uint_as_float((uint32_t)(k + 127) << 23);
-            s_src[r] = src;
-            if (part == 0) p.inv[(int64_t)gran * GT + r] = __uint_as_float((uint32_t)(127 - k) << 23);
+            s_scale[warp] = __uint_as_float((uint32_t)(k + 127) << 23);
+            s_src[warp] = src;
+            if (part == 0) p.inv[(int64_t)gran * GT + sub * kPrepRows + warp] = __uint_as_float((uint32_t)(127 - k) << 23);
         }
     }
     __syncthreads();
-    // Units: thread (r, c) writes inputs 8c.. of a slice of token r (its high
-    // and its low term).
-    constexpr int kUnits = GT * 8;
-    const int r = (tid & 7) + (GT == 16 ? ((tid >> 6) & 1) * 8 : 0), c = (tid >> 3) & 7;
+    // Units: thread (r, c) writes inputs 8c.. of a slice of row r (its high
+    // and its low term), kPrepThreads / 64 slices at a time.
+    constexpr int kStep = kPrepThreads / (8 * kPrepRows);
+    const int r = tid & 7, c = (tid >> 3) & 7;
     const float scale = s_scale[r];
     const int64_t src = s_src[r];
     const T *x = static_cast<const T *>(p.X) + (src >= 0 ? src * p.ldx : 0);
     const int first = c >> 2, u = c & 3;
     const int ka = 32 * first + (p.order8 == kOrderPlain ? 8 * u : 4 * u);
     const int kb = ka + (p.order8 == kOrderPlain ? 4 : 16);
-    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * kGranBytes +
-                   (GT == 16 ? (r >> 3) * 1024 : 0) + c * 128 + (r & 7) * 16;
+    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * kGranBytes + sub * 1024 + c * 128 + r * 16;
     const int64_t step = (int64_t)s_n * kGranBytes;
-    for (int s = part * (kPrepThreads / kUnits) + tid / kUnits; s < p.nst; s += p.parts * (kPrepThreads / kUnits)) {
+#pragma unroll 4
+    for (int s = part * kStep + (tid >> 6); s < p.nst; s += p.parts * kStep) {
         float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f}, f[8];
         const int k0 = s * kSliceK;
         if (src >= 0 && k0 + 32 * first < p.in_dim) {   // (whole blocks)
@@ -393,11 +395,12 @@ rf_status launch_prep(const ChunkShape &sh, const Source &x, uint8_t *ws, cudaSt
     p.tiles = reinterpret_cast<ChunkTile *>(ws + sh.at_tiles);
     p.inv = reinterpret_cast<float *>(ws + sh.at_inv);
     p.img = ws + sh.at_img;
-    // A granule's slices are shared out while there are few granules (each
-    // share finds the rows' maxima again).
-    const int64_t busy = std::min<int64_t>(sh.cap_gran, sh.n_row);   // granules with rows, at most
-    p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((sh.nst + 3) / 4, 2 * num_sms() / std::max<int64_t>(1, busy)));
-    const int64_t blocks = sh.cap_gran * p.parts;
+    // Rows' slices are shared out among CTAs while there are few rows (each
+    // finds its rows' maxima again).
+    const int64_t share = sh.gran_tokens() / kPrepRows;
+    const int64_t busy = std::min<int64_t>(sh.cap_gran * share, sh.n_row);   // CTAs with rows, at most
+    p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((sh.nst + 3) / 4, 4 * num_sms() / std::max<int64_t>(1, busy)));
+    const int64_t blocks = sh.cap_gran * share * p.parts;
     if (blocks > 0x7ffffffeLL) return RF_ERR_TOO_LARGE;
     if (x.dtype == RF_F32)
         return sh.xt == 2 ? launch_prep_t<RF_F32, 2>(p, blocks, s) : launch_prep_t<RF_F32, 1>(p, blocks, s);

@@ -70,7 +70,7 @@ template <> struct Raw<RF_MXFP4> { static constexpr int BS = 17, BE = 32, BPC = 
 template <> struct Raw<RF_Q4_K> { static constexpr int BS = 144, BE = 256, BPC = 1; };
 
 // Box bytes: the chunk's, with what rounding its first byte down takes, as an
-// odd number of 16-byte units (see Win::load); with 16 matrix rows to a
+// odd number of 16-byte units (see Block::load); with 16 matrix rows to a
 // super-row an even one, which keeps the boxes 128 bytes aligned.
 __host__ __device__ constexpr int box_bytes(int fmt, int P)
 {
@@ -165,44 +165,32 @@ __host__ __device__ constexpr uint32_t idesc_n(int n)
 }
 
 // ------------------------------------------------------------------ decoding
-// A slice's bytes (two blocks of 32 weights) as words from its first byte;
-// word<B>, byte<B>, half<B> at byte B.
-template <int BYTES>
-struct Win {
-    static constexpr int NO = (BYTES + 3) / 4, NU = (15 + BYTES + 15) / 16;
-    uint32_t w[NO];
-    template <int B> __device__ __forceinline__ uint32_t word() const
-    {
-        if constexpr (B % 4 == 0) return w[B / 4];
-        else return __funnelshift_r(w[B / 4], w[B / 4 + 1], 8 * (B % 4));
-    }
-    template <int B> __device__ __forceinline__ uint32_t byte() const { return (w[B / 4] >> (8 * (B % 4))) & 0xFFu; }
-    template <int B> __device__ __forceinline__ uint32_t half() const
-    {
-        static_assert(B % 2 == 0, "fp16 scale at an odd byte");
-        return (w[B / 4] >> (8 * (B % 4))) & 0xFFFFu;
-    }
-    // From shared memory at any byte: the 16-byte units that hold them (eight
-    // lanes' rows are an odd number of units apart, so their loads meet no
-    // bank twice), then words' and bytes' shifts.
+// One block of 32 weights from any byte of shared memory: its scale's bits and
+// its quant words.  8-byte loads (eight lanes' rows are an odd number of
+// 16-byte units apart, so that they meet few banks twice), then a word's shift
+// and, with the scale's bytes stepped over, a byte's.
+template <int FMT>
+struct Block {
+    static constexpr int NS = FMT == RF_MXFP4 ? 1 : 2, NW = FMT == RF_Q8_0 ? 8 : 4;   // scale bytes, quant words
+    static constexpr int ND = (7 + NS + 4 * NW) / 8;
+    uint32_t q[NW], s;
     __device__ __forceinline__ void load(const uint8_t *row, int at)
     {
-        uint32_t x[4 * NU];
+        uint32_t x[2 * ND];
         const uint32_t off = smem_addr(row) + (uint32_t)at;
-        const uint4 *s = reinterpret_cast<const uint4 *>(row + at - (off & 15u));
+        const uint2 *src = reinterpret_cast<const uint2 *>(row + at - (off & 7u));
 #pragma unroll
-        for (int i = 0; i < NU; ++i) {
-            const uint4 v = s[i];
-            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        for (int i = 0; i < ND; ++i) {
+            const uint2 v = src[i];
+            x[2 * i] = v.x, x[2 * i + 1] = v.y;
         }
-        const bool two = (off & 8u) != 0, one = (off & 4u) != 0;
+        const bool odd = (off & 4u) != 0;
         const uint32_t sh = 8u * (off & 3u);
 #pragma unroll
-        for (int i = 0; i < NO + 2; ++i) x[i] = two ? x[i + 2] : x[i];
+        for (int i = 0; i < NW + 1; ++i) x[i] = odd ? x[i + 1] : x[i];
+        s = (x[0] >> sh) & (NS == 1 ? 0xFFu : 0xFFFFu);
 #pragma unroll
-        for (int i = 0; i < NO + 1; ++i) x[i] = one ? x[i + 1] : x[i];
-#pragma unroll
-        for (int i = 0; i < NO; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], sh);
+        for (int i = 0; i < NW; ++i) q[i] = __funnelshift_rc(x[i], x[i + 1], sh + 8 * NS);
     }
 };
 
@@ -352,25 +340,12 @@ __device__ __forceinline__ void q4k_block(const uint8_t *s, int Q, int T, uint32
     }
 }
 
-// Block BLK of a slice.
-template <int FMT, int L, int BLK, class W>
-__device__ __forceinline__ void block_pairs(const W &win, uint32_t (&hi)[16], uint32_t (&lo)[16])
+template <int FMT, int L>
+__device__ __forceinline__ void block_pairs(const Block<FMT> &b, uint32_t (&hi)[16], uint32_t (&lo)[16])
 {
-    constexpr int O = BLK * Raw<FMT>::BS;
-    if constexpr (FMT == RF_Q4_0) {
-        const uint32_t q[4] = {win.template word<O + 2>(), win.template word<O + 6>(), win.template word<O + 10>(),
-                               win.template word<O + 14>()};
-        q4_0_block<L>(win.template half<O>(), q, hi, lo);
-    } else if constexpr (FMT == RF_Q8_0) {
-        const uint32_t q[8] = {win.template word<O + 2>(),  win.template word<O + 6>(),  win.template word<O + 10>(),
-                               win.template word<O + 14>(), win.template word<O + 18>(), win.template word<O + 22>(),
-                               win.template word<O + 26>(), win.template word<O + 30>()};
-        q8_0_block<L>(win.template half<O>(), q, hi, lo);
-    } else {
-        const uint32_t q[4] = {win.template word<O + 1>(), win.template word<O + 5>(), win.template word<O + 9>(),
-                               win.template word<O + 13>()};
-        mxfp4_block(win.template byte<O>(), q, hi);
-    }
+    if constexpr (FMT == RF_Q4_0) q4_0_block<L>(b.s, b.q, hi, lo);
+    else if constexpr (FMT == RF_Q8_0) q8_0_block<L>(b.s, b.q, hi, lo);
+    else mxfp4_block(b.s, b.q, hi);
 }
 
 // ---------------------------------------------------------------- activations
@@ -828,11 +803,12 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                             store(C::ASLICE * e + 16);
                         } else {
                             constexpr int BS = Raw<FMT>::BS;
-                            Win<2 * BS> win;
-                            win.load(src, sl * 2 * BS);
-                            block_pairs<FMT, C::LOW, 0>(win, hi, lo);
+                            Block<FMT> blk[2];
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) blk[t].load(src, (2 * sl + t) * BS);
+                            block_pairs<FMT, C::LOW>(blk[0], hi, lo);
                             if (!(ok = store(C::ASLICE * e))) break;
-                            block_pairs<FMT, C::LOW, 1>(win, hi, lo);
+                            block_pairs<FMT, C::LOW>(blk[1], hi, lo);
                             if (2 * (c * QPC + sl) + 1 >= p.nb) {   // behind the last block: the next row's bytes
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0u;
