@@ -61,6 +61,7 @@ constexpr int kM = 128;              // matrix rows per item (MMA M)
 constexpr int kDec0 = 4;             // first decoder warp; the epilogue's four follow the decoders
 constexpr int kItems = 4;            // items drawn ahead
 constexpr int kInFlight = 16;        // stages of activations in flight at most
+constexpr int kRaws = 8;             // raw chunks in flight at most
 
 // Raw chunk: BPC blocks (of BE weights, BS bytes) of each row.
 template <int FMT> struct Raw;
@@ -100,8 +101,6 @@ struct Cfg {
     static constexpr int REPI = (G + 2) * REGS - RROLES - G * RDEC;
     static constexpr int BT = NT * kSliceK * 2;                        // activation bytes per slice at most
     static constexpr int RAW = kM * BW;
-    static constexpr int R = RAW > 32768 ? 2 : 3;                      // raw chunks in flight
-    static constexpr int RING = (230000 - R * RAW) / 2048 * 2048;      // bytes of activations in flight
     static constexpr int LOW = WT == 1 ? 0 : (XT == 1 ? 1 : 2);        // Low
     // Columns of one item's sums (with two terms of both: T of high products,
     // T of the others).
@@ -113,17 +112,22 @@ struct Cfg {
     // cores truncate each addition (about 1e-8 of the sum, always towards
     // zero), rounded additions in registers do not drift.
     static constexpr int FLUSH = XT == 2 ? 4 : 1 << 30;                // slices
-    static constexpr size_t SMEM = (size_t)RING + (size_t)R * RAW + 16;
+    // Shared memory: stages of activations, raw chunks, and 16 bytes that a
+    // last load may touch.  Activations come from L2 in about as long as eight
+    // slices take; the weights come from memory and get the rest.
+    static constexpr int SHARED = 230000;
+    static constexpr size_t SMEM = SHARED + 16;
+    static constexpr int LEAST = (NT > 128 ? 6 : 8) / KS;              // stages of activations at least
     // Barriers, by number.
     static constexpr int FULL = 0, ADONE = FULL + S, BFULL = ADONE + S, BDONE = BFULL + kInFlight, RFULL = BDONE + kInFlight,
-                         REMPTY = RFULL + R, ACCF = REMPTY + R, ACCE = ACCF + NBUF, IFULL = ACCE + NBUF, IEMPTY = IFULL + kItems,
+                         REMPTY = RFULL + kRaws, ACCF = REMPTY + kRaws, ACCE = ACCF + NBUF, IFULL = ACCE + NBUF, IEMPTY = IFULL + kItems,
                          DRAIN = IEMPTY + kItems, BARS = DRAIN + 1;
     static_assert(ACC * NBUF <= ACOL, "tensor memory");
     static_assert(QPC % KS == 0 && FLUSH % KS == 0, "a stage lies in one chunk and between two flushes");
     static_assert(T % 16 == 0, "the epilogue takes 16 tokens at a time");
     static_assert(G == S && (G & (G - 1)) == 0, "each group has a stage of its own");
     static_assert(REPI <= 248 && REPI % 8 == 0 && RROLES < REGS, "registers");
-    static_assert(KS * BT <= RING && S <= kInFlight, "a stage fits the ring");
+    static_assert(LEAST * KS * BT + 2 * RAW <= SHARED && LEAST <= kInFlight, "the least stages and two chunks fit");
 };
 
 struct Item {
@@ -141,8 +145,8 @@ struct Params {
     int32_t P, logP;          // matrix rows per super-row
     int32_t bw;               // box bytes: chunk bytes, 16 more when P > 1
     int32_t copies;           // 0: every row is behind the last super-row
-    int32_t slots;            // stages of activations in shared memory,
-    uint32_t slot;            // and the bytes of a slice of one
+    int32_t slots, raws;      // stages of activations and raw chunks in shared memory,
+    uint32_t slot, raw_at;    // bytes of a slice of such a stage, and where the chunks begin
     int32_t rows, nst, nch, nb, nrt, gated;   // rows of Y; slices, chunks, blocks of a row; row tiles
     int32_t act, dtype;
     float alpha, limit;
@@ -151,7 +155,7 @@ struct Params {
     int64_t ldr, ldy;
     void *Y;
     int32_t withhold;         // test hook: CTA 0 never copies this slice's activations
-    unsigned long long limit_ns;
+    long long limit_cycles;   // of a wait
 };
 
 // Row of a half of the tile for each of its 64 threads (tensor-memory lanes):
@@ -516,10 +520,10 @@ template <int FMT, int NT, int XT, int WT>
 __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<FMT, NT, XT, WT>;
-    constexpr int S = C::S, KS = C::KS, R = C::R, QPC = C::QPC, NBUF = C::NBUF, GT = kGranRows / XT;
+    constexpr int S = C::S, KS = C::KS, QPC = C::QPC, NBUF = C::NBUF, GT = kGranRows / XT;
     constexpr int G = C::G, kEpi0 = C::EPI0;
-    extern __shared__ __align__(1024) uint8_t smem[];   // [RING], [R][RAW], 16 bytes that a last load may touch
-    uint8_t *raw = smem + C::RING;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *raw = smem + p.raw_at;
     // FULL: a stage's weights are decoded (an arrival per decoder warp); BFULL: its activations have landed; ADONE, BDONE: its products
     // are through; RFULL, REMPTY: raw chunks; ACCF, ACCE: sums; IFULL, IEMPTY:
     // items.
@@ -552,22 +556,20 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     const uint32_t bar0 = smem_addr(bars);
     auto bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
+    // Bounded by the SM's clock (reading the global timer takes as long as a
+    // stage's products).  Short, because every role has a few of it in its
+    // loop, and a role's instructions are fetched anew whenever the other
+    // roles' have pushed them out.
     auto wait = [&](uint32_t at, uint32_t parity) -> bool {
-        // (The timer is read only after a long wait: it takes as long as a
-        // stage's products.)
-        if (bar_try(at, parity) || bar_try_ns(at, parity, 20000u)) return true;
-        const unsigned long long t0 = globaltimer_ns();
-        while (!*stop) {
-            if (bar_try_ns(at, parity, 20000u)) return true;
-            const unsigned long long dt = globaltimer_ns() - t0;
-            if (dt > p.limit_ns) {
+        if (bar_try(at, parity)) return true;
+        const long long t0 = clock64();
+        while (!bar_try_ns(at, parity, 20000u))
+            if (*stop || *reinterpret_cast<volatile int *>(&g_chunk_status) != 0 || clock64() - t0 > p.limit_cycles) {
                 record_status(&g_chunk_status, RF_ERR_TIMEOUT);
                 *stop = 1;
-            } else if (dt > 20000ull && *reinterpret_cast<volatile int *>(&g_chunk_status) != 0) {
-                *stop = 1;   // another CTA's wait has given up
+                return false;
             }
-        }
-        return false;
+        return true;
     };
     // A warp's waits; the next item, copied from its slot (one arrival a warp).
     auto waits = [&](uint32_t at, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(at, parity)); };
@@ -629,13 +631,15 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 __syncwarp();
                 if (copies) copy_box(dst + r * C::RAW, map, ((xj + c * C::CB) & ~15) >> 1, y, bar(C::RFULL + r));
                 ++rc;
-                if (++r == R) r = 0, ph ^= 1u;
+                if (++r == (uint32_t)p.raws) r = 0, ph ^= 1u;
             }
             if (!ok) break;
         }
         // Every copy issued lands before the CTA can exit.
-        if (lane == 0)
-            for (uint32_t i = rc > R ? rc - R : 0; i < rc; ++i) bar_drain(bar(C::RFULL + i % R), (i / R) & 1);
+        if (lane == 0) {
+            const uint32_t raws = (uint32_t)p.raws;
+            for (uint32_t i = rc > raws ? rc - raws : 0; i < rc; ++i) bar_drain(bar(C::RFULL + i % raws), (i / raws) & 1);
+        }
         __syncwarp();
     } else if (warp == 1) {
         // Activations, a stage at a time.
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     const bool b_next = bar_test(bar(C::BFULL + ib), pb), f_next = bar_test(bar(C::FULL + sa), pa);
                     tc_fence_after();
                     any = true;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < KS; ++i) {
                         if (i > 0 && !two) break;
                         const uint32_t a = a0 + (uint32_t)(i * C::ASLICE);
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                         if constexpr (WT == 2) tmem_st16(a + 32 + at_col, lo);
                         return true;
                     };
-#pragma unroll
+#pragma unroll 1
                     for (int e = 0; e < KS; ++e) {
                         const int sl = q * KS + e;   // slice of the chunk
                         if (e > 0 && sl >= nq) break;
@@ -826,7 +830,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 if (tail) fence_async_smem();   // the next copy follows these stores
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(C::REMPTY + r));
-                if (++r == R) r = 0, ph ^= 1u;
+                if (++r == (uint32_t)p.raws) r = 0, ph ^= 1u;
                 m += ns;
             }
         }
@@ -934,7 +938,10 @@ rf_status launch(Params &p, int grid, cudaStream_t s)
         cudaGetLastError();
     });
     if (!ok[dev & 63]) return RF_ERR_CUDA;
-    p.slots = std::min<int>(kInFlight, C::RING / (C::KS * p.slot));
+    const int stage = C::KS * (int)p.slot;
+    p.raws = std::min(kRaws, (C::SHARED - C::LEAST * stage) / C::RAW);
+    p.slots = std::min(kInFlight, (C::SHARED - p.raws * C::RAW) / stage);
+    p.raw_at = (uint32_t)(p.slots * stage);
     chunk_kernel<FMT, NT, XT, WT><<<grid, C::THREADS, C::SMEM, s>>>(p);
     return last_cuda_error();
 }
@@ -1007,10 +1014,10 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
     p.dtype = g.dtype;
     p.Y = g.Y;
     p.ldy = g.ldy;
-    p.limit_ns = kWaitLimitNs;
+    p.limit_cycles = 2 * (long long)kWaitLimitNs;   // (at most 2.07 GHz)
     p.withhold = -1;
     if (const unsigned long long lim = take_wait_fault()) {
-        p.limit_ns = lim;
+        p.limit_cycles = 2 * (long long)lim;
         p.withhold = sh.nst > 1 ? 1 : 0;
     }
     p.slot = (uint32_t)sh.nt * kSliceK * 2;
