@@ -197,13 +197,14 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-_DTYPES = _empty = _empty_like = _F32_TYPE = _U8_TYPE = None
+_DTYPES = _empty = _empty_like = _F32_TYPE = _U8_TYPE = _I32_TYPE = None
 
 
 def _look_up() -> None:
     """torch's names, once: an import statement in a function costs each call 0.5 us."""
-    global _DTYPES, _empty, _empty_like, _F32_TYPE, _U8_TYPE
+    global _DTYPES, _empty, _empty_like, _F32_TYPE, _U8_TYPE, _I32_TYPE
     import torch
+    _I32_TYPE = torch.int32
     _empty, _empty_like, _F32_TYPE, _U8_TYPE = torch.empty, torch.empty_like, torch.float32, torch.uint8
     _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
@@ -918,34 +919,18 @@ def gemm_grouped(fmt: int, W, rows: int, in_dim: int, X, offsets, order=None, pe
 
 
 class MoERouting:
-    """What rf_moe_route_tokens gives, over one int32 device tensor: idx and
-    w (n_tok, top_k), offsets (n_expert + 1,), order and place (n_tok * top_k,)."""
+    """What rf_moe_route_tokens gives: idx (int32) and w (float32), (n_tok,
+    top_k); offsets (n_expert + 1,), order and place (n_tok * top_k,), int32."""
 
     def __init__(self, n_tok: int, n_expert: int, top_k: int, device, stream=None):
-        import torch
+        if _empty is None:
+            _look_up()
         n = n_tok * top_k
-        self.n_tok, self.n_expert, self.top_k, self.n_row = n_tok, n_expert, top_k, n
-        self.memory = _new(stream, 4 * n + n_expert + 1, torch.int32, device)
-
-    @property
-    def idx(self):
-        return self.memory[:self.n_row].view(self.n_tok, self.top_k)
-
-    @property
-    def w(self):
-        return self.memory[self.n_row:2 * self.n_row].view(_F32_TYPE).view(self.n_tok, self.top_k)
-
-    @property
-    def order(self):
-        return self.memory[2 * self.n_row:3 * self.n_row]
-
-    @property
-    def place(self):
-        return self.memory[3 * self.n_row:4 * self.n_row]
-
-    @property
-    def offsets(self):
-        return self.memory[4 * self.n_row:]
+        self.idx = _new(stream, (n_tok, top_k), _I32_TYPE, device)
+        self.w = _new(stream, (n_tok, top_k), _F32_TYPE, device)
+        self.offsets = _new(stream, n_expert + 1, _I32_TYPE, device)
+        self.order = _new(stream, n, _I32_TYPE, device)
+        self.place = _new(stream, n, _I32_TYPE, device)
 
 
 def moe_route_tokens(logits, top_k: int, workspace=None, stream=None) -> MoERouting:
@@ -956,9 +941,9 @@ def moe_route_tokens(logits, top_k: int, workspace=None, stream=None) -> MoERout
     if workspace is None:
         need = lib().rf_moe_route_tokens_workspace_bytes(n_tok, n_expert, top_k)
     workspace, ws, ws_bytes = _space(workspace, need if workspace is None else 0, stream, logits.device)
-    at, n = r.memory.data_ptr(), 4 * r.n_row
-    _check(lib().rf_moe_route_tokens(dt, pl, ld, n_tok, n_expert, top_k, at, at + n, at + 4 * n, at + 2 * n, at + 3 * n,
-                                     ws, ws_bytes, _stream(stream)), "rf_moe_route_tokens")
+    _check(lib().rf_moe_route_tokens(dt, pl, ld, n_tok, n_expert, top_k, r.idx.data_ptr(), r.w.data_ptr(),
+                                     r.offsets.data_ptr(), r.order.data_ptr(), r.place.data_ptr(), ws, ws_bytes,
+                                     _stream(stream)), "rf_moe_route_tokens")
     return r
 
 

@@ -31,13 +31,13 @@ __device__ int g_chunk_invalid = 0;   // offsets or order entries out of range
 constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = 8;         // tokens per CTA of the pre-pass
 constexpr int64_t kMaxPieces = 1LL << 30;
+constexpr int64_t kMaxSums = 16LL << 20;   // floats of parts' sums at most
 
 template <int DT> struct Elem;
 template <> struct Elem<RF_F32> { using T = float; };
 template <> struct Elem<RF_F16> { using T = __half; };
 template <> struct Elem<RF_BF16> { using T = __nv_bfloat16; };
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
@@ -313,11 +313,39 @@ bool dtype_ok(int d) { return d == RF_F32 || d == RF_F16 || d == RF_BF16; }
 int dtype_size(int d) { return d == RF_F32 ? 4 : 2; }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// Parts of the rows' inputs.  With fewer items than fill the SMs evenly, an
+// item's inputs are shared out, and a second launch adds the parts' sums:
+// worth it while it saves a tenth of the SMs' rounds after what that launch,
+// the sums' traffic and the items' starts cost.  In SM cycles, as measured: a
+// slice's by what bounds it (see MEASURED at the kernel), 4,000 an item, 6,000
+// a launch, 1,500 bytes of sums a cycle.
+void choose_parts(ChunkShape &sh, bool gated)
+{
+    const int64_t tiles = sh.n_group == 1 ? (sh.n_row + sh.tile_tokens() - 1) / sh.tile_tokens()
+                                          : std::min(sh.cap_tiles, std::max(sh.n_row / sh.tile_tokens(), std::min(sh.n_group, sh.n_row)));
+    const int64_t items = tiles * ((sh.rows + (gated ? 63 : 127)) / (gated ? 64 : 128)), sms = num_sms();
+    const int64_t per = chunk_weights(sh.fmt) / kSliceK, nch = (sh.nst + per - 1) / per;
+    const int64_t slice = sh.wt == 2 ? (sh.fmt == RF_Q4_K ? 1400 : 1000) : (sh.nt > 128 ? 640 : 420);
+    auto cost = [&](int64_t parts) {
+        const int64_t slices = std::min<int64_t>((nch + parts - 1) / parts * per, sh.nst);
+        const int64_t sums = parts > 1 ? 6000 + parts * (1 + gated) * sh.n_row * sh.rows * 8 / 1500 : 0;
+        return (items * parts + sms - 1) / sms * (slice * slices + 4000) + sums;
+    };
+    int64_t best = 1;
+    if (items < 4 * sms)
+        for (int64_t parts = 2; parts <= std::min<int64_t>(nch, 16); ++parts)
+            if (10 * cost(parts) < 9 * cost(1) && cost(parts) < cost(best) &&
+                parts * (1 + gated) * sh.n_row * sh.rows <= kMaxSums)
+                best = parts;
+    sh.part_chunks = (int)((nch + best - 1) / best);
+    sh.parts = (int)((nch + sh.part_chunks - 1) / sh.part_chunks);
+}
+
 // The operands of a product of n_row rows shared by n_group groups.  Tiles of
 // 192 operand rows where the groups fill them (a weight slice is decoded once
 // per tile), of 128 where they do not; both let tensor memory hold two items'
 // sums, so that an epilogue runs beside the next item's products.
-ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row)
+ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row, bool gated)
 {
     ChunkShape sh;
     sh.fmt = fmt;
@@ -331,10 +359,13 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     const int64_t T = sh.tile_tokens(), GT = sh.gran_tokens();
     sh.cap_tiles = std::min<int64_t>(n_row, n_row / T + n_group);
     sh.cap_gran = n_row / GT + n_group;
+    choose_parts(sh, gated);
     size_t at = sizeof(ChunkPlan);
     sh.at_tiles = at, at = up256(at + (size_t)sh.cap_tiles * sizeof(ChunkTile));
     sh.at_inv = at, at = up256(at + (size_t)sh.cap_gran * GT * sizeof(float));
     sh.at_img = at, at = up256(at + (size_t)sh.cap_gran * sh.nst * kGranBytes);
+    sh.at_sums = at;
+    if (sh.parts > 1) at = up256(at + (size_t)sh.parts * (1 + gated) * n_row * rows * sizeof(float));
     sh.bytes = at;
     return sh;
 }
@@ -345,7 +376,7 @@ rf_status check_sizes(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t
     if (!fmt_has_chunks(fmt) || !dtype_ok(dtype)) return RF_ERR_UNSUPPORTED_FMT;
     if (n_group < 1 || rows < 0 || n_row < 0 || in_dim <= 0 || in_dim % block_elems_of(fmt) != 0) return RF_ERR_INVALID_ARG;
     if (in_dim > (1 << 20) || rows > 0x7fffffffLL || n_group > 65536 || n_row > kMaxPieces) return RF_ERR_TOO_LARGE;
-    const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row);
+    const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, false);
     if (sh.cap_gran > kMaxPieces || sh.cap_tiles * ((rows + 63) / 64) > kMaxPieces) return RF_ERR_TOO_LARGE;
     return RF_OK;
 }
@@ -444,8 +475,8 @@ MoeLayout moe_layout(int fmt, int n_expert, int top_k, int64_t n_ff, int64_t n_e
 {
     MoeLayout m;
     const int64_t n_row = n_tok * top_k;
-    m.up = chunk_shape(fmt, dtype, n_expert, n_ff, n_embd, n_row);
-    m.down = chunk_shape(fmt, dtype, n_expert, n_embd, n_ff, n_row);
+    m.up = chunk_shape(fmt, dtype, n_expert, n_ff, n_embd, n_row, true);
+    m.down = chunk_shape(fmt, dtype, n_expert, n_embd, n_ff, n_row, false);
     m.ldd = n_embd;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -495,7 +526,8 @@ extern "C" {
 size_t rf_gemm_grouped_workspace_bytes(int fmt, int n_group, int64_t rows, int64_t in_dim, int dtype, int64_t n_row)
 {
     if (check_sizes(fmt, dtype, n_group, rows, in_dim, n_row) != RF_OK || rows == 0 || n_row == 0) return 0;
-    return chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row).bytes;
+    return std::max(chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, false).bytes,
+                    chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, true).bytes);
 }
 
 size_t rf_gemm_fused_workspace_bytes(int fmt, int64_t rows, int64_t in_dim, int dtype, int64_t n_tok)
@@ -519,7 +551,7 @@ rf_status rf_gemm_fused(int fmt, const void *W, const void *up, int64_t row_star
         !aligned(e.bias, 4) || !aligned(e.up_bias, 4))
         return RF_ERR_MISALIGNED;
     if (rows == 0 || n_tok == 0) return RF_OK;
-    const ChunkShape sh = chunk_shape(fmt, dtype, 1, rows, in_dim, n_tok);
+    const ChunkShape sh = chunk_shape(fmt, dtype, 1, rows, in_dim, n_tok, up != nullptr);
     if ((st = check_workspace(workspace, workspace_bytes, sh.bytes)) != RF_OK) return st;
     const Source x = {dtype, X, ldx, n_tok, nullptr, nullptr, 1};
     return run_product(sh, x, W, up, row_start, rows, row_end, e, dtype, Y, ldy, workspace, static_cast<cudaStream_t>(stream));
@@ -542,7 +574,7 @@ rf_status rf_gemm_grouped(int fmt, const void *W, const void *up, int n_group, i
         !aligned(e.bias, 4) || !aligned(e.up_bias, 4) || !aligned(offsets, 4) || !aligned(order, 4))
         return RF_ERR_MISALIGNED;
     if (rows == 0 || n_row == 0) return RF_OK;
-    const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row);
+    const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, up != nullptr);
     if ((st = check_workspace(workspace, workspace_bytes, sh.bytes)) != RF_OK) return st;
     const Source x = {dtype, X, ldx, n_x, offsets, order, per};
     return run_product(sh, x, W, up, 0, rows, (int64_t)n_group * rows, e, dtype, Y, ldy, workspace,

@@ -17,6 +17,10 @@ struct ChunkPlan {
     int32_t pad[62];
 };
 
+// Raw chunk of each format: weights and bytes of a row that are copied at once.
+__host__ __device__ constexpr int chunk_bytes(int fmt) { return fmt == RF_Q4_0 || fmt == RF_Q4_K ? 144 : 272; }
+__host__ __device__ constexpr int chunk_weights(int fmt) { return fmt == RF_MXFP4 ? 512 : 256; }
+
 constexpr int kSliceK = 64;                  // inputs per operand slice: two 32-weight blocks
 constexpr int kGranRows = 16;                // operand rows per granule (the step of the MMA's N)
 constexpr int kGranBytes = kGranRows * kSliceK * 2;   // ... and its bytes per slice
@@ -29,7 +33,8 @@ struct ChunkShape {
     int64_t n_row, n_group, rows, in_dim;
     int nst;                                 // slices
     int64_t cap_tiles, cap_gran;             // token tiles and granules at most
-    size_t at_tiles, at_inv, at_img, bytes;  // workspace: plan, tiles, 1 / row scale, images
+    int parts, part_chunks;                  // parts of a row's raw chunks, and chunks per part
+    size_t at_tiles, at_inv, at_img, at_sums, bytes;   // workspace: plan, tiles, 1 / row scale, images, parts' sums
     int tile_tokens() const { return nt / xt; }
     int gran_tokens() const { return kGranRows / xt; }
 };

@@ -63,20 +63,14 @@ constexpr int kItems = 4;            // items drawn ahead
 constexpr int kInFlight = 16;        // stages of activations in flight at most
 constexpr int kRaws = 8;             // raw chunks in flight at most
 
-// Raw chunk: BPC blocks (of BE weights, BS bytes) of each row.
-template <int FMT> struct Raw;
-template <> struct Raw<RF_Q4_0> { static constexpr int BS = 18, BE = 32, BPC = 8; };
-template <> struct Raw<RF_Q8_0> { static constexpr int BS = 34, BE = 32, BPC = 8; };
-template <> struct Raw<RF_MXFP4> { static constexpr int BS = 17, BE = 32, BPC = 16; };
-template <> struct Raw<RF_Q4_K> { static constexpr int BS = 144, BE = 256, BPC = 1; };
+__host__ __device__ constexpr int block_size(int fmt) { return fmt == RF_Q4_0 ? 18 : (fmt == RF_Q8_0 ? 34 : (fmt == RF_MXFP4 ? 17 : 144)); }
 
 // Box bytes: the chunk's, with what rounding its first byte down takes, as an
 // odd number of 16-byte units (see Block::load); with 16 matrix rows to a
 // super-row an even one, which keeps the boxes 128 bytes aligned.
 __host__ __device__ constexpr int box_bytes(int fmt, int P)
 {
-    const int cb = fmt == RF_Q4_0 || fmt == RF_Q4_K ? 144 : 272;
-    const int n = fmt == RF_Q4_K ? cb : cb + (P > 1 ? 16 : 0);
+    const int n = chunk_bytes(fmt) + (fmt != RF_Q4_K && P > 1 ? 16 : 0);
     return P < 16 && n / 16 % 2 == 0 ? n + 16 : n;
 }
 
@@ -86,8 +80,8 @@ __host__ __device__ constexpr int box_bytes(int fmt, int P)
 // chain of wait, issue and commit is paid half as often.
 template <int FMT, int NT, int XT, int WT>
 struct Cfg {
-    static constexpr int CB = Raw<FMT>::BPC * Raw<FMT>::BS;            // chunk bytes per row
-    static constexpr int QPC = Raw<FMT>::BPC * Raw<FMT>::BE / kSliceK; // slices per chunk
+    static constexpr int CB = chunk_bytes(FMT);                        // chunk bytes per row
+    static constexpr int QPC = chunk_weights(FMT) / kSliceK;           // slices per chunk
     static constexpr int BW = box_bytes(FMT, 8);                       // box bytes at most
     static constexpr int T = NT / XT;                                  // tokens
     static constexpr int KS = NT == 128 && WT == 1 ? 2 : 1;
@@ -131,7 +125,7 @@ struct Cfg {
 };
 
 struct Item {
-    int32_t group, row0, cnt, gran, rt, stop, pad[2];
+    int32_t group, row0, cnt, gran, rt, stop, part, pad;
 };
 
 struct Params {
@@ -154,6 +148,8 @@ struct Params {
     const void *residual;
     int64_t ldr, ldy;
     void *Y;
+    float *sums;              // with several parts: [part][projection][row of the call][rows]
+    int32_t parts, part_chunks, n_row;
     int32_t withhold;         // test hook: CTA 0 never copies this slice's activations
     long long limit_cycles;   // of a wait
 };
@@ -441,6 +437,15 @@ __device__ __forceinline__ void finish(const Params &p, float (&z)[16], const fl
             if (in && u < n) y[u * p.ldy] = O::put(z[u] + add[u]);
     }
 }
+// The same for a part of the row's inputs: the sums alone.
+__device__ __forceinline__ void keep(const Params &p, const float (&z)[16], const float (&inv)[16], int part, int64_t r0, int n,
+                                     int col, bool in, int half)
+{
+    float *y = p.sums + ((int64_t)(part * (1 + p.gated) + (p.gated ? half : 0)) * p.n_row + r0) * p.rows + col;
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+        if (in && u < n) y[(int64_t)u * p.rows] = z[u] * inv[u];
+}
 __device__ __forceinline__ void finish_typed(const Params &p, float (&z)[16], const float (&inv)[16], float bias, int64_t r0,
                                              int n, int col, bool in, int half)
 {
@@ -580,6 +585,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
         w.group = __shfl_sync(0xffffffffu, src[0], 0), w.row0 = __shfl_sync(0xffffffffu, src[1], 0);
         w.cnt = __shfl_sync(0xffffffffu, src[2], 0), w.gran = __shfl_sync(0xffffffffu, src[3], 0);
         w.rt = __shfl_sync(0xffffffffu, src[4], 0), w.stop = __shfl_sync(0xffffffffu, src[5], 0);
+        w.part = __shfl_sync(0xffffffffu, src[6], 0);
         __syncwarp();
         if (lane == 0) bar_arrive(bar(C::IEMPTY + slot));
         return w.stop == 0;
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RROLES));
     if (warp == 3) {
         if (lane == 0) {
-            const int total = p.plan->n_tiles * p.nrt;   // at most 2^30
+            const int total = p.plan->n_tiles * p.nrt * p.parts;   // at most 2^30
             for (uint32_t it = 0;; ++it) {
                 const int slot = it % kItems;
                 if (!wait(bar(C::IEMPTY + slot), ((it / kItems) & 1) ^ 1)) break;
@@ -598,9 +604,11 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 const int index = atomicAdd(&p.plan->next, 1);
                 w.stop = index >= total;
                 if (!w.stop) {
-                    const ChunkTile t = p.tiles[index / p.nrt];
+                    const int at = index / p.parts;
+                    const ChunkTile t = p.tiles[at / p.nrt];
                     w.group = t.group, w.row0 = t.row0, w.cnt = t.cnt, w.gran = t.gran;
-                    w.rt = index % p.nrt;
+                    w.rt = at % p.nrt;
+                    w.part = index % p.parts;
                 }
                 const bool end = w.stop != 0;
                 bar_arrive(bar(C::IFULL + slot));
@@ -622,7 +630,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                                   (p.gated ? (int64_t)w.rt * 64 : (int64_t)w.rt * 128 + 64 * half);
             const int y = (int)((first - j + p.P - 1) >> p.logP);   // first super-row with position j in the tile
             bool ok = true;
-            for (int c = 0; c < p.nch; ++c) {
+            for (int c = w.part * p.part_chunks, end = min(p.nch, c + p.part_chunks); c < end; ++c) {
                 if (!(ok = waits(bar(C::REMPTY + r), ph))) break;
                 if (lane == 0) {
                     if (p.copies) bar_expect(bar(C::RFULL + r), (uint32_t)(kM * p.bw));
@@ -652,16 +660,17 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 const int slot = it % kItems;
                 if (!wait(bar(C::IFULL + slot), (it / kItems) & 1)) break;
                 const int grans = (items[slot].cnt + GT - 1) / GT, gran = items[slot].gran, end = items[slot].stop;
+                const int from = items[slot].part * p.part_chunks * QPC, nsl = min(p.nst - from, p.part_chunks * QPC);
                 bar_arrive(bar(C::IEMPTY + slot));
                 if (end) break;
                 const uint32_t slice = (uint32_t)grans * kGranBytes;
-                const uint8_t *src = p.img + (int64_t)gran * p.nst * kGranBytes;
-                for (int b = 0; b < p.nst; b += KS, ++n) {
+                const uint8_t *src = p.img + (int64_t)gran * p.nst * kGranBytes + (int64_t)from * slice;
+                for (int b = 0; b < nsl; b += KS, ++n) {
                     if (!(ok = wait(bar(C::BDONE + ib), ph))) break;
                     if (blockIdx.x == 0 && n == (uint32_t)p.withhold) {
                         skipped = n;
                     } else {
-                        const int slices = KS > 1 && b + 1 < p.nst ? KS : 1;
+                        const int slices = KS > 1 && b + 1 < nsl ? KS : 1;
                         bar_expect(bar(C::BFULL + ib), slices * slice);
                         for (int i = 0; i < slices; ++i)
                             copy_bulk(ring + (ib * KS + i) * p.slot, src + i * slice, slice, bar(C::BFULL + ib));
@@ -693,10 +702,11 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 const int slot = it % kItems;
                 if (!wait(bar(C::IFULL + slot), (it / kItems) & 1)) break;
                 const int grans = (items[slot].cnt + GT - 1) / GT, end = items[slot].stop;
+                const int nsl = min(p.nst - items[slot].part * p.part_chunks * QPC, p.part_chunks * QPC);
                 bar_arrive(bar(C::IEMPTY + slot));
                 if (end) break;
                 const uint32_t id = WT == 2 && XT == 2 ? idesc_n((grans + 1) / 2 * 16) : idesc_n(kGranRows * grans);
-                for (int b = 0; b < p.nst;) {
+                for (int b = 0; b < nsl;) {
                     const bool fresh = b % C::FLUSH == 0;
                     const uint32_t acc = tmem + (seg % NBUF) * C::ACC;
                     if (fresh) {
@@ -705,7 +715,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     if (!ready && !(ok = wait(bar(C::BFULL + ib), pb) && wait(bar(C::FULL + sa), pa))) break;
                     const uint32_t a_done = bar(C::ADONE + sa), b_done = bar(C::BDONE + ib);
                     const uint32_t a0 = tmem + C::ACOL + sa * C::ASTAGE, at = (ib * KS * p.slot) >> 4;
-                    const bool two = KS > 1 && b + 1 < p.nst;
+                    const bool two = KS > 1 && b + 1 < nsl;
                     // The next stage's barriers are read (about 130 cycles
                     // each) beside this one's products.
                     if (++sa == S) sa = 0, pa ^= 1u;
@@ -735,7 +745,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     bar_commit(b_done);
                     ready = b_next && f_next;
                     b += KS;
-                    if (b >= p.nst || b % C::FLUSH == 0) {
+                    if (b >= nsl || b % C::FLUSH == 0) {
                         bar_commit(bar(C::ACCF + seg % NBUF));
                         ++seg;
                     }
@@ -771,7 +781,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
             const uint32_t at = (uint32_t)((half << p.logP) + j) * (uint32_t)((64 >> p.logP) * p.bw) + (uint32_t)(s * p.bw) +
                                 ((uint32_t)(j * p.rb) & 15u);
             const bool tail = row >= copied && row < p.total_rows;
-            for (int c = 0; ok && c < p.nch; ++c) {
+            for (int c = w.part * p.part_chunks, end = min(p.nch, c + p.part_chunks); ok && c < end; ++c) {
                 const int nq = min(QPC, p.nst - c * QPC), ns = (nq + KS - 1) / KS;   // its slices and stages
                 if (!(ok = waits(bar(C::RFULL + r), ph))) break;
                 uint8_t *src = raw + r * C::RAW + at;
@@ -806,7 +816,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                             q4k_block<C::LOW>(src, sl, 1, hi, lo);
                             store(C::ASLICE * e + 16);
                         } else {
-                            constexpr int BS = Raw<FMT>::BS;
+                            constexpr int BS = block_size(FMT);
                             Block<FMT> blk[2];
 #pragma unroll
                             for (int t = 0; t < 2; ++t) blk[t].load(src, (2 * sl + t) * BS);
@@ -871,16 +881,18 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
 #pragma unroll
                     for (int u = 0; u < 16; ++u) z[u] = __uint_as_float(v[u]);
                     if (t0 + 16 >= w.cnt) release();
-                    finish_typed(p, z, f, b, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
+                    if (p.parts > 1) keep(p, z, f, w.part, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
+                    else finish_typed(p, z, f, b, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
                 }
             } else {
+                const int nsl = min(p.nst - w.part * p.part_chunks * QPC, p.part_chunks * QPC);
                 // 64 tokens' sums in registers, over the item's flushes.
                 float sum[C::T];
                 bool ok = true;
 #pragma unroll
                 for (int u = 0; u < C::T; ++u) sum[u] = 0.f;
 #pragma unroll 1
-                for (int b0 = 0; b0 < p.nst; b0 += C::FLUSH) {
+                for (int b0 = 0; b0 < nsl; b0 += C::FLUSH) {
                     if (!(ok = waits(bar(C::ACCF + seg % NBUF), (seg / NBUF) & 1))) break;
                     tc_fence_after();
                     const uint32_t acc = tmem + lanes + (seg % NBUF) * C::ACC;
@@ -907,7 +919,8 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                         load_inv(inv + t0, f);
 #pragma unroll
                         for (int u = 0; u < 16; ++u) z[u] = sum[t0 + u];
-                        finish<RF_F32>(p, z, f, b, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
+                        if (p.parts > 1) keep(p, z, f, w.part, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
+                        else finish<RF_F32>(p, z, f, b, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
                     }
                 }
             }
@@ -918,6 +931,54 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
     if (warp == 3) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// The parts' sums of each row, added in order of the parts, and what follows
+// the product.  blockIdx.y: kJoinRows rows of a token tile.
+constexpr int kJoinRows = 4;
+__global__ void __launch_bounds__(128) join_parts_kernel(const __grid_constant__ Params p, int pieces)
+{
+    const int at = (int)blockIdx.y / pieces, t0 = (int)blockIdx.y % pieces * kJoinRows;
+    if (at >= p.plan->n_tiles) return;
+    const ChunkTile w = p.tiles[at];
+    const int col = (int)blockIdx.x * 128 + (int)threadIdx.x, n = min(w.cnt - t0, kJoinRows);
+    if (col >= p.rows || n <= 0) return;
+    const int64_t step = (int64_t)p.n_row * p.rows;   // from one projection to the next
+    const float b0 = p.bias[0] ? p.bias[0][(int64_t)w.group * p.rows + col] : 0.f;
+    const float b1 = p.bias[1] ? p.bias[1][(int64_t)w.group * p.rows + col] : 0.f;
+    const float *s = p.sums + (int64_t)(w.row0 + t0) * p.rows + col;
+    float z[kJoinRows], u[kJoinRows];
+#pragma unroll
+    for (int t = 0; t < kJoinRows; ++t) z[t] = u[t] = 0.f;
+    for (int i = 0; i < p.parts; ++i) {
+#pragma unroll
+        for (int t = 0; t < kJoinRows; ++t)
+            if (t < n) {
+                z[t] += s[(int64_t)t * p.rows];
+                if (p.gated) u[t] += s[step + (int64_t)t * p.rows];
+            }
+        s += (1 + p.gated) * step;
+    }
+#pragma unroll
+    for (int t = 0; t < kJoinRows; ++t) {
+        if (t >= n) break;
+        float y = z[t] + b0;
+        if (p.act == RF_ACT_SILU) y = sigmoid_times(y, y);
+        else if (p.act == RF_ACT_GELU) y = 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
+        else if (p.act == RF_ACT_SWIGLU) y = sigmoid_times(y, y) * (u[t] + b1);
+        else if (p.act == RF_ACT_SWIGLU_CLAMPED) y = clamped_of(y, u[t] + b1, p.alpha, p.limit);
+        const int64_t row = w.row0 + t0 + t, from = row * p.ldr + col, to = row * p.ldy + col;
+        if (p.dtype == RF_F32) {
+            if (p.residual) y += static_cast<const float *>(p.residual)[from];
+            static_cast<float *>(p.Y)[to] = y;
+        } else if (p.dtype == RF_F16) {
+            if (p.residual) y += Out<RF_F16>::get(static_cast<const __half *>(p.residual)[from]);
+            static_cast<__half *>(p.Y)[to] = Out<RF_F16>::put(y);
+        } else {
+            if (p.residual) y += Out<RF_BF16>::get(static_cast<const __nv_bfloat16 *>(p.residual)[from]);
+            static_cast<__nv_bfloat16 *>(p.Y)[to] = Out<RF_BF16>::put(y);
+        }
     }
 }
 
@@ -981,7 +1042,7 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
     while (P > 1 && p.rb * (P / 2) % 16 == 0) P /= 2;
     p.P = P;
     while ((1 << p.logP) < P) ++p.logP;
-    const int cb = sh.fmt == RF_Q4_0 || sh.fmt == RF_Q4_K ? 144 : 272;
+    const int cb = chunk_bytes(sh.fmt);
     p.bw = box_bytes(sh.fmt, P);
     p.gated = g.up != nullptr;
     p.W[0] = g.W;
@@ -1021,13 +1082,22 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
         p.withhold = sh.nst > 1 ? 1 : 0;
     }
     p.slot = (uint32_t)sh.nt * kSliceK * 2;
-    const int grid = (int)std::min<int64_t>(num_sms(), sh.cap_tiles * p.nrt);
+    p.parts = sh.parts;
+    p.part_chunks = sh.part_chunks;
+    p.n_row = (int32_t)sh.n_row;
+    p.sums = reinterpret_cast<float *>(g.ws + sh.at_sums);
+    const int grid = (int)std::min<int64_t>(num_sms(), sh.cap_tiles * p.nrt * p.parts);
+    rf_status st;
     switch (sh.fmt) {
-    case RF_Q4_0: return launch_fmt<RF_Q4_0>(sh, p, grid, s);
-    case RF_Q8_0: return launch_fmt<RF_Q8_0>(sh, p, grid, s);
-    case RF_Q4_K: return launch_fmt<RF_Q4_K>(sh, p, grid, s);
-    default: return launch_fmt<RF_MXFP4>(sh, p, grid, s);
+    case RF_Q4_0: st = launch_fmt<RF_Q4_0>(sh, p, grid, s); break;
+    case RF_Q8_0: st = launch_fmt<RF_Q8_0>(sh, p, grid, s); break;
+    case RF_Q4_K: st = launch_fmt<RF_Q4_K>(sh, p, grid, s); break;
+    default: st = launch_fmt<RF_MXFP4>(sh, p, grid, s); break;
     }
+    if (st != RF_OK || p.parts == 1) return st;
+    const int pieces = (sh.tile_tokens() + kJoinRows - 1) / kJoinRows;
+    join_parts_kernel<<<dim3((unsigned)((p.rows + 127) / 128), (unsigned)(sh.cap_tiles * pieces)), 128, 0, s>>>(p, pieces);
+    return last_cuda_error();
 }
 
 }  // namespace rf

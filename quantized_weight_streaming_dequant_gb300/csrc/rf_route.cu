@@ -24,8 +24,9 @@
 namespace rf {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBlocks = 128;       // runs of tokens at most
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBlocks = 128;       // runs of tokens, unless they would be longer than kMaxRun
+constexpr int kMaxRun = 65535;     // (a run's counts are 16 bits)
 constexpr int kRunTokens = 32;     // tokens per run at least
 constexpr int kOneTokens = 64;     // up to here one block does both steps
 constexpr int kMaxExperts = 1024;
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const __grid_constant__ 
 __device__ __forceinline__ void place_run(const RouteParams &p, int b, bool own)
 {
     __shared__ int s_base[kMaxExperts];              // rows before this run's, by expert
-    __shared__ int s_warp[kWarps][kMaxExperts];      // ... and before this warp's, within the run
+    __shared__ uint16_t s_warp[kWarps][kMaxExperts]; // ... and before this warp's, within the run
+    __shared__ int s_all[kMaxExperts], s_earlier[kMaxExperts];   // rows of all runs, and of earlier ones, by expert
     __shared__ int s_part[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t f0 = (int64_t)b * p.run * p.top_k, f1 = min(p.n_tok, (int64_t)(b + 1) * p.run) * p.top_k;
@@ -122,14 +124,30 @@ __device__ __forceinline__ void place_run(const RouteParams &p, int b, bool own)
     for (int e = tid; e < p.n_expert; e += kThreads) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s_warp[w][e] = 0;   // (each warp's own counts)
+        s_all[e] = s_earlier[e] = 0;
     }
     __syncthreads();
+    if (!own) {
+        // The runs' counts, by expert and share of the runs.
+        const int width = (p.n_expert + 31) / 32 * 32, shares = max(1, kThreads / width);
+        for (int e = tid % width + (tid / width >= shares ? p.n_expert : 0); e < p.n_expert; e += kThreads) {
+            int all = 0, earlier = 0;
+#pragma unroll 8
+            for (int r = shares > 1 ? tid / width : 0; r < p.runs; r += shares) {
+                const int c = p.counts[(int64_t)r * p.n_expert + e];
+                all += c;
+                if (r < b) earlier += c;
+            }
+            atomicAdd(&s_all[e], all);
+            atomicAdd(&s_earlier[e], earlier);
+        }
+    }
     // Counts by warp.
     const int from = warp * each, to = min(n, from + each);
     for (int i0 = from; i0 < to; i0 += 32) {
         const int e = i0 + lane < to ? p.idx[f0 + i0 + lane] : -1;
         const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) s_warp[warp][e] += __popc(same);
+        if (e >= 0 && lane == __ffs(same) - 1) s_warp[warp][e] += (uint16_t)__popc(same);
         __syncwarp();
     }
     __syncthreads();
@@ -144,18 +162,11 @@ __device__ __forceinline__ void place_run(const RouteParams &p, int b, bool own)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const int c = s_warp[w][e];
-                s_warp[w][e] = run;
+                s_warp[w][e] = (uint16_t)run;
                 run += c;
             }
-            if (own) all = run;
-            else {
-#pragma unroll 8
-                for (int r = 0; r < p.runs; ++r) {
-                    const int c = p.counts[(int64_t)r * p.n_expert + e];
-                    all += c;
-                    if (r < b) earlier += c;
-                }
-            }
+            all = own ? run : s_all[e];
+            earlier = s_earlier[e];
         }
         int x = all;
 #pragma unroll
@@ -189,7 +200,7 @@ __device__ __forceinline__ void place_run(const RouteParams &p, int b, bool own)
         const unsigned same = __match_any_sync(0xffffffffu, e);
         const int at = e < 0 ? 0 : s_base[e] + s_warp[warp][e] + __popc(same & ((1u << lane) - 1u));
         __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1) s_warp[warp][e] += __popc(same);
+        if (e >= 0 && lane == __ffs(same) - 1) s_warp[warp][e] += (uint16_t)__popc(same);
         __syncwarp();
         if (e >= 0) {
             p.order[at] = (int32_t)(f0 + i);
@@ -219,7 +230,7 @@ __global__ void zero_kernel(int32_t *offsets, int n)
 
 int run_tokens(int64_t n_tok)
 {
-    return (int)std::max<int64_t>(kRunTokens, (n_tok + kBlocks - 1) / kBlocks);
+    return (int)std::min<int64_t>(kMaxRun, std::max<int64_t>(kRunTokens, (n_tok + kBlocks - 1) / kBlocks));
 }
 
 template <class T, int EPL>
@@ -229,9 +240,9 @@ rf_status launch_one(const RouteParams &p, cudaStream_t s)
         route_kernel<T, EPL><<<1, kThreads, 0, s>>>(p);
         return last_cuda_error();
     }
-    pick_kernel<T, EPL><<<p.runs, kThreads, 0, s>>>(p);
+    pick_kernel<T, EPL><<<(unsigned)p.runs, kThreads, 0, s>>>(p);
     if (last_cuda_error() != RF_OK) return RF_ERR_CUDA;
-    place_kernel<<<p.runs, kThreads, 0, s>>>(p);
+    place_kernel<<<(unsigned)p.runs, kThreads, 0, s>>>(p);
     return last_cuda_error();
 }
 template <class T>
