@@ -544,7 +544,7 @@ rf_status rf_gemm_fused(int fmt, const void *W, const void *up, int64_t row_star
     if (row_start < 0 || row_end < row_start) return RF_ERR_INVALID_ARG;
     rf_status st = check_sizes(fmt, dtype, 1, rows, in_dim, n_tok);
     if (st != RF_OK) return st;
-    if (!W || (n_tok > 0 && (!X || !Y)) || ldx < in_dim || ldy < rows) return RF_ERR_INVALID_ARG;
+    if (!W || (n_tok > 0 && rows > 0 && (!X || !Y)) || ldx < in_dim || ldy < rows) return RF_ERR_INVALID_ARG;
     if ((st = check_epilogue(e, up, dtype, rows)) != RF_OK) return st;
     const int size = dtype_size(dtype);
     if (!aligned(W, 16) || !aligned(up, 16) || !aligned(X, size) || !aligned(Y, size) || !aligned(e.residual, size) ||
@@ -565,7 +565,7 @@ rf_status rf_gemm_grouped(int fmt, const void *W, const void *up, int n_group, i
     const rf_epilogue e = epi ? *epi : kNoEpilogue;
     rf_status st = check_sizes(fmt, dtype, n_group, rows, in_dim, n_row);
     if (st != RF_OK) return st;
-    if (!W || !offsets || (n_row > 0 && !Y) || (n_x > 0 && !X) || n_x < 0 || ldx < in_dim || ldy < rows || per < 1 ||
+    if (!W || !offsets || (n_row > 0 && rows > 0 && !Y) || (n_x > 0 && !X) || n_x < 0 || ldx < in_dim || ldy < rows || per < 1 ||
         (!order && n_x < n_row))
         return RF_ERR_INVALID_ARG;
     if ((st = check_epilogue(e, up, dtype, rows)) != RF_OK) return st;

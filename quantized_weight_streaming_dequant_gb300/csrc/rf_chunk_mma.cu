@@ -104,8 +104,10 @@ struct Cfg {
     static constexpr int NBUF = 2 * ACC <= ACOL ? 2 : 1;
     // Sums of fp32 calls leave tensor memory every FLUSH slices: the tensor
     // cores truncate each addition (about 1e-8 of the sum, always towards
-    // zero), rounded additions in registers do not drift.
-    static constexpr int FLUSH = XT == 2 ? 4 : 1 << 30;                // slices
+    // zero), rounded additions in registers do not drift.  Q4_K's weights have
+    // a mean, so that its sums grow over a row: sooner (1.3e-6 against 0.7e-6
+    // from 64 bits in a routed FFN).
+    static constexpr int FLUSH = XT == 1 ? 1 << 30 : (FMT == RF_Q4_K ? 2 : 4);
     // Shared memory: stages of activations, raw chunks, and 16 bytes that a
     // last load may touch.  Activations come from L2 in about as long as eight
     // slices take; the weights come from memory and get the rest.

@@ -10,6 +10,9 @@ DenseLayer -- one dense decode layer held resident in HBM: the Q, K and V
 DecoderLayer -- the whole decoder layer over a paged KV cache, from residual
   stream to residual stream, for single tokens and chunks of a prompt: norm,
   Q/K/V, rotation and append, attention, O, norm, SwiGLU FFN.
+RoutedFFN -- the FFN of a layer of experts over a chunk of tokens, from
+  residual stream to residual stream: norm, router, routed FFN with the
+  residual sum.
 StreamedFFN -- a dense FFN whose weights stay in page-locked host memory: up
   (host-streamed), GELU, down (host-streamed), all through one arena; or the
   same FFN read in place over the host link (zero copy).
@@ -147,6 +150,46 @@ class DecoderLayer:
         `weight`): (residual, normed)."""
         return rf.norm_residual(residual, delta, post_weight=self.post_ffn, scale=self.residual_scale,
                                 weight=weight, eps=self.eps, stream=stream)
+
+
+@dataclass
+class RoutedFFN:
+    """The FFN half of a layer of experts.  gate and up (n_expert, d_ff,
+    d_model) and down (n_expert, d_model, d_ff) are stacked quantized tensors;
+    router is a quantized (n_expert, d_model) matrix of its own format; norm
+    weights and biases are float32; with alpha and limit the SwiGLU is clamped."""
+    fmt: int
+    n_expert: int
+    top_k: int
+    d_model: int
+    d_ff: int
+    gate: object
+    up: object
+    down: object
+    router_fmt: int
+    router: object
+    norm: object
+    router_bias: object = None
+    gate_bias: object = None
+    up_bias: object = None
+    down_bias: object = None
+    alpha: float | None = None
+    limit: float | None = None
+    eps: float = 1e-5
+
+    def step(self, residual, workspace=None, stream=None):
+        """residual (n_tok, d_model), float32, float16 or bfloat16, through the
+        FFN.  Returns a dict: the normed input "x", the router's "logits" and
+        the new residual stream "y"."""
+        o = {}
+        _, o["x"] = rf.norm_residual(residual, weight=self.norm, eps=self.eps, stream=stream)
+        o["logits"] = rf.gemm_fused(self.router_fmt, self.router, 0, self.n_expert, self.d_model, o["x"],
+                                    bias=self.router_bias, stream=stream)
+        o["y"] = rf.moe_ffn_tokens(self.fmt, o["logits"], self.top_k, self.gate, self.up, self.down, self.d_ff,
+                                   self.d_model, o["x"], gate_bias=self.gate_bias, up_bias=self.up_bias,
+                                   down_bias=self.down_bias, alpha=self.alpha, limit=self.limit, residual=residual,
+                                   workspace=workspace, stream=stream)
+        return o
 
 
 @dataclass
