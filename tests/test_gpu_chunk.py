@@ -34,7 +34,7 @@ def f32(rng, *shape):
 
 def inputs(fmt, n):
     """n 32-weight blocks, as the format takes them."""
-    return -(-n // 8) * 256 if fmt == rf.Q4_K else 32 * n
+    return max(1, n // 8) * 256 if fmt == rf.Q4_K else 32 * n
 
 
 # ------------------------------------------------------------------ routing
