@@ -451,7 +451,8 @@ rf_status rf_device_status(void)
     rf_status first = a;
     for (rf_status (*word)() : {read_and_clear_gemm_status, read_and_clear_kv_status, read_and_clear_attn_status,
                                 read_and_clear_attn_tile_status,
-                                read_and_clear_chunk_status, read_and_clear_chunk_invalid}) {
+                                read_and_clear_chunk_status, read_and_clear_few_status,
+                                read_and_clear_chunk_invalid}) {
         const rf_status b = word();
         if (first == RF_OK) first = b;
     }

@@ -72,7 +72,7 @@ struct PrepParams {
     const int32_t *order;
     int32_t per, n_row, n_group;
     int32_t in_dim, nst, order8;   // order8: which inputs a 16-byte unit holds
-    int32_t tile_tokens, cap_tiles, cap_gran, parts, vec;
+    int32_t tile_tokens, cap_tiles, cap_gran, parts, vec, few, spread;
     ChunkPlan *plan;
     ChunkTile *tiles;
     float *inv;               // by place in the granules
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
     const int first = c >> 2, u = c & 3;
     const int ka = 32 * first + (p.order8 == kOrderPlain ? 8 * u : 4 * u);
     const int kb = ka + (p.order8 == kOrderPlain ? 4 : 16);
-    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * kGranBytes + sub * 1024 + c * 128 + r * 16;
+    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * kGranBytes + sub * 1024 + c * 128;
     const int64_t step = (int64_t)s_n * kGranBytes;
 #pragma unroll 4
     for (int s = part * kStep + (tid >> 6); s < p.nst; s += p.parts * kStep) {
@@ -257,8 +257,13 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
                                                  fabsf(w.y) < INFINITY ? (f1 - w.y) * 2048.f : 0.f));
             }
         }
-        *reinterpret_cast<uint4 *>(out + s * step) = make_uint4(h[0], h[1], h[2], h[3]);
-        if constexpr (XT == 2) *reinterpret_cast<uint4 *>(out + s * step + 1024) = make_uint4(l[0], l[1], l[2], l[3]);
+        // Few tokens' kernel reads a row's units of four slices at once (of
+        // MXFP4, every other one of eight): they lie one after the other, each
+        // slice's turned in its 128 bytes, for the banks.
+        const int at = p.spread ? (s & ~7) | (s & 1) << 2 | (s >> 1 & 3) : s;
+        uint8_t *to = out + at * step + (p.few ? (r ^ (2 * (at & 3))) * 16 : r * 16);
+        *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+        if constexpr (XT == 2) *reinterpret_cast<uint4 *>(to + 1024) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
@@ -325,11 +330,12 @@ void choose_parts(ChunkShape &sh, bool gated)
                                           : std::min(sh.cap_tiles, std::max(sh.n_row / sh.tile_tokens(), std::min(sh.n_group, sh.n_row)));
     const int64_t items = tiles * ((sh.rows + (gated ? 63 : 127)) / (gated ? 64 : 128)), sms = num_sms();
     const int64_t per = chunk_weights(sh.fmt) / kSliceK, nch = (sh.nst + per - 1) / per;
-    const int64_t slice = sh.wt == 2 ? (sh.fmt == RF_Q4_K ? 1400 : 1000) : (sh.nt > 128 ? 640 : 420);
+    const int64_t slice = sh.few ? std::max<int64_t>(sh.wt == 2 ? 500 : 375, 128 * (sh.xt + sh.wt - 1) * (sh.tile_tokens() / 8))
+                          : sh.wt == 2 ? (sh.fmt == RF_Q4_K ? 1400 : 1000) : (sh.nt > 128 ? 640 : 420);
     auto cost = [&](int64_t parts) {
         const int64_t slices = std::min<int64_t>((nch + parts - 1) / parts * per, sh.nst);
         const int64_t sums = parts > 1 ? 6000 + parts * (1 + gated) * sh.n_row * sh.rows * 8 / 1500 : 0;
-        return (items * parts + sms - 1) / sms * (slice * slices + 4000) + sums;
+        return (items * parts + sms - 1) / sms * (slice * slices + (sh.few ? 2500 : 4000)) + sums;
     };
     int64_t best = 1;
     if (items < 4 * sms)
@@ -353,9 +359,12 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     sh.wt = dtype != RF_BF16 && fmt != RF_MXFP4 ? 2 : 1;
     sh.n_row = n_row, sh.n_group = n_group, sh.rows = rows, sh.in_dim = in_dim;
     sh.nst = (int)((in_dim + kSliceK - 1) / kSliceK);
-    // Twice the average, so that most groups have one tile.
-    const int64_t each = 2 * sh.xt * ((n_row + n_group - 1) / n_group);   // operand rows
+    // Operand rows of a group: twice the average, so that most groups have one tile.
+    const int64_t each = n_group == 1 ? sh.xt * n_row : 2 * sh.xt * ((n_row + n_group - 1) / n_group);
     sh.nt = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : sh.wt == 1 && sh.xt == 1 && each > 256 ? 192 : 128;
+    sh.few = sh.nt <= 32;
+    const int per = chunk_weights(fmt) / kSliceK;
+    if (sh.few) sh.nst = (sh.nst + per - 1) / per * per;
     const int64_t T = sh.tile_tokens(), GT = sh.gran_tokens();
     sh.cap_tiles = std::min<int64_t>(n_row, n_row / T + n_group);
     sh.cap_gran = n_row / GT + n_group;
@@ -419,6 +428,8 @@ rf_status launch_prep(const ChunkShape &sh, const Source &x, uint8_t *ws, cudaSt
     p.in_dim = (int32_t)sh.in_dim, p.nst = sh.nst;
     p.order8 = sh.fmt == RF_MXFP4 ? kOrderPairs : (sh.fmt == RF_Q4_0 ? kOrderSpread : kOrderPlain);
     p.tile_tokens = sh.tile_tokens();
+    p.few = sh.few;
+    p.spread = sh.few && sh.fmt == RF_MXFP4;
     p.cap_tiles = (int32_t)sh.cap_tiles, p.cap_gran = (int32_t)sh.cap_gran;
     const int size = dtype_size(x.dtype);
     p.vec = aligned(x.X, 4 * size) && (x.ldx * size) % (4 * size) == 0;

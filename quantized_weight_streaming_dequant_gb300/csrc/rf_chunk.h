@@ -1,5 +1,5 @@
 // rf_chunk.h -- host-side interface between the chunk operators' entry points
-// (rf_chunk.cu) and their product kernel (rf_chunk_mma.cu).
+// (rf_chunk.cu) and their product kernels (rf_chunk_mma.cu, rf_chunk_few.cu).
 #pragma once
 
 #include "rf_internal.h"
@@ -30,8 +30,9 @@ constexpr int kGranBytes = kGranRows * kSliceK * 2;   // ... and its bytes per s
 // are two).  wt: fp16 terms per weight.  nt: operand rows per token tile.
 struct ChunkShape {
     int fmt, xt, wt, nt;
+    bool few;                                // for rf_chunk_few.cu's kernel
     int64_t n_row, n_group, rows, in_dim;
-    int nst;                                 // slices
+    int nst;                                 // slices (few: whole chunks, the last ones zeros)
     int64_t cap_tiles, cap_gran;             // token tiles and granules at most
     int parts, part_chunks;                  // parts of a row's raw chunks, and chunks per part
     size_t at_tiles, at_inv, at_img, at_sums, bytes;   // workspace: plan, tiles, 1 / row scale, images, parts' sums

@@ -1,0 +1,466 @@
+// rf_chunk_few.cu -- products of the chunk operators where a group has few
+// tokens: the same items, images and results as rf_chunk_mma.cu's, for token
+// tiles of up to 32 operand rows.
+//
+// There a decoded slice passes through tensor memory, with a barrier before and
+// one behind it, and a tile of few tokens waits for those more than for its
+// products.  Here a warp decodes 16 rows straight into the fragments of
+// mma.sync.m16n8k16 and multiplies them itself: nothing stands between a
+// weight's bytes and its product but registers.  A decoded weight is used for
+// at most 16 tokens, so the tensor cores' rate hardly matters.
+//
+// A CTA (two per SM) draws items of 128 matrix rows (64 of W and 64 of U with a
+// gated activation) of a token tile.  One warp copies raw chunks and the
+// tile's operand slices; each of the other eight takes 8 rows of either half of
+// the tile.  Lane (g, t), of eight by four, owns row g of both halves and
+// slice t of every four: a slice's two blocks are the fragments' columns,
+// in the order in which the decoder has them (the sum over inputs does not
+// care), and the token g of a tile of eight has its inputs in the same order.
+// So gate and up of a neuron end in one thread.
+#include <algorithm>
+#include <mutex>
+
+#include "rf_chunk.cuh"
+
+namespace rf {
+using namespace chunk;
+namespace {
+
+__device__ int g_few_status = 0;   // bounded waits that gave up
+
+constexpr int kWarps = 8;          // that multiply; one more copies
+
+// NG: granules of operand rows per token tile; XT, WT: fp16 terms per
+// activation, weight.
+template <int FMT, int NG, int XT, int WT>
+struct Few {
+    static constexpr int CB = chunk_bytes(FMT), QPC = chunk_weights(FMT) / kSliceK;
+    static constexpr int GT = kGranRows / XT, T = NG * GT, NJ = T / 8;   // tokens, and tiles of eight of them
+    // MXFP4: a four of slices are every other one of a chunk (see Weights).
+    static constexpr bool SPREAD = FMT == RF_MXFP4;
+    static constexpr int N = XT + WT - 1;                                // kinds of products
+    // Q4_K's low terms in fp32 calls are scaled; the others' are exact as they are.
+    static constexpr int LOW = WT == 1 ? kOne : (XT == 2 && FMT == RF_Q4_K ? kScaled : kPlain);
+    // Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.
+    static constexpr int SHARED = 115200;
+    static constexpr int RAW = kM * box_bytes(FMT, 8);
+    static constexpr int QB = NG * 4 * kGranBytes;                       // operand bytes of four slices
+    static constexpr int RS = (SHARED - 2 * QB) / RAW < 4 ? (SHARED - 2 * QB) / RAW : 4;   // raw chunks
+    static constexpr int BS = (SHARED - RS * RAW) / QB < 4 ? (SHARED - RS * RAW) / QB : 4; // fours of slices
+    static constexpr int SMEM = RS * RAW + BS * QB;
+    static constexpr int RFULL = 0, REMPTY = RFULL + RS, BFULL = REMPTY + RS, BEMPTY = BFULL + BS, BARS = BEMPTY + BS;
+    static_assert(RS >= 2 && BS >= 2, "two stages of both");
+    static_assert(QPC == (SPREAD ? 8 : 4), "fours of slices of a chunk");
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A block of 32 weights of a row, decoded four pairs at a time.  4-byte loads
+// from any byte of shared memory: the rows of a warp's eight g are an odd
+// number of 16-byte units apart, the slices of its four t 4 * (1 mod 4) bytes,
+// so that its 32 lanes meet 32 banks.
+template <int FMT, int L>
+struct Weights {
+    static constexpr int NS = FMT == RF_MXFP4 ? 1 : 2, NW = FMT == RF_Q8_0 ? 8 : 4;   // scale bytes, quant words
+    uint32_t q[NW], s1, s2;
+    bool two;     // (MXFP4, the warp's) scales that need a second factor
+    // The block `at` bytes behind byte `mis` of the word at `row`.
+    __device__ __forceinline__ void load(const uint8_t *row, uint32_t mis, int at)
+    {
+        const uint32_t off = mis + (uint32_t)at, sh = 8u * (off & 3u);
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(row + (off & ~3u));
+        uint32_t x[NW + 1];
+#pragma unroll
+        for (int i = 0; i < NW + 1; ++i) x[i] = src[i];
+        s1 = (x[0] >> sh) & (NS == 1 ? 0xFFu : 0xFFFFu);
+#pragma unroll
+        for (int i = 0; i < NW; ++i) q[i] = __funnelshift_rc(x[i], x[i + 1], sh + 8 * NS);
+        if constexpr (FMT != RF_MXFP4) s1 *= 0x00010001u;
+    }
+    // MXFP4: the factor 2^k, k = E - 127 (`normal`: fp16 has it as a normal
+    // number, for the whole warp), in two where fp16 has no such number.
+    static __device__ __forceinline__ bool outside(uint32_t E) { return E - 113u >= 30u; }
+    __device__ __forceinline__ void scale(bool normal)
+    {
+        const uint32_t E = s1;
+        s1 = E * 0x04000400u - 112u * 0x04000400u;
+        two = !normal;
+        if (two) {
+            const int k = (int)E - 127;
+            s2 = 0x3C003C00u;
+            if (E == 255u) s1 = 0x7E007E00u;   // NaN
+            else if (k > 15) s1 = 0x78007800u, s2 = pow2_h(min(k - 15, 15)) * 0x00010001u;
+            else if (k < -24) s1 = 0x0C000C00u, s2 = k + 12 >= -24 ? pow2_h(k + 12) * 0x00010001u : 0u;
+            else s1 = pow2_h(k) * 0x00010001u;
+        }
+    }
+    // A block behind the row's last one.
+    __device__ __forceinline__ void clear()
+    {
+        s1 = s2 = 0u;
+    }
+    __device__ __forceinline__ void pairs(int m, uint32_t (&hi)[4], uint32_t (&lo)[4]) const
+    {
+        if constexpr (FMT == RF_MXFP4) {
+            e2m1x8(q[m], hi);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) hi[k] = hmul2(hi[k], s1);
+            if (two) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) hi[k] = hmul2(hi[k], s2);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (FMT == RF_Q4_0) product<L>(q4_0_pair(q[m], k), s1, hi[k], lo[k]);
+                else product<L>(q8_0_pair(q[2 * m + (k >> 1)], k & 1), s1, hi[k], lo[k]);
+            }
+        }
+    }
+};
+template <int L>
+struct Weights<RF_Q4_K, L> {
+    Q4K b;
+    __device__ __forceinline__ void clear() { b.ds = b.dm = 0.f; }
+    __device__ __forceinline__ void pairs(int m, uint32_t (&hi)[4], uint32_t (&lo)[4]) const
+    {
+        b.template pairs<L>(2 * m, hi[0], lo[0], hi[1], lo[1]);
+        b.template pairs<L>(2 * m + 1, hi[2], lo[2], hi[3], lo[3]);
+    }
+};
+
+template <int FMT, int NG, int XT, int WT>
+__global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_constant__ Params p)
+{
+    using C = Few<FMT, NG, XT, WT>;
+    constexpr int NJ = C::NJ, QPC = C::QPC;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *ops = smem + C::RS * C::RAW;
+    __shared__ uint64_t bars[C::BARS];
+    __shared__ int s_stop;
+    volatile int *stop = &s_stop;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::BARS; ++i) mbar_init(&bars[i], (i >= C::REMPTY && i < C::BFULL) || i >= C::BEMPTY ? kWarps : 1);
+        s_stop = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const uint32_t bar0 = smem_addr(bars);
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
+    auto wait = [&](uint32_t at, uint32_t parity) -> bool {
+        if (bar_try(at, parity)) return true;
+        const long long t0 = clock64();
+        while (!bar_try_ns(at, parity, 20000u))
+            if (*stop || *reinterpret_cast<volatile int *>(&g_few_status) != 0 || clock64() - t0 > p.limit_cycles) {
+                record_status(&g_few_status, RF_ERR_TIMEOUT);
+                *stop = 1;
+                return false;
+            }
+        return true;
+    };
+    auto waits = [&](uint32_t at, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(at, parity)); };
+    const int total = p.plan->n_tiles * p.nrt * p.parts;   // at most 2^30
+
+    if (warp == kWarps) {
+        // Lane l copies box l of a chunk (half l / P, position l % P), lane 0
+        // the operand slices too.
+        const int half = lane >> p.logP, j = lane & (p.P - 1);
+        const bool copies = half < 2 && p.copies;
+        const uint32_t dst = smem_addr(smem) + (uint32_t)lane * (uint32_t)((64 >> p.logP) * p.bw), dst_ops = smem_addr(ops);
+        const int xj = (int)((int64_t)j * p.rb);
+        const CUtensorMap *map = &p.map[p.gated ? half & 1 : 0];
+        uint32_t rc = 0, r = 0, rph = 1, bc = 0, b = 0, bph = 1;   // copies of both kinds; places and phases
+        uint32_t skipped = 0xffffffffu;
+        bool ok = true;
+        for (int index = blockIdx.x; ok && index < total; index += gridDim.x) {
+            const int at = index / p.parts, part = index % p.parts;
+            const ChunkTile w = p.tiles[at / p.nrt];
+            const int rt = at % p.nrt;
+            const int64_t first = p.row0 + (int64_t)w.group * p.group_rows +
+                                  (p.gated ? (int64_t)rt * 64 : (int64_t)rt * 128 + 64 * half);
+            const int y = (int)((first - j + p.P - 1) >> p.logP);   // first super-row with position j in the tile
+            const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * kGranBytes;
+            const uint8_t *src = p.img + (int64_t)w.gran * p.nst * kGranBytes + (int64_t)(part * p.part_chunks * QPC) * slice;
+            for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); ok && c < end; ++c) {
+                if (!(ok = waits(bar(C::REMPTY + r), rph))) break;
+                if (lane == 0) {
+                    if (p.copies) bar_expect(bar(C::RFULL + r), (uint32_t)(kM * p.bw));
+                    else bar_arrive(bar(C::RFULL + r));
+                }
+                __syncwarp();
+                if (copies) copy_box(dst + r * C::RAW, map, ((xj + c * C::CB) & ~15) >> 1, y, bar(C::RFULL + r));
+                ++rc;
+                if (++r == C::RS) r = 0, rph ^= 1u;
+                for (int q = 0; q < QPC; q += 4) {
+                    if (!(ok = waits(bar(C::BEMPTY + b), bph))) break;
+                    if (lane == 0) {
+                        if (blockIdx.x == 0 && bc == 0 && p.withhold >= 0) {
+                            skipped = bc;
+                        } else {
+                            bar_expect(bar(C::BFULL + b), 4 * slice);
+                            copy_bulk(dst_ops + b * C::QB, src, 4 * slice, bar(C::BFULL + b));
+                        }
+                    }
+                    src += 4 * slice;
+                    ++bc;
+                    if (++b == C::BS) b = 0, bph ^= 1u;
+                }
+            }
+        }
+        // Every copy issued lands before the CTA can exit.
+        if (lane == 0) {
+            for (uint32_t i = rc > C::RS ? rc - C::RS : 0; i < rc; ++i) bar_drain(bar(C::RFULL + i % C::RS), (i / C::RS) & 1);
+            for (uint32_t i = bc > C::BS ? bc - C::BS : 0; i < bc; ++i)
+                if (i != skipped) bar_drain(bar(C::BFULL + i % C::BS), (i / C::BS) & 1);
+        }
+        return;
+    }
+
+    const int g = lane >> 2, t = lane & 3, i = lane_row(8 * warp + g, p.logP);
+    const int64_t copied = p.copies ? p.total_rows & ~(int64_t)(p.P - 1) : 0;   // rows in whole super-rows
+    const int swz = ((g ^ (2 * t)) & 7) * 16;   // see prep_kernel
+    uint32_t r = 0, rph = 0, b = 0, bph = 0;
+    ChunkTile next = {};
+    if ((int)blockIdx.x < total) next = p.tiles[blockIdx.x / p.parts / p.nrt];
+    for (int index = blockIdx.x; index < total; index += gridDim.x) {
+        const int at = index / p.parts, part = index % p.parts;
+        const ChunkTile w = next;
+        const int rt = at % p.nrt;
+        const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * kGranBytes;
+        uint32_t off[2], mis[2];
+        int64_t row[2];
+        bool tail[2];
+        uint32_t start[2];   // (of the row)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t first = p.row0 + (int64_t)w.group * p.group_rows + (p.gated ? (int64_t)rt * 64 : (int64_t)rt * 128 + 64 * h);
+            row[h] = first + i;
+            const int j = (int)(row[h] & (p.P - 1));
+            const int s = (int)((row[h] >> p.logP) - ((first - j + p.P - 1) >> p.logP));
+            off[h] = (uint32_t)((h << p.logP) + j) * (uint32_t)((64 >> p.logP) * p.bw) + (uint32_t)(s * p.bw) + ((uint32_t)(j * p.rb) & 15u);
+            tail[h] = row[h] >= copied && row[h] < p.total_rows;
+            start[h] = off[h];
+            // This lane's first block, and the word in which it begins.
+            if constexpr (FMT != RF_Q4_K) off[h] += t * (C::SPREAD ? 4 : 2) * block_size(FMT);
+            mis[h] = off[h] & 3u;
+            off[h] -= mis[h];
+        }
+        const bool tails = __any_sync(0xffffffffu, tail[0] || tail[1]);
+        // Sums of (row g of half h, token 8 q + 2 t + e): [..][q][2 h + e].
+        // One for each kind of product (chains of products are slow: a single
+        // kind has two).  fp32: rounded additions move them to `sum` every four
+        // slices (Q4_K: two), because the tensor cores truncate each of theirs.
+        float acc[C::N == 1 ? 2 : C::N][NJ][4], sum[NJ][4];
+        auto flush = [&] {
+#pragma unroll
+            for (int q = 0; q < NJ; ++q)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (XT == 2) {
+                        float low = acc[1][q][k];
+                        if constexpr (C::LOW == kScaled) low += acc[2][q][k];
+                        float high = acc[0][q][k];
+                        if constexpr (C::LOW == kPlain) high += acc[2][q][k];
+                        sum[q][k] += fmaf(low, 1.f / 2048.f, high);
+                    } else {
+                        sum[q][k] = acc[0][q][k] + acc[1][q][k];
+                    }
+                    if constexpr (XT == 2) {
+#pragma unroll
+                        for (int n = 0; n < C::N; ++n) acc[n][q][k] = 0.f;
+                    }
+                }
+        };
+#pragma unroll
+        for (int q = 0; q < NJ; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sum[q][k] = 0.f;
+#pragma unroll
+                for (int n = 0; n < (C::N == 1 ? 2 : C::N); ++n) acc[n][q][k] = 0.f;
+            }
+        // What the end of the item needs, asked for early.
+        float bias[2];
+        int col[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            col[h] = p.gated ? rt * 64 + i : rt * 128 + 64 * h + i;
+            const float *from = p.gated && h ? p.bias[1] : p.bias[0];
+            bias[h] = from && p.parts == 1 && col[h] < p.rows ? from[(int64_t)w.group * p.rows + col[h]] : 0.f;
+        }
+        float inv[NJ][2];
+#pragma unroll
+        for (int q = 0; q < NJ; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) inv[q][e] = __ldg(p.inv + (int64_t)w.gran * C::GT + min(8 * q + 2 * t + e, w.cnt - 1));
+        if (index + (int)gridDim.x < total) next = p.tiles[(index + (int)gridDim.x) / p.parts / p.nrt];
+        for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); c < end; ++c) {
+            if (!waits(bar(C::RFULL + r), rph)) return;
+            uint8_t *src = smem + r * C::RAW;
+            if (tails) {
+                // Rows that the boxes do not reach, copied to where they would
+                // put them.
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (tail[h]) {
+                        const uint8_t *from = p.W[p.gated ? h : 0] + row[h] * p.rb + (int64_t)c * C::CB;
+                        const int n = (int)min((int64_t)C::CB, p.rb - (int64_t)c * C::CB);
+#pragma unroll 1
+                        for (int k = t; k < n; k += 4) src[start[h] + k] = __ldg(from + k);
+                    }
+                __syncwarp();
+            }
+            for (int q4 = 0; q4 < QPC; q4 += 4) {
+                if (!waits(bar(C::BFULL + b), bph)) return;
+                const int sl = C::SPREAD ? 2 * t + q4 / 4 : q4 + t;   // slice of the chunk
+                const uint8_t *x = ops + b * C::QB + t * slice + swz;
+                const bool ragged = FMT != RF_Q4_K && 2 * (c + 1) * QPC > p.nb;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    Weights<FMT, C::LOW> wt[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (FMT == RF_Q4_K) wt[h].b.load(src + off[h], t, e);
+                        else wt[h].load(src + off[h], mis[h], (2 * (C::SPREAD ? q4 / 4 : 0) + e) * block_size(FMT));
+                    }
+                    if constexpr (FMT == RF_MXFP4) {
+                        const bool normal = !__any_sync(0xffffffffu, wt[0].outside(wt[0].s1) || wt[1].outside(wt[1].s1));
+                        wt[0].scale(normal), wt[1].scale(normal);
+                    }
+                    if (ragged) {
+                        const bool dead = 2 * (c * QPC + sl) + e >= p.nb;   // the bytes are the next row's
+                        if (dead) wt[0].clear(), wt[1].clear();
+                    }
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) wt[h].pairs(m, hi[h], lo[h]);
+#pragma unroll
+                        for (int q = 0; q < NJ; ++q) {
+                            if (8 * q >= w.cnt) break;
+                            // XT 1: granules of two tiles of eight; 2: of one, its low terms behind it.
+                            const uint8_t *xm = x + (XT == 2 ? 2 * q : q) * 1024 + (4 * e + m) * 128;
+                            const uint4 v = *reinterpret_cast<const uint4 *>(xm);
+                            mma16816(acc[0][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], v.x, v.y);
+                            mma16816(acc[C::N == 1 ? 1 : 0][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], v.z, v.w);
+                            if constexpr (XT == 2) {
+                                const uint4 l = *reinterpret_cast<const uint4 *>(xm + 1024);
+                                mma16816(acc[1][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], l.x, l.y);
+                                mma16816(acc[1][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], l.z, l.w);
+                            }
+                            if constexpr (WT == 2) {
+                                mma16816(acc[XT][q], lo[0][0], lo[1][0], lo[0][1], lo[1][1], v.x, v.y);
+                                mma16816(acc[XT][q], lo[0][2], lo[1][2], lo[0][3], lo[1][3], v.z, v.w);
+                            }
+                        }
+                    }
+                    if constexpr (XT == 2) {
+                        if (e == 1 || FMT == RF_Q4_K) flush();
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(C::BEMPTY + b));
+                if (++b == C::BS) b = 0, bph ^= 1u;
+            }
+            if (tails) fence_async_smem();   // the next copy follows these stores
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(C::REMPTY + r));
+            if (++r == C::RS) r = 0, rph ^= 1u;
+        }
+        if constexpr (XT == 1) flush();
+        // What follows the product.
+#pragma unroll
+        for (int q = 0; q < NJ; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int tok = 8 * q + 2 * t + e;
+                if (tok >= w.cnt) continue;
+                const int64_t y = w.row0 + tok;
+                float z[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) z[h] = fmaf(sum[q][2 * h + e], inv[q][e], bias[h]);
+                if (p.parts > 1) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (col[h] < p.rows)
+                            p.sums[((int64_t)(part * (1 + p.gated) + (p.gated ? h : 0)) * p.n_row + y) * p.rows + col[h]] = z[h];
+                } else if (p.gated) {
+                    if (col[0] < p.rows) finish_one(p, y, col[0], z[0], z[1]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (col[h] < p.rows) finish_one(p, y, col[h], z[h], 0.f);
+                }
+            }
+    }
+}
+
+template <int FMT, int NG, int XT, int WT>
+rf_status launch(const Params &p, int grid, cudaStream_t s)
+{
+    using C = Few<FMT, NG, XT, WT>;
+    static std::once_flag once[64];
+    static bool ok[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return RF_ERR_CUDA;
+    }
+    std::call_once(once[dev & 63], [dev] {
+        ok[dev & 63] = cudaFuncSetAttribute(few_kernel<FMT, NG, XT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
+                       cudaSuccess;
+        cudaGetLastError();
+    });
+    if (!ok[dev & 63]) return RF_ERR_CUDA;
+    few_kernel<FMT, NG, XT, WT><<<grid, 32 * (kWarps + 1), C::SMEM, s>>>(p);
+    return last_cuda_error();
+}
+
+template <int FMT, int NG>
+rf_status launch_terms(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
+{
+    if constexpr (FMT != RF_MXFP4) {
+        if (sh.wt == 2) return sh.xt == 2 ? launch<FMT, NG, 2, 2>(p, grid, s) : launch<FMT, NG, 1, 2>(p, grid, s);
+    } else {
+        if (sh.xt == 2) return launch<FMT, NG, 2, 1>(p, grid, s);
+    }
+    return launch<FMT, NG, 1, 1>(p, grid, s);
+}
+template <int FMT>
+rf_status launch_fmt(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
+{
+    return sh.nt > kGranRows ? launch_terms<FMT, 2>(sh, p, grid, s) : launch_terms<FMT, 1>(sh, p, grid, s);
+}
+
+}  // namespace
+
+rf_status read_and_clear_few_status()
+{
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_few_status, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
+    if (v != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_few_status, &zero, sizeof(int)) != cudaSuccess) return RF_ERR_CUDA;
+    }
+    return static_cast<rf_status>(v);
+}
+
+rf_status launch_chunk_few(const ChunkShape &sh, const Params &p, cudaStream_t s)
+{
+    const int grid = (int)std::min<int64_t>(2 * num_sms(), sh.cap_tiles * p.nrt * p.parts);
+    switch (sh.fmt) {
+    case RF_Q4_0: return launch_fmt<RF_Q4_0>(sh, p, grid, s);
+    case RF_Q8_0: return launch_fmt<RF_Q8_0>(sh, p, grid, s);
+    case RF_Q4_K: return launch_fmt<RF_Q4_K>(sh, p, grid, s);
+    default: return launch_fmt<RF_MXFP4>(sh, p, grid, s);
+    }
+}
+
+}  // namespace rf

@@ -22,14 +22,6 @@
 //   epilogue     four warps read the sums out of tensor memory, while the
 //                others are at the next item.
 //
-// Rows of any length by tensor copies.  A tensor map's rows have to be
-// multiples of 16 bytes apart; rows of rb bytes are not, but P = 16 /
-// gcd(rb, 16) of them together are.  The map's rows are such super-rows, and a
-// chunk of 64 matrix rows is P boxes, one for each position j in the
-// super-row, whose first byte j * rb + c * (chunk bytes) is rounded down to 16;
-// a thread skips the remainder.  Rows behind the last whole super-row (fewer
-// than 16 of a tensor) are copied by their threads.
-//
 // Order of the inputs.  A product does not care in which order its inputs are
 // summed, so a slice's inputs are in the order in which the decoder finds them
 // cheapest (slice_order in rf_chunk.cu): for MXFP4 the two nibbles of a byte,
@@ -46,33 +38,18 @@
 #include <cstring>
 #include <mutex>
 
-#include <cuda_bf16.h>
-
-#include "rf_chunk.h"
-#include "rf_half.cuh"
-#include "rf_tcgen05.cuh"
+#include "rf_chunk.cuh"
 
 namespace rf {
+using namespace chunk;
 namespace {
 
 __device__ int g_chunk_status = 0;   // bounded waits that gave up
 
-constexpr int kM = 128;              // matrix rows per item (MMA M)
 constexpr int kDec0 = 4;             // first decoder warp; the epilogue's four follow the decoders
 constexpr int kItems = 4;            // items drawn ahead
 constexpr int kInFlight = 16;        // stages of activations in flight at most
 constexpr int kRaws = 8;             // raw chunks in flight at most
-
-__host__ __device__ constexpr int block_size(int fmt) { return fmt == RF_Q4_0 ? 18 : (fmt == RF_Q8_0 ? 34 : (fmt == RF_MXFP4 ? 17 : 144)); }
-
-// Box bytes: the chunk's, with what rounding its first byte down takes, as an
-// odd number of 16-byte units (see Block::load); with 16 matrix rows to a
-// super-row an even one, which keeps the boxes 128 bytes aligned.
-__host__ __device__ constexpr int box_bytes(int fmt, int P)
-{
-    const int n = chunk_bytes(fmt) + (fmt != RF_Q4_K && P > 1 ? 16 : 0);
-    return P < 16 && n / 16 % 2 == 0 ? n + 16 : n;
-}
 
 // NT: operand rows per token tile at most; XT, WT: fp16 terms per activation, weight.
 // A stage is KS slices of weights (tensor memory) and activations (shared
@@ -130,253 +107,10 @@ struct Item {
     int32_t group, row0, cnt, gran, rt, stop, part, pad;
 };
 
-struct Params {
-    CUtensorMap map[2];
-    const uint8_t *W[2];
-    int64_t rb, row0, group_rows, total_rows;
-    const uint8_t *img;
-    const float *inv;
-    ChunkPlan *plan;
-    const ChunkTile *tiles;
-    int32_t P, logP;          // matrix rows per super-row
-    int32_t bw;               // box bytes: chunk bytes, 16 more when P > 1
-    int32_t copies;           // 0: every row is behind the last super-row
-    int32_t slots, raws;      // stages of activations and raw chunks in shared memory,
-    uint32_t slot, raw_at;    // bytes of a slice of such a stage, and where the chunks begin
-    int32_t rows, nst, nch, nb, nrt, gated;   // rows of Y; slices, chunks, blocks of a row; row tiles
-    int32_t act, dtype;
-    float alpha, limit;
-    const float *bias[2];
-    const void *residual;
-    int64_t ldr, ldy;
-    void *Y;
-    float *sums;              // with several parts: [part][projection][row of the call][rows]
-    int32_t parts, part_chunks, n_row;
-    int32_t withhold;         // test hook: CTA 0 never copies this slice's activations
-    long long limit_cycles;   // of a wait
-};
-
-// Row of a half of the tile for each of its 64 threads (tensor-memory lanes):
-// neighbours take rows at the same position of successive super-rows, which
-// lie box_bytes apart.
-__device__ __forceinline__ int lane_row(int e, int logP) { return ((e & ((64 >> logP) - 1)) << logP) + (e >> (6 - logP)); }
-
 __host__ __device__ constexpr uint32_t idesc_n(int n)
 {
     return (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
 }
-
-// ------------------------------------------------------------------ decoding
-// One block of 32 weights from any byte of shared memory: its scale's bits and
-// its quant words.  8-byte loads (eight lanes' rows are an odd number of
-// 16-byte units apart, so that they meet few banks twice), then a word's shift
-// and, with the scale's bytes stepped over, a byte's.
-template <int FMT>
-struct Block {
-    static constexpr int NS = FMT == RF_MXFP4 ? 1 : 2, NW = FMT == RF_Q8_0 ? 8 : 4;   // scale bytes, quant words
-    static constexpr int ND = (7 + NS + 4 * NW) / 8;
-    uint32_t q[NW], s;
-    __device__ __forceinline__ void load(const uint8_t *row, int at)
-    {
-        uint32_t x[2 * ND];
-        const uint32_t off = smem_addr(row) + (uint32_t)at;
-        const uint2 *src = reinterpret_cast<const uint2 *>(row + at - (off & 7u));
-#pragma unroll
-        for (int i = 0; i < ND; ++i) {
-            const uint2 v = src[i];
-            x[2 * i] = v.x, x[2 * i + 1] = v.y;
-        }
-        const bool odd = (off & 4u) != 0;
-        const uint32_t sh = 8u * (off & 3u);
-#pragma unroll
-        for (int i = 0; i < NW + 1; ++i) x[i] = odd ? x[i + 1] : x[i];
-        s = (x[0] >> sh) & (NS == 1 ? 0xFFu : 0xFFFFu);
-#pragma unroll
-        for (int i = 0; i < NW; ++i) q[i] = __funnelshift_rc(x[i], x[i + 1], sh + 8 * NS);
-    }
-};
-
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-
-// How low terms are kept.  kOne: none.  kPlain: as they are (16-bit
-// activations: their products join the high ones' sums; a weight is then off
-// by 2^-25 at most).  kScaled: times 2^11 (fp32: 22 bits of the weight).
-enum Low { kOne, kPlain, kScaled };
-
-// fp32 weights as a pair of fp16 values and the pair of what they leave.
-template <int L>
-__device__ __forceinline__ void two_terms(float w0, float w1, uint32_t &hi, uint32_t &lo)
-{
-    const __half2 h = __floats2half2_rn(w0, w1);
-    hi = h2_bits(h);
-    if constexpr (L != kOne) {
-        const float2 f = __half22float2(h);
-        const float m = L == kScaled ? 2048.f : 1.f;
-        lo = h2_bits(__floats2half2_rn((w0 - f.x) * m, (w1 - f.y) * m));
-    }
-}
-// The same for products n * d of small integers (|n| <= N, fp16 pairs that
-// number(j) gives) and an fp16 scale, in fp16: hi rounds the product, and what
-// it leaves has at most 11 bits, so that one fused multiply-add gives it
-// exactly.  Scaled: n * (2^11 d) - 2^11 hi, in fp32 where that might overflow
-// (N |d| >= 32).
-template <int L, int N, class F>
-__device__ __forceinline__ void products(uint32_t d, F number, uint32_t (&hi)[16], uint32_t (&lo)[16])
-{
-    const uint32_t dd = d * 0x00010001u, dl = L == kScaled ? hmul2(dd, 0x68006800u) : dd;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const uint32_t n = number(j);
-        hi[j] = hmul2(n, dd);
-        if constexpr (L != kOne) lo[j] = hfma2(n, dl, L == kScaled ? hmul2(hi[j], 0xE800E800u) : hi[j] ^ 0x80008000u);
-    }
-    if constexpr (L == kScaled) {
-        const float f = __half2float(__ushort_as_half((unsigned short)d));
-        if (!(fabsf(f) * N < 32.f)) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t n = number(j);
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&n));
-                two_terms<L>(v.x * f, v.y * f, hi[j], lo[j]);
-            }
-        }
-    }
-}
-
-// Q4_0, d and its four quant words: pair 4 m + s holds nibbles s and s + 4 of
-// word m.  0x6400 | n is the fp16 value 1024 + n (and 0x6400 | 16 n is 1024 +
-// 16 n), so n - 8 is exact; one multiply by d rounds the weight once.
-template <int L>
-__device__ __forceinline__ void q4_0_block(uint32_t d, const uint32_t (&q)[4], uint32_t (&hi)[16], uint32_t (&lo)[16])
-{
-    products<L, 8>(d, [&](int j) {
-        const uint32_t t = (j & 2) ? q[j >> 2] >> 8 : q[j >> 2];
-        return (j & 1) ? hfma2((t & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u)   // x / 16 - 72
-                       : hsub2((t & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-    }, hi, lo);
-}
-// Q8_0: with the sign bit flipped, 0x6400 | u is 1024 + q + 128.
-template <int L>
-__device__ __forceinline__ void q8_0_block(uint32_t d, const uint32_t (&q)[8], uint32_t (&hi)[16], uint32_t (&lo)[16])
-{
-    products<L, 128>(d, [&](int j) {
-        return hsub2(prmt(q[j >> 1] ^ 0x80808080u, 0x64646464u, (j & 1) ? 0x7362u : 0x5140u), 0x64806480u);
-    }, hi, lo);
-}
-// Four bytes of two E2M1 codes each as four fp16 pairs (low nibble, high).
-__device__ __forceinline__ void e2m1x8(uint32_t q, uint32_t (&h)[4])
-{
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "mov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(q));
-}
-// MXFP4: pair j holds byte j's two codes, scaled by 2^(E - 127): exact whenever
-// the product is representable, in two steps outside fp16's exponents (one
-// rounding).
-__device__ __forceinline__ void mxfp4_block(uint32_t E, const uint32_t (&q)[4], uint32_t (&hi)[16])
-{
-    const bool normal = E - 113u < 30u;                     // 2^-14 .. 2^15
-    uint32_t s1 = E * 0x04000400u - 112u * 0x04000400u, s2 = 0u;
-    if (!normal) {
-        const int k = (int)E - 127;
-        uint32_t t = 0x0C00u;                               // 2^-12
-        if (E == 255u) t = 0x7E00u;                         // NaN scale
-        else if (k > 15) t = 0x7800u, s2 = pow2_h(min(k - 15, 15));
-        else if (k >= -24) t = pow2_h(k), s2 = 0x3C00u;
-        else s2 = k + 12 >= -24 ? pow2_h(k + 12) : 0u;
-        s1 = t * 0x00010001u, s2 *= 0x00010001u;
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        uint32_t h[4];
-        e2m1x8(q[m], h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) hi[4 * m + e] = hmul2(h[e], s1);
-    }
-    if (!normal && E != 255u) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) hi[j] = hmul2(hi[j], s2);
-    }
-}
-// Half T (0: low nibbles, 1: high) of slice Q of a Q4_K super-block at `s`
-// (16-byte aligned): sub-block 2 Q + T, d * sc * q - dmin * m by one fused
-// multiply-add in fp32 (its products are exact).
-template <int L>
-__device__ __forceinline__ void q4k_block(const uint8_t *s, int Q, int T, uint32_t (&hi)[16], uint32_t (&lo)[16])
-{
-    const uint4 h = *reinterpret_cast<const uint4 *>(s);
-    const uint4 qa = *reinterpret_cast<const uint4 *>(s + 16 + 32 * Q), qb = *reinterpret_cast<const uint4 *>(s + 32 + 32 * Q);
-    const float d = __half2float(__ushort_as_half((unsigned short)(h.x & 0xFFFFu)));
-    const float dmin = __half2float(__ushort_as_half((unsigned short)(h.x >> 16)));
-    const int j = 2 * Q + T;
-    uint32_t sc, m;
-    if (j < 4) {
-        sc = (h.y >> (8 * j)) & 63u;
-        m = (h.z >> (8 * j)) & 63u;
-    } else {
-        const uint32_t b = (h.w >> (8 * (j - 4))) & 0xFFu;
-        sc = (b & 15u) | (((h.y >> (8 * (j - 4) + 6)) & 3u) << 4);
-        m = (b >> 4) | (((h.z >> (8 * (j - 4) + 6)) & 3u) << 4);
-    }
-    const float ds = d * (float)sc, dm = dmin * (float)m;
-    const uint32_t qw[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t v = (qw[k] >> (4 * T)) & 0x0F0F0F0Fu;
-        float f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            f[e] = fmaf(ds, __uint_as_float(prmt(v, 0x4B000000u, 0x7440u + e)) - 8388608.f, -dm);
-        two_terms<L>(f[0], f[1], hi[2 * k], lo[2 * k]);
-        two_terms<L>(f[2], f[3], hi[2 * k + 1], lo[2 * k + 1]);
-    }
-}
-
-template <int FMT, int L>
-__device__ __forceinline__ void block_pairs(const Block<FMT> &b, uint32_t (&hi)[16], uint32_t (&lo)[16])
-{
-    if constexpr (FMT == RF_Q4_0) q4_0_block<L>(b.s, b.q, hi, lo);
-    else if constexpr (FMT == RF_Q8_0) q8_0_block<L>(b.s, b.q, hi, lo);
-    else mxfp4_block(b.s, b.q, hi);
-}
-
-// ---------------------------------------------------------------- activations
-// (A quotient by reciprocal, 2 ulp: without the exact division's slow path the
-// lanes' values are computed side by side.  1 + exp overflows to 0, the limit.)
-__device__ __forceinline__ float sigmoid_times(float z, float arg) { return __fdividef(z, 1.f + expf(-arg)); }
-__device__ __forceinline__ float clamped_of(float g, float u, float alpha, float limit)
-{
-    g = g > limit ? limit : g;   // (NaN stays)
-    u = u > limit ? limit : (u < -limit ? -limit : u);
-    return sigmoid_times(g, alpha * g) * (u + 1.f);
-}
-
-template <int DT> struct Out;
-template <> struct Out<RF_F32> {
-    using T = float;
-    static __device__ __forceinline__ float get(T v) { return v; }
-    static __device__ __forceinline__ T put(float v) { return v; }
-};
-template <> struct Out<RF_F16> {
-    using T = __half;
-    static __device__ __forceinline__ float get(T v) { return __half2float(v); }
-    static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
-};
-template <> struct Out<RF_BF16> {
-    using T = __nv_bfloat16;
-    static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
-    static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
-};
 
 // Sixteen tokens' sums z of this lane's matrix row, as rows r0.. of Y (the
 // first n of them): bias, activation, residual, stores.  Gated: lanes 16 apart
@@ -464,63 +198,9 @@ __device__ __forceinline__ void load_inv(const float *inv, float (&f)[16])
     }
 }
 
-// Barriers and copies by shared-memory address: the roles' loops are chains of
-// a few instructions, and a generic pointer's conversion would be among them.
-__device__ __forceinline__ void bar_arrive(uint32_t bar)
-{
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-// Whether phase `parity` has completed: at once (test), within the hardware's
-// own time (try), or within `ns` nanoseconds, the thread set aside meanwhile.
-__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool bar_try_ns(uint32_t bar, uint32_t parity, uint32_t ns)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(ns) : "memory");
-    return ok != 0;
-}
 __device__ __forceinline__ void bar_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-                     "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-                 : "memory");
-}
-// A copy that was issued lands whatever else failed: wait for it (bounded,
-// ignoring the status word), so that none is under way when the CTA exits.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity)
-{
-    const unsigned long long t0 = globaltimer_ns();
-    while (!bar_try_ns(bar, parity, 20000u) && globaltimer_ns() - t0 < kWaitLimitNs) {
-    }
 }
 
 template <int FMT, int NT, int XT, int WT>
@@ -965,22 +645,7 @@ __global__ void __launch_bounds__(128) join_parts_kernel(const __grid_constant__
 #pragma unroll
     for (int t = 0; t < kJoinRows; ++t) {
         if (t >= n) break;
-        float y = z[t] + b0;
-        if (p.act == RF_ACT_SILU) y = sigmoid_times(y, y);
-        else if (p.act == RF_ACT_GELU) y = 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
-        else if (p.act == RF_ACT_SWIGLU) y = sigmoid_times(y, y) * (u[t] + b1);
-        else if (p.act == RF_ACT_SWIGLU_CLAMPED) y = clamped_of(y, u[t] + b1, p.alpha, p.limit);
-        const int64_t row = w.row0 + t0 + t, from = row * p.ldr + col, to = row * p.ldy + col;
-        if (p.dtype == RF_F32) {
-            if (p.residual) y += static_cast<const float *>(p.residual)[from];
-            static_cast<float *>(p.Y)[to] = y;
-        } else if (p.dtype == RF_F16) {
-            if (p.residual) y += Out<RF_F16>::get(static_cast<const __half *>(p.residual)[from]);
-            static_cast<__half *>(p.Y)[to] = Out<RF_F16>::put(y);
-        } else {
-            if (p.residual) y += Out<RF_BF16>::get(static_cast<const __nv_bfloat16 *>(p.residual)[from]);
-            static_cast<__nv_bfloat16 *>(p.Y)[to] = Out<RF_BF16>::put(y);
-        }
+        finish_one(p, w.row0 + t0 + t, col, z[t] + b0, u[t] + b1);
     }
 }
 
@@ -1090,7 +755,8 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
     p.sums = reinterpret_cast<float *>(g.ws + sh.at_sums);
     const int grid = (int)std::min<int64_t>(num_sms(), sh.cap_tiles * p.nrt * p.parts);
     rf_status st;
-    switch (sh.fmt) {
+    if (sh.few) st = launch_chunk_few(sh, p, s);
+    else switch (sh.fmt) {
     case RF_Q4_0: st = launch_fmt<RF_Q4_0>(sh, p, grid, s); break;
     case RF_Q8_0: st = launch_fmt<RF_Q8_0>(sh, p, grid, s); break;
     case RF_Q4_K: st = launch_fmt<RF_Q4_K>(sh, p, grid, s); break;

@@ -112,6 +112,7 @@ rf_status read_and_clear_attn_tile_status();
 // The chunk operators' bounded waits, and offsets or order entries out of
 // range, read and cleared.
 rf_status read_and_clear_chunk_status();
+rf_status read_and_clear_few_status();
 rf_status read_and_clear_chunk_invalid();
 // Arms the one-shot wait fault of the next producer-mode launch
 // (rf_debug_arm_wait_fault).
