@@ -72,7 +72,7 @@ struct PrepParams {
     const int32_t *order;
     int32_t per, n_row, n_group;
     int32_t in_dim, nst, order8;   // order8: which inputs a 16-byte unit holds
-    int32_t tile_tokens, cap_tiles, cap_gran, parts, vec, few, spread;
+    int32_t gran_tokens, tile_tokens, cap_tiles, cap_gran, parts, vec, few, spread;
     ChunkPlan *plan;
     ChunkTile *tiles;
     float *inv;               // by place in the granules
@@ -111,9 +111,9 @@ __device__ __forceinline__ int scan_block(int v, int *part, int *total)
     return base + x - v;
 }
 
-template <int GT>
 __device__ void list_tiles(const PrepParams &p)
 {
+    const int GT = p.gran_tokens;
     __shared__ int part[kPrepThreads / 32];
     int next = 0;
     for (int g0 = 0; g0 < p.n_group; g0 += kPrepThreads) {
@@ -159,9 +159,10 @@ template <int DT, int XT>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ PrepParams p)
 {
     using T = typename Elem<DT>::T;
-    constexpr int GT = kGranRows / XT, H = GT / kPrepRows;   // tokens of a granule, CTAs that share it
+    constexpr int H = XT == 1 ? kGranRows / kPrepRows : 1;   // CTAs that share a granule
+    const int GT = p.gran_tokens;
     if (blockIdx.x == gridDim.x - 1) {
-        list_tiles<GT>(p);
+        list_tiles(p);
         return;
     }
     const int part = blockIdx.x % p.parts, gran = blockIdx.x / p.parts / H, sub = blockIdx.x / p.parts % H;
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         const int tt = p.tile_tokens / GT;   // granules per whole tile
         s_group = g;
         s_row = a + q * GT + sub * kPrepRows;
-        s_cnt = min(kPrepRows, b - s_row);
+        s_cnt = min(min(kPrepRows, GT), b - s_row);
         s_at = gran - q + q / tt * tt;       // the tile's first granule
         s_n = min(tt, (b - a - q / tt * p.tile_tokens + GT - 1) / GT);
     }
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         if (lane == 0) {
             s_scale[warp] = __uint_as_float((uint32_t)(k + 127) << 23);
             s_src[warp] = src;
-            if (part == 0) p.inv[(int64_t)gran * GT + sub * kPrepRows + warp] = __uint_as_float((uint32_t)(127 - k) << 23);
+            if (part == 0 && warp < GT) p.inv[(int64_t)gran * GT + sub * kPrepRows + warp] = __uint_as_float((uint32_t)(127 - k) << 23);
         }
     }
     __syncthreads();
@@ -228,14 +229,16 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
     // and its low term), kPrepThreads / 64 slices at a time.
     constexpr int kStep = kPrepThreads / (8 * kPrepRows);
     const int r = tid & 7, c = (tid >> 3) & 7;
+    if (r >= GT) return;
     const float scale = s_scale[r];
     const int64_t src = s_src[r];
     const T *x = static_cast<const T *>(p.X) + (src >= 0 ? src * p.ldx : 0);
     const int first = c >> 2, u = c & 3;
     const int ka = 32 * first + (p.order8 == kOrderPlain ? 8 * u : 4 * u);
     const int kb = ka + (p.order8 == kOrderPlain ? 4 : 16);
-    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * kGranBytes + sub * 1024 + c * 128;
-    const int64_t step = (int64_t)s_n * kGranBytes;
+    const int bytes = GT * XT * kSliceK * 2;
+    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * bytes + sub * 1024 + c * 128;
+    const int64_t step = (int64_t)s_n * bytes;
 #pragma unroll 4
     for (int s = part * kStep + (tid >> 6); s < p.nst; s += p.parts * kStep) {
         float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f}, f[8];
@@ -261,9 +264,14 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         // MXFP4, every other one of eight): they lie one after the other, each
         // slice's turned in its 128 bytes, for the banks.
         const int at = p.spread ? (s & ~7) | (s & 1) << 2 | (s >> 1 & 3) : s;
-        uint8_t *to = out + at * step + (p.few ? (r ^ (2 * (at & 3))) * 16 : r * 16);
-        *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-        if constexpr (XT == 2) *reinterpret_cast<uint4 *>(to + 1024) = make_uint4(l[0], l[1], l[2], l[3]);
+        // (The low terms' rows follow the high ones'.)
+        const int turn = p.few ? 2 * (at & 3) : 0;
+        uint8_t *to = out + at * step;
+        *reinterpret_cast<uint4 *>(to + (r ^ turn) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+        if constexpr (XT == 2) {
+            to += GT == 8 ? 1024 + (r ^ turn) * 16 : ((GT + r) ^ turn) * 16;
+            *reinterpret_cast<uint4 *>(to) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
     }
 }
 
@@ -330,7 +338,7 @@ void choose_parts(ChunkShape &sh, bool gated)
                                           : std::min(sh.cap_tiles, std::max(sh.n_row / sh.tile_tokens(), std::min(sh.n_group, sh.n_row)));
     const int64_t items = tiles * ((sh.rows + (gated ? 63 : 127)) / (gated ? 64 : 128)), sms = num_sms();
     const int64_t per = chunk_weights(sh.fmt) / kSliceK, nch = (sh.nst + per - 1) / per;
-    const int64_t slice = sh.few ? std::max<int64_t>(sh.wt == 2 ? 500 : 375, 128 * (sh.xt + sh.wt - 1) * (sh.tile_tokens() / 8))
+    const int64_t slice = sh.few ? std::max<int64_t>(sh.wt == 2 ? 500 : 375, 128 * (sh.nt == 8 ? sh.wt : (sh.xt + sh.wt - 1) * (sh.tile_tokens() / 8)))
                           : sh.wt == 2 ? (sh.fmt == RF_Q4_K ? 1400 : 1000) : (sh.nt > 128 ? 640 : 420);
     auto cost = [&](int64_t parts) {
         const int64_t slices = std::min<int64_t>((nch + parts - 1) / parts * per, sh.nst);
@@ -361,7 +369,7 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     sh.nst = (int)((in_dim + kSliceK - 1) / kSliceK);
     // Operand rows of a group: twice the average, so that most groups have one tile.
     const int64_t each = n_group == 1 ? sh.xt * n_row : 2 * sh.xt * ((n_row + n_group - 1) / n_group);
-    sh.nt = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : sh.wt == 1 && sh.xt == 1 && each > 256 ? 192 : 128;
+    sh.nt = each <= 8 && sh.xt == 2 ? 8 : each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : sh.wt == 1 && sh.xt == 1 && each > 256 ? 192 : 128;
     sh.few = sh.nt <= 32;
     const int per = chunk_weights(fmt) / kSliceK;
     if (sh.few) sh.nst = (sh.nst + per - 1) / per * per;
@@ -372,7 +380,7 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     size_t at = sizeof(ChunkPlan);
     sh.at_tiles = at, at = up256(at + (size_t)sh.cap_tiles * sizeof(ChunkTile));
     sh.at_inv = at, at = up256(at + (size_t)sh.cap_gran * GT * sizeof(float));
-    sh.at_img = at, at = up256(at + (size_t)sh.cap_gran * sh.nst * kGranBytes);
+    sh.at_img = at, at = up256(at + (size_t)sh.cap_gran * sh.nst * sh.gran_bytes());
     sh.at_sums = at;
     if (sh.parts > 1) at = up256(at + (size_t)sh.parts * (1 + gated) * n_row * rows * sizeof(float));
     sh.bytes = at;
@@ -427,6 +435,7 @@ rf_status launch_prep(const ChunkShape &sh, const Source &x, uint8_t *ws, cudaSt
     p.n_row = (int32_t)sh.n_row, p.n_group = (int32_t)sh.n_group;
     p.in_dim = (int32_t)sh.in_dim, p.nst = sh.nst;
     p.order8 = sh.fmt == RF_MXFP4 ? kOrderPairs : (sh.fmt == RF_Q4_0 ? kOrderSpread : kOrderPlain);
+    p.gran_tokens = sh.gran_tokens();
     p.tile_tokens = sh.tile_tokens();
     p.few = sh.few;
     p.spread = sh.few && sh.fmt == RF_MXFP4;
@@ -439,7 +448,7 @@ rf_status launch_prep(const ChunkShape &sh, const Source &x, uint8_t *ws, cudaSt
     p.img = ws + sh.at_img;
     // Rows' slices are shared out among CTAs while there are few rows (each
     // finds its rows' maxima again).
-    const int64_t share = sh.gran_tokens() / kPrepRows;
+    const int64_t share = std::max(1, sh.gran_tokens() / kPrepRows);
     const int64_t busy = std::min<int64_t>(sh.cap_gran * share, sh.n_row);   // CTAs with rows, at most
     p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((sh.nst + 3) / 4, 4 * num_sms() / std::max<int64_t>(1, busy)));
     const int64_t blocks = sh.cap_gran * share * p.parts;

@@ -30,21 +30,24 @@ __device__ int g_few_status = 0;   // bounded waits that gave up
 
 constexpr int kWarps = 8;          // that multiply; one more copies
 
-// NG: granules of operand rows per token tile; XT, WT: fp16 terms per
+// NG: granules of operand rows per token tile (0: half a one, four tokens of two
+// terms, which are one tile of eight columns); XT, WT: fp16 terms per
 // activation, weight.
 template <int FMT, int NG, int XT, int WT>
 struct Few {
     static constexpr int CB = chunk_bytes(FMT), QPC = chunk_weights(FMT) / kSliceK;
-    static constexpr int GT = kGranRows / XT, T = NG * GT, NJ = T / 8;   // tokens, and tiles of eight of them
+    static constexpr bool BOTH = NG == 0;                                // a column of either term
+    static constexpr int GT = BOTH ? 4 : kGranRows / XT, GB = BOTH ? kGranBytes / 2 : kGranBytes;
+    static constexpr int T = BOTH ? 4 : NG * GT, NJ = BOTH ? 1 : T / 8;  // tokens, and tiles of eight of them
     // MXFP4: a four of slices are every other one of a chunk (see Weights).
     static constexpr bool SPREAD = FMT == RF_MXFP4;
-    static constexpr int N = XT + WT - 1;                                // kinds of products
+    static constexpr int N = BOTH ? WT : XT + WT - 1;                    // kinds of products
     // Q4_K's low terms in fp32 calls are scaled; the others' are exact as they are.
     static constexpr int LOW = WT == 1 ? kOne : (XT == 2 && FMT == RF_Q4_K ? kScaled : kPlain);
     // Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.
     static constexpr int SHARED = 115200;
     static constexpr int RAW = kM * box_bytes(FMT, 8);
-    static constexpr int QB = NG * 4 * kGranBytes;                       // operand bytes of four slices
+    static constexpr int QB = (BOTH ? 1 : NG) * 4 * GB;                      // operand bytes of four slices
     static constexpr int RS = (SHARED - 2 * QB) / RAW < 4 ? (SHARED - 2 * QB) / RAW : 4;   // raw chunks
     static constexpr int BS = (SHARED - RS * RAW) / QB < 4 ? (SHARED - RS * RAW) / QB : 4; // fours of slices
     static constexpr int SMEM = RS * RAW + BS * QB;
@@ -185,8 +188,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             const int64_t first = p.row0 + (int64_t)w.group * p.group_rows +
                                   (p.gated ? (int64_t)rt * 64 : (int64_t)rt * 128 + 64 * half);
             const int y = (int)((first - j + p.P - 1) >> p.logP);   // first super-row with position j in the tile
-            const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * kGranBytes;
-            const uint8_t *src = p.img + (int64_t)w.gran * p.nst * kGranBytes + (int64_t)(part * p.part_chunks * QPC) * slice;
+            const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * C::GB;
+            const uint8_t *src = p.img + (int64_t)w.gran * p.nst * C::GB + (int64_t)(part * p.part_chunks * QPC) * slice;
             for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); ok && c < end; ++c) {
                 if (!(ok = waits(bar(C::REMPTY + r), rph))) break;
                 if (lane == 0) {
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
         const int at = index / p.parts, part = index % p.parts;
         const ChunkTile w = next;
         const int rt = at % p.nrt;
-        const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * kGranBytes;
+        const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * C::GB;
         uint32_t off[2], mis[2];
         int64_t row[2];
         bool tail[2];
@@ -263,17 +266,24 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if constexpr (XT == 2) {
-                        float low = acc[1][q][k];
-                        if constexpr (C::LOW == kScaled) low += acc[2][q][k];
-                        float high = acc[0][q][k];
-                        if constexpr (C::LOW == kPlain) high += acc[2][q][k];
-                        sum[q][k] += fmaf(low, 1.f / 2048.f, high);
+                        // By terms of (weight, activation): high high, high low, low high.
+                        float high = acc[0][q][k], low = acc[1][q][k];
+                        if constexpr (C::BOTH) {
+                            // (The column says which of the activation's.)
+                            if constexpr (WT == 1) high += low;
+                            else high = C::LOW == kScaled ? fmaf(low, 1.f / 2048.f, high) : high + low;
+                            sum[q][k] += high;
+                        } else {
+                            if constexpr (C::LOW == kScaled) low += acc[2][q][k];
+                            if constexpr (C::LOW == kPlain) high += acc[2][q][k];
+                            sum[q][k] += fmaf(low, 1.f / 2048.f, high);
+                        }
                     } else {
                         sum[q][k] = acc[0][q][k] + acc[1][q][k];
                     }
                     if constexpr (XT == 2) {
 #pragma unroll
-                        for (int n = 0; n < C::N; ++n) acc[n][q][k] = 0.f;
+                        for (int n = 0; n < (C::N == 1 ? 2 : C::N); ++n) acc[n][q][k] = 0.f;
                     }
                 }
         };
@@ -350,14 +360,14 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                             const uint4 v = *reinterpret_cast<const uint4 *>(xm);
                             mma16816(acc[0][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], v.x, v.y);
                             mma16816(acc[C::N == 1 ? 1 : 0][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], v.z, v.w);
-                            if constexpr (XT == 2) {
+                            if constexpr (XT == 2 && !C::BOTH) {
                                 const uint4 l = *reinterpret_cast<const uint4 *>(xm + 1024);
                                 mma16816(acc[1][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], l.x, l.y);
                                 mma16816(acc[1][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], l.z, l.w);
                             }
                             if constexpr (WT == 2) {
-                                mma16816(acc[XT][q], lo[0][0], lo[1][0], lo[0][1], lo[1][1], v.x, v.y);
-                                mma16816(acc[XT][q], lo[0][2], lo[1][2], lo[0][3], lo[1][3], v.z, v.w);
+                                mma16816(acc[C::N - 1][q], lo[0][0], lo[1][0], lo[0][1], lo[1][1], v.x, v.y);
+                                mma16816(acc[C::N - 1][q], lo[0][2], lo[1][2], lo[0][3], lo[1][3], v.z, v.w);
                             }
                         }
                     }
@@ -375,13 +385,17 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             if (++r == C::RS) r = 0, rph ^= 1u;
         }
         if constexpr (XT == 1) flush();
+        if constexpr (C::BOTH) {   // the low terms' columns are two lanes on
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum[0][k] = fmaf(__shfl_xor_sync(0xffffffffu, sum[0][k], 2), 1.f / 2048.f, sum[0][k]);
+        }
         // What follows the product.
 #pragma unroll
         for (int q = 0; q < NJ; ++q)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int tok = 8 * q + 2 * t + e;
-                if (tok >= w.cnt) continue;
+                if (tok >= w.cnt) continue;   // (at most C::T)
                 const int64_t y = w.row0 + tok;
                 float z[2];
 #pragma unroll
@@ -426,16 +440,19 @@ rf_status launch(const Params &p, int grid, cudaStream_t s)
 template <int FMT, int NG>
 rf_status launch_terms(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
 {
-    if constexpr (FMT != RF_MXFP4) {
-        if (sh.wt == 2) return sh.xt == 2 ? launch<FMT, NG, 2, 2>(p, grid, s) : launch<FMT, NG, 1, 2>(p, grid, s);
+    if (sh.xt == 2) return launch<FMT, NG, 2, FMT == RF_MXFP4 ? 1 : 2>(p, grid, s);
+    if constexpr (NG > 0) {
+        if constexpr (FMT != RF_MXFP4)
+            if (sh.wt == 2) return launch<FMT, NG, 1, 2>(p, grid, s);
+        return launch<FMT, NG, 1, 1>(p, grid, s);
     } else {
-        if (sh.xt == 2) return launch<FMT, NG, 2, 1>(p, grid, s);
+        return RF_ERR_INVALID_ARG;   // (tiles of four tokens have two terms)
     }
-    return launch<FMT, NG, 1, 1>(p, grid, s);
 }
 template <int FMT>
 rf_status launch_fmt(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
 {
+    if (sh.nt < kGranRows) return launch_terms<FMT, 0>(sh, p, grid, s);
     return sh.nt > kGranRows ? launch_terms<FMT, 2>(sh, p, grid, s) : launch_terms<FMT, 1>(sh, p, grid, s);
 }
 
