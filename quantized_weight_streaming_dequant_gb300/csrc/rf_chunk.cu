@@ -159,8 +159,7 @@ template <int DT, int XT>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ PrepParams p)
 {
     using T = typename Elem<DT>::T;
-    constexpr int H = XT == 1 ? kGranRows / kPrepRows : 1;   // CTAs that share a granule
-    const int GT = p.gran_tokens;
+    const int GT = p.gran_tokens, H = max(1, GT / kPrepRows);   // tokens of a granule, CTAs that share it
     if (blockIdx.x == gridDim.x - 1) {
         list_tiles(p);
         return;
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         uint8_t *to = out + at * step;
         *reinterpret_cast<uint4 *>(to + (r ^ turn) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
         if constexpr (XT == 2) {
-            to += GT == 8 ? 1024 + (r ^ turn) * 16 : ((GT + r) ^ turn) * 16;
+            to += GT == kPrepRows ? 1024 + (r ^ turn) * 16 : ((GT + r) ^ turn) * 16;
             *reinterpret_cast<uint4 *>(to) = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
@@ -369,7 +368,7 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     sh.nst = (int)((in_dim + kSliceK - 1) / kSliceK);
     // Operand rows of a group: twice the average, so that most groups have one tile.
     const int64_t each = n_group == 1 ? sh.xt * n_row : 2 * sh.xt * ((n_row + n_group - 1) / n_group);
-    sh.nt = each <= 8 && sh.xt == 2 ? 8 : each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : sh.wt == 1 && sh.xt == 1 && each > 256 ? 192 : 128;
+    sh.nt = each <= 8 ? 8 : each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : sh.wt == 1 && sh.xt == 1 && each > 256 ? 192 : 128;
     sh.few = sh.nt <= 32;
     const int per = chunk_weights(fmt) / kSliceK;
     if (sh.few) sh.nst = (sh.nst + per - 1) / per * per;

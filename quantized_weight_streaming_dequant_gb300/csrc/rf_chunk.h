@@ -29,7 +29,7 @@ constexpr int kGranBytes = kGranRows * kSliceK * 2;   // ... and its bytes per s
 
 // Operands of one product.  xt: fp16 terms per activation (a granule holds
 // kGranRows / xt tokens: 8 rows of high terms, then 8 of low ones, when there
-// are two; with tiles of four tokens, half that of both).  wt: fp16 terms per weight.  nt: operand rows per token tile.
+// are two; tiles of eight operand rows have granules of eight).  wt: fp16 terms per weight.  nt: operand rows per token tile.
 struct ChunkShape {
     int fmt, xt, wt, nt;
     bool few;                                // for rf_chunk_few.cu's kernel
@@ -39,7 +39,7 @@ struct ChunkShape {
     int parts, part_chunks;                  // parts of a row's raw chunks, and chunks per part
     size_t at_tiles, at_inv, at_img, at_sums, bytes;   // workspace: plan, tiles, 1 / row scale, images, parts' sums
     int tile_tokens() const { return nt / xt; }
-    int gran_rows() const { return std::min(nt, kGranRows); }   // 8: four tokens of two terms
+    int gran_rows() const { return std::min(nt, kGranRows); }   // (8: half a granule)
     int gran_tokens() const { return gran_rows() / xt; }
     int gran_bytes() const { return gran_rows() * kSliceK * 2; }
 };

@@ -19,6 +19,7 @@
 // So gate and up of a neuron end in one thread.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "rf_chunk.cuh"
 
@@ -30,15 +31,15 @@ __device__ int g_few_status = 0;   // bounded waits that gave up
 
 constexpr int kWarps = 8;          // that multiply; one more copies
 
-// NG: granules of operand rows per token tile (0: half a one, four tokens of two
-// terms, which are one tile of eight columns); XT, WT: fp16 terms per
+// NG: granules of operand rows per token tile (0: half a one, eight tokens or
+// four of two terms, one tile of eight columns); XT, WT: fp16 terms per
 // activation, weight.
 template <int FMT, int NG, int XT, int WT>
 struct Few {
     static constexpr int CB = chunk_bytes(FMT), QPC = chunk_weights(FMT) / kSliceK;
-    static constexpr bool BOTH = NG == 0;                                // a column of either term
-    static constexpr int GT = BOTH ? 4 : kGranRows / XT, GB = BOTH ? kGranBytes / 2 : kGranBytes;
-    static constexpr int T = BOTH ? 4 : NG * GT, NJ = BOTH ? 1 : T / 8;  // tokens, and tiles of eight of them
+    static constexpr bool BOTH = NG == 0 && XT == 2;                     // a column of either term
+    static constexpr int GR = NG == 0 ? kGranRows / 2 : kGranRows, GT = GR / XT, GB = GR * kSliceK * 2;   // a granule
+    static constexpr int T = (NG == 0 ? 1 : NG) * GT, NJ = (T + 7) / 8;  // tokens, and tiles of eight of them
     // MXFP4: a four of slices are every other one of a chunk (see Weights).
     static constexpr bool SPREAD = FMT == RF_MXFP4;
     static constexpr int N = BOTH ? WT : XT + WT - 1;                    // kinds of products
@@ -47,7 +48,7 @@ struct Few {
     // Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.
     static constexpr int SHARED = 115200;
     static constexpr int RAW = kM * box_bytes(FMT, 8);
-    static constexpr int QB = (BOTH ? 1 : NG) * 4 * GB;                      // operand bytes of four slices
+    static constexpr int QB = (NG == 0 ? 1 : NG) * 4 * GB;                   // operand bytes of four slices
     static constexpr int RS = (SHARED - 2 * QB) / RAW < 4 ? (SHARED - 2 * QB) / RAW : 4;   // raw chunks
     static constexpr int BS = (SHARED - RS * RAW) / QB < 4 ? (SHARED - RS * RAW) / QB : 4; // fours of slices
     static constexpr int SMEM = RS * RAW + BS * QB;
@@ -71,12 +72,10 @@ template <int FMT, int L>
 struct Weights {
     static constexpr int NS = FMT == RF_MXFP4 ? 1 : 2, NW = FMT == RF_Q8_0 ? 8 : 4;   // scale bytes, quant words
     uint32_t q[NW], s1, s2;
-    bool two;     // (MXFP4, the warp's) scales that need a second factor
-    // The block `at` bytes behind byte `mis` of the word at `row`.
-    __device__ __forceinline__ void load(const uint8_t *row, uint32_t mis, int at)
+    // From byte sh / 8 of the word at `src`.
+    __device__ __forceinline__ void load(const uint8_t *from, uint32_t sh)
     {
-        const uint32_t off = mis + (uint32_t)at, sh = 8u * (off & 3u);
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(row + (off & ~3u));
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(from);
         uint32_t x[NW + 1];
 #pragma unroll
         for (int i = 0; i < NW + 1; ++i) x[i] = src[i];
@@ -85,35 +84,30 @@ struct Weights {
         for (int i = 0; i < NW; ++i) q[i] = __funnelshift_rc(x[i], x[i + 1], sh + 8 * NS);
         if constexpr (FMT != RF_MXFP4) s1 *= 0x00010001u;
     }
-    // MXFP4: the factor 2^k, k = E - 127 (`normal`: fp16 has it as a normal
-    // number, for the whole warp), in two where fp16 has no such number.
-    static __device__ __forceinline__ bool outside(uint32_t E) { return E - 113u >= 30u; }
-    __device__ __forceinline__ void scale(bool normal)
+    // MXFP4: the factor 2^k, k = E - 127, where fp16 has it as a normal number;
+    // anywhere, in two.
+    static __device__ __forceinline__ uint32_t place(uint32_t E) { return E - 113u; }   // (below 30: normal)
+    __device__ __forceinline__ void scale() { s1 = s1 * 0x04000400u - 112u * 0x04000400u; }
+    __device__ __forceinline__ void scale_any()
     {
         const uint32_t E = s1;
-        s1 = E * 0x04000400u - 112u * 0x04000400u;
-        two = !normal;
-        if (two) {
-            const int k = (int)E - 127;
-            s2 = 0x3C003C00u;
-            if (E == 255u) s1 = 0x7E007E00u;   // NaN
-            else if (k > 15) s1 = 0x78007800u, s2 = pow2_h(min(k - 15, 15)) * 0x00010001u;
-            else if (k < -24) s1 = 0x0C000C00u, s2 = k + 12 >= -24 ? pow2_h(k + 12) * 0x00010001u : 0u;
-            else s1 = pow2_h(k) * 0x00010001u;
-        }
+        const int k = (int)E - 127;
+        s2 = 0x3C003C00u;
+        if (E == 255u) s1 = 0x7E007E00u;   // NaN
+        else if (k > 15) s1 = 0x78007800u, s2 = pow2_h(min(k - 15, 15)) * 0x00010001u;
+        else if (k < -24) s1 = 0x0C000C00u, s2 = k + 12 >= -24 ? pow2_h(k + 12) * 0x00010001u : 0u;
+        else s1 = pow2_h(k) * 0x00010001u;
     }
     // A block behind the row's last one.
-    __device__ __forceinline__ void clear()
-    {
-        s1 = s2 = 0u;
-    }
+    __device__ __forceinline__ void clear() { s1 = s2 = 0u; }
+    template <bool ANY>
     __device__ __forceinline__ void pairs(int m, uint32_t (&hi)[4], uint32_t (&lo)[4]) const
     {
         if constexpr (FMT == RF_MXFP4) {
             e2m1x8(q[m], hi);
 #pragma unroll
             for (int k = 0; k < 4; ++k) hi[k] = hmul2(hi[k], s1);
-            if (two) {
+            if constexpr (ANY) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) hi[k] = hmul2(hi[k], s2);
             }
@@ -130,6 +124,7 @@ template <int L>
 struct Weights<RF_Q4_K, L> {
     Q4K b;
     __device__ __forceinline__ void clear() { b.ds = b.dm = 0.f; }
+    template <bool ANY>
     __device__ __forceinline__ void pairs(int m, uint32_t (&hi)[4], uint32_t (&lo)[4]) const
     {
         b.template pairs<L>(2 * m, hi[0], lo[0], hi[1], lo[1]);
@@ -236,24 +231,22 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
         const ChunkTile w = next;
         const int rt = at % p.nrt;
         const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * C::GB;
-        uint32_t off[2], mis[2];
+        // The row of half 1 lies 64 rows of a box behind half 0's: P divides 64.
         int64_t row[2];
         bool tail[2];
-        uint32_t start[2];   // (of the row)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t first = p.row0 + (int64_t)w.group * p.group_rows + (p.gated ? (int64_t)rt * 64 : (int64_t)rt * 128 + 64 * h);
-            row[h] = first + i;
-            const int j = (int)(row[h] & (p.P - 1));
-            const int s = (int)((row[h] >> p.logP) - ((first - j + p.P - 1) >> p.logP));
-            off[h] = (uint32_t)((h << p.logP) + j) * (uint32_t)((64 >> p.logP) * p.bw) + (uint32_t)(s * p.bw) + ((uint32_t)(j * p.rb) & 15u);
+            row[h] = p.row0 + (int64_t)w.group * p.group_rows + (p.gated ? (int64_t)rt * 64 : (int64_t)rt * 128 + 64 * h) + i;
             tail[h] = row[h] >= copied && row[h] < p.total_rows;
-            start[h] = off[h];
-            // This lane's first block, and the word in which it begins.
-            if constexpr (FMT != RF_Q4_K) off[h] += t * (C::SPREAD ? 4 : 2) * block_size(FMT);
-            mis[h] = off[h] & 3u;
-            off[h] -= mis[h];
         }
+        const int64_t first = row[0] - i;
+        const int j = (int)(row[0] & (p.P - 1));
+        const int s = (int)((row[0] >> p.logP) - ((first - j + p.P - 1) >> p.logP));
+        const uint32_t half = (uint32_t)(64 * p.bw);
+        const uint32_t start = (uint32_t)j * (uint32_t)((64 >> p.logP) * p.bw) + (uint32_t)(s * p.bw) + ((uint32_t)(j * p.rb) & 15u);
+        // This lane's first block (Q4_K: super-block), and the word in which it begins.
+        const uint32_t off = start + (FMT == RF_Q4_K ? 0 : t * (C::SPREAD ? 4 : 2) * block_size(FMT));
+        const uint32_t mis = off & 3u, word = off - mis;
         const bool tails = __any_sync(0xffffffffu, tail[0] || tail[1]);
         // Sums of (row g of half h, token 8 q + 2 t + e): [..][q][2 h + e].
         // One for each kind of product (chains of products are slow: a single
@@ -312,7 +305,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
         if (index + (int)gridDim.x < total) next = p.tiles[(index + (int)gridDim.x) / p.parts / p.nrt];
         for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); c < end; ++c) {
             if (!waits(bar(C::RFULL + r), rph)) return;
-            uint8_t *src = smem + r * C::RAW;
+            uint8_t *src = smem + r * C::RAW, *lane_src = src + word;
             if (tails) {
                 // Rows that the boxes do not reach, copied to where they would
                 // put them.
@@ -322,7 +315,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                         const uint8_t *from = p.W[p.gated ? h : 0] + row[h] * p.rb + (int64_t)c * C::CB;
                         const int n = (int)min((int64_t)C::CB, p.rb - (int64_t)c * C::CB);
 #pragma unroll 1
-                        for (int k = t; k < n; k += 4) src[start[h] + k] = __ldg(from + k);
+                        for (int k = t; k < n; k += 4) src[start + h * half + k] = __ldg(from + k);
                     }
                 __syncwarp();
             }
@@ -334,43 +327,51 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     Weights<FMT, C::LOW> wt[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if constexpr (FMT == RF_Q4_K) wt[h].b.load(src + off[h], t, e);
-                        else wt[h].load(src + off[h], mis[h], (2 * (C::SPREAD ? q4 / 4 : 0) + e) * block_size(FMT));
+                    if constexpr (FMT == RF_Q4_K) {
+                        wt[0].b.load(lane_src, t, e), wt[1].b.load(lane_src + half, t, e);
+                    } else {
+                        const uint32_t at = mis + (2 * (C::SPREAD ? q4 / 4 : 0) + e) * block_size(FMT);
+                        const uint8_t *from = lane_src + (at & ~3u);
+                        wt[0].load(from, 8u * (at & 3u)), wt[1].load(from + half, 8u * (at & 3u));
                     }
+                    bool any = false;
                     if constexpr (FMT == RF_MXFP4) {
-                        const bool normal = !__any_sync(0xffffffffu, wt[0].outside(wt[0].s1) || wt[1].outside(wt[1].s1));
-                        wt[0].scale(normal), wt[1].scale(normal);
+                        any = __any_sync(0xffffffffu, max(wt[0].place(wt[0].s1), wt[1].place(wt[1].s1)) >= 30u);
+                        if (any) wt[0].scale_any(), wt[1].scale_any();
+                        else wt[0].scale(), wt[1].scale();
                     }
                     if (ragged) {
                         const bool dead = 2 * (c * QPC + sl) + e >= p.nb;   // the bytes are the next row's
                         if (dead) wt[0].clear(), wt[1].clear();
                     }
+                    auto multiply = [&](auto any_scale) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        uint32_t hi[2][4], lo[2][4];
+                        for (int m = 0; m < 4; ++m) {
+                            uint32_t hi[2][4], lo[2][4];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) wt[h].pairs(m, hi[h], lo[h]);
+                            for (int h = 0; h < 2; ++h) wt[h].template pairs<decltype(any_scale)::value>(m, hi[h], lo[h]);
 #pragma unroll
-                        for (int q = 0; q < NJ; ++q) {
-                            if (8 * q >= w.cnt) break;
-                            // XT 1: granules of two tiles of eight; 2: of one, its low terms behind it.
-                            const uint8_t *xm = x + (XT == 2 ? 2 * q : q) * 1024 + (4 * e + m) * 128;
-                            const uint4 v = *reinterpret_cast<const uint4 *>(xm);
-                            mma16816(acc[0][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], v.x, v.y);
-                            mma16816(acc[C::N == 1 ? 1 : 0][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], v.z, v.w);
-                            if constexpr (XT == 2 && !C::BOTH) {
-                                const uint4 l = *reinterpret_cast<const uint4 *>(xm + 1024);
-                                mma16816(acc[1][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], l.x, l.y);
-                                mma16816(acc[1][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], l.z, l.w);
-                            }
-                            if constexpr (WT == 2) {
-                                mma16816(acc[C::N - 1][q], lo[0][0], lo[1][0], lo[0][1], lo[1][1], v.x, v.y);
-                                mma16816(acc[C::N - 1][q], lo[0][2], lo[1][2], lo[0][3], lo[1][3], v.z, v.w);
+                            for (int q = 0; q < NJ; ++q) {
+                                if (NJ > 1 && 8 * q >= w.cnt) break;
+                                // XT 1: granules of two tiles of eight; 2: of one, its low terms behind it.
+                                const uint8_t *xm = x + (XT == 2 ? 2 * q : q) * 1024 + (4 * e + m) * 128;
+                                const uint4 v = *reinterpret_cast<const uint4 *>(xm);
+                                mma16816(acc[0][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], v.x, v.y);
+                                mma16816(acc[C::N == 1 ? 1 : 0][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], v.z, v.w);
+                                if constexpr (XT == 2 && !C::BOTH) {
+                                    const uint4 l = *reinterpret_cast<const uint4 *>(xm + 1024);
+                                    mma16816(acc[1][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], l.x, l.y);
+                                    mma16816(acc[1][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], l.z, l.w);
+                                }
+                                if constexpr (WT == 2) {
+                                    mma16816(acc[C::N - 1][q], lo[0][0], lo[1][0], lo[0][1], lo[1][1], v.x, v.y);
+                                    mma16816(acc[C::N - 1][q], lo[0][2], lo[1][2], lo[0][3], lo[1][3], v.z, v.w);
+                                }
                             }
                         }
-                    }
+                    };
+                    if (FMT == RF_MXFP4 && any) multiply(std::true_type());
+                    else multiply(std::false_type());
                     if constexpr (XT == 2) {
                         if (e == 1 || FMT == RF_Q4_K) flush();
                     }
@@ -441,13 +442,9 @@ template <int FMT, int NG>
 rf_status launch_terms(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
 {
     if (sh.xt == 2) return launch<FMT, NG, 2, FMT == RF_MXFP4 ? 1 : 2>(p, grid, s);
-    if constexpr (NG > 0) {
-        if constexpr (FMT != RF_MXFP4)
-            if (sh.wt == 2) return launch<FMT, NG, 1, 2>(p, grid, s);
-        return launch<FMT, NG, 1, 1>(p, grid, s);
-    } else {
-        return RF_ERR_INVALID_ARG;   // (tiles of four tokens have two terms)
-    }
+    if constexpr (FMT != RF_MXFP4)
+        if (sh.wt == 2) return launch<FMT, NG, 1, 2>(p, grid, s);
+    return launch<FMT, NG, 1, 1>(p, grid, s);
 }
 template <int FMT>
 rf_status launch_fmt(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
