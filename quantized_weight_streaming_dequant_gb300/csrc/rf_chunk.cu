@@ -369,7 +369,7 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     // Operand rows of a group: twice the average, so that most groups have one tile.
     const int64_t each = n_group == 1 ? sh.xt * n_row : 2 * sh.xt * ((n_row + n_group - 1) / n_group);
     sh.nt = each <= 8 ? 8 : each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : sh.wt == 1 && sh.xt == 1 && each > 256 ? 192 : 128;
-    sh.few = sh.nt <= 32;
+    sh.few = sh.nt <= 16;
     const int per = chunk_weights(fmt) / kSliceK;
     if (sh.few) sh.nst = (sh.nst + per - 1) / per * per;
     const int64_t T = sh.tile_tokens(), GT = sh.gran_tokens();

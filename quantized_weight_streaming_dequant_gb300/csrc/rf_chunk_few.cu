@@ -1,13 +1,13 @@
 // rf_chunk_few.cu -- products of the chunk operators where a group has few
 // tokens: the same items, images and results as rf_chunk_mma.cu's, for token
-// tiles of up to 32 operand rows.
+// tiles of up to 16 operand rows.
 //
 // There a decoded slice passes through tensor memory, with a barrier before and
 // one behind it, and a tile of few tokens waits for those more than for its
 // products.  Here a warp decodes 16 rows straight into the fragments of
 // mma.sync.m16n8k16 and multiplies them itself: nothing stands between a
 // weight's bytes and its product but registers.  A decoded weight is used for
-// at most 16 tokens, so the tensor cores' rate hardly matters.
+// at most 16 tokens, so the tensor cores' rate matters less.
 //
 // A CTA (two per SM) draws items of 128 matrix rows (64 of W and 64 of U with a
 // gated activation) of a token tile.  One warp copies raw chunks and the
@@ -31,15 +31,14 @@ __device__ int g_few_status = 0;   // bounded waits that gave up
 
 constexpr int kWarps = 8;          // that multiply; one more copies
 
-// NG: granules of operand rows per token tile (0: half a one, eight tokens or
-// four of two terms, one tile of eight columns); XT, WT: fp16 terms per
-// activation, weight.
-template <int FMT, int NG, int XT, int WT>
+// NT: operand rows per token tile, 8 (of two terms: four tokens, whose terms are
+// columns of one product) or 16; XT, WT: fp16 terms per activation, weight.
+template <int FMT, int NT, int XT, int WT>
 struct Few {
     static constexpr int CB = chunk_bytes(FMT), QPC = chunk_weights(FMT) / kSliceK;
-    static constexpr bool BOTH = NG == 0 && XT == 2;                     // a column of either term
-    static constexpr int GR = NG == 0 ? kGranRows / 2 : kGranRows, GT = GR / XT, GB = GR * kSliceK * 2;   // a granule
-    static constexpr int T = (NG == 0 ? 1 : NG) * GT, NJ = (T + 7) / 8;  // tokens, and tiles of eight of them
+    static constexpr bool BOTH = NT == 8 && XT == 2;                     // a column of either term
+    static constexpr int T = NT / XT, NJ = (T + 7) / 8;                  // tokens, and tiles of eight of them
+    static constexpr int GB = NT * kSliceK * 2;                          // operand bytes of a slice
     // MXFP4: a four of slices are every other one of a chunk (see Weights).
     static constexpr bool SPREAD = FMT == RF_MXFP4;
     static constexpr int N = BOTH ? WT : XT + WT - 1;                    // kinds of products
@@ -48,7 +47,7 @@ struct Few {
     // Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.
     static constexpr int SHARED = 115200;
     static constexpr int RAW = kM * box_bytes(FMT, 8);
-    static constexpr int QB = (NG == 0 ? 1 : NG) * 4 * GB;                   // operand bytes of four slices
+    static constexpr int QB = 4 * GB;                                    // operand bytes of four slices
     static constexpr int RS = (SHARED - 2 * QB) / RAW < 4 ? (SHARED - 2 * QB) / RAW : 4;   // raw chunks
     static constexpr int BS = (SHARED - RS * RAW) / QB < 4 ? (SHARED - RS * RAW) / QB : 4; // fours of slices
     static constexpr int SMEM = RS * RAW + BS * QB;
@@ -132,10 +131,10 @@ struct Weights<RF_Q4_K, L> {
     }
 };
 
-template <int FMT, int NG, int XT, int WT>
+template <int FMT, int NT, int XT, int WT>
 __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_constant__ Params p)
 {
-    using C = Few<FMT, NG, XT, WT>;
+    using C = Few<FMT, NT, XT, WT>;
     constexpr int NJ = C::NJ, QPC = C::QPC;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ops = smem + C::RS * C::RAW;
@@ -183,8 +182,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             const int64_t first = p.row0 + (int64_t)w.group * p.group_rows +
                                   (p.gated ? (int64_t)rt * 64 : (int64_t)rt * 128 + 64 * half);
             const int y = (int)((first - j + p.P - 1) >> p.logP);   // first super-row with position j in the tile
-            const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * C::GB;
-            const uint8_t *src = p.img + (int64_t)w.gran * p.nst * C::GB + (int64_t)(part * p.part_chunks * QPC) * slice;
+            const uint8_t *src = p.img + ((int64_t)w.gran * p.nst + part * p.part_chunks * QPC) * C::GB;
             for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); ok && c < end; ++c) {
                 if (!(ok = waits(bar(C::REMPTY + r), rph))) break;
                 if (lane == 0) {
@@ -201,11 +199,11 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                         if (blockIdx.x == 0 && bc == 0 && p.withhold >= 0) {
                             skipped = bc;
                         } else {
-                            bar_expect(bar(C::BFULL + b), 4 * slice);
-                            copy_bulk(dst_ops + b * C::QB, src, 4 * slice, bar(C::BFULL + b));
+                            bar_expect(bar(C::BFULL + b), C::QB);
+                            copy_bulk(dst_ops + b * C::QB, src, C::QB, bar(C::BFULL + b));
                         }
                     }
-                    src += 4 * slice;
+                    src += C::QB;
                     ++bc;
                     if (++b == C::BS) b = 0, bph ^= 1u;
                 }
@@ -230,7 +228,6 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
         const int at = index / p.parts, part = index % p.parts;
         const ChunkTile w = next;
         const int rt = at % p.nrt;
-        const uint32_t slice = (uint32_t)((w.cnt + C::GT - 1) / C::GT) * C::GB;
         // The row of half 1 lies 64 rows of a box behind half 0's: P divides 64.
         int64_t row[2];
         bool tail[2];
@@ -301,7 +298,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
 #pragma unroll
         for (int q = 0; q < NJ; ++q)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) inv[q][e] = __ldg(p.inv + (int64_t)w.gran * C::GT + min(8 * q + 2 * t + e, w.cnt - 1));
+            for (int e = 0; e < 2; ++e) inv[q][e] = __ldg(p.inv + (int64_t)w.gran * C::T + min(8 * q + 2 * t + e, w.cnt - 1));
         if (index + (int)gridDim.x < total) next = p.tiles[(index + (int)gridDim.x) / p.parts / p.nrt];
         for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); c < end; ++c) {
             if (!waits(bar(C::RFULL + r), rph)) return;
@@ -322,7 +319,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             for (int q4 = 0; q4 < QPC; q4 += 4) {
                 if (!waits(bar(C::BFULL + b), bph)) return;
                 const int sl = C::SPREAD ? 2 * t + q4 / 4 : q4 + t;   // slice of the chunk
-                const uint8_t *x = ops + b * C::QB + t * slice + swz;
+                const uint8_t *x = ops + b * C::QB + t * C::GB + swz;
                 const bool ragged = FMT != RF_Q4_K && 2 * (c + 1) * QPC > p.nb;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -353,8 +350,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
 #pragma unroll
                             for (int q = 0; q < NJ; ++q) {
                                 if (NJ > 1 && 8 * q >= w.cnt) break;
-                                // XT 1: granules of two tiles of eight; 2: of one, its low terms behind it.
-                                const uint8_t *xm = x + (XT == 2 ? 2 * q : q) * 1024 + (4 * e + m) * 128;
+                                // (Of two terms the low ones' eight rows are behind the high ones'.)
+                                const uint8_t *xm = x + q * 1024 + (4 * e + m) * 128;
                                 const uint4 v = *reinterpret_cast<const uint4 *>(xm);
                                 mma16816(acc[0][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], v.x, v.y);
                                 mma16816(acc[C::N == 1 ? 1 : 0][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], v.z, v.w);
@@ -417,10 +414,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
     }
 }
 
-template <int FMT, int NG, int XT, int WT>
+template <int FMT, int NT, int XT, int WT>
 rf_status launch(const Params &p, int grid, cudaStream_t s)
 {
-    using C = Few<FMT, NG, XT, WT>;
+    using C = Few<FMT, NT, XT, WT>;
     static std::once_flag once[64];
     static bool ok[64];
     int dev = 0;
@@ -429,28 +426,27 @@ rf_status launch(const Params &p, int grid, cudaStream_t s)
         return RF_ERR_CUDA;
     }
     std::call_once(once[dev & 63], [dev] {
-        ok[dev & 63] = cudaFuncSetAttribute(few_kernel<FMT, NG, XT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
+        ok[dev & 63] = cudaFuncSetAttribute(few_kernel<FMT, NT, XT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
                        cudaSuccess;
         cudaGetLastError();
     });
     if (!ok[dev & 63]) return RF_ERR_CUDA;
-    few_kernel<FMT, NG, XT, WT><<<grid, 32 * (kWarps + 1), C::SMEM, s>>>(p);
+    few_kernel<FMT, NT, XT, WT><<<grid, 32 * (kWarps + 1), C::SMEM, s>>>(p);
     return last_cuda_error();
 }
 
-template <int FMT, int NG>
+template <int FMT, int NT>
 rf_status launch_terms(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
 {
-    if (sh.xt == 2) return launch<FMT, NG, 2, FMT == RF_MXFP4 ? 1 : 2>(p, grid, s);
+    if (sh.xt == 2) return launch<FMT, NT, 2, FMT == RF_MXFP4 ? 1 : 2>(p, grid, s);
     if constexpr (FMT != RF_MXFP4)
-        if (sh.wt == 2) return launch<FMT, NG, 1, 2>(p, grid, s);
-    return launch<FMT, NG, 1, 1>(p, grid, s);
+        if (sh.wt == 2) return launch<FMT, NT, 1, 2>(p, grid, s);
+    return launch<FMT, NT, 1, 1>(p, grid, s);
 }
 template <int FMT>
 rf_status launch_fmt(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
 {
-    if (sh.nt < kGranRows) return launch_terms<FMT, 0>(sh, p, grid, s);
-    return sh.nt > kGranRows ? launch_terms<FMT, 2>(sh, p, grid, s) : launch_terms<FMT, 1>(sh, p, grid, s);
+    return sh.nt > 8 ? launch_terms<FMT, 16>(sh, p, grid, s) : launch_terms<FMT, 8>(sh, p, grid, s);
 }
 
 }  // namespace
