@@ -84,18 +84,21 @@ struct Weights {
         if constexpr (FMT != RF_MXFP4) s1 *= 0x00010001u;
     }
     // MXFP4: the factor 2^k, k = E - 127, where fp16 has it as a normal number;
-    // anywhere, in two.
+    // anywhere (ANY), in two.
     static __device__ __forceinline__ uint32_t place(uint32_t E) { return E - 113u; }   // (below 30: normal)
-    __device__ __forceinline__ void scale() { s1 = s1 * 0x04000400u - 112u * 0x04000400u; }
-    __device__ __forceinline__ void scale_any()
+    template <bool ANY>
+    __device__ __forceinline__ void scale()
     {
         const uint32_t E = s1;
-        const int k = (int)E - 127;
-        s2 = 0x3C003C00u;
-        if (E == 255u) s1 = 0x7E007E00u;   // NaN
-        else if (k > 15) s1 = 0x78007800u, s2 = pow2_h(min(k - 15, 15)) * 0x00010001u;
-        else if (k < -24) s1 = 0x0C000C00u, s2 = k + 12 >= -24 ? pow2_h(k + 12) * 0x00010001u : 0u;
-        else s1 = pow2_h(k) * 0x00010001u;
+        s1 = E * 0x04000400u - 112u * 0x04000400u;
+        if constexpr (ANY) {
+            const int k = (int)E - 127;
+            s2 = 0x3C003C00u;
+            if (E == 255u) s1 = 0x7E007E00u;   // NaN
+            else if (k > 15) s1 = 0x78007800u, s2 = pow2_h(min(k - 15, 15)) * 0x00010001u;
+            else if (k < -24) s1 = 0x0C000C00u, s2 = k + 12 >= -24 ? pow2_h(k + 12) * 0x00010001u : 0u;
+            else s1 = pow2_h(k) * 0x00010001u;
+        }
     }
     // A block behind the row's last one.
     __device__ __forceinline__ void clear() { s1 = s2 = 0u; }
@@ -245,36 +248,32 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
         const uint32_t off = start + (FMT == RF_Q4_K ? 0 : t * (C::SPREAD ? 4 : 2) * block_size(FMT));
         const uint32_t mis = off & 3u, word = off - mis;
         const bool tails = __any_sync(0xffffffffu, tail[0] || tail[1]);
-        // Sums of (row g of half h, token 8 q + 2 t + e): [..][q][2 h + e].
-        // One for each kind of product (chains of products are slow: a single
-        // kind has two).  fp32: rounded additions move them to `sum` every four
-        // slices (Q4_K: two), because the tensor cores truncate each of theirs.
-        float acc[C::N == 1 ? 2 : C::N][NJ][4], sum[NJ][4];
+        // Sums of (row g of half h, token 8 q + 2 t + e): [..][q][2 h + e], for
+        // each kind of product.  fp32: rounded additions move them to
+        // `sum` every four slices (Q4_K: two), because the tensor cores truncate
+        // each of theirs.
+        float acc[C::N][NJ][4], sum[NJ][4];
         auto flush = [&] {
 #pragma unroll
             for (int q = 0; q < NJ; ++q)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if constexpr (XT == 2) {
-                        // By terms of (weight, activation): high high, high low, low high.
-                        float high = acc[0][q][k], low = acc[1][q][k];
-                        if constexpr (C::BOTH) {
-                            // (The column says which of the activation's.)
-                            if constexpr (WT == 1) high += low;
-                            else high = C::LOW == kScaled ? fmaf(low, 1.f / 2048.f, high) : high + low;
-                            sum[q][k] += high;
-                        } else {
-                            if constexpr (C::LOW == kScaled) low += acc[2][q][k];
-                            if constexpr (C::LOW == kPlain) high += acc[2][q][k];
-                            sum[q][k] += fmaf(low, 1.f / 2048.f, high);
-                        }
-                    } else {
-                        sum[q][k] = acc[0][q][k] + acc[1][q][k];
-                    }
-                    if constexpr (XT == 2) {
+                    // By terms of (weight, activation): high high, high low, low high.
+                    float f[C::N];
 #pragma unroll
-                        for (int n = 0; n < (C::N == 1 ? 2 : C::N); ++n) acc[n][q][k] = 0.f;
+                    for (int n = 0; n < C::N; ++n) f[n] = acc[n][q][k];
+                    const float scaled = 1.f / 2048.f;
+                    if constexpr (C::BOTH) {   // (the column says which of the activation's)
+                        if constexpr (WT == 2) f[0] = C::LOW == kScaled ? fmaf(f[1], scaled, f[0]) : f[0] + f[1];
+                    } else if constexpr (XT == 2) {
+                        if constexpr (WT == 2) f[C::LOW == kScaled ? 1 : 0] += f[2];
+                        f[0] = fmaf(f[1], scaled, f[0]);
+                    } else if constexpr (WT == 2) {
+                        f[0] += f[1];
                     }
+                    sum[q][k] += f[0];
+#pragma unroll
+                    for (int n = 0; n < C::N; ++n) acc[n][q][k] = 0.f;
                 }
         };
 #pragma unroll
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             for (int k = 0; k < 4; ++k) {
                 sum[q][k] = 0.f;
 #pragma unroll
-                for (int n = 0; n < (C::N == 1 ? 2 : C::N); ++n) acc[n][q][k] = 0.f;
+                for (int n = 0; n < C::N; ++n) acc[n][q][k] = 0.f;
             }
         // What the end of the item needs, asked for early.
         float bias[2];
@@ -316,11 +315,23 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                     }
                 __syncwarp();
             }
-            for (int q4 = 0; q4 < QPC; q4 += 4) {
-                if (!waits(bar(C::BFULL + b), bph)) return;
-                const int sl = C::SPREAD ? 2 * t + q4 / 4 : q4 + t;   // slice of the chunk
+            // Whether a scale of the warp's blocks is none of fp16's normal numbers.
+            bool any = false;
+            if constexpr (FMT == RF_MXFP4) {
+                uint32_t place = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        place = max(place, Weights<FMT, C::LOW>::place(src[start + h * half + (4 * t + k) * block_size(FMT)]));
+                any = __any_sync(0xffffffffu, place >= 30u);
+            }
+            const bool ragged = FMT != RF_Q4_K && 2 * (c + 1) * QPC > p.nb;
+            // Four slices.
+            auto four = [&](int q4, auto any_scale) -> bool {
+                constexpr bool ANY = decltype(any_scale)::value;
+                if (!waits(bar(C::BFULL + b), bph)) return false;
                 const uint8_t *x = ops + b * C::QB + t * C::GB + swz;
-                const bool ragged = FMT != RF_Q4_K && 2 * (c + 1) * QPC > p.nb;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     Weights<FMT, C::LOW> wt[2];
@@ -331,44 +342,37 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                         const uint8_t *from = lane_src + (at & ~3u);
                         wt[0].load(from, 8u * (at & 3u)), wt[1].load(from + half, 8u * (at & 3u));
                     }
-                    bool any = false;
-                    if constexpr (FMT == RF_MXFP4) {
-                        any = __any_sync(0xffffffffu, max(wt[0].place(wt[0].s1), wt[1].place(wt[1].s1)) >= 30u);
-                        if (any) wt[0].scale_any(), wt[1].scale_any();
-                        else wt[0].scale(), wt[1].scale();
-                    }
+                    if constexpr (FMT == RF_MXFP4) wt[0].template scale<ANY>(), wt[1].template scale<ANY>();
                     if (ragged) {
-                        const bool dead = 2 * (c * QPC + sl) + e >= p.nb;   // the bytes are the next row's
+                        const int sl = C::SPREAD ? 2 * t + q4 / 4 : q4 + t;   // slice of the chunk
+                        const bool dead = 2 * (c * QPC + sl) + e >= p.nb;     // the bytes are the next row's
                         if (dead) wt[0].clear(), wt[1].clear();
                     }
-                    auto multiply = [&](auto any_scale) {
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            uint32_t hi[2][4], lo[2][4];
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t hi[2][4], lo[2][4];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) wt[h].template pairs<decltype(any_scale)::value>(m, hi[h], lo[h]);
+                        for (int h = 0; h < 2; ++h) wt[h].template pairs<ANY>(m, hi[h], lo[h]);
 #pragma unroll
-                            for (int q = 0; q < NJ; ++q) {
-                                if (NJ > 1 && 8 * q >= w.cnt) break;
-                                // (Of two terms the low ones' eight rows are behind the high ones'.)
-                                const uint8_t *xm = x + q * 1024 + (4 * e + m) * 128;
-                                const uint4 v = *reinterpret_cast<const uint4 *>(xm);
-                                mma16816(acc[0][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], v.x, v.y);
-                                mma16816(acc[C::N == 1 ? 1 : 0][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], v.z, v.w);
-                                if constexpr (XT == 2 && !C::BOTH) {
-                                    const uint4 l = *reinterpret_cast<const uint4 *>(xm + 1024);
-                                    mma16816(acc[1][q], hi[0][0], hi[1][0], hi[0][1], hi[1][1], l.x, l.y);
-                                    mma16816(acc[1][q], hi[0][2], hi[1][2], hi[0][3], hi[1][3], l.z, l.w);
-                                }
-                                if constexpr (WT == 2) {
-                                    mma16816(acc[C::N - 1][q], lo[0][0], lo[1][0], lo[0][1], lo[1][1], v.x, v.y);
-                                    mma16816(acc[C::N - 1][q], lo[0][2], lo[1][2], lo[0][3], lo[1][3], v.z, v.w);
-                                }
+                        for (int q = 0; q < NJ; ++q) {
+                            if (NJ > 1 && 8 * q >= w.cnt) break;
+                            // (Of two terms the low ones' eight rows are behind the high ones'.)
+                            const uint8_t *xm = x + q * 1024 + (4 * e + m) * 128;
+                            const uint4 v = *reinterpret_cast<const uint4 *>(xm);
+                            [[maybe_unused]] uint4 l = {};
+                            if constexpr (XT == 2 && !C::BOTH) l = *reinterpret_cast<const uint4 *>(xm + 1024);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t b0 = k ? v.z : v.x, b1 = k ? v.w : v.y;
+                                mma16816(acc[0][q], hi[0][2 * k], hi[1][2 * k], hi[0][2 * k + 1], hi[1][2 * k + 1], b0, b1);
+                                if constexpr (XT == 2 && !C::BOTH)
+                                    mma16816(acc[1][q], hi[0][2 * k], hi[1][2 * k], hi[0][2 * k + 1], hi[1][2 * k + 1],
+                                             k ? l.z : l.x, k ? l.w : l.y);
+                                if constexpr (WT == 2)
+                                    mma16816(acc[C::N - 1][q], lo[0][2 * k], lo[1][2 * k], lo[0][2 * k + 1], lo[1][2 * k + 1], b0, b1);
                             }
                         }
-                    };
-                    if (FMT == RF_MXFP4 && any) multiply(std::true_type());
-                    else multiply(std::false_type());
+                    }
                     if constexpr (XT == 2) {
                         if (e == 1 || FMT == RF_Q4_K) flush();
                     }
@@ -376,6 +380,16 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(C::BEMPTY + b));
                 if (++b == C::BS) b = 0, bph ^= 1u;
+                return true;
+            };
+            if (FMT == RF_MXFP4 && any) {
+#pragma unroll 1
+                for (int q4 = 0; q4 < QPC; q4 += 4)
+                    if (!four(q4, std::true_type())) return;
+            } else {
+#pragma unroll
+                for (int q4 = 0; q4 < QPC; q4 += 4)
+                    if (!four(q4, std::false_type())) return;
             }
             if (tails) fence_async_smem();   // the next copy follows these stores
             __syncwarp();
