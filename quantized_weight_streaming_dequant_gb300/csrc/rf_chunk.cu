@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "rf_chunk.h"
 #include "rf_device.cuh"
@@ -65,6 +66,56 @@ __device__ __forceinline__ void load4(const T *x, bool vec, float (&f)[4])
     for (int e = 0; e < 4; ++e) f[e] = to_f32(t[e]);
 }
 
+// N consecutive elements' bits (vec: aligned to them all, or to 16 bytes).
+template <class T, int N> struct Some { uint32_t w[N * sizeof(T) / 4]; };
+template <class T, int N>
+__device__ __forceinline__ void load(const T *x, bool vec, Some<T, N> &v)
+{
+    constexpr int W = N * sizeof(T) / 4;
+    static_assert(W == 2 || W == 4, "8 or 16 bytes");
+    if (vec) {
+        if constexpr (W == 4) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(x);
+            v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2 *>(x);
+            v.w[0] = q.x, v.w[1] = q.y;
+        }
+    } else {
+        T t[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) t[e] = x[e];
+        memcpy(v.w, t, sizeof(t));
+    }
+}
+template <class T, int N>
+__device__ __forceinline__ float element(const Some<T, N> &v, int e)
+{
+    if constexpr (sizeof(T) == 4) return __uint_as_float(v.w[e]);
+    else if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)(v.w[e / 2] >> (e & 1) * 16)));
+    else return __uint_as_float(e & 1 ? v.w[e / 2] & 0xFFFF0000u : v.w[e / 2] << 16);
+}
+// The larger magnitudes of m and of all words (of halfword pairs: of either),
+// as bits; and the largest of those as a value.
+template <class T, int N>
+__device__ __forceinline__ uint32_t larger(uint32_t m, const Some<T, N> &v)
+{
+#pragma unroll
+    for (uint32_t w : v.w) {
+        if constexpr (sizeof(T) == 4) m = max(m, w & 0x7FFFFFFFu);
+        else m = __vmaxu2(m, w & 0x7FFF7FFFu);
+    }
+    return m;
+}
+template <class T>
+__device__ __forceinline__ float largest(uint32_t m)
+{
+    if constexpr (sizeof(T) == 4) return __uint_as_float(m);
+    const uint32_t h = max(m & 0xFFFFu, m >> 16);
+    if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)h));
+    return __uint_as_float(h << 16);
+}
+
 struct PrepParams {
     const void *X;
     int64_t ldx, n_x;
@@ -72,7 +123,7 @@ struct PrepParams {
     const int32_t *order;
     int32_t per, n_row, n_group;
     int32_t in_dim, nst, order8;   // order8: which inputs a 16-byte unit holds
-    int32_t gran_tokens, tile_tokens, cap_tiles, cap_gran, parts, vec, few, spread;
+    int32_t gran_tokens, tile_tokens, cap_tiles, cap_gran, parts, by_row, vec, few, spread;
     ChunkPlan *plan;
     ChunkTile *tiles;
     float *inv;               // by place in the granules
@@ -155,7 +206,8 @@ __device__ __forceinline__ void slice_order(int order, const float (&a)[4], cons
     }
 }
 
-template <int DT, int XT>
+// FOURS: fours of slices of a row in flight.
+template <int DT, int XT, int FOURS>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ PrepParams p)
 {
     using T = typename Elem<DT>::T;
@@ -164,113 +216,146 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         list_tiles(p);
         return;
     }
-    const int part = blockIdx.x % p.parts, gran = blockIdx.x / p.parts / H, sub = blockIdx.x / p.parts % H;
+    // A CTA's place: a share of a granule; or a row, if it is the first of one
+    // (rows fewer than the granules that there might be).
+    const int part = blockIdx.x % p.parts, place_of = blockIdx.x / p.parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ int s_group, s_row, s_cnt, s_n, s_at;
-    __shared__ float s_scale[kPrepRows];
-    __shared__ int64_t s_src[kPrepRows];
+    __shared__ int s_group, s_row, s_cnt, s_n, s_at, s_gran, s_sub;
     if (tid == 0) s_group = -1;
     __syncthreads();
     for (int g = tid; g < p.n_group; g += kPrepThreads) {
         int a, b;
         if (!group_rows(p, g, a, b)) continue;
-        const int q = gran - (a / GT + g);
-        if (q < 0 || q >= (b - a + GT - 1) / GT) continue;
+        int row = place_of, q;
+        if (p.by_row) {
+            q = (row - a) / GT;
+            if (row < a || row >= b || (row - a) % min(GT, kPrepRows) != 0) continue;
+        } else {
+            q = place_of / H - (a / GT + g);
+            if (q < 0 || q >= (b - a + GT - 1) / GT) continue;
+            row = a + q * GT + place_of % H * kPrepRows;
+        }
         const int tt = p.tile_tokens / GT;   // granules per whole tile
         s_group = g;
-        s_row = a + q * GT + sub * kPrepRows;
-        s_cnt = min(min(kPrepRows, GT), b - s_row);
-        s_at = gran - q + q / tt * tt;       // the tile's first granule
+        s_gran = a / GT + g + q;
+        s_row = row;
+        s_cnt = min(min(kPrepRows, GT), b - row);
+        s_at = s_gran - q + q / tt * tt;     // the tile's first granule
         s_n = min(tt, (b - a - q / tt * p.tile_tokens + GT - 1) / GT);
+        s_sub = (row - a) % GT / kPrepRows;
     }
     __syncthreads();
     if (s_group < 0) return;
-    // Scales: a warp per row.
-    {
-        static_assert(kPrepRows == kPrepThreads / 32, "a warp per row");
-        int64_t src = -1;
-        if (warp < s_cnt) {
-            const int row = s_row + warp;
-            src = p.order ? p.order[row] / p.per : row;
-            if (p.order && (p.order[row] < 0 || src >= p.n_x)) {
-                src = -1;
-                if (lane == 0) record_status(&g_chunk_invalid, RF_ERR_INVALID_ARG);
-            }
-        }
-        float m = 0.f;
-        if (src >= 0) {
-            const T *x = static_cast<const T *>(p.X) + src * p.ldx;
-#pragma unroll 8
-            for (int k = 4 * lane; k < p.in_dim; k += 128) {
-                float f[4];
-                load4(x + k, p.vec, f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = fabsf(f[e]);
-                    if (v < INFINITY) m = fmaxf(m, v);
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // The largest value to [2^14, 2^15), by a factor within fp32's normal
-        // numbers (so is its inverse).
-        const int e = (int)(__float_as_uint(m) >> 23) - 127;
-        const int k = m == 0.f ? 0 : max(-126, min(126, 14 - e));
-        if (lane == 0) {
-            s_scale[warp] = __uint_as_float((uint32_t)(k + 127) << 23);
-            s_src[warp] = src;
-            if (part == 0 && warp < GT) p.inv[(int64_t)gran * GT + sub * kPrepRows + warp] = __uint_as_float((uint32_t)(127 - k) << 23);
+    const int gran = s_gran, sub = s_sub;
+    // A warp takes a row: its largest value, hence its scale, then its inputs.
+    static_assert(kPrepRows == kPrepThreads / 32, "a warp per row");
+    int64_t src = -1;
+    if (warp < s_cnt) {
+        const int row = s_row + warp;
+        src = p.order ? p.order[row] / p.per : row;
+        if (p.order && (p.order[row] < 0 || src >= p.n_x)) {
+            src = -1;
+            if (lane == 0) record_status(&g_chunk_invalid, RF_ERR_INVALID_ARG);
         }
     }
-    __syncthreads();
-    // Units: thread (r, c) writes inputs 8c.. of a slice of row r (its high
-    // and its low term), kPrepThreads / 64 slices at a time.
-    constexpr int kStep = kPrepThreads / (8 * kPrepRows);
-    const int r = tid & 7, c = (tid >> 3) & 7;
-    if (r >= GT) return;
-    const float scale = s_scale[r];
-    const int64_t src = s_src[r];
     const T *x = static_cast<const T *>(p.X) + (src >= 0 ? src * p.ldx : 0);
-    const int first = c >> 2, u = c & 3;
-    const int ka = 32 * first + (p.order8 == kOrderPlain ? 8 * u : 4 * u);
-    const int kb = ka + (p.order8 == kOrderPlain ? 4 : 16);
-    const int bytes = GT * XT * kSliceK * 2;
-    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * bytes + sub * 1024 + c * 128;
-    const int64_t step = (int64_t)s_n * bytes;
-#pragma unroll 4
-    for (int s = part * kStep + (tid >> 6); s < p.nst; s += p.parts * kStep) {
-        float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f}, f[8];
-        const int k0 = s * kSliceK;
-        if (src >= 0 && k0 + 32 * first < p.in_dim) {   // (whole blocks)
-            load4(x + k0 + ka, p.vec, a);
-            load4(x + k0 + kb, p.vec, b);
+    float m = 0.f;
+    if (src >= 0) {
+        constexpr int E = 16 / sizeof(T);
+        uint32_t bits = 0;
+#pragma unroll 8
+        for (int k = E * lane; k < p.in_dim; k += 32 * E) {
+            Some<T, E> v;
+            load(x + k, p.vec, v);
+            bits = larger(bits, v);
         }
-        slice_order(p.order8, a, b, f);
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float f0 = f[2 * e] * scale, f1 = f[2 * e + 1] * scale;
-            const __half2 v = __floats2half2_rn(f0, f1);
-            h[e] = h2_bits(v);
-            if constexpr (XT == 2) {
-                const float2 w = __half22float2(v);
-                l[e] = h2_bits(__floats2half2_rn(fabsf(w.x) < INFINITY ? (f0 - w.x) * 2048.f : 0.f,
-                                                 fabsf(w.y) < INFINITY ? (f1 - w.y) * 2048.f : 0.f));
+        m = largest<T>(bits);
+        if (!(m < INFINITY)) {   // what is not finite does not count
+            m = 0.f;
+            for (int k = lane; k < p.in_dim; k += 32) {
+                const float f = fabsf((float)x[k]);
+                if (f < INFINITY) m = fmaxf(m, f);
             }
         }
-        // Few tokens' kernel reads a row's units of four slices at once (of
-        // MXFP4, every other one of eight): they lie one after the other, each
-        // slice's turned in its 128 bytes, for the banks.
-        const int at = p.spread ? (s & ~7) | (s & 1) << 2 | (s >> 1 & 3) : s;
-        // (The low terms' rows follow the high ones'.)
-        const int turn = p.few ? 2 * (at & 3) : 0;
-        uint8_t *to = out + at * step;
-        *reinterpret_cast<uint4 *>(to + (r ^ turn) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-        if constexpr (XT == 2) {
-            to += GT == kPrepRows ? 1024 + (r ^ turn) * 16 : ((GT + r) ^ turn) * 16;
-            *reinterpret_cast<uint4 *>(to) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // The largest value to [2^14, 2^15), by a factor within fp32's normal
+    // numbers (so is its inverse).
+    const int exponent = (int)(__float_as_uint(m) >> 23) - 127;
+    const int k2 = m == 0.f ? 0 : max(-126, min(126, 14 - exponent));
+    const float scale = __uint_as_float((uint32_t)(k2 + 127) << 23);
+    if (part == 0 && lane == 0 && warp < GT)
+        p.inv[(int64_t)gran * GT + sub * kPrepRows + warp] = __uint_as_float((uint32_t)(127 - k2) << 23);
+
+    // Four slices of a row are two loads of four elements a lane.  The unit of
+    // a lane is made of its own elements and its neighbour's `with` lanes on
+    // (slice_order): the lower one's from the first load, the other's from the
+    // second.  In shared memory the eight rows' units of a slice meet, each
+    // turned by its place for the banks, and leave as whole lines.
+    __shared__ uint4 tile[FOURS * 4 * XT][64];
+    const int with = p.order8 == kOrderPlain ? 1 : 4;
+    const bool upper = (lane & with) != 0;
+    const int place = lane & 7, u = p.order8 == kOrderPlain ? place >> 1 : place & 3;
+    const int block = (lane >> 3) + (upper ? 4 : 0), c = 4 * (block & 1) + u;   // of the four slices, and the unit in its slice
+    const int bytes = GT * XT * kSliceK * 2, fours = (p.nst + 3) / 4;
+    uint8_t *out = p.img + ((int64_t)s_at * p.nst + (gran - s_at)) * bytes + sub * 1024;
+    const int64_t step = (int64_t)s_n * bytes;
+    for (int q0 = part; q0 < fours; q0 += p.parts * FOURS) {
+        Some<T, 4> v[FOURS][2];
+#pragma unroll
+        for (int i = 0; i < FOURS; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int k = 256 * (q0 + i * p.parts) + 128 * n + 4 * lane;
+                v[i][n] = {};
+                if (src >= 0 && k < p.in_dim) load(x + k, p.vec, v[i][n]);
+            }
+#pragma unroll
+        for (int i = 0; i < FOURS; ++i) {
+            Some<T, 4> other;
+#pragma unroll
+            for (int w = 0; w < (int)sizeof(T); ++w)
+                other.w[w] = __shfl_xor_sync(0xffffffffu, upper ? v[i][0].w[w] : v[i][1].w[w], with);
+            float a[4], b[4], f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[e] = upper ? element(other, e) : element(v[i][0], e);
+                b[e] = upper ? element(v[i][1], e) : element(other, e);
+            }
+            slice_order(p.order8, a, b, f);
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float f0 = f[2 * e] * scale, f1 = f[2 * e + 1] * scale;
+                const __half2 g = __floats2half2_rn(f0, f1);
+                h[e] = h2_bits(g);
+                if constexpr (XT == 2) {
+                    const float2 w = __half22float2(g);
+                    l[e] = h2_bits(__floats2half2_rn(fabsf(w.x) < INFINITY ? (f0 - w.x) * 2048.f : 0.f,
+                                                     fabsf(w.y) < INFINITY ? (f1 - w.y) * 2048.f : 0.f));
+                }
+            }
+            const int sl = 4 * i + (block >> 1);
+            tile[sl * XT][8 * c + (warp ^ c)] = make_uint4(h[0], h[1], h[2], h[3]);
+            if constexpr (XT == 2) tile[sl * XT + 1][8 * c + (warp ^ c)] = make_uint4(l[0], l[1], l[2], l[3]);
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < FOURS * XT; ++i) {
+            const int n = i * kPrepThreads + tid, of = n >> 6, sl = of / XT, term = of % XT, cc = (n >> 3) & 7, r = n & 7;
+            const int s = 4 * (q0 + sl / 4 * p.parts) + (sl & 3);
+            if (s >= p.nst || r >= GT) continue;
+            // Few tokens' kernel reads a row's units of four slices at once (of
+            // MXFP4, every other one of eight): they lie one after the other,
+            // each slice's turned in its 128 bytes, for the banks.
+            const int at = p.spread ? (s & ~7) | (s & 1) << 2 | (s >> 1 & 3) : s;
+            const int turn = p.few ? 2 * (at & 3) : 0;
+            // (The low terms' rows follow the high ones'.)
+            uint8_t *to = out + at * step + cc * 128 + (GT < kPrepRows ? ((term * GT + r) ^ turn) * 16 : term * 1024 + (r ^ turn) * 16);
+            *reinterpret_cast<uint4 *>(to) = tile[of][8 * cc + (r ^ cc)];
+        }
+        __syncthreads();
     }
 }
 
@@ -421,7 +506,8 @@ struct Source {
 template <int DT, int XT>
 rf_status launch_prep_t(const PrepParams &p, int64_t blocks, cudaStream_t s)
 {
-    prep_kernel<DT, XT><<<(unsigned)(blocks + 1), kPrepThreads, 0, s>>>(p);
+    if ((p.nst + 3) / 4 <= p.parts) prep_kernel<DT, XT, 1><<<(unsigned)(blocks + 1), kPrepThreads, 0, s>>>(p);
+    else prep_kernel<DT, XT, 4><<<(unsigned)(blocks + 1), kPrepThreads, 0, s>>>(p);
     return last_cuda_error();
 }
 
@@ -440,7 +526,7 @@ rf_status launch_prep(const ChunkShape &sh, const Source &x, uint8_t *ws, cudaSt
     p.spread = sh.few && sh.fmt == RF_MXFP4;
     p.cap_tiles = (int32_t)sh.cap_tiles, p.cap_gran = (int32_t)sh.cap_gran;
     const int size = dtype_size(x.dtype);
-    p.vec = aligned(x.X, 4 * size) && (x.ldx * size) % (4 * size) == 0;
+    p.vec = aligned(x.X, 16) && (x.ldx * size) % 16 == 0;
     p.plan = reinterpret_cast<ChunkPlan *>(ws);
     p.tiles = reinterpret_cast<ChunkTile *>(ws + sh.at_tiles);
     p.inv = reinterpret_cast<float *>(ws + sh.at_inv);
@@ -450,7 +536,8 @@ rf_status launch_prep(const ChunkShape &sh, const Source &x, uint8_t *ws, cudaSt
     const int64_t share = std::max(1, sh.gran_tokens() / kPrepRows);
     const int64_t busy = std::min<int64_t>(sh.cap_gran * share, sh.n_row);   // CTAs with rows, at most
     p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((sh.nst + 3) / 4, 4 * num_sms() / std::max<int64_t>(1, busy)));
-    const int64_t blocks = sh.cap_gran * share * p.parts;
+    p.by_row = sh.n_row < sh.cap_gran * share;
+    const int64_t blocks = busy * p.parts;
     if (blocks > 0x7ffffffeLL) return RF_ERR_TOO_LARGE;
     if (x.dtype == RF_F32)
         return sh.xt == 2 ? launch_prep_t<RF_F32, 2>(p, blocks, s) : launch_prep_t<RF_F32, 1>(p, blocks, s);
