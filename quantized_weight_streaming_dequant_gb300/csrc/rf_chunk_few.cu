@@ -83,22 +83,13 @@ struct Weights {
         for (int i = 0; i < NW; ++i) q[i] = __funnelshift_rc(x[i], x[i + 1], sh + 8 * NS);
         if constexpr (FMT != RF_MXFP4) s1 *= 0x00010001u;
     }
-    // MXFP4: the factor 2^k, k = E - 127, where fp16 has it as a normal number;
-    // anywhere (ANY), in two.
-    static __device__ __forceinline__ uint32_t place(uint32_t E) { return E - 113u; }   // (below 30: normal)
+    // MXFP4's factor (ANY: a warp's lane needs it split).
     template <bool ANY>
     __device__ __forceinline__ void scale()
     {
         const uint32_t E = s1;
-        s1 = E * 0x04000400u - 112u * 0x04000400u;
-        if constexpr (ANY) {
-            const int k = (int)E - 127;
-            s2 = 0x3C003C00u;
-            if (E == 255u) s1 = 0x7E007E00u;   // NaN
-            else if (k > 15) s1 = 0x78007800u, s2 = pow2_h(min(k - 15, 15)) * 0x00010001u;
-            else if (k < -24) s1 = 0x0C000C00u, s2 = k + 12 >= -24 ? pow2_h(k + 12) * 0x00010001u : 0u;
-            else s1 = pow2_h(k) * 0x00010001u;
-        }
+        s1 = e8m0_factor(E);
+        if constexpr (ANY) e8m0_factors(E, s1, s2);
     }
     // A block behind the row's last one.
     __device__ __forceinline__ void clear() { s1 = s2 = 0u; }
@@ -323,8 +314,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        place = max(place, Weights<FMT, C::LOW>::place(src[start + h * half + (4 * t + k) * block_size(FMT)]));
-                any = __any_sync(0xffffffffu, place >= 30u);
+                        place = max(place, e8m0_place(src[start + h * half + (4 * t + k) * block_size(FMT)]));
+                any = e8m0_far(place);
             }
             const bool ragged = FMT != RF_Q4_K && 2 * (c + 1) * QPC > p.nb;
             // Four slices.

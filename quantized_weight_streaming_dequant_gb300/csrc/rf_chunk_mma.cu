@@ -478,6 +478,13 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 for (int q = (grp - (int)m) & (G - 1); q < ns; q += G) {
                     uint32_t hi[16], lo[16];
                     bool open = false;   // the stage is known to be free
+                    bool any = false;    // a scale far from 1 in the stage
+                    if constexpr (FMT == RF_MXFP4) {
+                        uint32_t place = 0;
+#pragma unroll
+                        for (int k = 0; k < 2 * KS; ++k) place = max(place, e8m0_place(src[(2 * KS * q + k) * block_size(FMT)]));
+                        any = e8m0_far(place);
+                    }
                     auto store = [&](int at_col) -> bool {
                         if (!open) {
                             if (!waits(bar(C::ADONE + grp), (((m + (uint32_t)q) / G) & 1) ^ 1)) return false;
@@ -502,9 +509,9 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                             Block<FMT> blk[2];
 #pragma unroll
                             for (int t = 0; t < 2; ++t) blk[t].load(src, (2 * sl + t) * BS);
-                            block_pairs<FMT, C::LOW>(blk[0], hi, lo);
+                            block_pairs<FMT, C::LOW>(blk[0], any, hi, lo);
                             if (!(ok = store(C::ASLICE * e))) break;
-                            block_pairs<FMT, C::LOW>(blk[1], hi, lo);
+                            block_pairs<FMT, C::LOW>(blk[1], any, hi, lo);
                             if (2 * (c * QPC + sl) + 1 >= p.nb) {   // behind the last block: the next row's bytes
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0u;
