@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         }
     }
     const T *x = static_cast<const T *>(p.X) + (src >= 0 ? src * p.ldx : 0);
+    // (fp16 values are operands as they are.)
     float m = 0.f;
-    if (src >= 0) {
+    if (!std::is_same<T, __half>::value && src >= 0) {
         constexpr int E = 16 / sizeof(T);
         uint32_t bits = 0;
 #pragma unroll 8
