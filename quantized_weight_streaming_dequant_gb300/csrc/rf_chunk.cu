@@ -1,19 +1,27 @@
 // rf_chunk.cu -- entry points of the chunk operators and the kernels around
-// their product (rf_chunk_mma.cu): the token tiles and operand images before
-// it, the sum over a token's experts after it.
+// their products (rf_chunk_mma.cu, rf_chunk_few.cu): the token tiles and operand
+// images before them, the sum over a token's experts after them.
 //
 // prep_kernel, one launch:
 //   * its last CTA lists the token tiles: up to T rows of one group each.
 //   * the others write the images.  A granule is 16 operand rows (16 tokens,
-//     or 8 tokens of two terms) of a group; granule q of group g is granule
-//     offsets[g] / GT + g + q of the images: no two groups meet, and no scan
-//     over the groups is needed to find a place.  A CTA takes a granule, or a
-//     share of its slices: the rows' largest values give their powers of two,
-//     then the rows are rounded to fp16 in the layout of the MMA's operand
-//     (K-major core matrices, 2 KB a granule and slice, written whole).
-// It reads X once from memory (the second pass over a row finds it in cache)
-// and writes 2 bytes an element (4 with two terms).  At most a few percent of
-// a prompt's time; with few rows, its latency.
+//     or 8 tokens of two terms; half of that for tiles of 8 operand rows) of a
+//     group of GT tokens; granule q of group g is granule offsets[g] / GT + g +
+//     q of the images: no two groups meet, and no scan over the groups is
+//     needed to find a place.  A CTA takes eight rows of a granule, or a share
+//     of their slices: a warp finds its row's largest value, hence a power of
+//     two, then rounds the row to fp16; the eight rows' units of 16 bytes meet
+//     in shared memory in the layout of the products' operand (K-major core
+//     matrices, 2 KB a granule and slice) and leave as whole lines.
+// It reads X once from memory (the second pass over a row finds it in L2 or
+// closer) and writes 2 bytes an element (4 with two terms).  Bound: latency of
+// its chain offsets - row - scale - row - lines, and with long rows the loads in
+// flight: 2048 x 11008 bf16 in 26 us (3.4 TB/s, in and out), 2002 x 11008 fp32
+// in 33 us, 8192 x 2880 fp32 in 36 us.  Units written by the threads that
+// loaded them, eight rows a warp: 33, 48 and 49 us.  A few rows: 5 to 8 us.
+//
+// join_kernel adds a token's experts: 94 MB in and 12 MB out in 18 us (5.9
+// TB/s), bound by memory.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -415,8 +423,11 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // item's inputs are shared out, and a second launch adds the parts' sums:
 // worth it while it saves a tenth of the SMs' rounds after what that launch,
 // the sums' traffic and the items' starts cost.  In SM cycles, as measured: a
-// slice's by what bounds it (see MEASURED at the kernel), 4,000 an item, 6,000
-// a launch, 1,500 bytes of sums a cycle.
+// slice's by what bounds it, 4,000 an item (2,500 where two CTAs share the SM),
+// 6,000 a launch, 1,500 bytes of sums a cycle.  9 fp32 tokens through
+// 2 x 11008 x 4096 Q4_0: 4 parts, 54 us; 1 part, 73 us.  (The last part's warps
+// adding the sums in the product's launch instead of a second one: 60 us
+// against 55, they read them one latency after another.)
 void choose_parts(ChunkShape &sh, bool gated)
 {
     const int64_t tiles = sh.n_group == 1 ? (sh.n_row + sh.tile_tokens() - 1) / sh.tile_tokens()
@@ -443,7 +454,12 @@ void choose_parts(ChunkShape &sh, bool gated)
 // The operands of a product of n_row rows shared by n_group groups.  Tiles of
 // 192 operand rows where the groups fill them (a weight slice is decoded once
 // per tile), of 128 where they do not; both let tensor memory hold two items'
-// sums, so that an epilogue runs beside the next item's products.
+// sums, so that an epilogue runs beside the next item's products.  Tiles of up
+// to 16 operand rows multiply from registers (rf_chunk_few.cu): 8 bf16 tokens
+// through 2 x 11008 x 4096 Q4_0 31 us against 45, 16 tokens 37 against 46, but
+// 32 tokens 50 against 46 (16 fp32 tokens 53 against 53, 32 fp16 tokens through
+// Q8_0 66 against 53); 128 fp32 tokens through 128 MXFP4 experts 528 against
+// 623, 256 tokens 805 against 689.
 ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row, bool gated)
 {
     ChunkShape sh;

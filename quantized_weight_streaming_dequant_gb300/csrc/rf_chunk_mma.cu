@@ -15,10 +15,11 @@
 //   warp 2       issues the products;
 //   warp 3       draws the items;
 //   decoders     four groups of four warps: each takes every fourth stage (one
-//                or two 64-input slices), a thread its row, turns the raw bytes into fp16 pairs
-//                and stores them to tensor memory, from where tcgen05.mma reads
-//                the weights: they cost no shared-memory bandwidth, which is
-//                what bounds tiles whose operands both lie there;
+//                or two 64-input slices), a thread its row, turns the raw bytes
+//                into fp16 pairs and stores them to tensor memory, from where
+//                tcgen05.mma reads the weights: they cost no shared-memory
+//                bandwidth, which is what bounds tiles whose operands both lie
+//                there;
 //   epilogue     four warps read the sums out of tensor memory, while the
 //                others are at the next item.
 //
@@ -34,6 +35,28 @@
 //
 // Every wait is bounded; after a failure every role stops, copies and products
 // already issued are waited for, and tensor memory is freed.
+//
+// Bound.  A slice of 128 x 64 weights costs its decoding (half-rate integer
+// instructions of 16 warps: about 190 cycles for Q4_0 and MXFP4, twice that for
+// two terms), its products (192 cycles at 192 rows) and its copies; the roles
+// run side by side, but a stage passes from one to the next by barriers (100 to
+// 200 cycles each), so that a slice takes 420 to 640 cycles where each of the
+// three alone would take 200 to 300.  Measured (us a launch):
+//   2048 bf16 rows, 2 x 11008 x 4096 Q4_0      258   1.43 PFLOP/s (0.75 of the
+//                                                    measured cuBLAS rate)
+//   2048 bf16 rows, 4096 x 11008 Q8_0          182   1.01 PFLOP/s
+//   8192 bf16 rows, 128 experts of 2880 x 2880 MXFP4, gate, up and down:
+//                                              684   0.60 PFLOP/s, 2.5 TB/s
+//   5000 fp16 rows (two terms), 24 groups of 4000 x 2080 Q4_0:   142
+// The first with products alone (no copies, no decoding): 195; the third: 440.
+// Tried and not kept (the first case, us, against 268 at the time unless said
+// otherwise): tiles of 256 rows, whose sums fit once, 308; activations in a ring
+// of bytes instead of slots, 460 against 295; the issuing role in lane 0 by
+// number, 388 against 300; an issuing loop that is not unrolled, 1027 against
+// 840 in the third case; six stages of weights for tiles of 64 rows, three
+// decoder groups, more raw chunks in flight, and fewer or larger stages of
+// activations: nothing; dependent launches, 54 against 38 in a small call; waits
+// that poll without the hardware's own pause, 10 to 20 % slower.
 #include <algorithm>
 #include <cstring>
 #include <mutex>
