@@ -425,7 +425,8 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // the sums' traffic and the items' starts cost.  In SM cycles, as measured: a
 // slice's by what bounds it, 4,000 an item (2,500 where two CTAs share the SM),
 // 6,000 a launch, 1,500 bytes of sums a cycle.  9 fp32 tokens through
-// 2 x 11008 x 4096 Q4_0: 4 parts, 54 us; 1 part, 73 us.  (The last part's warps
+// 2 x 11008 x 4096 Q4_0: 53 us, in one part 60; 77 through 4099 x 4096 Q4_K 41,
+// in one 60.  (The last part's warps
 // adding the sums in the product's launch instead of a second one: 60 us
 // against 55, they read them one latency after another.)
 void choose_parts(ChunkShape &sh, bool gated)

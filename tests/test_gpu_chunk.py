@@ -458,6 +458,104 @@ def test_a_withheld_copy_ends_the_launch_and_the_device_recovers():
     assert rf.device_status() == rf.OK
 
 
+# ------------------------------------------- few rows a group, and one more
+# (4 fp32 and 8 16-bit tokens share eight columns of a product, 8 and 16 take
+# tiles of their own, 9 and 17 the way through tensor memory)
+FEW = [1, 4, 5, 8, 9, 16, 17]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok", FEW)
+@pytest.mark.parametrize("fmt,scales", [(rf.MXFP4, (-40, -20)), (rf.MXFP4, (-15, -13)), (rf.MXFP4, (8, 12)), (rf.Q4_0, (1e-7, 1e-6)),
+                                        (rf.Q8_0, (1e-7, 1e-5)), (rf.Q8_0, (0.2, 6.0)), (rf.Q4_K, (0.05, 0.4))],
+                         ids=lambda v: NAMES.get(v, v) if isinstance(v, int) else str(v))
+def test_few_tokens_scales_at_the_ends_of_their_range(fmt, scales, n_tok, dtype):
+    in_dim, rows = inputs(fmt, 24), 70
+    rng = np.random.default_rng(n_tok)
+    W, w = raw(fmt, 1, rows, in_dim, 33, scale_range=scales)
+    x, xv = randn(rng, (n_tok, in_dim), dtype)
+    got = rf.gemm_fused(fmt, W, 0, rows, in_dim, x)
+    y, bound = reference(fmt, dtype, w[0], xv)
+    if dtype == "float16":
+        keep = np.abs(y) < 6e4
+        got, y, bound = torch.where(torch.from_numpy(keep).cuda(), got, torch.zeros_like(got)), y * keep, bound * keep
+    check(got, y, bound, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+def test_few_tokens_in_many_groups(fmt, dtype):
+    """Most groups empty, some with more rows than a tile has; blocks that end
+    inside four slices; rows behind the last super-row; Y's tail as it was."""
+    sizes = [0] * 30 + [1, 23, 0, 5, 4, 9, 17] + [0] * 20 + [2]
+    in_dim, rows, n = inputs(fmt, 27), 77, len(sizes)
+    used = sum(sizes)
+    rng = np.random.default_rng(6)
+    W, w = raw(fmt, n, rows, in_dim, 23)
+    x, xv = randn(rng, (used, in_dim), dtype)
+    b, bv = f32(rng, n, rows)
+    offsets = np.concatenate([[0], np.cumsum(sizes)])
+    Y = torch.full((used + 3, rows), 4.0, dtype=x.dtype, device="cuda")
+    rf.gemm_grouped(fmt, W, rows, in_dim, torch.cat([x, x[:3]]), i32(offsets), Y=Y, act=rf.ACT_SILU, bias=b)
+    assert (Y[used:] == 4).all()
+    for g in np.flatnonzero(sizes):
+        a, e = offsets[g], offsets[g + 1]
+        y, bound = reference(fmt, dtype, w[g], xv[a:e], kind=oc.SILU, bias=bv[g])
+        check(Y[a:e], y, bound, dtype, f"group {g}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok", [4, 8, 16])
+def test_few_tokens_not_finite_stay_in_their_row(n_tok, dtype):
+    """NaN and infinities of one token, and a weight row of NaN scales whose
+    blocks lie behind the row before it."""
+    in_dim, rows = 32 * 5, 90
+    rng = np.random.default_rng(12)
+    Wn = syn.quant_matrix(rf.MXFP4, rows, in_dim, 8).copy()
+    Wn[50, ::17] = 255
+    W, w = torch.from_numpy(Wn).cuda(), oc.weights(rf.MXFP4, Wn, 1, rows, in_dim)[0]
+    keep = [r for r in range(rows) if r != 50]
+    for bad in (float("nan"), float("inf")):
+        x, xv = randn(rng, (n_tok, in_dim), dtype)
+        x[1, 33] = bad
+        got = rf.gemm_fused(rf.MXFP4, W, 0, rows, in_dim, x)
+        assert torch.isnan(got[:, 50]).all() and not torch.isfinite(got[1]).any()
+        others = [t for t in range(n_tok) if t != 1]
+        y, bound = reference(rf.MXFP4, dtype, w[keep], xv[others])
+        check(got[others][:, keep], y, bound, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_few_tokens_do_not_depend_on_other_rows(dtype):
+    for fmt in FMTS:
+        W, _ = raw(fmt, 1, 100, 512, 5)
+        for n_tok in (4, 8, 16):
+            x, _ = randn(np.random.default_rng(2), (n_tok, 512), dtype)
+            a = rf.gemm_fused(fmt, W, 0, 100, 512, x)
+            x2 = x.clone()
+            x2[:2], x2[3:] = 100, float("inf")
+            assert torch.equal(a[2], rf.gemm_fused(fmt, W, 0, 100, 512, x2)[2])
+
+
+def test_a_withheld_copy_of_few_tokens_ends_the_launch():
+    import time
+    for fmt, in_dim in ((rf.Q8_0, 64), (rf.MXFP4, 2880)):
+        W, _ = raw(fmt, 1, 384, in_dim, 1)
+        for dtype in DTYPES:
+            x, _ = randn(np.random.default_rng(1), (4, in_dim), dtype)
+            want = rf.gemm_fused(fmt, W, 0, 384, in_dim, x)
+            assert rf.device_status() == rf.OK
+            rf.debug_arm_wait_fault(1000)
+            t0 = time.perf_counter()
+            rf.gemm_fused(fmt, W, 0, 384, in_dim, x)
+            assert rf.device_status() == 6
+            assert time.perf_counter() - t0 < 1.0
+            assert rf.device_status() == rf.OK
+            for _ in range(2):
+                assert torch.equal(rf.gemm_fused(fmt, W, 0, 384, in_dim, x), want)
+    assert rf.device_status() == rf.OK
+
+
 def test_a_layer_of_experts_as_it_is_used():
     """Norm, router, routed FFN with the residual, next norm: the run of a layer
     over a chunk, each step against 64 bits on the values it was given."""
