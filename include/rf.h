@@ -768,11 +768,12 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  * RF_ERR_UNSUPPORTED_FMT).  X, Y and residual are of one `dtype` (RF_F32,
  * RF_F16, RF_BF16); biases are fp32.  Y is computed in fp32 and rounded once.
  * Precision, from the operands of the tensor cores (products are exact, sums
- * fp32).  Each row of X is scaled by a power of two that puts its largest
- * finite value at [2^14, 2^15); its values enter
- *   RF_F32        as two fp16 terms (22 bits; below 2^-28 of the row's largest:
- *                 to 2^-50 of it),
- *   RF_F16, BF16  as they are (below 2^-28 of the largest, 2^-25 for RF_F16: to
+ * fp32).  X's values enter
+ *   RF_F16        as they are;
+ *   RF_F32, BF16  after their row was scaled by a power of two that puts its
+ *                 largest finite value at [2^14, 2^15): RF_F32 as two fp16
+ *                 terms (22 bits; below 2^-28 of the row's largest: to 2^-50
+ *                 of it), RF_BF16 as they are (below 2^-28 of the largest: to
  *                 2^-39 of it).
  * Weights (below 65504 in magnitude) enter
  *   MXFP4         as they are (below 2^-24: to 2^-25),
@@ -781,8 +782,9 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  *                 more); RF_BF16: rounded once to fp16, as rf_gemm's (2^-11 or
  *                 2^-25: an eighth of half a step of bf16).
  * A row of X that holds an infinity or a NaN has products that are infinite or
- * NaN (the activations clamp infinities, NaN stays); other rows do not see it.  Results do not depend on the other rows' values or on
- * timing (the number of rows chooses how sums are shared out).
+ * NaN (the activations clamp infinities, NaN stays); other rows do not see it.
+ * Results do not depend on the other rows' values or on timing (the number of
+ * rows and of groups chooses the kernel and how sums are shared out).
  * Weight tensors: 16-byte aligned, rows of rf_row_bytes each; all bytes of the
  * tensors given may be read.  Workspaces: device, 256-byte aligned, at least
  * the stated bytes, overwritten, used by one call at a time. */
@@ -844,9 +846,9 @@ RF_API size_t rf_gemm_fused_workspace_bytes(int fmt, int64_t rows, int64_t in_di
  * of Y at most (for the launch shape and the workspace); rows of Y that
  * belong to no group are left as they were.  n_x: rows of X (without `order`
  * at least n_row).  biases: (n_group, rows).  A group whose offsets decrease
- * or leave [0, n_row] is skipped, a row whose order entry leaves X counts as
- * zero (its Y is what zeros give), and rf_device_status reports
- * RF_ERR_INVALID_ARG.
+ * or leave [0, n_row] is skipped (the rows of Y of other groups that share
+ * rows then are undefined), a row whose order entry leaves X counts as zero
+ * (its Y is what zeros give), and rf_device_status reports RF_ERR_INVALID_ARG.
  * Errors: as rf_gemm_fused; RF_ERR_INVALID_ARG for n_group < 1, per < 1,
  * n_x < 0 or too few rows of X; RF_ERR_TOO_LARGE for n_group > 65536. */
 RF_API rf_status rf_gemm_grouped(int fmt, const void *W, const void *up, int n_group, int64_t rows,
@@ -905,8 +907,8 @@ RF_API size_t rf_moe_tokens_workspace_bytes(int fmt, int n_expert, int top_k, in
 /* --------------------------------------------------------------- status */
 /* Synchronizes the current device, then reports and clears the device status
  * word that kernels set when a bounded wait times out, or RF_ERR_INVALID_ARG
- * for a batch whose device arrays name positions or pages that do not exist
- * (RF_OK if none).
+ * for a batch whose device arrays name positions or pages that do not exist,
+ * or rows or groups outside a call's (rf_gemm_grouped) (RF_OK if none).
  * Returns RF_ERR_CUDA if the device reports an error. */
 RF_API rf_status rf_device_status(void);
 
@@ -914,12 +916,12 @@ RF_API rf_status rf_device_status(void);
  * lets the failure path be exercised without faulting a GPU).  Arms a
  * one-shot fault for the next launch on this process that copies with
  * tensor or bulk copies: a GEMV over device memory whose rows are 16-byte
- * aligned or take per-row bulk copies, or an rf_gemm.  In
- * that launch one copy of its first CTA is never issued (a stage of the
- * GEMV's weights; the GEMM's second activation tile), so the warps waiting
- * for it give up after limit_us microseconds,
- * record RF_ERR_TIMEOUT, and the launch ends with nothing in flight (its
- * outputs are undefined).
+ * aligned or take per-row bulk copies, an rf_gemm, or a product of the calls
+ * for chunks of tokens.  In that launch one copy of its first CTA is never
+ * issued (a stage of the GEMV's weights; the GEMM's second activation tile; the
+ * chunk product's first or second), so the warps waiting for it give up after
+ * limit_us microseconds, record RF_ERR_TIMEOUT, and the launch ends with
+ * nothing in flight (its outputs are undefined).
  * limit_us = 0 disarms.  Errors: RF_ERR_INVALID_ARG for limit_us above
  * 2,000,000. */
 RF_API rf_status rf_debug_arm_wait_fault(uint32_t limit_us);

@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstdint>
 #include <cstring>
 #include <type_traits>
 
@@ -228,14 +229,16 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
     // (rows fewer than the granules that there might be).
     const int part = blockIdx.x % p.parts, place_of = blockIdx.x / p.parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // The first group that has the place: more than one only when offsets
+    // decrease, and then what one CTA writes is still one group's.
     __shared__ int s_group, s_row, s_cnt, s_n, s_at, s_gran, s_sub;
-    if (tid == 0) s_group = -1;
+    if (tid == 0) s_group = INT32_MAX;
     __syncthreads();
-    for (int g = tid; g < p.n_group; g += kPrepThreads) {
-        int a, b;
+    int mine = INT32_MAX, row = 0, a = 0, b = 0, q = 0;
+    for (int g = tid; g < p.n_group && mine == INT32_MAX; g += kPrepThreads) {
         if (!group_rows(p, g, a, b)) continue;
-        int row = place_of, q;
         if (p.by_row) {
+            row = place_of;
             q = (row - a) / GT;
             if (row < a || row >= b || (row - a) % min(GT, kPrepRows) != 0) continue;
         } else {
@@ -243,9 +246,14 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
             if (q < 0 || q >= (b - a + GT - 1) / GT) continue;
             row = a + q * GT + place_of % H * kPrepRows;
         }
+        mine = g;
+    }
+    if (mine != INT32_MAX) atomicMin(&s_group, mine);
+    __syncthreads();
+    if (s_group == INT32_MAX) return;
+    if (mine == s_group) {
         const int tt = p.tile_tokens / GT;   // granules per whole tile
-        s_group = g;
-        s_gran = a / GT + g + q;
+        s_gran = a / GT + mine + q;
         s_row = row;
         s_cnt = min(min(kPrepRows, GT), b - row);
         s_at = s_gran - q + q / tt * tt;     // the tile's first granule
@@ -253,7 +261,6 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
         s_sub = (row - a) % GT / kPrepRows;
     }
     __syncthreads();
-    if (s_group < 0) return;
     const int gran = s_gran, sub = s_sub;
     // A warp takes a row: its largest value, hence its scale, then its inputs.
     static_assert(kPrepRows == kPrepThreads / 32, "a warp per row");
@@ -460,7 +467,8 @@ void choose_parts(ChunkShape &sh, bool gated)
 // through 2 x 11008 x 4096 Q4_0 31 us against 45, 16 tokens 37 against 46, but
 // 32 tokens 50 against 46 (16 fp32 tokens 53 against 53, 32 fp16 tokens through
 // Q8_0 66 against 53); 128 fp32 tokens through 128 MXFP4 experts 528 against
-// 623, 256 tokens 805 against 689.
+// 623, 256 tokens 805 against 689.  (Tiles of 160 rows, which fill the last
+// round of 2048 tokens through 4096 x 11008 better, take 214 us against 182.)
 ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row, bool gated)
 {
     ChunkShape sh;
@@ -495,8 +503,10 @@ rf_status check_sizes(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t
     if (!fmt_has_chunks(fmt) || !dtype_ok(dtype)) return RF_ERR_UNSUPPORTED_FMT;
     if (n_group < 1 || rows < 0 || n_row < 0 || in_dim <= 0 || in_dim % block_elems_of(fmt) != 0) return RF_ERR_INVALID_ARG;
     if (in_dim > (1 << 20) || rows > 0x7fffffffLL || n_group > 65536 || n_row > kMaxPieces) return RF_ERR_TOO_LARGE;
-    const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, false);
-    if (sh.cap_gran > kMaxPieces || sh.cap_tiles * ((rows + 63) / 64) > kMaxPieces) return RF_ERR_TOO_LARGE;
+    for (const bool gated : {false, true}) {
+        const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, gated);
+        if (sh.cap_gran > kMaxPieces || sh.cap_tiles * ((rows + 63) / 64) > kMaxPieces) return RF_ERR_TOO_LARGE;
+    }
     return RF_OK;
 }
 

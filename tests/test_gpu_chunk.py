@@ -274,6 +274,25 @@ def test_grouped_bad_offsets_and_rows_are_reported():
     assert rf.device_status() == rf.OK
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("offsets", [[0, 90, 10, 100], [0, 4, 0, 4, 0, 4, 0, 60], [0, 100, 0, 100, 0, 100], [8, 40, 3, 100, 99, 100]], ids=str)
+def test_grouped_offsets_that_make_groups_overlap(offsets, dtype):
+    """Reported, nothing outside Y's rows is written, and the next call is right."""
+    n, n_row, rows, in_dim = len(offsets) - 1, 100, 70, 96
+    rng = np.random.default_rng(5)
+    W, w = raw(rf.MXFP4, n, rows, in_dim, 2)
+    x, xv = randn(rng, (n_row, in_dim), dtype)
+    buf = torch.full((n_row + 20, rows), 3.0, dtype=x.dtype, device="cuda")
+    need = rf.gemm_grouped_workspace(rf.MXFP4, n, rows, in_dim, x, n_row).numel()
+    space = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    rf.gemm_grouped(rf.MXFP4, W, rows, in_dim, x, i32(offsets), Y=buf[10:10 + n_row], workspace=space[:need])
+    assert rf.device_status() == 1
+    assert (buf[:10] == 3).all() and (buf[10 + n_row:] == 3).all() and (space[need:] == 0x5A).all()
+    got = rf.gemm_grouped(rf.MXFP4, W, rows, in_dim, x, i32([0] * n + [n_row]))
+    y, bound = reference(rf.MXFP4, dtype, w[n - 1], xv)
+    check(got, y, bound, dtype)
+
+
 @pytest.mark.parametrize("n_group", [1000, 3000])
 def test_grouped_many_groups(n_group):
     rng = np.random.default_rng(6)
