@@ -84,9 +84,10 @@ struct Cfg {
     static constexpr int QPC = chunk_weights(FMT) / kSliceK;           // slices per chunk
     static constexpr int BW = box_bytes(FMT, 8);                       // box bytes at most
     static constexpr int T = NT / XT;                                  // tokens
-    static constexpr int KS = NT == 128 && WT == 1 ? 2 : 1;
-    static constexpr int S = 4;                                        // stages of weights
-    static constexpr int G = 4;                                        // decoder groups of four warps
+    static constexpr int KS = NT == 128 && WT == 1 ? 4 : 1;
+    static constexpr int S = KS == 4 ? 2 : 4;                          // stages of weights
+    static constexpr int G = 4, GPS = G / S;                           // decoder groups of four warps; those of a stage
+    static constexpr int KD = KS / GPS;                                // slices of a stage that one of them decodes
     static constexpr int EPI0 = kDec0 + 4 * G, THREADS = 32 * (EPI0 + 4);
     static constexpr int USERS = 3 + 4 * G + 4;                        // warps that take an item
     // Registers a thread: what a launch gives every warp, and what the roles
@@ -121,7 +122,7 @@ struct Cfg {
     static_assert(ACC * NBUF <= ACOL, "tensor memory");
     static_assert(QPC % KS == 0 && FLUSH % KS == 0, "a stage lies in one chunk and between two flushes");
     static_assert(T % 16 == 0, "the epilogue takes 16 tokens at a time");
-    static_assert(G == S && (G & (G - 1)) == 0, "each group has a stage of its own");
+    static_assert(G % S == 0 && (S & (S - 1)) == 0 && KS % GPS == 0, "each group has a stage, or a share of one");
     static_assert(REPI <= 248 && REPI % 8 == 0 && RROLES < REGS, "registers");
     static_assert(LEAST * KS * BT + 2 * RAW <= SHARED && LEAST <= kInFlight, "the least stages and two chunks fit");
 };
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::BARS; ++i) {
             uint32_t n = 1;
-            if (i < C::ADONE) n = 4;
+            if (i < C::ADONE) n = 4 * C::GPS;
             else if (i >= C::REMPTY && i < C::ACCF) n = 4 * G;
             else if (i >= C::ACCE && i < C::IFULL) n = 4;
             else if (i >= C::IEMPTY && i < C::DRAIN) n = C::USERS;
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     if (blockIdx.x == 0 && n == (uint32_t)p.withhold) {
                         skipped = n;
                     } else {
-                        const int slices = KS > 1 && b + 1 < nsl ? KS : 1;
+                        const int slices = KS > 1 ? min(KS, nsl - b) : 1;
                         bar_expect(bar(C::BFULL + ib), slices * slice);
                         for (int i = 0; i < slices; ++i)
                             copy_bulk(ring + (ib * KS + i) * p.slot, src + i * slice, slice, bar(C::BFULL + ib));
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     if (!ready && !(ok = wait(bar(C::BFULL + ib), pb) && wait(bar(C::FULL + sa), pa))) break;
                     const uint32_t a_done = bar(C::ADONE + sa), b_done = bar(C::BDONE + ib);
                     const uint32_t a0 = tmem + C::ACOL + sa * C::ASTAGE, at = (ib * KS * p.slot) >> 4;
-                    const bool two = KS > 1 && b + 1 < nsl;
+                    const int slices = KS > 1 ? min(KS, nsl - b) : 1;
                     // The next stage's barriers are read (about 130 cycles
                     // each) beside this one's products.
                     if (++sa == S) sa = 0, pa ^= 1u;
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     any = true;
 #pragma unroll 1
                     for (int i = 0; i < KS; ++i) {
-                        if (i > 0 && !two) break;
+                        if (i > 0 && i >= slices) break;
                         const uint32_t a = a0 + (uint32_t)(i * C::ASLICE);
                         const uint64_t at_i = at + i * (p.slot >> 4);
 #pragma unroll
@@ -472,7 +473,8 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
         const int half = lane >> 4, i = lane_row(16 * w4 + (lane & 15), p.logP);
         const uint32_t a0 = tmem + C::ACOL + ((uint32_t)(32 * w4) << 16);
         const int64_t copied = p.copies ? p.total_rows & ~(int64_t)(p.P - 1) : 0;   // rows in whole super-rows
-        const uint32_t a = a0 + (uint32_t)grp * C::ASTAGE;   // (as many stages as groups: each group has its own)
+        const int stage = grp / C::GPS, s0 = grp % C::GPS * C::KD;   // the group's stage, and its first slice there
+        const uint32_t a = a0 + (uint32_t)(stage * C::ASTAGE + s0 * C::ASLICE);
         uint32_t m = 0;                // stages before this chunk
         uint32_t r = 0, ph = 0;        // raw chunk and its phase
         bool ok = true;
@@ -498,30 +500,35 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
 #pragma unroll 1
                     for (int k = 0; k < n; ++k) src[k] = __ldg(g + k);
                 }
-                for (int q = (grp - (int)m) & (G - 1); q < ns; q += G) {
+                for (int q = (stage - (int)m) & (S - 1); q < ns; q += S) {
                     uint32_t hi[16], lo[16];
                     bool open = false;   // the stage is known to be free
                     bool any = false;    // a scale far from 1 in the stage
                     if constexpr (FMT == RF_MXFP4) {
                         uint32_t place = 0;
 #pragma unroll
-                        for (int k = 0; k < 2 * KS; ++k) place = max(place, e8m0_place(src[(2 * KS * q + k) * block_size(FMT)]));
+                        for (int k = 0; k < 2 * C::KD; ++k)
+                            place = max(place, e8m0_place(src[(2 * (KS * q + s0) + k) * block_size(FMT)]));
                         any = e8m0_far(place);
                     }
-                    auto store = [&](int at_col) -> bool {
+                    auto opened = [&]() -> bool {
                         if (!open) {
-                            if (!waits(bar(C::ADONE + grp), (((m + (uint32_t)q) / G) & 1) ^ 1)) return false;
+                            if (!waits(bar(C::ADONE + stage), (((m + (uint32_t)q) / S) & 1) ^ 1)) return false;
                             tc_fence_after();
                             open = true;
                         }
+                        return true;
+                    };
+                    auto store = [&](int at_col) -> bool {
+                        if (!opened()) return false;
                         tmem_st16(a + at_col, hi);
                         if constexpr (WT == 2) tmem_st16(a + 32 + at_col, lo);
                         return true;
                     };
 #pragma unroll 1
-                    for (int e = 0; e < KS; ++e) {
-                        const int sl = q * KS + e;   // slice of the chunk
-                        if (e > 0 && sl >= nq) break;
+                    for (int e = 0; e < C::KD; ++e) {
+                        const int sl = q * KS + s0 + e;   // slice of the chunk
+                        if ((C::GPS > 1 || e > 0) && sl >= nq) break;
                         if constexpr (FMT == RF_Q4_K) {
                             q4k_block<C::LOW>(src, sl, 0, hi, lo);
                             if (!(ok = store(C::ASLICE * e))) break;
@@ -542,11 +549,12 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                             store(C::ASLICE * e + 16);
                         }
                     }
+                    if (C::GPS > 1 && ok) ok = opened();   // (a share without slices)
                     if (!ok) break;
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(bar(C::FULL + grp));
+                    if (lane == 0) bar_arrive(bar(C::FULL + stage));
                 }
                 if (!ok) break;
                 if (tail) fence_async_smem();   // the next copy follows these stores
