@@ -14,12 +14,12 @@
 //   warp 1       copies the operand slices of the token tile (1-D bulk);
 //   warp 2       issues the products;
 //   warp 3       draws the items;
-//   decoders     four groups of four warps: each takes every fourth stage (one
-//                or two 64-input slices), a thread its row, turns the raw bytes
-//                into fp16 pairs and stores them to tensor memory, from where
-//                tcgen05.mma reads the weights: they cost no shared-memory
-//                bandwidth, which is what bounds tiles whose operands both lie
-//                there;
+//   decoders     four groups of four warps, each with a stage of its own (a
+//                64-input slice) or half of one of two (two or four slices): a
+//                thread takes its row, turns the raw bytes into fp16 pairs and
+//                stores them to tensor memory, from where tcgen05.mma reads the
+//                weights: they cost no shared-memory bandwidth, which is what
+//                bounds tiles whose operands both lie there;
 //   epilogue     four warps read the sums out of tensor memory, while the
 //                others are at the next item.
 //
@@ -38,17 +38,18 @@
 //
 // Bound.  A slice of 128 x 64 weights costs its decoding (half-rate integer
 // instructions of 16 warps: about 190 cycles for Q4_0 and MXFP4, twice that for
-// two terms), its products (192 cycles at 192 rows) and its copies; the roles
+// two terms), its products (384 cycles at 192 rows) and its copies; the roles
 // run side by side, but a stage passes from one to the next by barriers (100 to
-// 200 cycles each), so that a slice takes 420 to 640 cycles where each of the
-// three alone would take 200 to 300.  Measured (us a launch):
+// 200 cycles each), so that a slice takes 410 to 640 cycles where the longest of
+// the three alone would take 200 to 450.  Measured (us a launch):
 //   2048 bf16 rows, 2 x 11008 x 4096 Q4_0      258   1.43 PFLOP/s (0.75 of the
 //                                                    measured cuBLAS rate)
 //   2048 bf16 rows, 4096 x 11008 Q8_0          182   1.01 PFLOP/s
 //   8192 bf16 rows, 128 experts of 2880 x 2880 MXFP4, gate, up and down:
-//                                              684   0.60 PFLOP/s, 2.5 TB/s
+//                                              666   0.61 PFLOP/s, 2.5 TB/s
 //   5000 fp16 rows (two terms), 24 groups of 4000 x 2080 Q4_0:   142
-// The first with products alone (no copies, no decoding): 195; the third: 440.
+// The first with products alone (no copies, no decoding): 180; the third, with
+// stages of two slices: 440 (684 in all).
 // Tried and not kept (the first case, us, against 268 at the time unless said
 // otherwise): tiles of 256 rows, whose sums fit once, 308; activations in a ring
 // of bytes instead of slots, 460 against 295; the issuing role in lane 0 by
@@ -76,16 +77,21 @@ constexpr int kRaws = 8;             // raw chunks in flight at most
 
 // NT: operand rows per token tile at most; XT, WT: fp16 terms per activation, weight.
 // A stage is KS slices of weights (tensor memory) and activations (shared
-// memory): two where a slice's products are short, so that the issuing warp's
-// chain of wait, issue and commit is paid half as often.
+// memory): several where a slice's products are short, so that what a stage
+// costs to hand over (the issuing warp's waits and commits, about 140 cycles,
+// and the way to the decoders and back) is paid less often.  Four slices
+// instead of two: 512 bf16 rows through the experts below 592 against 681 us;
+// two instead of one for two terms of both: 512 fp32 tokens through
+// 2 x 11008 x 4096 Q4_0 281 against 287, but 5000 fp16 rows (one term of the
+// activations) 162 against 153, and 192 bf16 rows no difference.
 template <int FMT, int NT, int XT, int WT>
 struct Cfg {
     static constexpr int CB = chunk_bytes(FMT);                        // chunk bytes per row
     static constexpr int QPC = chunk_weights(FMT) / kSliceK;           // slices per chunk
     static constexpr int BW = box_bytes(FMT, 8);                       // box bytes at most
     static constexpr int T = NT / XT;                                  // tokens
-    static constexpr int KS = NT == 128 && WT == 1 ? 4 : 1;
-    static constexpr int S = KS == 4 ? 2 : 4;                          // stages of weights
+    static constexpr int KS = NT > 128 ? 1 : (WT == 1 ? 4 : XT);
+    static constexpr int S = KS > 1 ? 2 : 4;                           // stages of weights
     static constexpr int G = 4, GPS = G / S;                           // decoder groups of four warps; those of a stage
     static constexpr int KD = KS / GPS;                                // slices of a stage that one of them decodes
     static constexpr int EPI0 = kDec0 + 4 * G, THREADS = 32 * (EPI0 + 4);
