@@ -464,10 +464,11 @@ void choose_parts(ChunkShape &sh, bool gated)
 // per tile), of 128 where they do not; both let tensor memory hold two items'
 // sums, so that an epilogue runs beside the next item's products.  Tiles of up
 // to 16 operand rows multiply from registers (rf_chunk_few.cu): 8 bf16 tokens
-// through 2 x 11008 x 4096 Q4_0 31 us against 45, 16 tokens 37 against 46, but
-// 32 tokens 50 against 46 (16 fp32 tokens 53 against 53, 32 fp16 tokens through
-// Q8_0 66 against 53); 128 fp32 tokens through 128 MXFP4 experts 528 against
-// 623, 256 tokens 805 against 689.  (Tiles of 160 rows, which fill the last
+// through 2 x 11008 x 4096 Q4_0 31 us against 45, 16 tokens 37 against 45, 8
+// fp32 tokens 45 against 52, 128 fp32 tokens through 128 MXFP4 experts 505
+// against 529 (but 256 bf16 tokens 565 against 531); with 32 rows a tile they
+// were no faster (32 bf16 tokens 50 against 45, 32 fp16 tokens through Q8_0 66
+// against 50, 256 fp32 tokens through the experts 805 against 621).  (Tiles of 160 rows, which fill the last
 // round of 2048 tokens through 4096 x 11008 better, take 214 us against 182.)
 ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row, bool gated)
 {

@@ -80,7 +80,7 @@ constexpr int kRaws = 8;             // raw chunks in flight at most
 // memory): several where a slice's products are short, so that what a stage
 // costs to hand over (the issuing warp's waits and commits, about 140 cycles,
 // and the way to the decoders and back) is paid less often.  Four slices
-// instead of two: 512 bf16 rows through the experts below 592 against 681 us;
+// instead of two: 512 bf16 tokens through the experts below 592 against 681 us;
 // two instead of one for two terms of both: 512 fp32 tokens through
 // 2 x 11008 x 4096 Q4_0 281 against 287, but 5000 fp16 rows (one term of the
 // activations) 162 against 153, and 192 bf16 rows no difference.
