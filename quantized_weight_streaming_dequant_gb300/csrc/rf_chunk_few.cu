@@ -69,13 +69,12 @@ struct Few {
     static constexpr int LOW = WT == 1 ? kOne : (XT == 2 && FMT == RF_Q4_K ? kScaled : kPlain);
     // Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.
     static constexpr int SHARED = 115200;
-    static constexpr int RAW = kM * box_bytes(FMT, 8);
-    static constexpr int QB = 4 * GB;                                    // operand bytes of four slices
-    static constexpr int RS = (SHARED - 2 * QB) / RAW < 4 ? (SHARED - 2 * QB) / RAW : 4;   // raw chunks
-    static constexpr int BS = (SHARED - RS * RAW) / QB < 4 ? (SHARED - RS * RAW) / QB : 4; // fours of slices
-    static constexpr int SMEM = RS * RAW + BS * QB;
-    static constexpr int RFULL = 0, REMPTY = RFULL + RS, BFULL = REMPTY + RS, BEMPTY = BFULL + BS, BARS = BEMPTY + BS;
-    static_assert(RS >= 2 && BS >= 2, "two stages of both");
+    // A stage: a raw chunk and the tile's operand slices for it.
+    static constexpr int RAW = kM * box_bytes(FMT, 8), OPS = QPC * GB, STAGE = RAW + OPS;
+    static constexpr int S = SHARED / STAGE < 4 ? SHARED / STAGE : 4;
+    static constexpr int SMEM = S * STAGE;
+    static constexpr int FULL = 0, EMPTY = S, BARS = 2 * S;
+    static_assert(S >= 2, "two stages");
     static_assert(QPC == (SPREAD ? 8 : 4), "fours of slices of a chunk");
 };
 
@@ -154,13 +153,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
     using C = Few<FMT, NT, XT, WT>;
     constexpr int NJ = C::NJ, QPC = C::QPC;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *ops = smem + C::RS * C::RAW;
     __shared__ uint64_t bars[C::BARS];
     __shared__ int s_stop;
     volatile int *stop = &s_stop;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::BARS; ++i) mbar_init(&bars[i], (i >= C::REMPTY && i < C::BFULL) || i >= C::BEMPTY ? kWarps : 1);
+        for (int i = 0; i < C::BARS; ++i) mbar_init(&bars[i], i >= C::EMPTY ? kWarps : 1);
         s_stop = 0;
         fence_barrier_init();
     }
@@ -186,10 +184,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
         // the operand slices too.
         const int half = lane >> p.logP, j = lane & (p.P - 1);
         const bool copies = half < 2 && p.copies;
-        const uint32_t dst = smem_addr(smem) + (uint32_t)lane * (uint32_t)((64 >> p.logP) * p.bw), dst_ops = smem_addr(ops);
+        const uint32_t dst = smem_addr(smem) + (uint32_t)lane * (uint32_t)((64 >> p.logP) * p.bw), dst_ops = smem_addr(smem) + C::RAW;
         const int xj = (int)((int64_t)j * p.rb);
         const CUtensorMap *map = &p.map[p.gated ? half & 1 : 0];
-        uint32_t rc = 0, r = 0, rph = 1, bc = 0, b = 0, bph = 1;   // copies of both kinds; places and phases
+        uint32_t n = 0, r = 0, ph = 1;   // stages copied; place in the ring and phase
         uint32_t skipped = 0xffffffffu;
         bool ok = true;
         for (int index = blockIdx.x; ok && index < total; index += gridDim.x) {
@@ -201,44 +199,31 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             const int y = (int)((first - j + p.P - 1) >> p.logP);   // first super-row with position j in the tile
             const uint8_t *src = p.img + ((int64_t)w.gran * p.nst + part * p.part_chunks * QPC) * C::GB;
             for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); ok && c < end; ++c) {
-                if (!(ok = waits(bar(C::REMPTY + r), rph))) break;
-                if (lane == 0) {
-                    if (p.copies) bar_expect(bar(C::RFULL + r), (uint32_t)(kM * p.bw));
-                    else bar_arrive(bar(C::RFULL + r));
-                }
+                if (!(ok = waits(bar(C::EMPTY + r), ph))) break;
+                const bool withhold = blockIdx.x == 0 && n == 0 && p.withhold >= 0;
+                if (withhold) skipped = n;
+                if (lane == 0) bar_expect(bar(C::FULL + r), (uint32_t)(C::OPS + (p.copies ? kM * p.bw : 0)));
                 __syncwarp();
-                if (copies) copy_box(dst + r * C::RAW, map, ((xj + c * C::CB) & ~15) >> 1, y, bar(C::RFULL + r));
-                ++rc;
-                if (++r == C::RS) r = 0, rph ^= 1u;
-                for (int q = 0; q < QPC; q += 4) {
-                    if (!(ok = waits(bar(C::BEMPTY + b), bph))) break;
-                    if (lane == 0) {
-                        if (blockIdx.x == 0 && bc == 0 && p.withhold >= 0) {
-                            skipped = bc;
-                        } else {
-                            bar_expect(bar(C::BFULL + b), C::QB);
-                            copy_bulk(dst_ops + b * C::QB, src, C::QB, bar(C::BFULL + b));
-                        }
-                    }
-                    src += C::QB;
-                    ++bc;
-                    if (++b == C::BS) b = 0, bph ^= 1u;
+                if (!withhold) {
+                    if (copies) copy_box(dst + r * C::STAGE, map, ((xj + c * C::CB) & ~15) >> 1, y, bar(C::FULL + r));
+                    if (lane == 0) copy_bulk(dst_ops + r * C::STAGE, src, C::OPS, bar(C::FULL + r));
                 }
+                src += C::OPS;
+                ++n;
+                if (++r == C::S) r = 0, ph ^= 1u;
             }
         }
         // Every copy issued lands before the CTA can exit.
-        if (lane == 0) {
-            for (uint32_t i = rc > C::RS ? rc - C::RS : 0; i < rc; ++i) bar_drain(bar(C::RFULL + i % C::RS), (i / C::RS) & 1);
-            for (uint32_t i = bc > C::BS ? bc - C::BS : 0; i < bc; ++i)
-                if (i != skipped) bar_drain(bar(C::BFULL + i % C::BS), (i / C::BS) & 1);
-        }
+        if (lane == 0)
+            for (uint32_t i = n > C::S ? n - C::S : 0; i < n; ++i)
+                if (i != skipped) bar_drain(bar(C::FULL + i % C::S), (i / C::S) & 1);
         return;
     }
 
     const int g = lane >> 2, t = lane & 3, i = lane_row(8 * warp + g, p.logP);
     const int64_t copied = p.copies ? p.total_rows & ~(int64_t)(p.P - 1) : 0;   // rows in whole super-rows
     const int swz = ((g ^ (2 * t)) & 7) * 16;   // see prep_kernel
-    uint32_t r = 0, rph = 0, b = 0, bph = 0;
+    uint32_t r = 0, ph = 0;
     ChunkTile next = {};
     if ((int)blockIdx.x < total) next = p.tiles[blockIdx.x / p.parts / p.nrt];
     for (int index = blockIdx.x; index < total; index += gridDim.x) {
@@ -315,8 +300,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             for (int e = 0; e < 2; ++e) inv[q][e] = __ldg(p.inv + (int64_t)w.gran * C::T + min(8 * q + 2 * t + e, w.cnt - 1));
         if (index + (int)gridDim.x < total) next = p.tiles[(index + (int)gridDim.x) / p.parts / p.nrt];
         for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); c < end; ++c) {
-            if (!waits(bar(C::RFULL + r), rph)) return;
-            uint8_t *src = smem + r * C::RAW, *lane_src = src + word;
+            if (!waits(bar(C::FULL + r), ph)) return;
+            uint8_t *src = smem + r * C::STAGE, *lane_src = src + word;
+            const uint8_t *ops = src + C::RAW + t * C::GB + swz;
             if (tails) {
                 // Rows that the boxes do not reach, copied to where they would
                 // put them.
@@ -343,10 +329,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             }
             const bool ragged = FMT != RF_Q4_K && 2 * (c + 1) * QPC > p.nb;
             // Four slices.
-            auto four = [&](int q4, auto any_scale) -> bool {
+            auto four = [&](int q4, auto any_scale) {
                 constexpr bool ANY = decltype(any_scale)::value;
-                if (!waits(bar(C::BFULL + b), bph)) return false;
-                const uint8_t *x = ops + b * C::QB + t * C::GB + swz;
+                const uint8_t *x = ops + q4 * C::GB;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     Weights<FMT, C::LOW> wt[2];
@@ -390,24 +375,18 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
                     }
                     if constexpr (XT == 2) flush();
                 }
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(C::BEMPTY + b));
-                if (++b == C::BS) b = 0, bph ^= 1u;
-                return true;
             };
             if (FMT == RF_MXFP4 && any) {
 #pragma unroll 1
-                for (int q4 = 0; q4 < QPC; q4 += 4)
-                    if (!four(q4, std::true_type())) return;
+                for (int q4 = 0; q4 < QPC; q4 += 4) four(q4, std::true_type());
             } else {
 #pragma unroll
-                for (int q4 = 0; q4 < QPC; q4 += 4)
-                    if (!four(q4, std::false_type())) return;
+                for (int q4 = 0; q4 < QPC; q4 += 4) four(q4, std::false_type());
             }
             if (tails) fence_async_smem();   // the next copy follows these stores
             __syncwarp();
-            if (lane == 0) bar_arrive(bar(C::REMPTY + r));
-            if (++r == C::RS) r = 0, rph ^= 1u;
+            if (lane == 0) bar_arrive(bar(C::EMPTY + r));
+            if (++r == C::S) r = 0, ph ^= 1u;
         }
         if constexpr (XT == 1) flush();
         if constexpr (C::BOTH) {   // the low terms' columns are two lanes on
