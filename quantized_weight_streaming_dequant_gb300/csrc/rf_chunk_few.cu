@@ -25,21 +25,24 @@
 // its rounding is a multiple of fp16's least number; Q4_K: scaled by 2^11).
 //
 // Bound.  By 2048 weights (a warp's 16 rows x 128 inputs, MXFP4, one term) an
-// SM takes about 80 cycles: 32 of the tensor cores (16 a product and SM
+// SM takes about 75 cycles: 32 of the tensor cores (16 a product and SM
 // quarter), 40 of integer instructions, 46 of memory; 16 warps an SM overlap
 // them as far as their registers (96 a thread) let them.  The copies alone run
 // at the measured memory rate.  Measured, us a call on the GPU:
 //                                                   here   through tensor memory
-//   77 bf16 tokens, 128 experts of 2880 MXFP4        340   440   (copies alone: 224)
-//   6 fp32 tokens, the same                          107   150   (copies alone:  79)
-//   45 fp32 rows, 64 groups of 1408 x 2048 Q8_0       34    59   (copies alone:  28)
+//   77 bf16 tokens, 128 experts of 2880 MXFP4        317   440   (copies alone: 224)
+//   6 fp32 tokens, the same                          104   150   (copies alone:  79)
+//   45 fp32 rows, 64 groups of 1408 x 2048 Q8_0       35    59   (copies alone:  28)
 //   8 bf16 tokens, 2 x 11008 x 4096 Q4_0              31    45
-// Without the products the first takes 230, without the conversions 330.  Steps
-// (first case, us): 458 with all of a block decoded before its products and
-// 8-byte loads; 412 with 4-byte loads, the item's end prefetched and one address
-// for both rows; 370 with tiles of 8 operand rows; 348 with a chunk's scales
-// looked at together.  Tried and not kept: several chains of sums for each kind
-// of product (352 against 348); tiles of 32 operand rows (see chunk_shape).
+// Steps (first case, us): 458 with all of a block decoded before its products
+// and 8-byte loads; 412 with 4-byte loads, the item's end prefetched and one
+// address for both rows; 370 with tiles of 8 operand rows; 348 with a chunk's
+// scales looked at together; 317 with one stage for a raw chunk and its operand
+// slices (one barrier a chunk instead of three).  At 370 it took 244 without
+// the products.  Tried and not kept: several chains of sums for each kind of
+// product (352 against 348); scales looked at beside the products, which are
+// done again if need be (340 against 317: registers); tiles of 32 operand rows
+// (see chunk_shape).
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
