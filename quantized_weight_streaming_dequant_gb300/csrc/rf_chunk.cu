@@ -279,11 +279,17 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
     if (!std::is_same<T, __half>::value && src >= 0) {
         constexpr int E = 16 / sizeof(T);
         uint32_t bits = 0;
-#pragma unroll 8
-        for (int k = E * lane; k < p.in_dim; k += 32 * E) {
-            Some<T, E> v;
-            load(x + k, p.vec, v);
-            bits = larger(bits, v);
+        // (Eight loads at a time, the last ones too: a loop's remainder would
+        // wait for each.)
+        for (int k = E * lane; k < p.in_dim; k += 8 * 32 * E) {
+            Some<T, E> v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = {};
+                if (k + i * 32 * E < p.in_dim) load(x + k + i * 32 * E, p.vec, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bits = larger(bits, v[i]);
         }
         m = largest<T>(bits);
         if (!(m < INFINITY)) {   // what is not finite does not count
