@@ -667,29 +667,36 @@ __global__ void __launch_bounds__(128) join_parts_kernel(const __grid_constant__
 {
     const int at = (int)blockIdx.y / pieces, t0 = (int)blockIdx.y % pieces * kJoinRows;
     if (at >= p.plan->n_tiles) return;
-    const ChunkTile w = p.tiles[at];
-    const int col = (int)blockIdx.x * 128 + (int)threadIdx.x, n = min(w.cnt - t0, kJoinRows);
+    const ChunkTile tile = p.tiles[at];
+    const int col = (int)blockIdx.x * 128 + (int)threadIdx.x, n = min(tile.cnt - t0, kJoinRows);
     if (col >= p.rows || n <= 0) return;
     const int64_t step = (int64_t)p.n_row * p.rows;   // from one projection to the next
-    const float b0 = p.bias[0] ? p.bias[0][(int64_t)w.group * p.rows + col] : 0.f;
-    const float b1 = p.bias[1] ? p.bias[1][(int64_t)w.group * p.rows + col] : 0.f;
-    const float *s = p.sums + (int64_t)(w.row0 + t0) * p.rows + col;
+    const float b0 = p.bias[0] ? p.bias[0][(int64_t)tile.group * p.rows + col] : 0.f;
+    const float b1 = p.bias[1] ? p.bias[1][(int64_t)tile.group * p.rows + col] : 0.f;
+    const float *s = p.sums + (int64_t)(tile.row0 + t0) * p.rows + col;
     float z[kJoinRows], u[kJoinRows];
 #pragma unroll
     for (int t = 0; t < kJoinRows; ++t) z[t] = u[t] = 0.f;
-    for (int i = 0; i < p.parts; ++i) {
+    const int64_t part = (1 + p.gated) * step;
+    for (int i = 0; i < p.parts; i += 4, s += 4 * part) {   // (four parts' loads at a time)
+        float v[4][kJoinRows], w[4][kJoinRows];
 #pragma unroll
-        for (int t = 0; t < kJoinRows; ++t)
-            if (t < n) {
-                z[t] += s[(int64_t)t * p.rows];
-                if (p.gated) u[t] += s[step + (int64_t)t * p.rows];
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int t = 0; t < kJoinRows; ++t) {
+                const bool there = i + k < p.parts && t < n;
+                v[k][t] = there ? s[k * part + (int64_t)t * p.rows] : 0.f;
+                w[k][t] = there && p.gated ? s[k * part + step + (int64_t)t * p.rows] : 0.f;
             }
-        s += (1 + p.gated) * step;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int t = 0; t < kJoinRows; ++t) z[t] += v[k][t], u[t] += w[k][t];
     }
 #pragma unroll
     for (int t = 0; t < kJoinRows; ++t) {
         if (t >= n) break;
-        finish_one(p, w.row0 + t0 + t, col, z[t] + b0, u[t] + b1);
+        finish_one(p, tile.row0 + t0 + t, col, z[t] + b0, u[t] + b1);
     }
 }
 
