@@ -399,10 +399,22 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
     const int64_t c = 4 * ((int64_t)(blockIdx.x % p.nb) * 256 + threadIdx.x);
     if (c >= p.n) return;   // (a multiple of 32)
     float y[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < p.top_k; ++k) {
-        const float w = p.w[t * p.top_k + k];
-        const float4 v = *reinterpret_cast<const float4 *>(p.d + (int64_t)p.place[t * p.top_k + k] * p.ldd + c);
-        y[0] = fmaf(w, v.x, y[0]), y[1] = fmaf(w, v.y, y[1]), y[2] = fmaf(w, v.z, y[2]), y[3] = fmaf(w, v.w, y[3]);
+    for (int k0 = 0; k0 < p.top_k; k0 += 4) {   // (four experts' loads at a time)
+        float4 v[4];
+        float w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t at = t * p.top_k + k0 + k;
+            const bool there = k0 + k < p.top_k;
+            w[k] = there ? p.w[at] : 0.f;
+            v[k] = there ? *reinterpret_cast<const float4 *>(p.d + (int64_t)p.place[at] * p.ldd + c) : float4{};
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k0 + k >= p.top_k) break;
+            y[0] = fmaf(w[k], v[k].x, y[0]), y[1] = fmaf(w[k], v[k].y, y[1]);
+            y[2] = fmaf(w[k], v[k].z, y[2]), y[3] = fmaf(w[k], v[k].w, y[3]);
+        }
     }
     if (p.residual) {
         float f[4];
