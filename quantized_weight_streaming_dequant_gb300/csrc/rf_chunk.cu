@@ -16,11 +16,11 @@
 // It reads X once from memory (the second pass over a row finds it in L2 or
 // closer) and writes 2 bytes an element (4 with two terms).  Bound: latency of
 // its chain offsets - row - scale - row - lines, and with long rows the loads in
-// flight: 2048 x 11008 bf16 in 26 us (3.4 TB/s, in and out), 2002 x 11008 fp32
-// in 33 us, 8192 x 2880 fp32 in 36 us.  Units written by the threads that
-// loaded them, eight rows a warp: 33, 48 and 49 us.  A few rows: 5 to 8 us.
+// flight: 2048 x 11008 bf16 in 25 us (3.6 TB/s, in and out), 2002 x 11008 fp32
+// in 31 us, 8192 x 2880 fp32 in 31 us.  Units written by the threads that
+// loaded them, eight rows a warp: 33, 48 and 49 us.  A few rows: 5 us.
 //
-// join_kernel adds a token's experts: 94 MB in and 12 MB out in 18 us (5.9
+// join_kernel adds a token's experts: 94 MB in and 12 MB out in 17 us (6.2
 // TB/s), bound by memory.
 #include <cuda_bf16.h>
 
@@ -449,11 +449,11 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // worth it while it saves a tenth of the SMs' rounds after what that launch,
 // the sums' traffic and the items' starts cost.  In SM cycles, as measured: a
 // slice's by what bounds it, 4,000 an item (2,500 where two CTAs share the SM),
-// 6,000 a launch, 1,500 bytes of sums a cycle.  9 fp32 tokens through
-// 2 x 11008 x 4096 Q4_0: 53 us, in one part 60; 77 through 4099 x 4096 Q4_K 41,
-// in one 60.  (The last part's warps
-// adding the sums in the product's launch instead of a second one: 60 us
-// against 55, they read them one latency after another.)
+// 3,500 a launch, 1,500 bytes of sums a cycle.  9 fp32 tokens through
+// 2 x 11008 x 4096 Q4_0: 46 us, in one part 60; 8 tokens 36, in one part 43; 77
+// through 4099 x 4096 Q4_K 40, in one 60.  (The last part's warps adding the
+// sums in the product's launch instead of a second one: 60 us against 55 in the
+// first case, they read them one latency after another.)
 void choose_parts(ChunkShape &sh, bool gated)
 {
     const int64_t tiles = sh.n_group == 1 ? (sh.n_row + sh.tile_tokens() - 1) / sh.tile_tokens()
@@ -464,7 +464,7 @@ void choose_parts(ChunkShape &sh, bool gated)
                           : sh.wt == 2 ? (sh.fmt == RF_Q4_K ? 1400 : 1000) : (sh.nt > 128 ? 640 : 420);
     auto cost = [&](int64_t parts) {
         const int64_t slices = std::min<int64_t>((nch + parts - 1) / parts * per, sh.nst);
-        const int64_t sums = parts > 1 ? 6000 + parts * (1 + gated) * sh.n_row * sh.rows * 8 / 1500 : 0;
+        const int64_t sums = parts > 1 ? 3500 + parts * (1 + gated) * sh.n_row * sh.rows * 8 / 1500 : 0;
         return (items * parts + sms - 1) / sms * (slice * slices + (sh.few ? 2500 : 4000)) + sums;
     };
     int64_t best = 1;
@@ -483,7 +483,7 @@ void choose_parts(ChunkShape &sh, bool gated)
 // sums, so that an epilogue runs beside the next item's products.  Tiles of up
 // to 16 operand rows multiply from registers (rf_chunk_few.cu): 8 bf16 tokens
 // through 2 x 11008 x 4096 Q4_0 31 us against 45, 16 tokens 37 against 45, 8
-// fp32 tokens 45 against 52, 128 fp32 tokens through 128 MXFP4 experts 505
+// fp32 tokens 45 against 52 (with the parts and loads of then), 128 fp32 tokens through 128 MXFP4 experts 505
 // against 529 (but 256 bf16 tokens 565 against 531); with 32 rows a tile they
 // were no faster (32 bf16 tokens 50 against 45, 32 fp16 tokens through Q8_0 66
 // against 50, 256 fp32 tokens through the experts 805 against 621).  (Tiles of 160 rows, which fill the last
