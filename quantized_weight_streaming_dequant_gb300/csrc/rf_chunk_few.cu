@@ -31,7 +31,8 @@
 // at the measured memory rate.  Measured, us a call on the GPU:
 //                                                   here   through tensor memory
 //   77 bf16 tokens, 128 experts of 2880 MXFP4        312   440   (copies alone: 224)
-//   6 fp32 tokens, the same                           98   150   (copies alone:  73)
+//   6 fp32 tokens, the same                           98   150   (copies alone:  79,
+//                                                         with a slower pre-pass)
 //   45 fp32 rows, 64 groups of 1408 x 2048 Q8_0       34    59   (copies alone:  28)
 //   8 bf16 tokens, 2 x 11008 x 4096 Q4_0              31    45
 // Steps (first case, us): 458 with all of a block decoded before its products
