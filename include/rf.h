@@ -918,10 +918,11 @@ RF_API rf_status rf_device_status(void);
  * tensor or bulk copies: a GEMV over device memory whose rows are 16-byte
  * aligned or take per-row bulk copies, an rf_gemm, or a product of the calls
  * for chunks of tokens.  In that launch one copy of its first CTA is never
- * issued (a stage of the GEMV's weights; the GEMM's second activation tile; the
- * chunk product's first or second), so the warps waiting for it give up after
- * limit_us microseconds, record RF_ERR_TIMEOUT, and the launch ends with
- * nothing in flight (its outputs are undefined).
+ * issued (a stage of the GEMV's weights; the GEMM's second activation tile; of
+ * a chunk product the first activations of the first piece of work, whichever
+ * CTA has it), so the warps waiting for it give up after limit_us
+ * microseconds, record RF_ERR_TIMEOUT, and the launch ends with nothing in
+ * flight (its outputs are undefined).
  * limit_us = 0 disarms.  Errors: RF_ERR_INVALID_ARG for limit_us above
  * 2,000,000. */
 RF_API rf_status rf_debug_arm_wait_fault(uint32_t limit_us);

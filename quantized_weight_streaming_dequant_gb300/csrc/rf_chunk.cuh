@@ -56,7 +56,7 @@ struct Params {
     void *Y;
     float *sums;              // with several parts: [part][projection][row of the call][rows]
     int32_t parts, part_chunks, n_row;
-    int32_t withhold;         // test hook: CTA 0 never copies this slice's activations
+    int32_t withhold;         // test hook: the first stage of the first item is never copied
     long long limit_cycles;   // of a wait
 };
 

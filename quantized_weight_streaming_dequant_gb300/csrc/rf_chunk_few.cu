@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
             const uint8_t *src = p.img + ((int64_t)w.gran * p.nst + part * p.part_chunks * QPC) * C::GB;
             for (int c = part * p.part_chunks, end = min(p.nch, c + p.part_chunks); ok && c < end; ++c) {
                 if (!(ok = waits(bar(C::EMPTY + r), ph))) break;
-                const bool withhold = blockIdx.x == 0 && n == 0 && p.withhold >= 0;
+                const bool withhold = blockIdx.x == 0 && n == 0 && p.withhold;   // (CTA 0 has the first item)
                 if (withhold) skipped = n;
                 if (lane == 0) bar_expect(bar(C::FULL + r), (uint32_t)(C::OPS + (p.copies ? kM * p.bw : 0)));
                 __syncwarp();

@@ -134,7 +134,7 @@ struct Cfg {
 };
 
 struct Item {
-    int32_t group, row0, cnt, gran, rt, stop, part, pad;
+    int32_t group, row0, cnt, gran, rt, stop, part, first;   // first: the launch's first item
 };
 
 __host__ __device__ constexpr uint32_t idesc_n(int n)
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     w.group = t.group, w.row0 = t.row0, w.cnt = t.cnt, w.gran = t.gran;
                     w.rt = at % p.nrt;
                     w.part = index % p.parts;
+                    w.first = index == 0;
                 }
                 const bool end = w.stop != 0;
                 bar_arrive(bar(C::IFULL + slot));
@@ -373,13 +374,14 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 if (!wait(bar(C::IFULL + slot), (it / kItems) & 1)) break;
                 const int grans = (items[slot].cnt + GT - 1) / GT, gran = items[slot].gran, end = items[slot].stop;
                 const int from = items[slot].part * p.part_chunks * QPC, nsl = min(p.nst - from, p.part_chunks * QPC);
+                const bool withhold = p.withhold && items[slot].first;
                 bar_arrive(bar(C::IEMPTY + slot));
                 if (end) break;
                 const uint32_t slice = (uint32_t)grans * kGranBytes;
                 const uint8_t *src = p.img + (int64_t)gran * p.nst * kGranBytes + (int64_t)from * slice;
                 for (int b = 0; b < nsl; b += KS, ++n) {
                     if (!(ok = wait(bar(C::BDONE + ib), ph))) break;
-                    if (blockIdx.x == 0 && n == (uint32_t)p.withhold) {
+                    if (withhold && b == 0) {
                         skipped = n;
                     } else {
                         const int slices = KS > 1 ? min(KS, nsl - b) : 1;
@@ -794,10 +796,10 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
     p.Y = g.Y;
     p.ldy = g.ldy;
     p.limit_cycles = 2 * (long long)kWaitLimitNs;   // (at most 2.07 GHz)
-    p.withhold = -1;
+    p.withhold = 0;
     if (const unsigned long long lim = take_wait_fault()) {
         p.limit_cycles = 2 * (long long)lim;
-        p.withhold = sh.nst > 1 ? 1 : 0;
+        p.withhold = 1;
     }
     p.slot = (uint32_t)sh.nt * kSliceK * 2;
     p.parts = sh.parts;
