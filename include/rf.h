@@ -766,7 +766,10 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  *
  * Formats: RF_Q4_0, RF_Q8_0, RF_MXFP4, RF_Q4_K (others:
  * RF_ERR_UNSUPPORTED_FMT).  X, Y and residual are of one `dtype` (RF_F32,
- * RF_F16, RF_BF16); biases are fp32.  Y is computed in fp32 and rounded once.
+ * RF_F16, RF_BF16); with RF_Y_F32 added to it (rf_gemm_fused, rf_gemm_grouped
+ * and their workspaces) Y and residual are fp32 and the type is X's alone: a
+ * router's logits, which a 16-bit type would round to ties.  Biases are fp32.
+ * Y is computed in fp32 and rounded once.
  * Precision, from the operands of the tensor cores (products are exact, sums
  * fp32).  X's values enter
  *   RF_F16        as they are;
@@ -778,9 +781,10 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  * Weights (below 65504 in magnitude) enter
  *   MXFP4         as they are (below 2^-24: to 2^-25),
  *   others        RF_F32: as two fp16 terms (22 bits, small ones to 2^-36);
- *                 RF_F16: as two fp16 terms (to 2^-22 or 2^-25, whichever is
- *                 more); RF_BF16: rounded once to fp16, as rf_gemm's (2^-11 or
- *                 2^-25: an eighth of half a step of bf16).
+ *                 RF_F16, and RF_BF16 with RF_Y_F32: as two fp16 terms (to
+ *                 2^-22 or 2^-25, whichever is more); RF_BF16: rounded once to
+ *                 fp16, as rf_gemm's (2^-11 or 2^-25: an eighth of half a step
+ *                 of bf16).
  * A row of X that holds an infinity or a NaN has products that are infinite or
  * NaN (the activations clamp infinities, NaN stays); other rows do not see it.
  * Results do not depend on the other rows' values or on timing (the number of
@@ -788,6 +792,7 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  * Weight tensors: 16-byte aligned, rows of rf_row_bytes each; all bytes of the
  * tensors given may be read.  Workspaces: device, 256-byte aligned, at least
  * the stated bytes, overwritten, used by one call at a time. */
+#define RF_Y_F32 256
 #define RF_ACT_NONE 0           /* z */
 #define RF_ACT_SILU 1           /* z / (1 + exp(-z)) */
 #define RF_ACT_GELU 2           /* z / 2 * (1 + erf(z / sqrt(2))) */
@@ -798,8 +803,8 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
 /* What follows a product z = W x: y = residual + act(z + bias, U x + up_bias).
  * bias, up_bias: one float per output row of each matrix (stacked like the
  * matrices), or NULL; up_bias only with the gated activations (SWIGLU,
- * SWIGLU_CLAMPED), which take a second matrix U.  residual: rows of the
- * call's dtype ld_residual elements apart, one for each row of Y, or NULL.
+ * SWIGLU_CLAMPED), which take a second matrix U.  residual: rows of Y's type
+ * ld_residual elements apart, one for each row of Y, or NULL.
  * alpha, limit: SWIGLU_CLAMPED's, as rf_moe_ffn_biased's. */
 typedef struct rf_epilogue {
     const float *bias, *up_bias;

@@ -22,6 +22,7 @@ BLOCK_BYTES = {Q4_0: 18, Q8_0: 34, Q4_K: 144, Q6_K: 210, MXFP4: 17}
 BLOCK_ELEMS = {Q4_0: 32, Q8_0: 32, Q4_K: 256, Q6_K: 256, MXFP4: 32}
 
 F32, F16, BF16 = 0, 1, 30           # activation types
+Y_F32 = 256                         # added to a product's: fp32 outputs
 ROPE_HALF, ROPE_PAIRS = 0, 1        # rotation styles
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU, ACT_SWIGLU_CLAMPED = 0, 1, 2, 3, 4   # activations of rf_epilogue
 KV_BLOCK = 32                       # tokens that share a scale byte of the KV cache
@@ -847,28 +848,35 @@ def _space(workspace, need: int, stream, device):
     return workspace, _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
 
 
-def gemm_fused_workspace(fmt: int, rows: int, in_dim: int, X, stream=None):
+def _product_types(dt: int, y_f32: bool):
+    """(dtype of a product of X's type, Y's type)"""
+    return (dt | Y_F32, F32) if y_f32 else (dt, dt)
+
+
+def gemm_fused_workspace(fmt: int, rows: int, in_dim: int, X, stream=None, y_f32: bool = False):
     """Device workspace for gemm_fused() of X on `stream`, or None."""
-    n = lib().rf_gemm_fused_workspace_bytes(fmt, rows, in_dim, _dtype(X), X.shape[0])
+    n = lib().rf_gemm_fused_workspace_bytes(fmt, rows, in_dim, _product_types(_dtype(X), y_f32)[0], X.shape[0])
     return _new(stream, n, _U8_TYPE, X.device, out=False) if n else None
 
 
 def gemm_fused(fmt: int, W, row_start: int, row_end: int, in_dim: int, X, Y=None, *, act: int = ACT_NONE, up=None,
                bias=None, up_bias=None, alpha: float = 1.702, limit: float = 7.0, residual=None, workspace=None,
-               stream=None):
+               stream=None, y_f32: bool = False):
     """rf_gemm_fused: residual + act(W X + bias, up X + up_bias) for the rows
     [row_start, row_end).  X (n_tok, in_dim) and residual (n_tok, rows) are of
     one type (rows may be strided); biases are float32, one per row of the
-    window.  Returns Y (n_tok, rows), of X's type."""
+    window.  Returns Y (n_tok, rows), of X's type; with y_f32 Y and residual
+    are float32."""
     _known_fmt(fmt)
     px, ldx, n_tok, n, dt = _matrix_rows(X, "X")
     if n != in_dim:
         raise ValueError(f"X must be (n_tok, {in_dim})")
     rows = max(row_end - row_start, 0)
+    dt, dty = _product_types(dt, y_f32)
     if Y is None:
-        Y = _new(stream, (n_tok, rows), X.dtype, X.device)
-    py, ldy = _rows(Y, n_tok, rows, dt, "Y")
-    e = _epilogue(rows, n_tok, rows, dt, act, up, bias, up_bias, alpha, limit, residual)
+        Y = _new(stream, (n_tok, rows), _F32_TYPE if y_f32 else X.dtype, X.device)
+    py, ldy = _rows(Y, n_tok, rows, dty, "Y")
+    e = _epilogue(rows, n_tok, rows, dty, act, up, bias, up_bias, alpha, limit, residual)
     if workspace is None:
         need = lib().rf_gemm_fused_workspace_bytes(fmt, rows, in_dim, dt, n_tok)
     workspace, ws, ws_bytes = _space(workspace, need if workspace is None else 0, stream, X.device)
@@ -879,21 +887,23 @@ def gemm_fused(fmt: int, W, row_start: int, row_end: int, in_dim: int, X, Y=None
     return Y
 
 
-def gemm_grouped_workspace(fmt: int, n_group: int, rows: int, in_dim: int, X, n_row: int, stream=None):
+def gemm_grouped_workspace(fmt: int, n_group: int, rows: int, in_dim: int, X, n_row: int, stream=None,
+                           y_f32: bool = False):
     """Device workspace for gemm_grouped() of n_row rows on `stream`, or None."""
-    n = lib().rf_gemm_grouped_workspace_bytes(fmt, n_group, rows, in_dim, _dtype(X), n_row)
+    n = lib().rf_gemm_grouped_workspace_bytes(fmt, n_group, rows, in_dim, _product_types(_dtype(X), y_f32)[0], n_row)
     return _new(stream, n, _U8_TYPE, X.device, out=False) if n else None
 
 
 def gemm_grouped(fmt: int, W, rows: int, in_dim: int, X, offsets, order=None, per: int = 1, Y=None, *,
                  act: int = ACT_NONE, up=None, bias=None, up_bias=None, alpha: float = 1.702, limit: float = 7.0,
-                 residual=None, workspace=None, stream=None):
+                 residual=None, workspace=None, stream=None, y_f32: bool = False):
     """rf_gemm_grouped: row r of Y, in group g (offsets[g] <= r < offsets[g +
     1]), is residual + act(W_g x + bias_g, up_g x + up_bias_g), where x is row
     r of X, or row order[r] // per.  W and up are (n_group, rows, in_dim)
     quantized, offsets (n_group + 1,) and order (n_row,) int32 device tensors,
-    biases (n_group, rows) float32.  Rows of no group are left as they were (a
-    Y made here holds anything there)."""
+    biases (n_group, rows) float32.  Y and residual are of X's type, with y_f32
+    float32.  Rows of no group are left as they were (a Y made here holds
+    anything there)."""
     _known_fmt(fmt)
     px, ldx, n_x, n, dt = _matrix_rows(X, "X")
     if n != in_dim:
@@ -903,10 +913,11 @@ def gemm_grouped(fmt: int, W, rows: int, in_dim: int, X, offsets, order=None, pe
                               not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous int32 CUDA tensor")
     n_group, n_row = offsets.numel() - 1, n_x if order is None else order.numel()
+    dt, dty = _product_types(dt, y_f32)
     if Y is None:
-        Y = _new(stream, (n_row, rows), X.dtype, X.device)
-    py, ldy = _rows(Y, n_row, rows, dt, "Y")
-    e = _epilogue(max(n_group, 0) * rows, n_row, rows, dt, act, up, bias, up_bias, alpha, limit, residual)
+        Y = _new(stream, (n_row, rows), _F32_TYPE if y_f32 else X.dtype, X.device)
+    py, ldy = _rows(Y, n_row, rows, dty, "Y")
+    e = _epilogue(max(n_group, 0) * rows, n_row, rows, dty, act, up, bias, up_bias, alpha, limit, residual)
     if workspace is None:
         need = lib().rf_gemm_grouped_workspace_bytes(fmt, n_group, rows, in_dim, dt, n_row)
     workspace, ws, ws_bytes = _space(workspace, need if workspace is None else 0, stream, X.device)

@@ -441,6 +441,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
 
 bool fmt_has_chunks(int fmt) { return fmt == RF_Q4_0 || fmt == RF_Q8_0 || fmt == RF_MXFP4 || fmt == RF_Q4_K; }
 bool dtype_ok(int d) { return d == RF_F32 || d == RF_F16 || d == RF_BF16; }
+// X's and Y's types of a product's dtype (X's, with RF_Y_F32 or without).
+int x_dtype(int d) { return d & ~RF_Y_F32; }
+int y_dtype(int d) { return (d & RF_Y_F32) != 0 ? RF_F32 : d; }
 int dtype_size(int d) { return d == RF_F32 ? 4 : 2; }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -492,7 +495,8 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
 {
     ChunkShape sh;
     sh.fmt = fmt;
-    sh.xt = dtype == RF_F32 ? 2 : 1;
+    sh.xt = x_dtype(dtype) == RF_F32 ? 2 : 1;
+    // (A weight's rounding to fp16 is an eighth of half a step of a bf16 output, but most of what an fp32 one is off by.)
     sh.wt = dtype != RF_BF16 && fmt != RF_MXFP4 ? 2 : 1;
     sh.n_row = n_row, sh.n_group = n_group, sh.rows = rows, sh.in_dim = in_dim;
     sh.nst = (int)((in_dim + kSliceK - 1) / kSliceK);
@@ -519,7 +523,7 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
 // Sizes that a product takes, for the entry points and the workspace.
 rf_status check_sizes(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row)
 {
-    if (!fmt_has_chunks(fmt) || !dtype_ok(dtype)) return RF_ERR_UNSUPPORTED_FMT;
+    if (!fmt_has_chunks(fmt) || !dtype_ok(x_dtype(dtype))) return RF_ERR_UNSUPPORTED_FMT;
     if (n_group < 1 || rows < 0 || n_row < 0 || in_dim <= 0 || in_dim % block_elems_of(fmt) != 0) return RF_ERR_INVALID_ARG;
     if (in_dim > (1 << 20) || rows > 0x7fffffffLL || n_group > 65536 || n_row > kMaxPieces) return RF_ERR_TOO_LARGE;
     for (const bool gated : {false, true}) {
@@ -531,7 +535,7 @@ rf_status check_sizes(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t
 
 bool gated_act(int act) { return act == RF_ACT_SWIGLU || act == RF_ACT_SWIGLU_CLAMPED; }
 
-rf_status check_epilogue(const rf_epilogue &e, const void *up, int dtype, int64_t rows)
+rf_status check_epilogue(const rf_epilogue &e, const void *up, int64_t rows)
 {
     if (e.act < RF_ACT_NONE || e.act > RF_ACT_SWIGLU_CLAMPED || e.reserved != 0) return RF_ERR_INVALID_ARG;
     if (gated_act(e.act) != (up != nullptr) || (e.up_bias && !up)) return RF_ERR_INVALID_ARG;
@@ -698,16 +702,16 @@ rf_status rf_gemm_fused(int fmt, const void *W, const void *up, int64_t row_star
     rf_status st = check_sizes(fmt, dtype, 1, rows, in_dim, n_tok);
     if (st != RF_OK) return st;
     if (!W || (n_tok > 0 && rows > 0 && (!X || !Y)) || ldx < in_dim || ldy < rows) return RF_ERR_INVALID_ARG;
-    if ((st = check_epilogue(e, up, dtype, rows)) != RF_OK) return st;
-    const int size = dtype_size(dtype);
-    if (!aligned(W, 16) || !aligned(up, 16) || !aligned(X, size) || !aligned(Y, size) || !aligned(e.residual, size) ||
+    if ((st = check_epilogue(e, up, rows)) != RF_OK) return st;
+    const int size = dtype_size(x_dtype(dtype)), size_y = dtype_size(y_dtype(dtype));
+    if (!aligned(W, 16) || !aligned(up, 16) || !aligned(X, size) || !aligned(Y, size_y) || !aligned(e.residual, size_y) ||
         !aligned(e.bias, 4) || !aligned(e.up_bias, 4))
         return RF_ERR_MISALIGNED;
     if (rows == 0 || n_tok == 0) return RF_OK;
     const ChunkShape sh = chunk_shape(fmt, dtype, 1, rows, in_dim, n_tok, up != nullptr);
     if ((st = check_workspace(workspace, workspace_bytes, sh.bytes)) != RF_OK) return st;
-    const Source x = {dtype, X, ldx, n_tok, nullptr, nullptr, 1};
-    return run_product(sh, x, W, up, row_start, rows, row_end, e, dtype, Y, ldy, workspace, static_cast<cudaStream_t>(stream));
+    const Source x = {x_dtype(dtype), X, ldx, n_tok, nullptr, nullptr, 1};
+    return run_product(sh, x, W, up, row_start, rows, row_end, e, y_dtype(dtype), Y, ldy, workspace, static_cast<cudaStream_t>(stream));
 }
 
 rf_status rf_gemm_grouped(int fmt, const void *W, const void *up, int n_group, int64_t rows, int64_t in_dim, int dtype,
@@ -721,16 +725,16 @@ rf_status rf_gemm_grouped(int fmt, const void *W, const void *up, int n_group, i
     if (!W || !offsets || (n_row > 0 && rows > 0 && !Y) || (n_x > 0 && !X) || n_x < 0 || ldx < in_dim || ldy < rows || per < 1 ||
         (!order && n_x < n_row))
         return RF_ERR_INVALID_ARG;
-    if ((st = check_epilogue(e, up, dtype, rows)) != RF_OK) return st;
-    const int size = dtype_size(dtype);
-    if (!aligned(W, 16) || !aligned(up, 16) || !aligned(X, size) || !aligned(Y, size) || !aligned(e.residual, size) ||
+    if ((st = check_epilogue(e, up, rows)) != RF_OK) return st;
+    const int size = dtype_size(x_dtype(dtype)), size_y = dtype_size(y_dtype(dtype));
+    if (!aligned(W, 16) || !aligned(up, 16) || !aligned(X, size) || !aligned(Y, size_y) || !aligned(e.residual, size_y) ||
         !aligned(e.bias, 4) || !aligned(e.up_bias, 4) || !aligned(offsets, 4) || !aligned(order, 4))
         return RF_ERR_MISALIGNED;
     if (rows == 0 || n_row == 0) return RF_OK;
     const ChunkShape sh = chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, up != nullptr);
     if ((st = check_workspace(workspace, workspace_bytes, sh.bytes)) != RF_OK) return st;
-    const Source x = {dtype, X, ldx, n_x, offsets, order, per};
-    return run_product(sh, x, W, up, 0, rows, (int64_t)n_group * rows, e, dtype, Y, ldy, workspace,
+    const Source x = {x_dtype(dtype), X, ldx, n_x, offsets, order, per};
+    return run_product(sh, x, W, up, 0, rows, (int64_t)n_group * rows, e, y_dtype(dtype), Y, ldy, workspace,
                        static_cast<cudaStream_t>(stream));
 }
 
@@ -760,7 +764,7 @@ rf_status rf_moe_route_tokens(int dtype, const void *logits, int64_t ld, int64_t
 size_t rf_moe_tokens_workspace_bytes(int fmt, int n_expert, int top_k, int64_t n_ff, int64_t n_embd, int dtype, int64_t n_tok)
 {
     if (n_tok <= 0 || n_expert < 1 || n_expert > 1024 || top_k < 1 || top_k > 8 || top_k > n_expert ||
-        n_tok > kMaxPieces / top_k || n_ff <= 0 || n_embd <= 0)
+        n_tok > kMaxPieces / top_k || n_ff <= 0 || n_embd <= 0 || !dtype_ok(dtype))
         return 0;
     if (check_sizes(fmt, dtype, n_expert, n_ff, n_embd, n_tok * top_k) != RF_OK ||
         check_sizes(fmt, dtype, n_expert, n_embd, n_ff, n_tok * top_k) != RF_OK)
@@ -777,6 +781,7 @@ rf_status rf_moe_ffn_tokens(int fmt, int dtype, int logits_dtype, const void *lo
     rf_status st = check_route(logits_dtype, logits, ld_logits, n_tok, n_expert, top_k);
     if (st != RF_OK) return st;
     if (n_ff <= 0 || n_embd <= 0) return RF_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return RF_ERR_UNSUPPORTED_FMT;
     if ((st = check_sizes(fmt, dtype, n_expert, n_ff, n_embd, n_tok * top_k)) != RF_OK ||
         (st = check_sizes(fmt, dtype, n_expert, n_embd, n_ff, n_tok * top_k)) != RF_OK)
         return st;
@@ -784,7 +789,7 @@ rf_status rf_moe_ffn_tokens(int fmt, int dtype, int logits_dtype, const void *lo
         (residual && ld_residual < n_embd) || !gated_act(act))
         return RF_ERR_INVALID_ARG;
     const rf_epilogue first = {gate_bias, up_bias, nullptr, 0, act, alpha, limit, 0};
-    if ((st = check_epilogue(first, up, dtype, n_ff)) != RF_OK) return st;
+    if ((st = check_epilogue(first, up, n_ff)) != RF_OK) return st;
     const int size = dtype_size(dtype);
     if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(down, 16) || !aligned(X, size) || !aligned(Y, size) ||
         !aligned(residual, size) || !aligned(gate_bias, 4) || !aligned(up_bias, 4) || !aligned(down_bias, 4))

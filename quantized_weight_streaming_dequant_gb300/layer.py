@@ -179,12 +179,13 @@ class RoutedFFN:
 
     def step(self, residual, workspace=None, stream=None):
         """residual (n_tok, d_model), float32, float16 or bfloat16, through the
-        FFN.  Returns a dict: the normed input "x", the router's "logits" and
-        the new residual stream "y"."""
+        FFN.  Returns a dict: the normed input "x", the router's "logits"
+        (float32: in 16 bits they would round to ties) and the new residual
+        stream "y"."""
         o = {}
         _, o["x"] = rf.norm_residual(residual, weight=self.norm, eps=self.eps, stream=stream)
         o["logits"] = rf.gemm_fused(self.router_fmt, self.router, 0, self.n_expert, self.d_model, o["x"],
-                                    bias=self.router_bias, stream=stream)
+                                    bias=self.router_bias, stream=stream, y_f32=True)
         o["y"] = rf.moe_ffn_tokens(self.fmt, o["logits"], self.top_k, self.gate, self.up, self.down, self.d_ff,
                                    self.d_model, o["x"], gate_bias=self.gate_bias, up_bias=self.up_bias,
                                    down_bias=self.down_bias, alpha=self.alpha, limit=self.limit, residual=residual,
