@@ -480,6 +480,13 @@ void choose_parts(ChunkShape &sh, bool gated)
     sh.parts = (int)((nch + sh.part_chunks - 1) / sh.part_chunks);
 }
 
+// Slices after which a 16-bit call's sums leave tensor memory for a rounded
+// addition.  The tensor cores truncate theirs, always towards zero, so that a
+// sum of one sign drifts with its length: 2^20 inputs in one go end 6.9e-3 low
+// (fourteen times half a step of fp16), 16,384 1.2e-4, 4,096 3e-5.  bf16 outputs
+// do not see 1.2e-4; what is rounded more finely leaves sooner.
+constexpr int kSegment = 64, kSegmentBf16 = 256;
+
 // The operands of a product of n_row rows shared by n_group groups.  Tiles of
 // 192 operand rows where the groups fill them (a weight slice is decoded once
 // per tile), of 128 where they do not; both let tensor memory hold two items'
@@ -510,12 +517,16 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     sh.cap_tiles = std::min<int64_t>(n_row, n_row / T + n_group);
     sh.cap_gran = n_row / GT + n_group;
     choose_parts(sh, gated);
+    sh.segment = dtype == RF_BF16 ? kSegmentBf16 : kSegment;
+    sh.held = !sh.few && sh.xt == 1 && std::min(sh.nst, sh.part_chunks * per) > sh.segment;
     size_t at = sizeof(ChunkPlan);
     sh.at_tiles = at, at = up256(at + (size_t)sh.cap_tiles * sizeof(ChunkTile));
     sh.at_inv = at, at = up256(at + (size_t)sh.cap_gran * GT * sizeof(float));
     sh.at_img = at, at = up256(at + (size_t)sh.cap_gran * sh.nst * sh.gran_bytes());
     sh.at_sums = at;
     if (sh.parts > 1) at = up256(at + (size_t)sh.parts * (1 + gated) * n_row * rows * sizeof(float));
+    sh.at_held = at;
+    if (sh.held) at = up256(at + (size_t)num_sms() * sh.nt * 128 * sizeof(float));
     sh.bytes = at;
     return sh;
 }

@@ -55,6 +55,8 @@ struct Params {
     int64_t ldr, ldy;
     void *Y;
     float *sums;              // with several parts: [part][projection][row of the call][rows]
+    float *held;              // 16-bit calls' sums between segments: [CTA][operand row][kM]
+    int32_t segment, held_rows;   // slices of a segment, operand rows of a CTA's share
     int32_t parts, part_chunks, n_row;
     int32_t withhold;         // test hook: the first stage of the first item is never copied
     long long limit_cycles;   // of a wait

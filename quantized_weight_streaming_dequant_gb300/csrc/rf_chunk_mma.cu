@@ -114,7 +114,8 @@ struct Cfg {
     // zero), rounded additions in registers do not drift.  Q4_K's weights have
     // a mean, so that its sums grow over a row: sooner (1.3e-6 against 0.7e-6
     // from 64 bits in a routed FFN).
-    static constexpr int FLUSH = XT == 1 ? 1 << 30 : (FMT == RF_Q4_K ? 2 : 4);
+    // (16-bit calls: Params::segment slices, see chunk_shape.)
+    static constexpr int FLUSH = XT == 1 ? 4 : (FMT == RF_Q4_K ? 2 : 4);
     // Shared memory: stages of activations, raw chunks, and 16 bytes that a
     // last load may touch.  Activations come from L2 in about as long as eight
     // slices take; the weights come from memory and get the rest.
@@ -420,8 +421,9 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 bar_arrive(bar(C::IEMPTY + slot));
                 if (end) break;
                 const uint32_t id = WT == 2 && XT == 2 ? idesc_n((grans + 1) / 2 * 16) : idesc_n(kGranRows * grans);
+                const int flush = (XT == 1 ? p.segment : C::FLUSH) - 1;
                 for (int b = 0; b < nsl;) {
-                    const bool fresh = b % C::FLUSH == 0;
+                    const bool fresh = (b & flush) == 0;
                     const uint32_t acc = tmem + (seg % NBUF) * C::ACC;
                     if (fresh) {
                         if (!(ok = wait(bar(C::ACCE + seg % NBUF), ((seg / NBUF) & 1) ^ 1))) break;
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     bar_commit(b_done);
                     ready = b_next && f_next;
                     b += KS;
-                    if (b >= nsl || b % C::FLUSH == 0) {
+                    if (b >= nsl || (b & flush) == 0) {
                         bar_commit(bar(C::ACCF + seg % NBUF));
                         ++seg;
                     }
@@ -591,29 +593,47 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 if (lane == 0) bar_arrive(bar(C::ACCE + seg % NBUF));
                 ++seg;
             };
+            const int nsl = min(p.nst - w.part * p.part_chunks * QPC, p.part_chunks * QPC);
             if constexpr (XT == 1) {
-                float next[16];
-                load_inv(inv, next);
-                if (!waits(bar(C::ACCF + seg % NBUF), (seg / NBUF) & 1)) break;
-                tc_fence_after();
-                const uint32_t acc = tmem + lanes + (seg % NBUF) * C::ACC;
+                bool ok = true;
 #pragma unroll 1
-                for (int t0 = 0; t0 < w.cnt; t0 += 16) {
-                    float z[16], f[16];
-                    uint32_t v[16];
-                    tmem_ld16(acc + t0, v);
+                for (int b0 = 0; b0 < nsl; b0 += p.segment) {
+                    // Sums so far, this thread's own: of a row that has several segments.
+                    float *held = p.held + ((int64_t)blockIdx.x * p.held_rows * kM + 32 * w4 + lane);
+                    const bool last = b0 + p.segment >= nsl;
+                    float next[16];
+                    load_inv(inv, next);
+                    if (!(ok = waits(bar(C::ACCF + seg % NBUF), (seg / NBUF) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem + lanes + (seg % NBUF) * C::ACC;
+#pragma unroll 1
+                    for (int t0 = 0; t0 < w.cnt; t0 += 16) {
+                        float z[16], f[16];
+                        uint32_t v[16];
+                        tmem_ld16(acc + t0, v);
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) f[u] = next[u];
-                    if (t0 + 16 < w.cnt) load_inv(inv + t0 + 16, next);
-                    tmem_ld_wait();
+                        for (int u = 0; u < 16; ++u) f[u] = next[u];
+                        if (t0 + 16 < w.cnt) load_inv(inv + t0 + 16, next);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) z[u] = __uint_as_float(v[u]);
-                    if (t0 + 16 >= w.cnt) release();
-                    if (p.parts > 1) keep(p, z, f, w.part, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
-                    else finish_typed(p, z, f, b, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
+                        for (int u = 0; u < 16; ++u) z[u] = __uint_as_float(v[u]);
+                        if (t0 + 16 >= w.cnt) release();
+                        if (b0 > 0) {
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) z[u] += held[(t0 + u) * kM];
+                        }
+                        if (!last) {
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) held[(t0 + u) * kM] = z[u];
+                        } else if (p.parts > 1) {
+                            keep(p, z, f, w.part, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
+                        } else {
+                            finish_typed(p, z, f, b, (int64_t)w.row0 + t0, w.cnt - t0, col, in, half);
+                        }
+                    }
                 }
+                if (!ok) break;
             } else {
-                const int nsl = min(p.nst - w.part * p.part_chunks * QPC, p.part_chunks * QPC);
                 // 64 tokens' sums in registers, over the item's flushes.
                 float sum[C::T];
                 bool ok = true;
@@ -806,6 +826,9 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
     p.part_chunks = sh.part_chunks;
     p.n_row = (int32_t)sh.n_row;
     p.sums = reinterpret_cast<float *>(g.ws + sh.at_sums);
+    p.held = reinterpret_cast<float *>(g.ws + sh.at_held);
+    p.segment = sh.segment;
+    p.held_rows = sh.held ? sh.nt : 0;
     const int grid = (int)std::min<int64_t>(num_sms(), sh.cap_tiles * p.nrt * p.parts);
     rf_status st;
     if (sh.few) st = launch_chunk_few(sh, p, s);
