@@ -770,8 +770,11 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  * and their workspaces) Y and residual are fp32 and the type is X's alone: a
  * router's logits, which a 16-bit type would round to ties.  Biases are fp32.
  * Y is computed in fp32 and rounded once.
- * Precision, from the operands of the tensor cores (products are exact, sums
- * fp32).  X's values enter
+ * Precision, from the operands of the tensor cores.  Products are exact, sums
+ * fp32; the tensor cores truncate an addition (of 16 inputs' products, off by
+ * 2^-22 of the sum of their magnitudes at most), so sums leave them for rounded
+ * additions after 256 inputs (RF_F32), 4,096 (RF_F16, and with RF_Y_F32) or
+ * 16,384 (RF_BF16) at most.  X's values enter
  *   RF_F16        as they are;
  *   RF_F32, BF16  after their row was scaled by a power of two that puts its
  *                 largest finite value at [2^14, 2^15): RF_F32 as two fp16

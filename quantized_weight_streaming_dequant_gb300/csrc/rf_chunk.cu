@@ -480,7 +480,7 @@ void choose_parts(ChunkShape &sh, bool gated)
     sh.parts = (int)((nch + sh.part_chunks - 1) / sh.part_chunks);
 }
 
-// Slices after which a 16-bit call's sums leave tensor memory for a rounded
+// Slices after which a 16-bit call's sums leave the tensor cores for a rounded
 // addition.  The tensor cores truncate theirs, always towards zero, so that a
 // sum of one sign drifts with its length: 2^20 inputs in one go end 6.9e-3 low
 // (fourteen times half a step of fp16), 16,384 1.2e-4, 4,096 3e-5.  bf16 outputs
@@ -518,7 +518,7 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     sh.cap_gran = n_row / GT + n_group;
     choose_parts(sh, gated);
     sh.segment = dtype == RF_BF16 ? kSegmentBf16 : kSegment;
-    sh.held = !sh.few && sh.xt == 1 && std::min(sh.nst, sh.part_chunks * per) > sh.segment;
+    sh.segments = sh.xt == 1 && std::min(sh.nst, sh.part_chunks * per) > sh.segment;
     size_t at = sizeof(ChunkPlan);
     sh.at_tiles = at, at = up256(at + (size_t)sh.cap_tiles * sizeof(ChunkTile));
     sh.at_inv = at, at = up256(at + (size_t)sh.cap_gran * GT * sizeof(float));
@@ -526,7 +526,7 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     sh.at_sums = at;
     if (sh.parts > 1) at = up256(at + (size_t)sh.parts * (1 + gated) * n_row * rows * sizeof(float));
     sh.at_held = at;
-    if (sh.held) at = up256(at + (size_t)num_sms() * sh.nt * 128 * sizeof(float));
+    if (sh.segments && !sh.few) at = up256(at + (size_t)num_sms() * sh.nt * 128 * sizeof(float));
     sh.bytes = at;
     return sh;
 }

@@ -37,8 +37,8 @@ struct ChunkShape {
     int nst;                                 // slices (few: whole chunks, the last ones zeros)
     int64_t cap_tiles, cap_gran;             // token tiles and granules at most
     int parts, part_chunks;                  // parts of a row's raw chunks, and chunks per part
-    int segment;                             // slices after which 16-bit calls' sums leave tensor memory (a power of two)
-    bool held;                               // a part has several such segments
+    int segment;                             // slices after which 16-bit calls' sums leave the tensor cores (a power of two)
+    bool segments;                           // a part has several such segments
     size_t at_tiles, at_inv, at_img, at_sums, at_held, bytes;   // workspace: plan, tiles, 1 / row scale, images, parts'
                                                                 // sums, segments' sums (a tile for each CTA)
     int tile_tokens() const { return nt / xt; }

@@ -151,7 +151,12 @@ struct Weights<RF_Q4_K, L> {
     }
 };
 
-template <int FMT, int NT, int XT, int WT>
+// LONG: sums of 16-bit calls leave the tensor cores' truncated additions with
+// every raw chunk, as rows of several segments need it (see chunk_shape); the
+// registers for both sums cost shorter rows 0 to 4 % (77 bf16 tokens through the
+// experts 308 against 305 us, 150 fp16 tokens 435 against 422, 16 fp16 tokens
+// through 22016 x 4096 Q8_0 50.6 against 48.7).
+template <int FMT, int NT, int XT, int WT, bool LONG>
 __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_constant__ Params p)
 {
     using C = Few<FMT, NT, XT, WT>;
@@ -387,12 +392,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
 #pragma unroll
                 for (int q4 = 0; q4 < QPC; q4 += 4) four(q4, std::false_type());
             }
+            if constexpr (LONG) flush();
             if (tails) fence_async_smem();   // the next copy follows these stores
             __syncwarp();
             if (lane == 0) bar_arrive(bar(C::EMPTY + r));
             if (++r == C::S) r = 0, ph ^= 1u;
         }
-        if constexpr (XT == 1) flush();
+        if constexpr (XT == 1 && !LONG) flush();
         if constexpr (C::BOTH) {   // the low terms' columns are two lanes on
 #pragma unroll
             for (int k = 0; k < 4; ++k) sum[0][k] = fmaf(__shfl_xor_sync(0xffffffffu, sum[0][k], 2), 1.f / 2048.f, sum[0][k]);
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 2) few_kernel(const __grid_
     }
 }
 
-template <int FMT, int NT, int XT, int WT>
+template <int FMT, int NT, int XT, int WT, bool LONG>
 rf_status launch(const Params &p, int grid, cudaStream_t s)
 {
     using C = Few<FMT, NT, XT, WT>;
@@ -436,22 +442,22 @@ rf_status launch(const Params &p, int grid, cudaStream_t s)
         return RF_ERR_CUDA;
     }
     std::call_once(once[dev & 63], [dev] {
-        ok[dev & 63] = cudaFuncSetAttribute(few_kernel<FMT, NT, XT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
+        ok[dev & 63] = cudaFuncSetAttribute(few_kernel<FMT, NT, XT, WT, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
                        cudaSuccess;
         cudaGetLastError();
     });
     if (!ok[dev & 63]) return RF_ERR_CUDA;
-    few_kernel<FMT, NT, XT, WT><<<grid, 32 * (kWarps + 1), C::SMEM, s>>>(p);
+    few_kernel<FMT, NT, XT, WT, LONG><<<grid, 32 * (kWarps + 1), C::SMEM, s>>>(p);
     return last_cuda_error();
 }
 
 template <int FMT, int NT>
 rf_status launch_terms(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)
 {
-    if (sh.xt == 2) return launch<FMT, NT, 2, FMT == RF_MXFP4 ? 1 : 2>(p, grid, s);
+    if (sh.xt == 2) return launch<FMT, NT, 2, FMT == RF_MXFP4 ? 1 : 2, false>(p, grid, s);
     if constexpr (FMT != RF_MXFP4)
-        if (sh.wt == 2) return launch<FMT, NT, 1, 2>(p, grid, s);
-    return launch<FMT, NT, 1, 1>(p, grid, s);
+        if (sh.wt == 2) return sh.segments ? launch<FMT, NT, 1, 2, true>(p, grid, s) : launch<FMT, NT, 1, 2, false>(p, grid, s);
+    return sh.segments ? launch<FMT, NT, 1, 1, true>(p, grid, s) : launch<FMT, NT, 1, 1, false>(p, grid, s);
 }
 template <int FMT>
 rf_status launch_fmt(const ChunkShape &sh, const Params &p, int grid, cudaStream_t s)

@@ -828,7 +828,7 @@ rf_status launch_chunk_mma(const ChunkGemm &g, cudaStream_t s)
     p.sums = reinterpret_cast<float *>(g.ws + sh.at_sums);
     p.held = reinterpret_cast<float *>(g.ws + sh.at_held);
     p.segment = sh.segment;
-    p.held_rows = sh.held ? sh.nt : 0;
+    p.held_rows = sh.segments ? sh.nt : 0;
     const int grid = (int)std::min<int64_t>(num_sms(), sh.cap_tiles * p.nrt * p.parts);
     rf_status st;
     if (sh.few) st = launch_chunk_few(sh, p, s);
