@@ -114,8 +114,8 @@ struct Cfg {
     // zero), rounded additions in registers do not drift.  Q4_K's weights have
     // a mean, so that its sums grow over a row: sooner (1.3e-6 against 0.7e-6
     // from 64 bits in a routed FFN).
-    // (16-bit calls: Params::segment slices, see chunk_shape.)
-    static constexpr int FLUSH = XT == 1 ? 4 : (FMT == RF_Q4_K ? 2 : 4);
+    // 16-bit calls' leave it at the end of the row, or of a segment of it (LONG).
+    static constexpr int FLUSH = XT == 1 ? 1 << 30 : (FMT == RF_Q4_K ? 2 : 4);
     // Shared memory: stages of activations, raw chunks, and 16 bytes that a
     // last load may touch.  Activations come from L2 in about as long as eight
     // slices take; the weights come from memory and get the rest.
@@ -234,7 +234,13 @@ __device__ __forceinline__ void bar_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <int FMT, int NT, int XT, int WT>
+// LONG: 16-bit rows of several segments.  A form of its own, because with the
+// segment's length as a variable every row pays (2048 bf16 tokens through
+// 2 x 11008 x 4096 274 against 272 us, 5000 fp16 rows of 24 groups 158 against
+// 156, the routed FFN of 2048 tokens 749 against 743); segments cost long rows 0
+// to 1 % (2048 bf16 tokens through 4096 x 32768 506 us either way, fp16 through
+// 4096 x 11008 308 against 305).
+template <int FMT, int NT, int XT, int WT, bool LONG>
 __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<FMT, NT, XT, WT>;
@@ -421,9 +427,9 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                 bar_arrive(bar(C::IEMPTY + slot));
                 if (end) break;
                 const uint32_t id = WT == 2 && XT == 2 ? idesc_n((grans + 1) / 2 * 16) : idesc_n(kGranRows * grans);
-                const int flush = (XT == 1 ? p.segment : C::FLUSH) - 1;
+                const int flush = LONG ? p.segment : C::FLUSH;
                 for (int b = 0; b < nsl;) {
-                    const bool fresh = (b & flush) == 0;
+                    const bool fresh = (b & (flush - 1)) == 0;
                     const uint32_t acc = tmem + (seg % NBUF) * C::ACC;
                     if (fresh) {
                         if (!(ok = wait(bar(C::ACCE + seg % NBUF), ((seg / NBUF) & 1) ^ 1))) break;
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
                     bar_commit(b_done);
                     ready = b_next && f_next;
                     b += KS;
-                    if (b >= nsl || (b & flush) == 0) {
+                    if (b >= nsl || (b & (flush - 1)) == 0) {
                         bar_commit(bar(C::ACCF + seg % NBUF));
                         ++seg;
                     }
@@ -597,10 +603,10 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
             if constexpr (XT == 1) {
                 bool ok = true;
 #pragma unroll 1
-                for (int b0 = 0; b0 < nsl; b0 += p.segment) {
+                for (int b0 = 0; b0 < (LONG ? nsl : 1); b0 += LONG ? p.segment : 1) {
                     // Sums so far, this thread's own: of a row that has several segments.
-                    float *held = p.held + ((int64_t)blockIdx.x * p.held_rows * kM + 32 * w4 + lane);
-                    const bool last = b0 + p.segment >= nsl;
+                    [[maybe_unused]] float *held = LONG ? p.held + ((int64_t)blockIdx.x * p.held_rows * kM + 32 * w4 + lane) : nullptr;
+                    const bool last = !LONG || b0 + p.segment >= nsl;
                     float next[16];
                     load_inv(inv, next);
                     if (!(ok = waits(bar(C::ACCF + seg % NBUF), (seg / NBUF) & 1))) break;
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__((Cfg<FMT, NT, XT, WT>::THREADS), 1) chunk_kern
 #pragma unroll
                         for (int u = 0; u < 16; ++u) z[u] = __uint_as_float(v[u]);
                         if (t0 + 16 >= w.cnt) release();
-                        if (b0 > 0) {
+                        if (LONG && b0 > 0) {
 #pragma unroll
                             for (int u = 0; u < 16; ++u) z[u] += held[(t0 + u) * kM];
                         }
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(128) join_parts_kernel(const __grid_constant__
     }
 }
 
-template <int FMT, int NT, int XT, int WT>
+template <int FMT, int NT, int XT, int WT, bool LONG>
 rf_status launch(Params &p, int grid, cudaStream_t s)
 {
     using C = Cfg<FMT, NT, XT, WT>;
@@ -734,7 +740,7 @@ rf_status launch(Params &p, int grid, cudaStream_t s)
         return RF_ERR_CUDA;
     }
     std::call_once(once[dev & 63], [dev] {
-        ok[dev & 63] = cudaFuncSetAttribute(chunk_kernel<FMT, NT, XT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        ok[dev & 63] = cudaFuncSetAttribute(chunk_kernel<FMT, NT, XT, WT, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             (int)C::SMEM) == cudaSuccess;
         cudaGetLastError();
     });
@@ -743,19 +749,24 @@ rf_status launch(Params &p, int grid, cudaStream_t s)
     p.raws = std::min(kRaws, (C::SHARED - C::LEAST * stage) / C::RAW);
     p.slots = std::min(kInFlight, (C::SHARED - p.raws * C::RAW) / stage);
     p.raw_at = (uint32_t)(p.slots * stage);
-    chunk_kernel<FMT, NT, XT, WT><<<grid, C::THREADS, C::SMEM, s>>>(p);
+    chunk_kernel<FMT, NT, XT, WT, LONG><<<grid, C::THREADS, C::SMEM, s>>>(p);
     return last_cuda_error();
 }
 
+// One fp16 term an activation: rows of several segments, or of one.
+template <int FMT, int NT, int WT>
+rf_status launch_one(const ChunkShape &sh, Params &p, int grid, cudaStream_t s)
+{
+    return sh.segments ? launch<FMT, NT, 1, WT, true>(p, grid, s) : launch<FMT, NT, 1, WT, false>(p, grid, s);
+}
 template <int FMT>
 rf_status launch_fmt(const ChunkShape &sh, Params &p, int grid, cudaStream_t s)
 {
-    if constexpr (FMT != RF_MXFP4) {
-        if (sh.wt == 2) return sh.xt == 2 ? launch<FMT, 128, 2, 2>(p, grid, s) : launch<FMT, 128, 1, 2>(p, grid, s);
-    } else {
-        if (sh.xt == 2) return launch<FMT, 128, 2, 1>(p, grid, s);
-    }
-    return sh.nt > 128 ? launch<FMT, 192, 1, 1>(p, grid, s) : launch<FMT, 128, 1, 1>(p, grid, s);
+    constexpr int WT = FMT == RF_MXFP4 ? 1 : 2;
+    if (sh.xt == 2) return launch<FMT, 128, 2, WT, false>(p, grid, s);
+    if constexpr (WT == 2)
+        if (sh.wt == 2) return launch_one<FMT, 128, 2>(sh, p, grid, s);
+    return sh.nt > 128 ? launch_one<FMT, 192, 1>(sh, p, grid, s) : launch_one<FMT, 128, 1>(sh, p, grid, s);
 }
 
 }  // namespace
