@@ -794,7 +794,8 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  * rows and of groups chooses the kernel and how sums are shared out).
  * Weight tensors: 16-byte aligned, rows of rf_row_bytes each; all bytes of the
  * tensors given may be read.  Workspaces: device, 256-byte aligned, at least
- * the stated bytes, overwritten, used by one call at a time. */
+ * the stated bytes, overwritten, used by one call at a time; the bytes stated
+ * for some number of rows or tokens do for every call of fewer as well. */
 #define RF_Y_F32 256
 #define RF_ACT_NONE 0           /* z */
 #define RF_ACT_SILU 1           /* z / (1 + exp(-z)) */

@@ -42,6 +42,7 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = 8;         // tokens per CTA of the pre-pass
 constexpr int64_t kMaxPieces = 1LL << 30;
 constexpr int64_t kMaxSums = 16LL << 20;   // floats of parts' sums at most
+constexpr int64_t kMaxParts = 16;
 
 template <int DT> struct Elem;
 template <> struct Elem<RF_F32> { using T = float; };
@@ -472,7 +473,7 @@ void choose_parts(ChunkShape &sh, bool gated)
     };
     int64_t best = 1;
     if (items < 4 * sms)
-        for (int64_t parts = 2; parts <= std::min<int64_t>(nch, 16); ++parts)
+        for (int64_t parts = 2; parts <= std::min<int64_t>(nch, kMaxParts); ++parts)
             if (10 * cost(parts) < 9 * cost(1) && cost(parts) < cost(best) &&
                 parts * (1 + gated) * sh.n_row * sh.rows <= kMaxSums)
                 best = parts;
@@ -519,10 +520,20 @@ ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_
     choose_parts(sh, gated);
     sh.segment = dtype == RF_BF16 ? kSegmentBf16 : kSegment;
     sh.segments = sh.xt == 1 && std::min(sh.nst, sh.part_chunks * per) > sh.segment;
+    // Every region's size grows with the rows, whatever tile they take (images
+    // of whole chunks as few rows have them, tiles as of four tokens).
+    const int64_t nch = (sh.nst + per - 1) / per;
     size_t at = sizeof(ChunkPlan);
-    sh.at_tiles = at, at = up256(at + (size_t)sh.cap_tiles * sizeof(ChunkTile));
+    sh.at_tiles = at, at = up256(at + (size_t)(n_row / 4 + n_group) * sizeof(ChunkTile));
     sh.at_inv = at, at = up256(at + (size_t)sh.cap_gran * GT * sizeof(float));
-    sh.at_img = at, at = up256(at + (size_t)sh.cap_gran * sh.nst * sh.gran_bytes());
+    sh.at_img = at, at = up256(at + (size_t)sh.cap_gran * nch * per * sh.gran_bytes());
+    // Parts are for calls of few items, hence of fewer rows than n_part; all of
+    // them take segments that whole rows of a call may take.
+    const int64_t nrt = (rows + (gated ? 63 : 127)) / (gated ? 64 : 128), few_items = 4 * num_sms();
+    const int64_t n_part = nrt > 0 && nrt < few_items ? std::min(n_row, T * (few_items / nrt + 1)) : 0;
+    const int64_t sums = std::min(kMaxSums, std::min(nch, kMaxParts) * (1 + gated) * n_part * rows);
+    const bool held = sh.xt == 1 && !sh.few && sh.nst > sh.segment;
+    sh.upto = up256(at + (size_t)sums * sizeof(float)) + (held ? up256((size_t)num_sms() * sh.nt * 128 * sizeof(float)) : 0);
     sh.at_sums = at;
     if (sh.parts > 1) at = up256(at + (size_t)sh.parts * (1 + gated) * n_row * rows * sizeof(float));
     sh.at_held = at;
@@ -639,7 +650,7 @@ struct MoeLayout {
     size_t at_idx, at_w, at_offsets, at_order, at_place, at_route, at_product, at_h, bytes;
     int64_t ldd;   // row stride of the experts' outputs
 };
-MoeLayout moe_layout(int fmt, int n_expert, int top_k, int64_t n_ff, int64_t n_embd, int dtype, int64_t n_tok)
+MoeLayout moe_layout(int fmt, int n_expert, int top_k, int64_t n_ff, int64_t n_embd, int dtype, int64_t n_tok, bool upto = false)
 {
     MoeLayout m;
     const int64_t n_row = n_tok * top_k;
@@ -655,7 +666,8 @@ MoeLayout moe_layout(int fmt, int n_expert, int top_k, int64_t n_ff, int64_t n_e
     m.at_idx = take(4 * n_row), m.at_w = take(4 * n_row), m.at_offsets = take(4 * ((size_t)n_expert + 1));
     m.at_order = take(4 * n_row), m.at_place = take(4 * n_row);
     m.at_route = take(route_workspace(n_tok, n_expert, top_k));
-    m.at_product = take(std::max(m.up.bytes, m.down.bytes));   // the second product prepares after the first has run
+    // (upto: for this call and every one of fewer tokens.)
+    m.at_product = take(upto ? std::max(m.up.upto, m.down.upto) : std::max(m.up.bytes, m.down.bytes));   // the second product prepares after the first has run
     m.at_h = take(4 * (size_t)n_row * std::max(n_ff, n_embd)); // h, read before the experts' outputs are written
     m.bytes = at;
     return m;
@@ -694,8 +706,8 @@ extern "C" {
 size_t rf_gemm_grouped_workspace_bytes(int fmt, int n_group, int64_t rows, int64_t in_dim, int dtype, int64_t n_row)
 {
     if (check_sizes(fmt, dtype, n_group, rows, in_dim, n_row) != RF_OK || rows == 0 || n_row == 0) return 0;
-    return std::max(chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, false).bytes,
-                    chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, true).bytes);
+    return std::max(chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, false).upto,
+                    chunk_shape(fmt, dtype, n_group, rows, in_dim, n_row, true).upto);
 }
 
 size_t rf_gemm_fused_workspace_bytes(int fmt, int64_t rows, int64_t in_dim, int dtype, int64_t n_tok)
@@ -780,7 +792,7 @@ size_t rf_moe_tokens_workspace_bytes(int fmt, int n_expert, int top_k, int64_t n
     if (check_sizes(fmt, dtype, n_expert, n_ff, n_embd, n_tok * top_k) != RF_OK ||
         check_sizes(fmt, dtype, n_expert, n_embd, n_ff, n_tok * top_k) != RF_OK)
         return 0;
-    return moe_layout(fmt, n_expert, top_k, n_ff, n_embd, dtype, n_tok).bytes;
+    return moe_layout(fmt, n_expert, top_k, n_ff, n_embd, dtype, n_tok, true).bytes;
 }
 
 rf_status rf_moe_ffn_tokens(int fmt, int dtype, int logits_dtype, const void *logits, int64_t ld_logits, int n_expert,

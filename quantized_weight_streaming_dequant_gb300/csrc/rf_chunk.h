@@ -41,6 +41,7 @@ struct ChunkShape {
     bool segments;                           // a part has several such segments
     size_t at_tiles, at_inv, at_img, at_sums, at_held, bytes;   // workspace: plan, tiles, 1 / row scale, images, parts'
                                                                 // sums, segments' sums (a tile for each CTA)
+    size_t upto;                             // bytes that do for this call and every one of fewer rows
     int tile_tokens() const { return nt / xt; }
     int gran_rows() const { return std::min(nt, kGranRows); }   // (8: half a granule)
     int gran_tokens() const { return gran_rows() / xt; }

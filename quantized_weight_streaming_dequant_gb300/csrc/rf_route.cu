@@ -262,8 +262,9 @@ size_t route_workspace(int64_t n_tok, int n_expert, int top_k)
 {
     (void)top_k;
     if (n_tok <= kOneTokens) return 0;
-    const int64_t run = run_tokens(n_tok);
-    return (size_t)((n_tok + run - 1) / run) * n_expert * sizeof(int32_t);
+    // As many runs as any chunk of up to n_tok tokens has.
+    const int64_t runs = std::min<int64_t>((n_tok + kRunTokens - 1) / kRunTokens, std::max<int64_t>(kBlocks, (n_tok + kMaxRun - 1) / kMaxRun));
+    return (size_t)runs * n_expert * sizeof(int32_t);
 }
 
 rf_status launch_route_tokens(int dtype, const void *logits, int64_t ld, int64_t n_tok, int n_expert, int top_k,
