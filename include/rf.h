@@ -897,8 +897,9 @@ RF_API size_t rf_moe_route_tokens_workspace_bytes(int64_t n_tok, int n_expert, i
  * with the routing of rf_moe_route_tokens over `logits` (n_tok rows of
  * n_expert, of logits_dtype, ld_logits apart), act RF_ACT_SWIGLU or
  * RF_ACT_SWIGLU_CLAMPED (alpha, limit), the sum in selection order.  The h
- * are kept in fp32 and enter the second product like rows of X (16-bit
- * dtypes: rounded once to fp16).  Biases and residual may be NULL; Y may be
+ * are kept in fp32 and enter the second product, which RF_F16 calls do like
+ * RF_F32 ones, as two fp16 terms (RF_BF16: rounded once to fp16, an eighth of
+ * half a step of bf16).  Biases and residual may be NULL; Y may be
  * residual (with equal strides), other overlaps are not allowed.  No host
  * synchronisation; the call can be captured.
  * Errors: as rf_gemm_grouped and rf_moe_route_tokens. */

@@ -121,3 +121,30 @@ def test_a_layer_of_experts(n_tok, dtype):
     assert np.array_equal(idx[clear], oc.route(y, k)[0][clear])
     y, bound = moe_reference(rf.MXFP4, dtype, host(o["logits"]), k, g, u, d, x, residual=resv)
     check(o["y"], y, bound, dtype)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("n_tok", [7, 40, 300])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_a_routed_ffn_is_off_by_little_more_than_its_outputs_rounding(fmt, n_tok, dtype):
+    """Each rounding inside is an eighth of half a step of the output's type at
+    most: h in fp16 calls as two fp16 terms (2^-22 of a value), in bf16 calls to
+    fp16 (2^-11 against 2^-8), as their weights of all formats but MXFP4.  Errors
+    of that size that fall evenly add 1/8 of the output's own in root mean square
+    each, in quadrature: three from up's and down's weights and from h, and one
+    from gate's, times z silu'(z) / silu(z) = 1 + z (1 - sigmoid(z)), at most 1.28
+    where silu is not small: sqrt(1 + (3 + 1.28^2) / 64), 3.6 % over it; in fp16
+    calls nothing that shows."""
+    rng = np.random.default_rng([n_tok, 8])
+    E, k, ff, embd = 7, 2, 512, 768
+    G, g = raw(fmt, E, ff, embd, 1)
+    U, u = raw(fmt, E, ff, embd, 2)
+    D, d = raw(fmt, E, embd, ff, 3)
+    x, xv = randn(rng, (n_tok, embd), dtype)
+    logits, lv = randn(rng, (n_tok, E), "float32")
+    got = rf.moe_ffn_tokens(fmt, logits, k, G, U, D, ff, embd, x)
+    y, b = moe_reference(fmt, dtype, lv, k, g, u, d, xv)
+    check(got, y, b, dtype)
+    rms = lambda a: float(np.sqrt(np.mean((a / np.abs(y).max(1, keepdims=True)) ** 2)))  # noqa: E731
+    own = rms(torch.from_numpy(y).to(x.dtype).double().numpy() - y)
+    assert rms(host(got) - y) <= (1.005 if dtype == "float16" else 1.036) * own
