@@ -776,8 +776,9 @@ RF_API size_t rf_attention_workspace_bytes(const rf_kv_cache *cache, const rf_kv
  * additions after 256 inputs (RF_F32), 4,096 (RF_F16, and with RF_Y_F32) or
  * 16,384 (RF_BF16) at most.  X's values enter
  *   RF_F16        as they are;
- *   RF_F32, BF16  after their row was scaled by a power of two that puts its
- *                 largest finite value at [2^14, 2^15): RF_F32 as two fp16
+ *   RF_F32, BF16  after their row was scaled by a power of two, at most 2^126,
+ *                 that puts its largest finite value (of rows from 2^-112 on) at
+ *                 [2^14, 2^15): RF_F32 as two fp16
  *                 terms (22 bits; below 2^-28 of the row's largest: to 2^-50
  *                 of it), RF_BF16 as they are (below 2^-28 of the largest: to
  *                 2^-39 of it).

@@ -455,9 +455,12 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // slice's by what bounds it, 4,000 an item (2,500 where two CTAs share the SM),
 // 3,500 a launch, 1,500 bytes of sums a cycle.  9 fp32 tokens through
 // 2 x 11008 x 4096 Q4_0: 46 us, in one part 60; 8 tokens 36, in one part 43; 77
-// through 4099 x 4096 Q4_K 40, in one 60.  (The last part's warps adding the
-// sums in the product's launch instead of a second one: 60 us against 55 in the
-// first case, they read them one latency after another.)
+// through 4099 x 4096 Q4_K 40, in one 60.  An estimate, fitted to such calls
+// through one matrix: it takes a round for one CTA an SM also where two share
+// it, and the tiles of groups for what the rows of a group on average need.
+// (The last part's warps adding the sums in the product's launch instead of a
+// second one: 60 us against 55 in the first case, they read them one latency
+// after another.)
 void choose_parts(ChunkShape &sh, bool gated)
 {
     const int64_t tiles = sh.n_group == 1 ? (sh.n_row + sh.tile_tokens() - 1) / sh.tile_tokens()
@@ -491,20 +494,27 @@ constexpr int kSegment = 64, kSegmentBf16 = 256;
 // The operands of a product of n_row rows shared by n_group groups.  Tiles of
 // 192 operand rows where the groups fill them (a weight slice is decoded once
 // per tile), of 128 where they do not; both let tensor memory hold two items'
-// sums, so that an epilogue runs beside the next item's products.  Tiles of up
-// to 16 operand rows multiply from registers (rf_chunk_few.cu): 8 bf16 tokens
-// through 2 x 11008 x 4096 Q4_0 31 us against 45, 16 tokens 37 against 45, 8
-// fp32 tokens 45 against 52 (with the parts and loads of then), 128 fp32 tokens through 128 MXFP4 experts 505
-// against 529 (but 256 bf16 tokens 565 against 531); with 32 rows a tile they
-// were no faster (32 bf16 tokens 50 against 45, 32 fp16 tokens through Q8_0 66
-// against 50, 256 fp32 tokens through the experts 805 against 621).  (Tiles of 160 rows, which fill the last
-// round of 2048 tokens through 4096 x 11008 better, take 214 us against 182.)
+// sums, so that an epilogue runs beside the next item's products.  (Tiles of 160
+// rows, which fill the last round of 2048 tokens through 4096 x 11008 better,
+// take 214 us against 182.)  Tiles of up to 16 operand rows multiply from
+// registers (rf_chunk_few.cu), us against the way through tensor memory: 8 bf16
+// tokens through 2 x 11008 x 4096 Q4_0 28 against 41, 16 32 against 41; 4 fp32
+// tokens 32 against 45, 8 35 against 46; 77 bf16 tokens through 128 MXFP4
+// experts of 2880 314 against 372, 128 396 against 422, 128 fp32 tokens 471
+// against 484.  Two terms of weights for 16 rows are the exceptions (fp16 tokens:
+// Q4_0 45 against 43, Q4_K 79 against 61), and groups well below 16 rows that
+// come in tiles of 16 (256 bf16 tokens through the experts 511 against 482).
+// Two such tiles instead of one of 32 rows: 32 bf16 tokens 47 against 43, 32 fp16
+// 63 against 47, 16 fp32 60 against 46.
 ChunkShape chunk_shape(int fmt, int dtype, int64_t n_group, int64_t rows, int64_t in_dim, int64_t n_row, bool gated)
 {
     ChunkShape sh;
     sh.fmt = fmt;
     sh.xt = x_dtype(dtype) == RF_F32 ? 2 : 1;
-    // (A weight's rounding to fp16 is an eighth of half a step of a bf16 output, but most of what an fp32 one is off by.)
+    // bf16 outputs: a weight's rounding to fp16 is an eighth of half a step.  2048
+    // tokens through 2 x 11008 x 4096 Q4_0 end 1.68e-3 from 64 bits (their own
+    // rounding: 1.66e-3) in 274 us; two terms take 472.  Of an fp32 output it
+    // would be most of the error.
     sh.wt = dtype != RF_BF16 && fmt != RF_MXFP4 ? 2 : 1;
     sh.n_row = n_row, sh.n_group = n_group, sh.rows = rows, sh.in_dim = in_dim;
     sh.nst = (int)((in_dim + kSliceK - 1) / kSliceK);

@@ -64,7 +64,7 @@ struct Params {
 
 // Row of a half of the tile for each of its 64 threads (tensor-memory lanes):
 // neighbours take rows at the same position of successive super-rows, which
-// lie box_bytes apart.
+// lie box_bytes apart (and store to columns P apart).
 __device__ __forceinline__ int lane_row(int e, int logP) { return ((e & ((64 >> logP) - 1)) << logP) + (e >> (6 - logP)); }
 
 // ------------------------------------------------------------------ decoding

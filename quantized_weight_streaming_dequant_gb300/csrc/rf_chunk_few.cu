@@ -27,14 +27,16 @@
 // Bound.  By 2048 weights (a warp's 16 rows x 128 inputs, MXFP4, one term) an
 // SM takes about 75 cycles: 32 of the tensor cores (16 a product and SM
 // quarter), 40 of integer instructions, 46 of memory; 16 warps an SM overlap
-// them as far as their registers (96 a thread) let them.  The copies alone run
-// at the measured memory rate.  Measured, us a call on the GPU:
+// them as far as their registers (96 a thread) let them.  The copies are a limit
+// of their own: alone they run at 5.2 TB/s in the first case (87 of the experts
+// have rows, 1.15 GB) and at 4.1 in the third, of 6.8 measured.  Measured, us a
+// call on the GPU:
 //                                                   here   through tensor memory
-//   77 bf16 tokens, 128 experts of 2880 MXFP4        312   440   (copies alone: 224)
-//   6 fp32 tokens, the same                           98   150   (copies alone:  79,
+//   77 bf16 tokens, 128 experts of 2880 MXFP4        314   372   (copies alone: 224)
+//   6 fp32 tokens, the same                           98   135   (copies alone:  79,
 //                                                         with a slower pre-pass)
-//   45 fp32 rows, 64 groups of 1408 x 2048 Q8_0       34    59   (copies alone:  28)
-//   8 bf16 tokens, 2 x 11008 x 4096 Q4_0              31    45
+//   45 fp32 rows, 64 groups of 1408 x 2048 Q8_0       34    51   (copies alone:  28)
+//   8 bf16 tokens, 2 x 11008 x 4096 Q4_0              28    41
 // Steps (first case, us): 458 with all of a block decoded before its products
 // and 8-byte loads; 412 with 4-byte loads, the item's end prefetched and one
 // address for both rows; 370 with tiles of 8 operand rows; 348 with a chunk's

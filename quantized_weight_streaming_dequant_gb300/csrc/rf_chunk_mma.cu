@@ -48,8 +48,11 @@
 //   8192 bf16 rows, 128 experts of 2880 x 2880 MXFP4, gate, up and down:
 //                                              666   0.61 PFLOP/s, 2.5 TB/s
 //   5000 fp16 rows (two terms), 24 groups of 4000 x 2080 Q4_0:   142
-// The first with products alone (no copies, no decoding): 180; the third, with
-// stages of two slices: 440 (684 in all).
+// The first with products alone (no copies, no decoding): 180.  Items are drawn
+// four ahead, so that a CTA's last four are fixed early: with few items an SM
+// nothing is left to even out.  Neighbouring lanes of an epilogue hold rows P
+// apart (lane_row): where rows are no multiples of 16 bytes (P = 8 for 2,880
+// MXFP4 inputs) a warp's store of 32 values touches 16 to 32 sectors.
 // Tried and not kept (the first case, us, against 268 at the time unless said
 // otherwise): tiles of 256 rows, whose sums fit once, 308; activations in a ring
 // of bytes instead of slots, 460 against 295; the issuing role in lane 0 by

@@ -11,9 +11,11 @@
 // Within a run, warps take consecutive pieces, and a warp's rows of the same
 // expert find their rank with one match.  Up to kOneTokens tokens take one
 // launch of one block, more take two launches.
-// Bound: latency of two short launches; 2.6 MB for 8192 tokens of 128 bf16
-// logits are 0.4 us of memory time, and the two launches take 5 and 7 (4 and 5
-// with the logits in L2); 5 tokens of 128 fp32 logits take 3.
+// Bound: chains of dependent steps in two short launches (place: the runs'
+// counts, a scan over the experts, ranks by match, each behind a barrier).
+// 2.6 MB for 8192 tokens of 128 bf16 logits are 0.4 us of memory time, and the
+// two launches take 5 and 7 (4 and 5 with the logits in L2); 5 tokens of 128
+// fp32 logits take 3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
